@@ -283,6 +283,108 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
                                  int64_t N, int bits, int group_size, int y_dtype, void *y,
                                  void *stream);
 
+/* ---- 4-bit key/value cache --------------------------------------------------
+ *
+ * What stands between the QKV product and the O product when a decoder serves:
+ * keys and values quantized as they enter a paged cache, and attention that
+ * reads the cache.  Codes and scales are the int4 ones of the definitions
+ * above, one scale per group_size consecutive elements of a head:
+ *   s = absmax / 7 (fp32, correctly rounded), q = clamp(rint(x / s), -8, 7),
+ *   stored nibble u = q + 8; the value a code stands for is s * (u - 8).
+ *
+ * A batch holds `batch` sequences.  Sequence b brings the rows
+ * row_start[b] .. row_start[b + 1] - 1 (n_b of them) to the call and holds
+ * kv_len[b] tokens in the cache once they are in it, so its row i is the token
+ * at position p = kv_len[b] - n_b + i.  A row at p < 0 is not there: append
+ * skips it, read and attention write zeros (a slot a program pads its batch
+ * with: one row, kv_len 0).
+ *
+ * Pages: a page holds 64 consecutive tokens of one sequence; token t of
+ * sequence b is in page pages[b][t / 64] at t % 64.  The cache is
+ * uint8 [num_pages][kv_heads][block], a block being one head of one page,
+ * 64 * D + 512 * (D / group_size) bytes (D = head_dim):
+ *   K codes   dword (t, j, m), t < 64, j < 4, m < D/32, row-major:
+ *             nibble e is element d = 32 m + 8 j + e of token t;
+ *   V codes   dword (B, g, j, c, x), B < 2, g < D/64, j < 4, c < 16, x < 4,
+ *             row-major: nibble 4 b + i is token 32 B + 16 b + 4 j + i,
+ *             element d = 64 g + 16 x + c;
+ *   K scales  fp32 [D / group_size][64],  V scales  fp32 [D / group_size][64].
+ * Memory of a page may hold anything before its tokens are written.
+ *
+ * The device arrays are read by the kernels only, with these bounds: kv_len
+ * outside [0, max_kv_len] is taken as the nearer end; a sequence whose row
+ * range is not inside [0, rows] or longer than max_rows is left out (its rows
+ * are not written); a page number outside [0, num_pages) is never followed
+ * (append skips its tokens, read writes zeros for them, attention does not
+ * see them).  max_kv_len and max_rows also size the launches, so calls
+ * captured into a graph replay with any lengths up to them.  Two sequences
+ * may share pages (a common prefix) as long as no call appends to them.
+ *
+ * Envelope: head_dim 64 or 128, group_size 64 or 128 dividing it,
+ * batch, rows, max_rows >= 0, 0 <= max_kv_len <= 64 * max_pages <= 2^30,
+ * 1 <= num_pages < 2^31, 1 <= kv_heads <= 65536, q_heads a multiple of
+ * kv_heads up to 65536, rows * q_heads <= 2^30, batch * kv_heads times the
+ * 32-token spans (16-column tiles) of a sequence < 2^31; pointers 16-byte
+ * aligned (int32 arrays: 4), row strides in elements, multiples of 8, at
+ * least the row's heads * head_dim.  batch, rows or max_rows 0 is a no-op. */
+typedef struct {
+    void *cache;              /* uint8 [num_pages][kv_heads][block] */
+    const int32_t *pages;     /* [batch][max_pages] */
+    const int32_t *row_start; /* [batch + 1], ascending */
+    const int32_t *kv_len;    /* [batch] tokens cached, this call's rows among them */
+    int64_t batch, rows;      /* sequences; rows of all of them in this call */
+    int64_t max_rows;         /* bound on the rows of one sequence */
+    int64_t max_kv_len;       /* bound on kv_len */
+    int64_t max_pages;        /* row length of `pages` */
+    int64_t num_pages, kv_heads, head_dim;
+    int group_size;
+} cider_kv4_batch;
+
+/* Bytes of a cache of this geometry; 0 outside the envelope. */
+size_t cider_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_dim, int group_size);
+
+/* Quantizes the batch's rows into the cache.  k, v: [rows][kv_heads][head_dim]
+   of type dtype with row strides ldk, ldv (the columns of a fused QKV
+   product's output are read in place).  Tokens already in a page stay as they
+   are; a token that is appended again is overwritten.  No two sequences of the
+   call may append to the same page. */
+cider_status cider_kv4_append(const cider_kv4_batch *b, const void *k, const void *v, int dtype,
+                              int64_t ldk, int64_t ldv, void *stream);
+
+/* Reads the cached values of the batch's rows back: the fp32 product s * (u - 8) rounded
+   to dtype (n_b = kv_len[b] reads a whole sequence).  k, v:
+   [rows][kv_heads][head_dim] with row strides ldk, ldv. */
+cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtype, int64_t ldk,
+                            int64_t ldv, void *stream);
+
+/* Causal attention of the batch's rows over the cache (grouped query heads:
+   query head h reads kv head h / (q_heads / kv_heads)):
+     t visible from p:  t <= p, and t > p - window or t < sinks (window > 0;
+                        window 0: every t <= p)
+     S[t] = scale * sum_d q[d] * K[t, d],  P[t] = exp(S[t] - max S)
+     y[d] = sum_t P[t] * V[t, d] / sum_t P[t];  no visible t: y = 0
+   with K, V the values the codes stand for, sums and softmax in fp32.  The
+   rows' own tokens must have been appended before.  q, y:
+   [rows][q_heads][head_dim] of types q_dtype, y_dtype, row strides ldq, ldy.
+   scale finite and positive; window, sinks >= 0 (the first `sinks` tokens stay
+   visible behind a window).  One row per sequence is a decoding step, a few
+   are drafted tokens, many a prompt or a chunk of one.
+   workspace: device scratch of any size, or null; given
+   cider_kv4_attention_workspace_bytes(...) bytes, long caches with few rows
+   are split over more workgroups (fp32 partial results, added in order:
+   results do not depend on timing); given fewer the call splits less or not
+   at all.  Calls that share a workspace must be ordered (one stream). */
+cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_dtype, int64_t ldq,
+                                 int64_t q_heads, float scale, int64_t window, int64_t sinks,
+                                 void *workspace, size_t workspace_bytes, void *y, int y_dtype,
+                                 int64_t ldy, void *stream);
+
+/* Bytes of workspace with which the attention call splits as far as it
+   measured faster (0 for shapes that are never split, and outside the
+   envelope).  Reads only the sizes of *b, no device memory. */
+size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
+                                           int64_t window, int64_t sinks);
+
 /* Test hook: force the product path for subsequent calls in this process.
    0 = automatic (M * K <= 65536 and M <= 8, or M <= 4 for int4 weights ->
    matrix-vector, else matrix cores),

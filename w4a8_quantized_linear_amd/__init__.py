@@ -37,7 +37,11 @@ EXPORTS = (
     "cider_quantize_weight_clipped", "cider_quantize_weight_ex", "cider_smooth_fold_weight",
     "cider_quantize_act_ex", "cider_gemm_ex", "cider_linear_ex", "cider_decode_linear",
     "cider_linear_ex_noalloc",
+    "cider_kv4_cache_bytes", "cider_kv4_append", "cider_kv4_read", "cider_kv4_attention",
+    "cider_kv4_attention_workspace_bytes",
 )
+
+KV4_PAGE_TOKENS = 64
 
 CIDER_DTYPE_F16 = 0
 CIDER_DTYPE_BF16 = 1
@@ -47,6 +51,22 @@ class CiderError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__("%s failed: %s (status %d)" % (what, cider_status_str(status), status))
+
+
+class cider_kv4_batch(ctypes.Structure):
+    """The batch of a cider_kv4_* call (the struct of include/cider.h): a paged
+    4-bit key/value cache, its page table, and the rows and lengths of each
+    sequence.  Tensors are kept alive as long as the object is."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("cache", "pages", "row_start", "kv_len")] +
+                [(n, ctypes.c_int64) for n in ("batch", "rows", "max_rows", "max_kv_len", "max_pages",
+                                               "num_pages", "kv_heads", "head_dim")] +
+                [("group_size", ctypes.c_int)])
+
+    def __init__(self, cache, pages, row_start, kv_len, batch, rows, max_rows, max_kv_len, max_pages,
+                 num_pages, kv_heads, head_dim, group_size):
+        super().__init__(_ptr(cache), _ptr(pages), _ptr(row_start), _ptr(kv_len), batch, rows, max_rows,
+                         max_kv_len, max_pages, num_pages, kv_heads, head_dim, group_size)
+        self._tensors = (cache, pages, row_start, kv_len)
 
 
 _lib: ctypes.CDLL | None = None
@@ -87,6 +107,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "cider_w8a8_linear": ([P, I64, I64, I64, P, P, I64, I, P, SZ, P, P], I),
         "cider_w4a8_linear": ([P, I64, I64, I64, P, P, I64, I, P, SZ, P, P], I),
         "cider_set_path": ([I], I),
+        "cider_kv4_cache_bytes": ([I64, I64, I64, I], SZ),
+        "cider_kv4_append": ([P, P, P, I, I64, I64, P], I),
+        "cider_kv4_read": ([P, P, P, I, I64, I64, P], I),
+        "cider_kv4_attention": ([P, P, I, I64, I64, ctypes.c_float, I64, I64, P, SZ, P, I, I64, P], I),
+        "cider_kv4_attention_workspace_bytes": ([P, I64, I64, I64], SZ),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -242,6 +267,36 @@ def cider_w4a8_linear(x_f16, M, K, ldx, wq4, s_w, N, group_size, workspace, work
     st = load().cider_w4a8_linear(_ptr(x_f16), M, K, ldx, _ptr(wq4), _ptr(s_w), N, group_size,
                                   _ptr(workspace), workspace_bytes, _ptr(y_f16), _stream(stream))
     return _ret(st, "cider_w4a8_linear", check)
+
+
+def cider_kv4_cache_bytes(num_pages, kv_heads, head_dim, group_size) -> int:
+    return int(load().cider_kv4_cache_bytes(num_pages, kv_heads, head_dim, group_size))
+
+
+def _batch(b):
+    return None if b is None else ctypes.addressof(b)
+
+
+def cider_kv4_append(b, k, v, dtype, ldk, ldv, stream=None, check=True):
+    st = load().cider_kv4_append(_batch(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
+    return _ret(st, "cider_kv4_append", check)
+
+
+def cider_kv4_read(b, k, v, dtype, ldk, ldv, stream=None, check=True):
+    st = load().cider_kv4_read(_batch(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
+    return _ret(st, "cider_kv4_read", check)
+
+
+def cider_kv4_attention(b, q, q_dtype, ldq, q_heads, scale, window, sinks, workspace,
+                        workspace_bytes, y, y_dtype, ldy, stream=None, check=True):
+    st = load().cider_kv4_attention(_batch(b), _ptr(q), q_dtype, ldq, q_heads, scale, window, sinks,
+                                    _ptr(workspace), workspace_bytes, _ptr(y), y_dtype, ldy,
+                                    _stream(stream))
+    return _ret(st, "cider_kv4_attention", check)
+
+
+def cider_kv4_attention_workspace_bytes(b, q_heads, window, sinks) -> int:
+    return int(load().cider_kv4_attention_workspace_bytes(_batch(b), q_heads, window, sinks))
 
 
 def cider_set_path(path: int) -> int:

@@ -13,6 +13,7 @@
 
 #include "cider.h"
 #include "cider_kernels.h"
+#include "kv4_layout.h"
 
 namespace {
 
@@ -343,6 +344,129 @@ cider_status run_quantize_weight(const void *w_f16, int w_dtype, int64_t N, int6
                                                      s_w, s));
 }
 
+constexpr int64_t kMaxHeads = 65536;
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions, and positions - window, fit an int
+
+// Geometry shared by every key/value cache call.
+cider_status check_kv4_geometry(int64_t num_pages, int64_t kv_heads, int64_t head_dim, int group_size)
+{
+    if (num_pages < 1 || kv_heads < 1 || head_dim < 1 || (group_size != 64 && group_size != 128))
+        return CIDER_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || head_dim % group_size != 0 || kv_heads > kMaxHeads ||
+        num_pages > kMaxInt)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    return CIDER_OK;
+}
+
+// Sizes of a batch (no pointer is looked at).
+cider_status check_kv4_sizes(const cider_kv4_batch *b)
+{
+    if (!b)
+        return CIDER_ERR_INVALID_ARG;
+    cider_status st = check_kv4_geometry(b->num_pages, b->kv_heads, b->head_dim, b->group_size);
+    if (st != CIDER_OK)
+        return st;
+    if (b->batch < 0 || b->rows < 0 || b->max_rows < 0 || b->max_kv_len < 0 || b->max_pages < 0)
+        return CIDER_ERR_INVALID_ARG;
+    if (b->batch > kMaxInt || b->rows > kMaxTokens || b->max_rows > kMaxTokens ||
+        b->max_pages > kMaxTokens / cider::kPageTokens)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    if (b->max_kv_len > b->max_pages * cider::kPageTokens)
+        return CIDER_ERR_INVALID_ARG;
+    return CIDER_OK;
+}
+
+bool kv4_empty(const cider_kv4_batch *b) { return b->batch == 0 || b->rows == 0 || b->max_rows == 0; }
+
+cider_status check_kv4_pointers(const cider_kv4_batch *b)
+{
+    if (!b->cache || !b->row_start || !b->kv_len || (b->max_pages && !b->pages))
+        return CIDER_ERR_INVALID_ARG;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(b->row_start) |
+                            reinterpret_cast<uintptr_t>(b->kv_len) | reinterpret_cast<uintptr_t>(b->pages);
+    if (!aligned16(b->cache) || (words & 3u))
+        return CIDER_ERR_MISALIGNED;
+    return CIDER_OK;
+}
+
+cider::Kv4Args kv4_args(const cider_kv4_batch *b)
+{
+    cider::Kv4Args a{};
+    a.cache = static_cast<uint8_t *>(b->cache);
+    a.pages = b->pages;
+    a.row_start = b->row_start;
+    a.kv_len = b->kv_len;
+    a.batch = (int)b->batch;
+    a.rows = (int)b->rows;
+    a.max_rows = (int)(b->max_rows < b->rows ? b->max_rows : b->rows);
+    a.max_kv_len = (int)b->max_kv_len;
+    a.max_pages = (int)b->max_pages;
+    a.num_pages = (int)b->num_pages;
+    a.kv_heads = (int)b->kv_heads;
+    a.head_dim = (int)b->head_dim;
+    a.group_size = b->group_size;
+    return a;
+}
+
+// Checks of the append and read calls; *run says whether anything is to be done.
+cider_status check_kv4_rows(const cider_kv4_batch *b, const void *k, const void *v, int dtype,
+                            int64_t ldk, int64_t ldv, bool *run)
+{
+    *run = false;
+    cider_status st = check_kv4_sizes(b);
+    if (st != CIDER_OK)
+        return st;
+    const int64_t width = b->kv_heads * b->head_dim;
+    if (!dtype_ok(dtype) || ldk < width || ldv < width)
+        return CIDER_ERR_INVALID_ARG;
+    // one workgroup per head and 32-token block that a sequence may touch
+    if (b->batch * b->kv_heads > kMaxInt ||
+        (b->max_rows / 32 + 2) > kMaxInt / (b->batch * b->kv_heads + 1))
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    if (kv4_empty(b))
+        return CIDER_OK;
+    if (!k || !v)
+        return CIDER_ERR_INVALID_ARG;
+    st = check_kv4_pointers(b);
+    if (st != CIDER_OK)
+        return st;
+    if (!aligned16(k) || !aligned16(v) || ldk % 8 != 0 || ldv % 8 != 0)
+        return CIDER_ERR_MISALIGNED;
+    if (!device_usable())
+        return CIDER_ERR_NO_DEVICE;
+    *run = true;
+    return CIDER_OK;
+}
+
+// Sizes and scalars of the attention call.
+cider_status check_kv4_attention(const cider_kv4_batch *b, int64_t q_heads, int64_t window, int64_t sinks)
+{
+    cider_status st = check_kv4_sizes(b);
+    if (st != CIDER_OK)
+        return st;
+    if (q_heads < 1 || window < 0 || sinks < 0)
+        return CIDER_ERR_INVALID_ARG;
+    if (q_heads % b->kv_heads != 0 || q_heads > kMaxHeads || b->rows * q_heads > kMaxTokens)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    // one workgroup per 16 (row, query head) pairs that share a key/value head
+    const int64_t pairs = (b->max_rows < b->rows ? b->max_rows : b->rows) * (q_heads / b->kv_heads);
+    if (b->batch * b->kv_heads > kMaxInt || (pairs / 16 + 1) > kMaxInt / (b->batch * b->kv_heads + 1))
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    return CIDER_OK;
+}
+
+cider::Kv4AttentionArgs kv4_attention_args(const cider_kv4_batch *b, int64_t q_heads, int64_t window,
+                                           int64_t sinks)
+{
+    cider::Kv4AttentionArgs a{};
+    a.kv = kv4_args(b);
+    a.q_heads = (int)q_heads;
+    a.window = (int)(window < kMaxTokens ? window : 0);  // a window past every length hides nothing
+    a.sinks = (int)(sinks < kMaxTokens ? sinks : kMaxTokens);
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -547,6 +671,80 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
     return from_hip(cider::launch_decode(static_cast<const uint16_t *>(x_f16), K, wq, s_w, N, bits,
                                          group_size, out_kind_of(y_dtype), y,
                                          static_cast<hipStream_t>(stream)));
+}
+
+size_t cider_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_dim, int group_size)
+{
+    if (check_kv4_geometry(num_pages, kv_heads, head_dim, group_size) != CIDER_OK)
+        return 0;
+    return (size_t)num_pages * (size_t)kv_heads * cider::kv4_block_bytes((int)head_dim, group_size);
+}
+
+cider_status cider_kv4_append(const cider_kv4_batch *b, const void *k, const void *v, int dtype,
+                              int64_t ldk, int64_t ldv, void *stream)
+{
+    bool run = false;
+    const cider_status st = check_kv4_rows(b, k, v, dtype, ldk, ldv, &run);
+    if (!run)
+        return st;
+    return from_hip(cider::launch_kv4_append(kv4_args(b), static_cast<const uint16_t *>(k),
+                                             static_cast<const uint16_t *>(v), dtype, ldk, ldv,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtype, int64_t ldk,
+                            int64_t ldv, void *stream)
+{
+    bool run = false;
+    const cider_status st = check_kv4_rows(b, k, v, dtype, ldk, ldv, &run);
+    if (!run)
+        return st;
+    return from_hip(cider::launch_kv4_read(kv4_args(b), static_cast<uint16_t *>(k),
+                                           static_cast<uint16_t *>(v), dtype, ldk, ldv,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_dtype, int64_t ldq,
+                                 int64_t q_heads, float scale, int64_t window, int64_t sinks,
+                                 void *workspace, size_t workspace_bytes, void *y, int y_dtype,
+                                 int64_t ldy, void *stream)
+{
+    cider_status st = check_kv4_attention(b, q_heads, window, sinks);
+    if (st != CIDER_OK)
+        return st;
+    const int64_t width = q_heads * b->head_dim;
+    if (!dtype_ok(q_dtype) || !dtype_ok(y_dtype) || ldq < width || ldy < width ||
+        !(scale > 0.0f && std::isfinite(scale)))  // NaN fails too
+        return CIDER_ERR_INVALID_ARG;
+    if (kv4_empty(b))
+        return CIDER_OK;
+    if (!q || !y)
+        return CIDER_ERR_INVALID_ARG;
+    st = check_kv4_pointers(b);
+    if (st != CIDER_OK)
+        return st;
+    if (!aligned16(q) || !aligned16(y) || ldq % 8 != 0 || ldy % 8 != 0 || !aligned16(workspace))
+        return CIDER_ERR_MISALIGNED;
+    if (!device_usable())
+        return CIDER_ERR_NO_DEVICE;
+    cider::Kv4AttentionArgs a = kv4_attention_args(b, q_heads, window, sinks);
+    a.q = static_cast<const uint16_t *>(q);
+    a.y = static_cast<uint16_t *>(y);
+    a.ldq = ldq;
+    a.ldy = ldy;
+    a.q_dtype = q_dtype;
+    a.y_dtype = y_dtype;
+    a.scale = scale;
+    (void)workspace_bytes;
+    return from_hip(cider::launch_kv4_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
+                                           int64_t window, int64_t sinks)
+{
+    if (check_kv4_attention(b, q_heads, window, sinks) != CIDER_OK)
+        return 0;
+    return 0;
 }
 
 int cider_set_path(int path)

@@ -133,4 +133,30 @@ hipError_t launch_gemv_fused(const uint16_t *x, int64_t M, int64_t K, int64_t ld
 hipError_t launch_decode(const uint16_t *x, int64_t K, const void *wq, const float *s_w, int64_t N,
                          int bits, int group_size, int out_kind, void *y, hipStream_t stream);
 
+// The 4-bit key/value cache (layout in include/cider.h and kv4_layout.h).
+struct Kv4Args {
+    uint8_t *cache;
+    const int32_t *pages;      // [batch][max_pages]
+    const int32_t *row_start;  // [batch + 1]
+    const int32_t *kv_len;     // [batch]
+    int batch, rows, max_rows, max_kv_len, max_pages, num_pages, kv_heads, head_dim, group_size;
+};
+
+// k, v: [rows][kv_heads][head_dim] of type dtype (DT_F16 / DT_BF16).
+hipError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, const uint16_t *v, int dtype,
+                             int64_t ldk, int64_t ldv, hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, int dtype, int64_t ldk,
+                           int64_t ldv, hipStream_t stream);
+
+struct Kv4AttentionArgs {
+    Kv4Args kv;
+    const uint16_t *q;
+    uint16_t *y;
+    int64_t ldq, ldy;
+    int q_dtype, y_dtype, q_heads;
+    float scale;
+    int window, sinks;  // window 0: none
+};
+hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, hipStream_t stream);
+
 }  // namespace cider
