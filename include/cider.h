@@ -324,8 +324,8 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
  * batch, rows, max_rows >= 0, 0 <= max_kv_len <= 64 * max_pages <= 2^30,
  * 1 <= num_pages < 2^31, 1 <= kv_heads <= 65536, q_heads a multiple of
  * kv_heads up to 65536, rows * q_heads <= 2^30, batch * kv_heads times the
- * 32-token spans (16-column tiles) of a sequence < 2^31; pointers 16-byte
- * aligned (int32 arrays: 4), row strides in elements, multiples of 8, at
+ * 32-token spans of max_rows (attention: batch * q_heads * max_rows) < 2^31;
+ * pointers 16-byte aligned (int32 arrays: 4), row strides in elements, multiples of 8, at
  * least the row's heads * head_dim.  batch, rows or max_rows 0 is a no-op. */
 typedef struct {
     void *cache;              /* uint8 [num_pages][kv_heads][block] */

@@ -449,9 +449,9 @@ cider_status check_kv4_attention(const cider_kv4_batch *b, int64_t q_heads, int6
         return CIDER_ERR_INVALID_ARG;
     if (q_heads % b->kv_heads != 0 || q_heads > kMaxHeads || b->rows * q_heads > kMaxTokens)
         return CIDER_ERR_UNSUPPORTED_SHAPE;
-    // one workgroup per 16 (row, query head) pairs that share a key/value head
+    // launches count workgroups in 32 bits: at most one per (row, query head) pair of the longest sequence
     const int64_t pairs = (b->max_rows < b->rows ? b->max_rows : b->rows) * (q_heads / b->kv_heads);
-    if (b->batch * b->kv_heads > kMaxInt || (pairs / 16 + 1) > kMaxInt / (b->batch * b->kv_heads + 1))
+    if (b->batch * b->kv_heads > kMaxInt || (pairs + 1) > kMaxInt / (b->batch * b->kv_heads + 1))
         return CIDER_ERR_UNSUPPORTED_SHAPE;
     return CIDER_OK;
 }
@@ -735,16 +735,15 @@ cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_
     a.q_dtype = q_dtype;
     a.y_dtype = y_dtype;
     a.scale = scale;
-    (void)workspace_bytes;
-    return from_hip(cider::launch_kv4_attention(a, static_cast<hipStream_t>(stream)));
+    return from_hip(cider::launch_kv4_attention(a, workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
 size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
                                            int64_t window, int64_t sinks)
 {
-    if (check_kv4_attention(b, q_heads, window, sinks) != CIDER_OK)
+    if (check_kv4_attention(b, q_heads, window, sinks) != CIDER_OK || kv4_empty(b))
         return 0;
-    return 0;
+    return cider::kv4_attention_workspace(kv4_attention_args(b, q_heads, window, sinks));
 }
 
 int cider_set_path(int path)

@@ -157,6 +157,10 @@ struct Kv4AttentionArgs {
     float scale;
     int window, sinks;  // window 0: none
 };
-hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, hipStream_t stream);
+// Scratch with which the call splits as far as it would, and the call itself
+// (less scratch, or none: fewer splits).
+size_t kv4_attention_workspace(const Kv4AttentionArgs &a);
+hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
 
 }  // namespace cider

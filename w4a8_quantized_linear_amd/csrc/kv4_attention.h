@@ -1,0 +1,177 @@
+// Device-side pieces that the attention kernels over the 4-bit key/value cache
+// share: the nibble operands, the queries' scaling, the pages a tile of columns
+// sees, and where its result goes.  The mathematics is stated in
+// kv4_few_rows.hip.
+#pragma once
+
+#include "kv4_layout.h"
+#include "quant_common.h"
+
+namespace cider {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Maximum of a value and the one 32 (16) lanes away (v_permlane32_swap: no LDS
+// round trip, unlike a shuffle).  The second operand is made another value in
+// the compiler's eyes: given one value twice it takes both results for equal.
+__device__ __forceinline__ float max_lane32(float v)
+{
+    unsigned u = __builtin_bit_cast(unsigned, v), w = u;
+    asm("" : "+v"(w));
+    const auto r = __builtin_amdgcn_permlane32_swap(u, w, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
+}
+__device__ __forceinline__ float max_lane16(float v)
+{
+    unsigned u = __builtin_bit_cast(unsigned, v), w = u;
+    asm("" : "+v"(w));
+    const auto r = __builtin_amdgcn_permlane16_swap(u, w, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
+}
+
+// Maximum over the wavefront, in every lane.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v)
+{
+    const int u = __builtin_bit_cast(int, v);
+    return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, CTRL, 0xF, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = max_dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = max_dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = max_dpp<0x141>(v);  // row_half_mirror
+    v = max_dpp<0x140>(v);  // row_mirror
+    return max_lane32(max_lane16(v));
+}
+
+// What a launch adds to the call's arguments.
+struct Kv4Launch {
+    int tiles;         // column tiles of the longest sequence
+    int splits;        // workgroups that a tile's pages may be dealt to
+    int pages;         // pages of one of them (splits > 1)
+    float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
+    float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
+};
+
+__device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
+
+// The 8 nibbles of a dword as fp16 operands u 2^-24, in the order 0 4 1 5 2 6
+// 3 7; elements 2, 3, 6, 7 of the result (nibbles 1, 5, 3, 7) are 16 times as
+// large.
+__device__ __forceinline__ uint4 nibble_halves(uint32_t w)
+{
+    const uint32_t hi = w >> 8;
+    return uint4{w & 0x000F000Fu, w & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u};
+}
+
+// -8 2^-24 and -128 2^-24: the codes' offset in the same order.
+constexpr uint32_t kOffset = 0x80088008u, kOffset16 = 0x80808080u;
+
+// Elements 8 i .. 8 i + 7 of a 16-bit row as fp32.
+__device__ __forceinline__ void widen8(uint4 w, int dtype, float (&x)[8])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if (dtype == DT_BF16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = widen_bits<DT_BF16>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = widen_bits<DT_F16>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+    }
+}
+
+// 8 query values times 2^shift as an operand against nibble_halves; returns
+// the operand's sum with the divided elements counted in full.
+__device__ __forceinline__ float query_operand(const float (&x)[8], int shift, half8 &op)
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int n = e / 2 + 4 * (e & 1);  // 0 4 1 5 2 6 3 7
+        const bool sixteenth = (e >> 1) & 1;
+        const _Float16 v = (_Float16)ldexp_f(x[n], sixteenth ? shift - 4 : shift);
+        op[e] = v;
+        sum += sixteenth ? 16.0f * (float)v : (float)v;
+    }
+    return sum;
+}
+
+// The pages that a tile of columns sees: [0, sink_pages) and [first, end).
+struct PageRange {
+    int sink_pages, first, count;
+    __device__ __forceinline__ int at(int i) const { return i < sink_pages ? i : first + i - sink_pages; }
+};
+
+// Columns at positions p_lo .. p_hi; count 0 where p_hi < 0.
+__device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, int sinks)
+{
+    PageRange r = {0, 0, 0};
+    if (p_hi < 0)
+        return r;
+    const int end = p_hi / kPageTokens + 1;
+    const int from = window > 0 && p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
+    r.first = from / kPageTokens;
+    const int kept = window > 0 ? (sinks < p_hi + 1 ? sinks : p_hi + 1) : 0;
+    const int kept_pages = (kept + kPageTokens - 1) / kPageTokens;
+    r.sink_pages = kept_pages < r.first ? kept_pages : r.first;
+    r.count = r.sink_pages + end - r.first;
+    return r;
+}
+
+// A tile of COLS columns of one (sequence, kv head): columns are the pairs
+// (row, query head of the group), c = row * G + g.
+struct Tile {
+    Kv4Sequence seq;
+    int h, G, tile, cols;  // cols: columns of the sequence
+    int p_lo, p_hi;        // positions of the tile's first and last column
+    PageRange range;
+};
+
+template <int COLS>
+__device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, int b, int h, int tile, Tile &t)
+{
+    t.seq = kv4_sequence(a.kv, b);
+    t.h = h;
+    t.G = a.q_heads / a.kv.kv_heads;
+    t.tile = tile;
+    t.cols = t.seq.n * t.G;
+    if ((int64_t)tile * COLS >= t.cols)
+        return false;
+    const int first = t.seq.kv - t.seq.n;
+    const int last = t.cols - tile * COLS < COLS ? t.cols - 1 : tile * COLS + COLS - 1;
+    t.p_lo = first + tile * COLS / t.G;
+    t.p_hi = first + last / t.G;
+    t.range = pages_seen(t.p_lo, t.p_hi, a.window, a.sinks);
+    return true;
+}
+
+// Where column `col` of a tile's result goes: 16-bit outputs, or one split's
+// part of them.
+__device__ __forceinline__ int64_t pair_of(const Kv4AttentionArgs &a, const Tile &t, int col)
+{
+    return (int64_t)(t.seq.row0 + col / t.G) * a.q_heads + t.h * t.G + col % t.G;
+}
+__device__ __forceinline__ uint16_t *output_of(const Kv4AttentionArgs &a, const Tile &t, int col)
+{
+    return a.y + (int64_t)(t.seq.row0 + col / t.G) * a.ldy + (int64_t)(t.h * t.G + col % t.G) * a.kv.head_dim;
+}
+
+__device__ __forceinline__ uint32_t pack_out(float a, float b, int dtype)
+{
+    return dtype == DT_BF16 ? pack2<OUT_BF16>(a, b) : pack2<OUT_F16>(a, b);
+}
+
+// The kernels, one launch each: columns tiles of 16 (few rows) and of 128.
+constexpr int kFewCols = 16, kManyCols = 128;
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+
+}  // namespace cider

@@ -1,0 +1,432 @@
+// Causal attention over the 4-bit key/value cache (include/cider.h,
+// cider_kv4_attention) for few rows per sequence: decoding steps and drafts.
+//
+// Mathematics.  For a row at position p and tokens t it sees,
+//   S[t] = scale * sum_d q[d] s_k[t,g(d)] (u_k[t,d] - 8)
+//   y[d] = sum_t e^(S[t] - m) s_v[t,g(d)] (u_v[t,d] - 8) / sum_t e^(S[t] - m)
+// in one pass over the tokens with the running maximum m.  The codes u are
+// never turned into values: a nibble put into the low bits of a half is the
+// fp16 number u 2^-24 (the next nibble up: 16 u 2^-24, whose partner operand
+// is divided by 16), exact in the matrix cores, which keep fp16 denormals and
+// sum in fp32.  So one AND per two codes (and half a shift) makes an operand;
+// the offset -8 enters as the score product's initial accumulator
+// (-8 sum_d q[d] per group) and, for V, as one more matrix product whose left
+// operand is the constant -8 2^-24; the scales multiply the fp32 scores and
+// the softmax weights.
+//
+// Rounding.  q is scaled per row by a power of two to a largest magnitude in
+// [2^13, 2^14) and held in fp16: exact unless an element is below 2^-23 of the
+// row's largest, then off by at most 2^-38 of it.  The weights e^(S - m) s_v
+// are fp32 rounded once to fp16 after scaling by a power of two that puts the
+// largest s_v seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the
+// largest possible weight, and sums of many weights average the error below
+// that of the 16-bit output.  Scores, maxima, sums and outputs are fp32.
+//
+// Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
+// head, tokens the rows of S^T = K Q^T (v_mfma_f32_16x16x32_f16), so lane
+// (j, c) ends with the scores of tokens 4 j + i of column c in its registers
+// and they are, rounded and packed, the right operand of O^T += V^T P^T: no
+// transpose, no LDS for either product.  A wavefront takes whole 64-token pages
+// (every kWaves-th of the workgroup's), loads the next page's codes as soon as
+// it has used this one's, and the wavefronts' maxima, sums and outputs meet in LDS at the end.
+#include "kv4_attention.h"
+
+namespace cider {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kCols = kFewCols;
+
+// Maximum and sum over the 4 lanes (j = 0 .. 3) of a column.
+__device__ __forceinline__ float column_max(float v) { return max_lane32(max_lane16(v)); }
+__device__ __forceinline__ float column_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// One page's codes as the lanes use them, and its scales by token (lane =
+// token).  K and V are loaded apart: the next page's K as soon as the scores
+// have used this one's, its V after the outputs have, so one page's registers
+// serve and other wavefronts cover what is left of the latency.
+template <int D, int GS>
+struct PageData {
+    uint32_t k[4][D / 32];
+    uint4 v[2][D / 64];
+    float ks[D / GS], vs[D / GS];
+};
+
+template <int D, int GS>
+__device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block, int lane)
+{
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const uint8_t *at = block + 16 * t * (D / 2);
+        const uint32_t off = lane % 16 * (D / 2) + lane / 16 * (D / 8);
+        if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(at + off);
+            p.k[t][0] = w.x;
+            p.k[t][1] = w.y;
+            p.k[t][2] = w.z;
+            p.k[t][3] = w.w;
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(at + off);
+            p.k[t][0] = w.x;
+            p.k[t][1] = w.y;
+        }
+    }
+    const float *s = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+#pragma unroll
+    for (int g = 0; g < D / GS; ++g)
+        p.ks[g] = s[g * kPageTokens + (uint32_t)lane];
+}
+
+template <int D, int GS>
+__device__ __forceinline__ void load_v(PageData<D, GS> &p, const uint8_t *block, int lane)
+{
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+            p.v[b][g] = *reinterpret_cast<const uint4 *>(block + kv4_v_offset(D) +
+                                                         (b * (D / 64) + g) * 1024 + (uint32_t)lane * 16);
+    const float *s = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+#pragma unroll
+    for (int g = 0; g < D / GS; ++g)
+        p.vs[g] = s[(D / GS + g) * kPageTokens + (uint32_t)lane];
+}
+
+__device__ __forceinline__ half8 halves(uint32_t w) { return __builtin_bit_cast(half8, nibble_halves(w)); }
+
+// Running state of a wavefront's columns.
+template <int D, int GS>
+struct State {
+    f32x4 acc[D / 16], off[D / 64];
+    float m, l;          // in units of q's scaled scores
+    int v_exp[D / GS];   // 2^v_exp is above every finite s_v seen
+    half8 q[D / 32];
+    float zero[D / GS], qmul;
+};
+
+// A wavefront's slot for one page's scales by token.
+template <int D, int GS>
+using Scales = float[D / GS][kPageTokens];
+
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Scores of a page: s[t][e] is token 16 t + 4 j + e of the lane's column.
+template <int D, int GS>
+__device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageData<D, GS> &pg,
+                                            Scales<D, GS> &scales, int lane, float (&s)[4][4])
+{
+    constexpr int NG = D / GS;
+    const int j = lane / 16;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        scales[g][lane] = pg.ks[g];
+    wave_lds_fence();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        f32x4 sum;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f32x4 r = {st.zero[g], st.zero[g], st.zero[g], st.zero[g]};
+#pragma unroll
+            for (int m = g * GS / 32; m < (g + 1) * GS / 32; ++m)
+                r = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(pg.k[t][m]), st.q[m], r, 0, 0, 0);
+            const f32x4 ks = *reinterpret_cast<const f32x4 *>(&scales[g][16 * t + 4 * j]);
+            sum = g == 0 ? r * ks : sum + r * ks;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s[t][e] = sum[e];
+    }
+}
+
+// Their weights, and the outputs.  seen: bit 4 t + e set where the lane's
+// column sees the token (read where the page is not whole); last: the last token
+// of the page that any column of the tile sees (63 and more: all).
+template <int D, int GS>
+__device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg,
+                                             Scales<D, GS> &scales, int lane, float (&s)[4][4],
+                                             bool whole, uint32_t seen, int last)
+{
+    constexpr int NG = D / GS, NT = D / 16;
+    const float inf = __builtin_inff();
+    const int j = lane / 16;
+    // V's scales by token; the weights' exponents move up first
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const float v = lane <= last ? pg.vs[g] : 0.0f;
+        if (__any(v >= ldexp_f(1.0f, st.v_exp[g]) && v < inf)) {
+            const float top = wave_max(v < inf ? v : 0.0f);
+            const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top));
+            const float f = ldexp_f(1.0f, st.v_exp[g] - e);
+            st.v_exp[g] = e;
+#pragma unroll
+            for (int x = g * GS / 16; x < (g + 1) * GS / 16; ++x)
+                st.acc[x] *= f;
+#pragma unroll
+            for (int y = g * GS / 64; y < (g + 1) * GS / 64; ++y)
+                st.off[y] *= f;
+        }
+        // the 16 times larger codes belong to tokens 1 and 3 of each 4
+        scales[g][lane] = ldexp_f(v, 14 - st.v_exp[g] - (lane & 1 ? 4 : 0));
+    }
+    wave_lds_fence();
+    float top = s[0][0];
+#pragma unroll
+    for (int n = 1; n < 16; ++n)
+        top = __builtin_fmaxf(top, s[n / 4][n % 4]);
+    const float m_new = __builtin_fmaxf(st.m, column_max(top));
+    const float m_sub = m_new == -inf ? 0.0f : m_new;
+    if (__any(m_new > st.m)) {
+        const float f = __builtin_amdgcn_exp2f((st.m - m_sub) * st.qmul);
+        st.l *= f;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+            st.acc[x] *= f;
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+            st.off[g] *= f;
+        st.m = m_new;
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+        float &x = s[n / 4][n % 4];
+        x = __builtin_amdgcn_exp2f((x - m_sub) * st.qmul);
+        st.l += x;
+    }
+    const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int B = 0; B < 2; ++B) {
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(&scales[g][32 * B + 4 * j]);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(&scales[g][32 * B + 16 + 4 * j]);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack2<OUT_F16>(s[2 * B][e] * lo[e], s[2 * B + 1][e] * hi[e]);
+            if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] &= ((seen >> (8 * B + e)) & 1u ? 0xFFFFu : 0u) |
+                            ((seen >> (8 * B + 4 + e)) & 1u ? 0xFFFF0000u : 0u);
+            }
+            const half8 weights = __builtin_bit_cast(half8, uint4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+            for (int y = g * GS / 64; y < (g + 1) * GS / 64; ++y) {
+                const uint32_t u[4] = {pg.v[B][y].x, pg.v[B][y].y, pg.v[B][y].z, pg.v[B][y].w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(u[x]), weights,
+                                                                               st.acc[4 * y + x], 0, 0, 0);
+                st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights, st.off[y], 0, 0, 0);
+            }
+        }
+    }
+}
+
+template <int D, int GS>
+__global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    constexpr int NM = D / 32;   // score products per 16 tokens
+    constexpr int NG = D / GS;   // scales per token
+    constexpr int NT = D / 16;   // output tiles
+    __shared__ __align__(16) float scales[kWaves][2][NG][kPageTokens];
+    __shared__ __align__(16) float part[kWaves][kCols][D + 4];
+    __shared__ float part_m[kWaves][kCols], part_l[kWaves][kCols];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane % 16, j = lane / 16;
+    // heads fastest, then sequences, splits and tiles
+    const unsigned bh = blockIdx.x % (unsigned)(a.kv.kv_heads * a.kv.batch);
+    const unsigned rest = blockIdx.x / (unsigned)(a.kv.kv_heads * a.kv.batch);
+    const int b = (int)(bh / (unsigned)a.kv.kv_heads);
+    const int split = (int)(rest % (unsigned)n.splits);
+    Tile t;
+    if (!tile_of<kCols>(a, b, (int)(bh % (unsigned)a.kv.kv_heads), (int)(rest / (unsigned)n.splits), t))
+        return;
+    const int begin = n.splits > 1 ? split * n.pages : 0;
+    if (split > 0 && begin >= t.range.count)
+        return;
+    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+
+    const int col = t.tile * kCols + c;
+    const bool valid = col < t.cols;
+    const int row = valid ? col / t.G : 0;
+    const int p = valid ? t.seq.kv - t.seq.n + row : -1;
+
+    State<D, GS> st;
+    {
+        float x[NM][8], top = 0.0f;
+        const uint16_t *q = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
+                            (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * j;
+        uint4 w[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            w[m] = *reinterpret_cast<const uint4 *>(q + 32 * m);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            widen8(w[m], a.q_dtype, x[m]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[m][e] = valid ? x[m][e] : 0.0f;
+                top = __builtin_fmaxf(top, __builtin_fabsf(x[m][e]));
+            }
+        }
+        top = column_max(top);
+        const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
+        st.qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            st.zero[g] = 0.0f;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            st.zero[m * 32 / GS] += query_operand(x[m], shift, st.q[m]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            st.zero[g] = column_sum(st.zero[g]) * -0x1p-21f;
+            st.v_exp[g] = -100;
+        }
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+            st.acc[x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+            st.off[g] = f32x4{0, 0, 0, 0};
+        st.m = -__builtin_inff();
+        st.l = 0.0f;
+    }
+
+    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
+    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
+    // a page number outside the cache is never followed: page 0 is loaded in
+    // its place and its tokens are left out
+    auto block_of = [&](int number) {
+        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+    };
+    // page numbers are read two pages ahead
+    PageData<D, GS> pg;
+    int i = begin + wave, n0 = -1, n1 = -1;
+    if (i < end) {
+        n0 = table[t.range.at(i)];
+        load_k<D, GS>(pg, block_of(n0), lane);
+        load_v<D, GS>(pg, block_of(n0), lane);
+    }
+    if (i + kWaves < end)
+        n1 = table[t.range.at(i + kWaves)];
+    for (; i < end; i += kWaves) {
+        int n2 = -1;
+        if (i + 2 * kWaves < end)
+            n2 = table[t.range.at(i + 2 * kWaves)];
+        // past the last page this one is loaded again (from the caches): a load
+        // under a branch would cost its registers twice
+        const uint8_t *ahead = block_of(i + kWaves < end ? n1 : n0);
+        const bool there = (unsigned)n0 < (unsigned)a.kv.num_pages;
+        const int t0 = t.range.at(i) * kPageTokens;
+        const bool whole = t0 + kPageTokens - 1 <= t.p_lo &&
+                           (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
+        float s[4][4];
+        page_scores<D, GS>(st, pg, scales[wave][0], lane, s);
+        load_k<D, GS>(pg, ahead, lane);
+        uint32_t seen = 0xFFFFu;
+        if (!whole) {
+            seen = 0;
+            // bounds of the token's offset from the lane's first
+            const int at = t0 + 4 * j, upto = p - at, kept = a.sinks - at;
+            const int after = a.window == 0 ? -1 : p - a.window - at;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int tok = 16 * (e / 4) + e % 4;
+                const bool see = tok <= upto && (tok > after || tok < kept);
+                seen |= (uint32_t)see << e;
+                s[e / 4][e % 4] = see ? s[e / 4][e % 4] : -__builtin_inff();
+            }
+        }
+        if (there)
+            page_outputs<D, GS>(st, pg, scales[wave][1], lane, s, whole, seen, t.p_hi - t0);
+        load_v<D, GS>(pg, ahead, lane);
+        n0 = n1;
+        n1 = n2;
+    }
+
+    // the wavefronts' parts: lane (j, c) holds elements 16 x + 4 j .. + 3 of column c
+    st.l = column_sum(st.l);
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        const f32x4 o = (st.acc[x] + st.off[x / 4]) * ldexp_f(1.0f, st.v_exp[x * 16 / GS] + 10);
+        *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) = o;
+    }
+    if (j == 0) {
+        // in units of log2, so that parts compare without the column's qmul
+        part_m[wave][c] = st.m == -__builtin_inff() ? st.m : st.m * st.qmul;
+        part_l[wave][c] = st.l;
+    }
+    __syncthreads();
+    constexpr int PER = D / 16;  // elements per thread
+    const int oc = threadIdx.x / 16, d0 = threadIdx.x % 16 * PER;
+    const int ocol = t.tile * kCols + oc;
+    if (ocol >= t.cols)
+        return;
+    float m = -__builtin_inff(), l = 0.0f, o[PER] = {};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        m = __builtin_fmaxf(m, part_m[w][oc]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (part_l[w][oc] == 0.0f)  // saw nothing
+            continue;
+        const float f = __builtin_amdgcn_exp2f(part_m[w][oc] - m);
+        l += part_l[w][oc] * f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            o[e] += part[w][oc][d0 + e] * f;
+    }
+    if (n.splits > 1 && t.range.count > n.pages) {
+        const int64_t at = pair_of(a, t, ocol) * n.splits + split;
+#pragma unroll
+        for (int e = 0; e < PER; e += 4)
+            *reinterpret_cast<f32x4 *>(n.part + at * D + d0 + e) = f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
+        if (d0 == 0) {
+            n.part_stat[2 * at] = m;
+            n.part_stat[2 * at + 1] = l;
+        }
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t w[PER / 2];
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+        w[e / 2] = pack_out(o[e] * inv, o[e + 1] * inv, a.y_dtype);
+    uint16_t *y = output_of(a, t, ocol) + d0;
+    if constexpr (PER == 8)
+        *reinterpret_cast<uint4 *>(y) = uint4{w[0], w[1], w[2], w[3]};
+    else
+        *reinterpret_cast<uint2 *>(y) = uint2{w[0], w[1]};
+}
+
+}  // namespace
+
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
+                          (unsigned)a.kv.batch;
+    if (a.kv.head_dim == 64)
+        kv4_few_rows_kernel<64, 64><<<grid, kThreads, 0, stream>>>(a, n);
+    else if (a.kv.group_size == 64)
+        kv4_few_rows_kernel<128, 64><<<grid, kThreads, 0, stream>>>(a, n);
+    else
+        kv4_few_rows_kernel<128, 128><<<grid, kThreads, 0, stream>>>(a, n);
+    return hipGetLastError();
+}
+
+}  // namespace cider
