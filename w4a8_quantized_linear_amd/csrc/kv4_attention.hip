@@ -93,16 +93,19 @@ int64_t most_pages(const Kv4AttentionArgs &a, int cols)
     return seen < all ? seen : all;
 }
 
+// Columns of the tiles of the kernel that takes the call.
+int tile_cols(const Kv4AttentionArgs &a) { return most_columns(a) > 48 ? kManyCols : kFewCols; }
+
 Kv4Launch plan(const Kv4AttentionArgs &a)
 {
     Kv4Launch n{};
-    const int cols = kFewCols;
+    const int cols = tile_cols(a);
     n.tiles = (int)tiles_of(a, cols);
     n.splits = 1;
     const int64_t pages = most_pages(a, cols);
     const int64_t units = n.tiles * (int64_t)a.kv.kv_heads * a.kv.batch;
     // chunks of at least kMinPages pages, as many as give kWanted workgroups
-    constexpr int64_t kMinPages = 16, kWanted = 2048;
+    const int64_t kMinPages = 16, kWanted = cols == kManyCols ? 512 : 2048;
     if (pages > kMinPages && units < kWanted) {
         int64_t splits = (kWanted + units - 1) / units;
         const int64_t most = (pages + kMinPages - 1) / kMinPages;
@@ -130,7 +133,10 @@ template <int D>
 void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
-    kv4_join_kernel<D, kFewCols><<<grid, 64 * kJoinWaves, 0, stream>>>(a, n);
+    if (tile_cols(a) == kManyCols)
+        kv4_join_kernel<D, kManyCols><<<grid, 64 * kJoinWaves, 0, stream>>>(a, n);
+    else
+        kv4_join_kernel<D, kFewCols><<<grid, 64 * kJoinWaves, 0, stream>>>(a, n);
 }
 
 }  // namespace
@@ -150,7 +156,8 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size
         n.part = static_cast<float *>(workspace);
         n.part_stat = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a, n));
     }
-    const hipError_t e = launch_kv4_few_rows(a, n, stream);
+    const hipError_t e = tile_cols(a) == kManyCols ? launch_kv4_many_rows(a, n, stream)
+                                                   : launch_kv4_few_rows(a, n, stream);
     if (e != hipSuccess || n.splits < 2)
         return e;
     if (a.kv.head_dim == 64)

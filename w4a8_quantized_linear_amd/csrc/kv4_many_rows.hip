@@ -1,0 +1,362 @@
+// Causal attention over the 4-bit key/value cache (include/cider.h,
+// cider_kv4_attention) for many rows per sequence: prompts and chunks of them.
+//
+// The mathematics, the scaling of q and the rounding of the weights are those
+// of kv4_few_rows.hip.  Here every page serves many columns, so what counts is
+// vector work per (column, token): a workgroup of 4 wavefronts shares each
+// page's unpacking.  A thread turns its 16 + 16 bytes of codes into fp16
+// operands (u - 8) 2^-24 (the odd nibbles 16 times as large, their partners
+// divided by 16; exact) and writes them to LDS in the order in which the
+// matrix instructions take them; a wavefront has 32 columns and computes
+//   S^T = K Q^T  and  O^T += V^T P^T   (v_mfma_f32_32x32x16_f16)
+// reading 1 KB fragments that are consecutive over the lanes.  Lane (h, c)
+// holds the scores of tokens 8 i + 4 h .. + 3 of column c, which V's code
+// order makes the right operand's own tokens, so the weights go from the
+// softmax to the second product in registers.  Two LDS buffers: while one page
+// is used the next is loaded and, at the end of the step, unpacked; one
+// barrier a page.
+#include "kv4_attention.h"
+
+namespace cider {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kWaveCols = kManyCols / kWaves;
+static_assert(kWaveCols == 32, "a wavefront's columns are one matrix operand");
+
+// One page in LDS.
+template <int D, int GS>
+struct Page {
+    uint4 k[2][D / 16][64];     // [32-token tile][16-element step][lane]
+    uint4 v[2][2][D / 32][64];  // [32-token tile][16-token step][32-element tile][lane]
+    float scale[2][D / GS][kPageTokens];
+    int v_exp[D / GS];          // V's scales are 2^(14 - v_exp) times as large
+};
+
+// A thread's share of a page on its way.
+template <int D>
+struct Share {
+    uint32_t k[D / 32], v[D / 32];
+    float scale;
+};
+
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t (&w)[N], const uint8_t *at)
+{
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[0] = x.x;
+        w[1] = x.y;
+    }
+}
+
+// (u - 8) 2^-24 of 8 nibbles, the odd ones 16 times as large.
+__device__ __forceinline__ uint4 code_halves(uint32_t w)
+{
+    const uint4 u = nibble_halves(w);
+    const half2_t one = __builtin_bit_cast(half2_t, kOffset), sixteen = __builtin_bit_cast(half2_t, kOffset16);
+    return uint4{__builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u.x) + one),
+                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u.y) + sixteen),
+                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u.z) + one),
+                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u.w) + sixteen)};
+}
+
+__device__ __forceinline__ f32x16 mfma(uint4 x, half8 y, f32x16 z)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, x), y, z, 0, 0, 0);
+}
+
+template <int D, int GS>
+__global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    constexpr int NG = D / GS;   // scales per token
+    constexpr int NK = D / 16;   // score products per 32 tokens
+    constexpr int NT = D / 32;   // output tiles
+    __shared__ Page<D, GS> pages[2];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane % 32, h = lane / 32;
+    const float inf = __builtin_inff();
+    // heads fastest (one kv head's pages stay in one XCD's L2), then sequences
+    // and splits; the last tiles, which see most, first
+    const unsigned bh = blockIdx.x % (unsigned)(a.kv.kv_heads * a.kv.batch);
+    const unsigned rest = blockIdx.x / (unsigned)(a.kv.kv_heads * a.kv.batch);
+    const int b = (int)(bh / (unsigned)a.kv.kv_heads);
+    const int split = (int)(rest % (unsigned)n.splits);
+    Tile t;
+    if (!tile_of<kManyCols>(a, b, (int)(bh % (unsigned)a.kv.kv_heads),
+                            n.tiles - 1 - (int)(rest / (unsigned)n.splits), t))
+        return;
+    const int begin = n.splits > 1 ? split * n.pages : 0;
+    if (split > 0 && begin >= t.range.count)
+        return;
+    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+
+    const int first = t.seq.kv - t.seq.n;  // position of row 0
+    const int col0 = t.tile * kManyCols + wave * kWaveCols;
+    const int col = col0 + c;
+    const bool valid = col < t.cols;
+    const int row = valid ? col / t.G : 0;
+    const int p = valid ? first + row : -1;
+    // positions of the wavefront's columns (hi below lo: it has none)
+    const int w_lo = first + col0 / t.G;
+    const int w_last = col0 + kWaveCols <= t.cols ? col0 + kWaveCols - 1 : t.cols - 1;
+    const int w_hi = col0 < t.cols ? first + w_last / t.G : -1;
+
+    half8 q[NK];
+    float qmul;
+    {
+        float x[NK][8], top = 0.0f;
+        const uint16_t *at = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
+                             (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * h;
+        uint4 w[NK];
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+            w[k] = *reinterpret_cast<const uint4 *>(at + 16 * k);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            widen8(w[k], a.q_dtype, x[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[k][e] = valid ? x[k][e] : 0.0f;
+                top = __builtin_fmaxf(top, __builtin_fabsf(x[k][e]));
+            }
+        }
+        top = max_lane32(top);
+        const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
+        qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+            (void)query_operand(x[k], shift, q[k]);
+    }
+
+    f32x16 acc[NT];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+        acc[x] = f32x16{};
+    float m_run = -inf, l_run = 0.0f;
+    int v_exp[NG];       // of the outputs so far
+    int v_exp_run = -100;  // of the wavefront that writes V's scales
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        v_exp[g] = -100;
+
+    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
+    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
+    // a page number outside the cache is never followed: page 0 is loaded in
+    // its place and its tokens are left out
+    auto fetch = [&](Share<D> &s, int number) {
+        const uint8_t *block = heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+        load_dwords(s.k, block + (uint32_t)tid * (D / 8));
+        load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)tid * (D / 8));
+        if (wave < 2 * NG)
+            s.scale = reinterpret_cast<const float *>(block + kv4_scale_offset(D))[(uint32_t)tid];
+    };
+    // where a thread's operands go, and where a lane finds its own: K's slots
+    // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
+    // hit different banks
+    const int kt = tid / 4, kj = tid % 4;
+    const int k_to = ((kj % 2) * 32 + kt % 32) ^ (2 * kj);
+    const int k_from[2] = {lane ^ (2 * h), lane ^ (4 + 2 * h)};
+    const int unit = D == 128 ? tid : tid / 2;
+    const int vx = D == 128 ? 0 : 2 * (tid % 2);
+    const int vc = unit % 16, vj = unit / 16 % 4, vg = unit / 64 % (D / 64), vb = unit / (64 * (D / 64));
+    auto stage = [&](Page<D, GS> &to, const Share<D> &s, int t0) {
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m)
+            to.k[kt / 32][2 * m + kj / 2][k_to] = code_halves(s.k[m]);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const int x = vx + e;
+            to.v[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
+        }
+        if (wave < NG) {
+            to.scale[0][wave][lane] = s.scale;
+        } else if (wave < 2 * NG) {
+            const float v = t0 + lane <= t.p_hi ? s.scale : 0.0f;
+            const int e = __builtin_amdgcn_readfirstlane(
+                __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
+            v_exp_run = e > v_exp_run ? e : v_exp_run;
+            // the 16 times larger codes belong to tokens 1 and 3 of each 4
+            to.scale[1][wave - NG][lane] = ldexp_f(v, 14 - v_exp_run - (lane & 1 ? 4 : 0));
+            if (lane == 0)
+                to.v_exp[wave - NG] = v_exp_run;
+        }
+    };
+
+    Share<D> share;
+    int n0 = -1, n1 = -1;
+    if (begin < end) {
+        n0 = table[t.range.at(begin)];
+        fetch(share, n0);
+        if (begin + 1 < end)
+            n1 = table[t.range.at(begin + 1)];
+        stage(pages[0], share, t.range.at(begin) * kPageTokens);
+    }
+    __syncthreads();
+    for (int i = begin; i < end; ++i) {
+        const Page<D, GS> &pg = pages[(i - begin) & 1];
+        const int n2 = i + 2 < end ? table[t.range.at(i + 2)] : -1;
+        fetch(share, i + 1 < end ? n1 : n0);
+        const int t0 = t.range.at(i) * kPageTokens;
+        const bool hidden = t0 > w_hi || (a.window > 0 && t0 + kPageTokens - 1 <= w_lo - a.window && t0 >= a.sinks);
+        if ((unsigned)n0 < (unsigned)a.kv.num_pages && !hidden) {
+            float s[2][16];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x16 r = f32x16{};
+#pragma unroll
+                    for (int k = g * GS / 16; k < (g + 1) * GS / 16; ++k)
+                        r = mfma(pg.k[tt][k][k_from[k % 2]], q[k], r);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&pg.scale[0][g][32 * tt + 2 * e + 4 * h]);
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            s[tt][e + f] = g == 0 ? r[e + f] * ks[f] : s[tt][e + f] + r[e + f] * ks[f];
+                    }
+                }
+            }
+            const bool whole = t0 + kPageTokens - 1 <= w_lo &&
+                               (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
+            uint32_t seen = ~0u;
+            if (!whole) {
+                seen = 0;
+                // bounds of the token's offset from the lane's first
+                const int at = t0 + 4 * h, upto = p - at, kept = a.sinks - at;
+                const int after = a.window == 0 ? -1 : p - a.window - at;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int tok = 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4;
+                    const bool see = tok <= upto && (tok > after || tok < kept);
+                    seen |= (uint32_t)see << e;
+                    s[e / 16][e % 16] = see ? s[e / 16][e % 16] : -inf;
+                }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int e = 1; e < 32; ++e)
+                top = __builtin_fmaxf(top, s[e / 16][e % 16]);
+            const float m_new = __builtin_fmaxf(m_run, max_lane32(top));
+            const float m_sub = m_new == -inf ? 0.0f : m_new;
+            if (__any(m_new > m_run)) {
+                const float f = __builtin_amdgcn_exp2f((m_run - m_sub) * qmul);
+                l_run *= f;
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                    acc[x] *= f;
+                m_run = m_new;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int e = __builtin_amdgcn_readfirstlane(pg.v_exp[g]);
+                if (e != v_exp[g]) {
+                    const float f = ldexp_f(1.0f, v_exp[g] - e);
+#pragma unroll
+                    for (int x = g * GS / 32; x < (g + 1) * GS / 32; ++x)
+                        acc[x] *= f;
+                    v_exp[g] = e;
+                }
+            }
+            const float shift = m_sub * qmul;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                float &x = s[e / 16][e % 16];
+                x = __builtin_amdgcn_exp2f(x * qmul - shift);
+                l_run += x;
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x4 vs[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        vs[e] = *reinterpret_cast<const f32x4 *>(&pg.scale[1][g][32 * tt + 8 * e + 4 * h]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<OUT_F16>(s[tt][4 * r + e] * vs[r][e], s[tt][8 + 4 * r + e] * vs[2 + r][e]);
+                        if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] &= ((seen >> (16 * tt + 4 * r + e)) & 1u ? 0xFFFFu : 0u) |
+                                        ((seen >> (16 * tt + 8 + 4 * r + e)) & 1u ? 0xFFFF0000u : 0u);
+                        }
+                        const half8 weights = __builtin_bit_cast(half8, uint4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+                        for (int x = g * GS / 32; x < (g + 1) * GS / 32; ++x)
+                            acc[x] = mfma(pg.v[tt][r][x][lane], weights, acc[x]);
+                    }
+                }
+            }
+        }
+        if (i + 1 < end)
+            stage(pages[(i + 1 - begin) & 1], share, t.range.at(i + 1) * kPageTokens);
+        n0 = n1;
+        n1 = n2;
+        __syncthreads();
+    }
+
+    // lane (h, c) holds elements 32 x + 8 i + 4 h .. + 3 of column c
+    l_run += __shfl_xor(l_run, 32);
+    if (!valid)
+        return;
+    if (n.splits > 1 && t.range.count > n.pages) {
+        const int64_t at = pair_of(a, t, col) * n.splits + split;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            const float f = ldexp_f(1.0f, v_exp[x * 32 / GS] + 10);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) =
+                    f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]} * f;
+        }
+        if (h == 0) {
+            n.part_stat[2 * at] = m_run == -inf ? m_run : m_run * qmul;  // in units of log2
+            n.part_stat[2 * at + 1] = l_run;
+        }
+        return;
+    }
+    const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+    uint16_t *y = output_of(a, t, col) + 4 * h;
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        const float f = ldexp_f(inv, v_exp[x * 32 / GS] + 10);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint2 *>(y + 32 * x + 8 * i) =
+                uint2{pack_out(acc[x][4 * i] * f, acc[x][4 * i + 1] * f, a.y_dtype),
+                      pack_out(acc[x][4 * i + 2] * f, acc[x][4 * i + 3] * f, a.y_dtype)};
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
+                          (unsigned)a.kv.batch;
+    if (a.kv.head_dim == 64)
+        kv4_many_rows_kernel<64, 64><<<grid, kThreads, 0, stream>>>(a, n);
+    else if (a.kv.group_size == 64)
+        kv4_many_rows_kernel<128, 64><<<grid, kThreads, 0, stream>>>(a, n);
+    else
+        kv4_many_rows_kernel<128, 128><<<grid, kThreads, 0, stream>>>(a, n);
+    return hipGetLastError();
+}
+
+}  // namespace cider
