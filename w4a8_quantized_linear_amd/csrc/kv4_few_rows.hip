@@ -246,13 +246,15 @@ __global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionA
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane % 16, j = lane / 16;
-    // heads fastest, then sequences, splits and tiles
-    const unsigned bh = blockIdx.x % (unsigned)(a.kv.kv_heads * a.kv.batch);
-    const unsigned rest = blockIdx.x / (unsigned)(a.kv.kv_heads * a.kv.batch);
-    const int b = (int)(bh / (unsigned)a.kv.kv_heads);
-    const int split = (int)(rest % (unsigned)n.splits);
+    // heads fastest, then splits, tiles and sequences
+    unsigned id = blockIdx.x;
+    const int head = (int)(id % (unsigned)a.kv.kv_heads);
+    id /= (unsigned)a.kv.kv_heads;
+    const int split = (int)(id % (unsigned)n.splits);
+    id /= (unsigned)n.splits;
+    const int tile = (int)(id % (unsigned)n.tiles), b = (int)(id / (unsigned)n.tiles);
     Tile t;
-    if (!tile_of<kCols>(a, b, (int)(bh % (unsigned)a.kv.kv_heads), (int)(rest / (unsigned)n.splits), t))
+    if (!tile_of<kCols>(a, b, head, tile, t))
         return;
     const int begin = n.splits > 1 ? split * n.pages : 0;
     if (split > 0 && begin >= t.range.count)

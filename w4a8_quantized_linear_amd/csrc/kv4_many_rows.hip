@@ -25,20 +25,30 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kWaveCols = kManyCols / kWaves;
 static_assert(kWaveCols == 32, "a wavefront's columns are one matrix operand");
 
+// The running maximum may lie this far (in units of log2) below the true one
+// before it is moved: weights reach 2^kSlack, and the outputs are rescaled in
+// few pages instead of nearly all (with 32 columns some column has a new
+// maximum in most pages).  kTop leaves fp16 the room: weights times V's scale
+// stay below 2^(kTop + kSlack) = 2^14.
+constexpr float kSlack = 3.0f;
+constexpr int kTop = 11;
+
 // One page in LDS.
 template <int D, int GS>
 struct Page {
     uint4 k[2][D / 16][64];     // [32-token tile][16-element step][lane]
     uint4 v[2][2][D / 32][64];  // [32-token tile][16-token step][32-element tile][lane]
-    float scale[2][D / GS][kPageTokens];
-    int v_exp[D / GS];          // V's scales are 2^(14 - v_exp) times as large
+    float k_scale[kPageTokens];  // of the scores, in units of log2: K's last group's scale times q's factor
+    float k_ratio[D / GS - 1 ? D / GS - 1 : 1][kPageTokens];  // K's first group's scale over the last one's
+    float v_scale[D / GS][kPageTokens];
+    int v_exp[D / GS];           // V's scales are 2^(kTop - v_exp) times as large
 };
 
 // A thread's share of a page on its way.
 template <int D>
 struct Share {
     uint32_t k[D / 32], v[D / 32];
-    float scale;
+    float scale, scale2;  // by token: wavefront 0 K's groups, wavefront 1 + g V's group g
 };
 
 template <int N>
@@ -80,20 +90,25 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     constexpr int NK = D / 16;   // score products per 32 tokens
     constexpr int NT = D / 32;   // output tiles
     __shared__ Page<D, GS> pages[2];
+    __shared__ float tile_top[kWaves];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane % 32, h = lane / 32;
     const float inf = __builtin_inff();
-    // heads fastest (one kv head's pages stay in one XCD's L2), then sequences
-    // and splits; the last tiles, which see most, first
-    const unsigned bh = blockIdx.x % (unsigned)(a.kv.kv_heads * a.kv.batch);
-    const unsigned rest = blockIdx.x / (unsigned)(a.kv.kv_heads * a.kv.batch);
-    const int b = (int)(bh / (unsigned)a.kv.kv_heads);
-    const int split = (int)(rest % (unsigned)n.splits);
+    // heads fastest (one kv head's pages stay in one XCD's L2), then splits and
+    // tiles, the last ones, which see most, first; sequences slowest: dealt in
+    // turn, workgroups of sequences of different lengths fall into step with the
+    // order in which an XCD fills its shader engines, and all long ones of a batch of 4
+    // land on one (ragged prompts up to 4096 rows: 617 us against 250)
+    unsigned id = blockIdx.x;
+    const int head = (int)(id % (unsigned)a.kv.kv_heads);
+    id /= (unsigned)a.kv.kv_heads;
+    const int split = (int)(id % (unsigned)n.splits);
+    id /= (unsigned)n.splits;
+    const int tile = n.tiles - 1 - (int)(id % (unsigned)n.tiles), b = (int)(id / (unsigned)n.tiles);
     Tile t;
-    if (!tile_of<kManyCols>(a, b, (int)(bh % (unsigned)a.kv.kv_heads),
-                            n.tiles - 1 - (int)(rest / (unsigned)n.splits), t))
+    if (!tile_of<kManyCols>(a, b, head, tile, t))
         return;
     const int begin = n.splits > 1 ? split * n.pages : 0;
     if (split > 0 && begin >= t.range.count)
@@ -111,6 +126,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     const int w_last = col0 + kWaveCols <= t.cols ? col0 + kWaveCols - 1 : t.cols - 1;
     const int w_hi = col0 < t.cols ? first + w_last / t.G : -1;
 
+    // q: one power of two for the whole tile, so that the scores' factor goes
+    // into K's scales once a page
     half8 q[NK];
     float qmul;
     {
@@ -127,10 +144,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[k][e] = valid ? x[k][e] : 0.0f;
-                top = __builtin_fmaxf(top, __builtin_fabsf(x[k][e]));
+                const float size = __builtin_fabsf(x[k][e]);
+                top = __builtin_fmaxf(top, size < inf ? size : 0.0f);
             }
         }
-        top = max_lane32(top);
+        top = wave_max(top);
+        if (lane == 0)
+            tile_top[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            top = __builtin_fmaxf(top, tile_top[w]);
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
         qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
 #pragma unroll
@@ -158,8 +182,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         const uint8_t *block = heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
         load_dwords(s.k, block + (uint32_t)tid * (D / 8));
         load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)tid * (D / 8));
-        if (wave < 2 * NG)
-            s.scale = reinterpret_cast<const float *>(block + kv4_scale_offset(D))[(uint32_t)tid];
+        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+        if (wave <= NG)
+            s.scale = (scales + (wave == 0 ? 0 : (NG + wave - 1) * kPageTokens))[(uint32_t)lane];
+        if (NG == 2 && wave == 0)
+            s.scale2 = scales[kPageTokens + (uint32_t)lane];
     };
     // where a thread's operands go, and where a lane finds its own: K's slots
     // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
@@ -179,17 +206,26 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
             const int x = vx + e;
             to.v[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
         }
-        if (wave < NG) {
-            to.scale[0][wave][lane] = s.scale;
-        } else if (wave < 2 * NG) {
+        if (wave == 0) {
+            if constexpr (NG == 1) {
+                to.k_scale[lane] = s.scale * qmul;
+            } else {
+                // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
+                // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
+                const float low = __builtin_fmaxf(s.scale * 0x1p-60f, 0x1p-149f);
+                const float last = s.scale2 < low ? low : s.scale2;  // NaN stays
+                to.k_scale[lane] = last * qmul;
+                to.k_ratio[0][lane] = s.scale / last;
+            }
+        } else if (wave <= NG) {
             const float v = t0 + lane <= t.p_hi ? s.scale : 0.0f;
             const int e = __builtin_amdgcn_readfirstlane(
                 __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
             v_exp_run = e > v_exp_run ? e : v_exp_run;
             // the 16 times larger codes belong to tokens 1 and 3 of each 4
-            to.scale[1][wave - NG][lane] = ldexp_f(v, 14 - v_exp_run - (lane & 1 ? 4 : 0));
+            to.v_scale[wave - 1][lane] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
             if (lane == 0)
-                to.v_exp[wave - NG] = v_exp_run;
+                to.v_exp[wave - 1] = v_exp_run;
         }
     };
 
@@ -210,22 +246,26 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         const int t0 = t.range.at(i) * kPageTokens;
         const bool hidden = t0 > w_hi || (a.window > 0 && t0 + kPageTokens - 1 <= w_lo - a.window && t0 >= a.sinks);
         if ((unsigned)n0 < (unsigned)a.kv.num_pages && !hidden) {
+            f32x16 r[2];
             float s[2][16];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    f32x16 r = f32x16{};
+                    if (g == 0) {
+                        r[tt] = f32x16{};
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const f32x4 f = *reinterpret_cast<const f32x4 *>(&pg.k_ratio[g - 1][32 * tt + 2 * e + 4 * h]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                r[tt][e + i] *= f[i];
+                        }
+                    }
 #pragma unroll
                     for (int k = g * GS / 16; k < (g + 1) * GS / 16; ++k)
-                        r = mfma(pg.k[tt][k][k_from[k % 2]], q[k], r);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&pg.scale[0][g][32 * tt + 2 * e + 4 * h]);
-#pragma unroll
-                        for (int f = 0; f < 4; ++f)
-                            s[tt][e + f] = g == 0 ? r[e + f] * ks[f] : s[tt][e + f] + r[e + f] * ks[f];
-                    }
+                        r[tt] = mfma(pg.k[tt][k][k_from[k % 2]], q[k], r[tt]);
                 }
             }
             const bool whole = t0 + kPageTokens - 1 <= w_lo &&
@@ -241,22 +281,42 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                     const int tok = 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4;
                     const bool see = tok <= upto && (tok > after || tok < kept);
                     seen |= (uint32_t)see << e;
-                    s[e / 16][e % 16] = see ? s[e / 16][e % 16] : -inf;
                 }
+            }
+            // scores less the running maximum
+            const float m_sub = m_run == -inf ? 0.0f : m_run;
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(&pg.k_scale[32 * tt + 2 * e + 4 * h]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[tt][e + i] = __builtin_fmaf(r[tt][e + i], ks[i], -m_sub);
+                }
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    s[e / 16][e % 16] = (seen >> e) & 1u ? s[e / 16][e % 16] : -inf;
             }
             float top = s[0][0];
 #pragma unroll
             for (int e = 1; e < 32; ++e)
                 top = __builtin_fmaxf(top, s[e / 16][e % 16]);
-            const float m_new = __builtin_fmaxf(m_run, max_lane32(top));
-            const float m_sub = m_new == -inf ? 0.0f : m_new;
-            if (__any(m_new > m_run)) {
-                const float f = __builtin_amdgcn_exp2f((m_run - m_sub) * qmul);
-                l_run *= f;
+            if (__any(top > (m_run == -inf ? -inf : kSlack))) {
+                top = max_lane32(top);
+                const float up = top > 0.0f || m_run == -inf ? top : 0.0f;  // of the maximum
+                if (up != -inf) {
+                    const float f = m_run == -inf ? 0.0f : __builtin_amdgcn_exp2f(-up);
+                    m_run = m_sub + up;
+                    l_run *= f;
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
-                    acc[x] *= f;
-                m_run = m_new;
+                    for (int x = 0; x < NT; ++x)
+                        acc[x] *= f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        s[e / 16][e % 16] -= up;
+                }
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -269,11 +329,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                     v_exp[g] = e;
                 }
             }
-            const float shift = m_sub * qmul;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 float &x = s[e / 16][e % 16];
-                x = __builtin_amdgcn_exp2f(x * qmul - shift);
+                x = __builtin_amdgcn_exp2f(x);
                 l_run += x;
             }
 #pragma unroll
@@ -283,7 +342,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                     f32x4 vs[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        vs[e] = *reinterpret_cast<const f32x4 *>(&pg.scale[1][g][32 * tt + 8 * e + 4 * h]);
+                        vs[e] = *reinterpret_cast<const f32x4 *>(&pg.v_scale[g][32 * tt + 8 * e + 4 * h]);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         uint32_t w[4];
@@ -319,14 +378,14 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         const int64_t at = pair_of(a, t, col) * n.splits + split;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            const float f = ldexp_f(1.0f, v_exp[x * 32 / GS] + 10);
+            const float f = ldexp_f(1.0f, v_exp[x * 32 / GS] + 24 - kTop);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) =
                     f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]} * f;
         }
         if (h == 0) {
-            n.part_stat[2 * at] = m_run == -inf ? m_run : m_run * qmul;  // in units of log2
+            n.part_stat[2 * at] = m_run;
             n.part_stat[2 * at + 1] = l_run;
         }
         return;
@@ -335,7 +394,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     uint16_t *y = output_of(a, t, col) + 4 * h;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-        const float f = ldexp_f(inv, v_exp[x * 32 / GS] + 10);
+        const float f = ldexp_f(inv, v_exp[x * 32 / GS] + 24 - kTop);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint2 *>(y + 32 * x + 8 * i) =
