@@ -33,22 +33,60 @@ static_assert(kWaveCols == 32, "a wavefront's columns are one matrix operand");
 constexpr float kSlack = 3.0f;
 constexpr int kTop = 11;
 
-// One page in LDS.
+// One page's K and V in LDS.  They are used one step apart (the scores of page
+// i + 1 are computed while page i's weights are), so each has its own pair of
+// buffers.
 template <int D, int GS>
-struct Page {
-    uint4 k[2][D / 16][64];     // [32-token tile][16-element step][lane]
-    uint4 v[2][2][D / 32][64];  // [32-token tile][16-token step][32-element tile][lane]
-    float k_scale[kPageTokens];  // of the scores, in units of log2: K's last group's scale times q's factor
-    float k_ratio[D / GS - 1 ? D / GS - 1 : 1][kPageTokens];  // K's first group's scale over the last one's
-    float v_scale[D / GS][kPageTokens];
-    int v_exp[D / GS];           // V's scales are 2^(kTop - v_exp) times as large
+struct PageK {
+    uint4 code[2][D / 16][64];  // [32-token tile][16-element step][lane]
+    float ratio[kPageTokens];   // groups of 64 in 128: the first group's scale over the second one's
+};  // scales stand at scale_slot(token)
+template <int D, int GS>
+struct PageV {
+    uint4 code[2][2][D / 32][64];     // [32-token tile][16-token step][32-element tile][lane]
+    float scale[D / GS][kPageTokens];
+    float k_scale[kPageTokens];       // of the scores, to units of log2: K's last group's scale times q's factor
+    int exp[D / GS];                  // V's scales are 2^(kTop - exp) times as large
 };
+
+// Scales by token.  Lane (h, c) needs those of the 16 tokens 8 i + 4 h + f of a
+// tile; each row of 16 lanes holds them one a lane, and the multiplications
+// take them by a broadcast within the row (DPP), so a tile's scales cost one
+// 4-byte LDS read instead of four 16-byte ones.
+__device__ __forceinline__ int scale_slot(int t) { return t / 32 * 32 + t / 4 % 2 * 16 + t / 8 % 4 * 4 + t % 4; }
+template <int N>
+__device__ __forceinline__ float row_lane(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
+}
+// x times the scale of the lane's token n of a tile.
+__device__ __forceinline__ float scaled(float x, float scales, int n)
+{
+    switch (n) {
+    case 0: return row_lane<0>(scales) * x;
+    case 1: return row_lane<1>(scales) * x;
+    case 2: return row_lane<2>(scales) * x;
+    case 3: return row_lane<3>(scales) * x;
+    case 4: return row_lane<4>(scales) * x;
+    case 5: return row_lane<5>(scales) * x;
+    case 6: return row_lane<6>(scales) * x;
+    case 7: return row_lane<7>(scales) * x;
+    case 8: return row_lane<8>(scales) * x;
+    case 9: return row_lane<9>(scales) * x;
+    case 10: return row_lane<10>(scales) * x;
+    case 11: return row_lane<11>(scales) * x;
+    case 12: return row_lane<12>(scales) * x;
+    case 13: return row_lane<13>(scales) * x;
+    case 14: return row_lane<14>(scales) * x;
+    default: return row_lane<15>(scales) * x;
+    }
+}
 
 // A thread's share of a page on its way.
 template <int D>
 struct Share {
     uint32_t k[D / 32], v[D / 32];
-    float scale, scale2;  // by token: wavefront 0 K's groups, wavefront 1 + g V's group g
+    float k_scale[2], v_scale;  // by token: wavefront 0 K's groups, wavefront 1 + g V's group g
 };
 
 template <int N>
@@ -89,7 +127,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     constexpr int NG = D / GS;   // scales per token
     constexpr int NK = D / 16;   // score products per 32 tokens
     constexpr int NT = D / 32;   // output tiles
-    __shared__ Page<D, GS> pages[2];
+    __shared__ PageK<D, GS> page_k[2];
+    __shared__ PageV<D, GS> page_v[2];
     __shared__ float tile_top[kWaves];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -178,195 +217,283 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
     // a page number outside the cache is never followed: page 0 is loaded in
     // its place and its tokens are left out
-    auto fetch = [&](Share<D> &s, int number) {
-        const uint8_t *block = heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+    auto block_of = [&](int number) {
+        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+    };
+    auto fetch_k = [&](Share<D> &s, int number) {
+        const uint8_t *block = block_of(number);
         load_dwords(s.k, block + (uint32_t)tid * (D / 8));
+        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            s.k_scale[g] = scales[g * kPageTokens + (uint32_t)lane];
+    };
+    auto fetch_v = [&](Share<D> &s, int number) {
+        const uint8_t *block = block_of(number);
         load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)tid * (D / 8));
         const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
-        if (wave <= NG)
-            s.scale = (scales + (wave == 0 ? 0 : (NG + wave - 1) * kPageTokens))[(uint32_t)lane];
-        if (NG == 2 && wave == 0)
-            s.scale2 = scales[kPageTokens + (uint32_t)lane];
+        s.v_scale = (scales + (NG + (wave == 2 && NG == 2 ? 1 : 0)) * kPageTokens)[(uint32_t)lane];
     };
     // where a thread's operands go, and where a lane finds its own: K's slots
     // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
     // hit different banks
+    const int slot = 16 * h + lane % 16;  // of the lane's own scale in a tile's
     const int kt = tid / 4, kj = tid % 4;
     const int k_to = ((kj % 2) * 32 + kt % 32) ^ (2 * kj);
     const int k_from[2] = {lane ^ (2 * h), lane ^ (4 + 2 * h)};
     const int unit = D == 128 ? tid : tid / 2;
     const int vx = D == 128 ? 0 : 2 * (tid % 2);
     const int vc = unit % 16, vj = unit / 16 % 4, vg = unit / 64 % (D / 64), vb = unit / (64 * (D / 64));
-    auto stage = [&](Page<D, GS> &to, const Share<D> &s, int t0) {
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m)
-            to.k[kt / 32][2 * m + kj / 2][k_to] = code_halves(s.k[m]);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const int x = vx + e;
-            to.v[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
+    float k_scale_next = 0.0f;  // wavefront 0: of the page whose K was staged last
+    auto stage_k_dword = [&](PageK<D, GS> &to, const Share<D> &s, int m) {
+        to.code[kt / 32][2 * m + kj / 2][k_to] = code_halves(s.k[m]);
+    };
+    auto stage_k_scales = [&](PageK<D, GS> &to, const Share<D> &s) {
+        if (NG == 1) {
+            k_scale_next = s.k_scale[0] * qmul;
+        } else {
+            // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
+            // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
+            const float low = __builtin_fmaxf(s.k_scale[0] * 0x1p-60f, 0x1p-149f);
+            const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
+            k_scale_next = last * qmul;
+            if (wave == 0)
+                to.ratio[scale_slot(lane)] = s.k_scale[0] / last;
         }
-        if (wave == 0) {
-            if constexpr (NG == 1) {
-                to.k_scale[lane] = s.scale * qmul;
-            } else {
-                // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
-                // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
-                const float low = __builtin_fmaxf(s.scale * 0x1p-60f, 0x1p-149f);
-                const float last = s.scale2 < low ? low : s.scale2;  // NaN stays
-                to.k_scale[lane] = last * qmul;
-                to.k_ratio[0][lane] = s.scale / last;
-            }
-        } else if (wave <= NG) {
-            const float v = t0 + lane <= t.p_hi ? s.scale : 0.0f;
+    };
+    auto stage_v_dword = [&](PageV<D, GS> &to, const Share<D> &s, int e) {
+        const int x = vx + e;
+        to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
+    };
+    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<D> &s, float k_scale, int t0) {
+        if (wave == 0)
+            to.k_scale[scale_slot(lane)] = k_scale;
+        if (wave >= 1 && wave <= NG) {
+            const float v = t0 + lane <= t.p_hi ? s.v_scale : 0.0f;
             const int e = __builtin_amdgcn_readfirstlane(
                 __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
             v_exp_run = e > v_exp_run ? e : v_exp_run;
             // the 16 times larger codes belong to tokens 1 and 3 of each 4
-            to.v_scale[wave - 1][lane] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
+            to.scale[wave - 1][scale_slot(lane)] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
             if (lane == 0)
-                to.v_exp[wave - 1] = v_exp_run;
+                to.exp[wave - 1] = v_exp_run;
         }
     };
+    // the K operands of step s of a page: steps go through both tiles' first
+    // group, then both tiles' second
+    constexpr int SG = GS / 16;  // steps of a group
+    auto k_tile = [](int s) { return s / SG % 2; };
+    auto k_step = [](int s) { return s / (2 * SG) * SG + s % SG; };
 
+    // page numbers: of page i + 1 (V) and i + 2 (K); read one step ahead
     Share<D> share;
-    int n0 = -1, n1 = -1;
+    const int last_page = end - 1;
+    auto number_of = [&](int i) { return table[t.range.at(i < last_page ? i : last_page)]; };
+    f32x16 r[2];
+    int n0 = -1, n1 = -1, n2 = -1;
     if (begin < end) {
-        n0 = table[t.range.at(begin)];
-        fetch(share, n0);
-        if (begin + 1 < end)
-            n1 = table[t.range.at(begin + 1)];
-        stage(pages[0], share, t.range.at(begin) * kPageTokens);
+        n0 = number_of(begin);
+        n1 = number_of(begin + 1);
+        n2 = number_of(begin + 2);
+        fetch_k(share, n0);
+        fetch_v(share, n0);
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+            stage_k_dword(page_k[0], share, m);
+            stage_v_dword(page_v[0], share, m);
+        }
+        stage_k_scales(page_k[0], share);
+        stage_v_scales(page_v[0], share, k_scale_next, t.range.at(begin) * kPageTokens);
+        fetch_k(share, n1);
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m)
+            stage_k_dword(page_k[1], share, m);
+        stage_k_scales(page_k[1], share);
     }
     __syncthreads();
+    if (begin < end) {
+#pragma unroll
+        for (int s = 0; s < 2 * NK; ++s) {
+            const int tt = k_tile(s), k = k_step(s);
+            if (k == 0)
+                r[tt] = f32x16{};
+            else if (k % SG == 0) {
+                const float ratio = page_k[0].ratio[32 * tt + slot];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    r[tt][e] = scaled(r[tt][e], ratio, e);
+            }
+            r[tt] = mfma(page_k[0].code[tt][k][k_from[k % 2]], q[k], r[tt]);
+        }
+    }
     for (int i = begin; i < end; ++i) {
-        const Page<D, GS> &pg = pages[(i - begin) & 1];
-        const int n2 = i + 2 < end ? table[t.range.at(i + 2)] : -1;
-        fetch(share, i + 1 < end ? n1 : n0);
+        const PageV<D, GS> &pv = page_v[(i - begin) & 1];
+        const PageK<D, GS> &pk = page_k[(i - begin + 1) & 1];
+        const int n3 = number_of(i + 3);
+        fetch_k(share, n2);
+        fetch_v(share, n1);
         const int t0 = t.range.at(i) * kPageTokens;
-        const bool hidden = t0 > w_hi || (a.window > 0 && t0 + kPageTokens - 1 <= w_lo - a.window && t0 >= a.sinks);
-        if ((unsigned)n0 < (unsigned)a.kv.num_pages && !hidden) {
-            f32x16 r[2];
-            float s[2][16];
+
+        // scores of page i less the running maximum
+        const float m_sub = m_run == -inf ? 0.0f : m_run;
+        float x[2][16];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
+        for (int tt = 0; tt < 2; ++tt) {
+            const float ks = pv.k_scale[32 * tt + slot];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    if (g == 0) {
-                        r[tt] = f32x16{};
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const f32x4 f = *reinterpret_cast<const f32x4 *>(&pg.k_ratio[g - 1][32 * tt + 2 * e + 4 * h]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                r[tt][e + i] *= f[i];
-                        }
-                    }
-#pragma unroll
-                    for (int k = g * GS / 16; k < (g + 1) * GS / 16; ++k)
-                        r[tt] = mfma(pg.k[tt][k][k_from[k % 2]], q[k], r[tt]);
-                }
-            }
-            const bool whole = t0 + kPageTokens - 1 <= w_lo &&
-                               (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
-            uint32_t seen = ~0u;
-            if (!whole) {
-                seen = 0;
-                // bounds of the token's offset from the lane's first
-                const int at = t0 + 4 * h, upto = p - at, kept = a.sinks - at;
-                const int after = a.window == 0 ? -1 : p - a.window - at;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int tok = 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4;
-                    const bool see = tok <= upto && (tok > after || tok < kept);
-                    seen |= (uint32_t)see << e;
-                }
-            }
-            // scores less the running maximum
-            const float m_sub = m_run == -inf ? 0.0f : m_run;
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(&pg.k_scale[32 * tt + 2 * e + 4 * h]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[tt][e + i] = __builtin_fmaf(r[tt][e + i], ks[i], -m_sub);
-                }
-            if (!whole) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    s[e / 16][e % 16] = (seen >> e) & 1u ? s[e / 16][e % 16] : -inf;
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int e = 1; e < 32; ++e)
-                top = __builtin_fmaxf(top, s[e / 16][e % 16]);
-            if (__any(top > (m_run == -inf ? -inf : kSlack))) {
-                top = max_lane32(top);
-                const float up = top > 0.0f || m_run == -inf ? top : 0.0f;  // of the maximum
-                if (up != -inf) {
-                    const float f = m_run == -inf ? 0.0f : __builtin_amdgcn_exp2f(-up);
-                    m_run = m_sub + up;
-                    l_run *= f;
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-                        acc[x] *= f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        s[e / 16][e % 16] -= up;
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const int e = __builtin_amdgcn_readfirstlane(pg.v_exp[g]);
-                if (e != v_exp[g]) {
-                    const float f = ldexp_f(1.0f, v_exp[g] - e);
-#pragma unroll
-                    for (int x = g * GS / 32; x < (g + 1) * GS / 32; ++x)
-                        acc[x] *= f;
-                    v_exp[g] = e;
-                }
-            }
+            for (int e = 0; e < 16; ++e)
+                x[tt][e] = scaled(r[tt][e], ks, e) - m_sub;
+        }
+        const bool whole = t0 + kPageTokens - 1 <= w_lo && (unsigned)n0 < (unsigned)a.kv.num_pages &&
+                           (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
+        uint32_t seen = ~0u;
+        if (!whole) {
+            seen = 0;
+            // bounds of the token's offset from the lane's first
+            const int at = t0 + 4 * h, kept = a.sinks - at;
+            const int upto = (unsigned)n0 < (unsigned)a.kv.num_pages ? p - at : -1;
+            const int after = a.window == 0 ? -1 : p - a.window - at;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                float &x = s[e / 16][e % 16];
-                x = __builtin_amdgcn_exp2f(x);
-                l_run += x;
+                const int tok = 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4;
+                const bool see = tok <= upto && (tok > after || tok < kept);
+                seen |= (uint32_t)see << e;
+                x[e / 16][e % 16] = see ? x[e / 16][e % 16] : -inf;
             }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e)
+            top = __builtin_fmaxf(top, x[e / 16][e % 16]);
+        if (__any(top > (m_run == -inf ? -inf : kSlack))) {
+            top = max_lane32(top);
+            const float up = top > 0.0f || m_run == -inf ? top : 0.0f;  // of the maximum
+            if (up != -inf) {
+                const float f = m_run == -inf ? 0.0f : __builtin_amdgcn_exp2f(-up);
+                m_run = m_sub + up;
+                l_run *= f;
+#pragma unroll
+                for (int y = 0; y < NT; ++y)
+                    acc[y] *= f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[e / 16][e % 16] -= up;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int e = __builtin_amdgcn_readfirstlane(pv.exp[g]);
+            if (e != v_exp[g]) {
+                const float f = ldexp_f(1.0f, v_exp[g] - e);
+#pragma unroll
+                for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
+                    acc[y] *= f;
+                v_exp[g] = e;
+            }
+        }
+
+        // The weights of page i, one pair of tokens a step, each step with one
+        // score product of page i + 1 in front of it: the matrix core works
+        // while the vector unit does.  LDS reads go out kAhead steps early, and
+        // the barriers keep the compiler from gathering the products.  (Past
+        // the last page the products take what lies in the buffer; unused.)
+        uint32_t w[2][NG][2][4];
+        {
+            constexpr int kSteps = 2 * NK, kAhead = 2;
+            uint4 kf[kAhead + 1];
+            float vs[2][NG], ratio[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    f32x4 vs[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        vs[e] = *reinterpret_cast<const f32x4 *>(&pg.v_scale[g][32 * tt + 8 * e + 4 * h]);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<OUT_F16>(s[tt][4 * r + e] * vs[r][e], s[tt][8 + 4 * r + e] * vs[2 + r][e]);
-                        if (!whole) {  // a hidden token's weight is 0, its scale may be anything
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] &= ((seen >> (16 * tt + 4 * r + e)) & 1u ? 0xFFFFu : 0u) |
-                                        ((seen >> (16 * tt + 8 + 4 * r + e)) & 1u ? 0xFFFF0000u : 0u);
-                        }
-                        const half8 weights = __builtin_bit_cast(half8, uint4{w[0], w[1], w[2], w[3]});
-#pragma unroll
-                        for (int x = g * GS / 32; x < (g + 1) * GS / 32; ++x)
-                            acc[x] = mfma(pg.v[tt][r][x][lane], weights, acc[x]);
-                    }
-                }
+                for (int g = 0; g < NG; ++g)
+                    vs[tt][g] = pv.scale[g][32 * tt + slot];
+                if (NG == 2)
+                    ratio[tt] = pk.ratio[32 * tt + slot];
             }
+            float sum[2] = {0.0f, 0.0f};
+            auto read_step = [&](int s) {  // what step s needs
+                if (s < kSteps)
+                    kf[s % (kAhead + 1)] = pk.code[k_tile(s)][k_step(s)][k_from[k_step(s) % 2]];
+            };
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+                read_step(s);
+            r[0] = f32x16{};
+            r[1] = f32x16{};
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                r[k_tile(s)] = mfma(kf[s % (kAhead + 1)], q[k_step(s)], r[k_tile(s)]);
+                read_step(s + kAhead);
+                // pairs of tokens of this step: one of 16 steps, two of 8
+#pragma unroll
+                for (int pair = s * 16 / kSteps; pair < (s + 1) * 16 / kSteps; ++pair) {
+                    const int tt = pair / 8, y = pair / 4 % 2, e = pair % 4;
+                    const float lo = __builtin_amdgcn_exp2f(x[tt][4 * y + e]);
+                    const float hi = __builtin_amdgcn_exp2f(x[tt][8 + 4 * y + e]);
+                    sum[0] += lo;
+                    sum[1] += hi;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        w[tt][g][y][e] = pack2<OUT_F16>(scaled(lo, vs[tt][g], 4 * y + e), scaled(hi, vs[tt][g], 8 + 4 * y + e));
+                }
+                // between a tile's groups its products are scaled, a quarter a step
+                if (NG == 2 && s >= SG && s < 3 * SG) {
+                    f32x16 &to = r[s / SG - 1];
+#pragma unroll
+                    for (int e = 4 * (s % SG); e < 4 * (s % SG) + 4; ++e)
+                        to[e] = scaled(to[e], ratio[s / SG - 1], e);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            l_run += sum[0] + sum[1];
         }
-        if (i + 1 < end)
-            stage(pages[(i + 1 - begin) & 1], share, t.range.at(i + 1) * kPageTokens);
+        if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int tt = e / 8, y = e / 4 % 2, f = e % 4;
+                    w[tt][g][y][f] &= ((seen >> (16 * tt + 4 * y + f)) & 1u ? 0xFFFFu : 0u) |
+                                      ((seen >> (16 * tt + 8 + 4 * y + f)) & 1u ? 0xFFFF0000u : 0u);
+                }
+        }
+
+        // The outputs of page i, with the unpacking of what comes next between
+        // them: K of page i + 2, V of page i + 1.
+        {
+            constexpr int kSteps = 4 * NT, kAhead = 2;
+            PageK<D, GS> &to_k = page_k[(i - begin) & 1];
+            PageV<D, GS> &to_v = page_v[(i - begin + 1) & 1];
+            uint4 vf[kAhead + 1];
+            auto read_step = [&](int s) {
+                if (s < kSteps)
+                    vf[s % (kAhead + 1)] = pv.code[s / (2 * NT)][s / NT % 2][s % NT][lane];
+            };
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+                read_step(s);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int tt = s / (2 * NT), y = s / NT % 2, z = s % NT;
+                const uint32_t(&o)[4] = w[tt][z * 32 / GS][y];
+                acc[z] = mfma(vf[s % (kAhead + 1)], __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]}), acc[z]);
+                read_step(s + kAhead);
+                if (s % 2 == 1) {
+                    if (s < kSteps / 2)
+                        stage_k_dword(to_k, share, s / 2);
+                    else
+                        stage_v_dword(to_v, share, s / 2 - kSteps / 4);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            stage_v_scales(to_v, share, k_scale_next, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
+            stage_k_scales(to_k, share);
+        }
         n0 = n1;
         n1 = n2;
+        n2 = n3;
         __syncthreads();
     }
 
