@@ -55,6 +55,7 @@ struct Kv4Launch {
     int tiles;         // column tiles of the longest sequence
     int splits;        // workgroups that a tile's pages may be dealt to
     int pages;         // pages of one of them (splits > 1)
+    int waves;         // wavefronts of a few-row workgroup, 4 or 8
     float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
     float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
 };

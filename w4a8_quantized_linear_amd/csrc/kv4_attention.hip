@@ -14,66 +14,75 @@
 namespace cider {
 namespace {
 
-constexpr int kJoinWaves = 4;
+constexpr int kMaxSplits = 256;
 
-// One workgroup per (row, query head); its wavefronts take every 4th part.
-template <int D, int COLS>
-__global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttentionArgs a, Kv4Launch n)
+// WAVES wavefronts per (row, query head), 4 / WAVES pairs per workgroup.  A
+// part's factor is computed once, by the lane of its number; then groups of
+// D / 4 lanes add up the parts, 16 bytes a lane.
+template <int D, int COLS, int WAVES>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
-    constexpr int PER = D / 64;
-    __shared__ float part[kJoinWaves][D], part_l[kJoinWaves];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int cols = a.kv.max_rows * (a.q_heads / a.kv.kv_heads);
-    const int col = (int)(blockIdx.x % (unsigned)cols);
-    const unsigned bh = blockIdx.x / (unsigned)cols;
+    constexpr int PAIRS = 4 / WAVES, LANES = 64 * WAVES, GROUPS = LANES / (D / 4);
+    constexpr int PARTS = WAVES == 1 ? 64 : kMaxSplits;  // per pair at most
+    __shared__ float factor[PAIRS][PARTS];
+    __shared__ f32x4 sums[PAIRS][GROUPS][D / 4];
+    __shared__ float wave_m[4], wave_l[4];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int pair = wave / WAVES, lane = (int)threadIdx.x % LANES;
+    const int64_t cols = (int64_t)a.kv.max_rows * (a.q_heads / a.kv.kv_heads);
+    const int64_t id = (int64_t)blockIdx.x * PAIRS + pair;
+    const int col = (int)(id % cols);
+    const int64_t bh = id / cols;
     Tile t;
-    if (!tile_of<COLS>(a, (int)(bh / (unsigned)a.kv.kv_heads), (int)(bh % (unsigned)a.kv.kv_heads), col / COLS, t) ||
-        col >= t.cols || t.range.count <= n.pages)
-        return;
-    const int parts = (t.range.count + n.pages - 1) / n.pages;
-    const int64_t at = pair_of(a, t, col) * n.splits;
-    float m = -__builtin_inff();
-    for (int i = lane; i < parts; i += 64)
-        m = __builtin_fmaxf(m, n.part_stat[2 * (at + i)]);
+    const bool mine = bh < (int64_t)a.kv.kv_heads * a.kv.batch &&
+                      tile_of<COLS>(a, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, t) &&
+                      col < t.cols && t.range.count > n.pages;
+    const int parts = mine ? (t.range.count + n.pages - 1) / n.pages : 0;
+    const int64_t at = mine ? pair_of(a, t, col) * n.splits : 0;
+    float m = -__builtin_inff(), l = 0.0f;
+    if (lane < parts) {
+        m = n.part_stat[2 * (at + lane)];
+        l = n.part_stat[2 * (at + lane) + 1];
+    }
+    float top = wave_max(m);
+    if constexpr (WAVES > 1) {
+        if (lane % 64 == 0)
+            wave_m[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            top = __builtin_fmaxf(top, wave_m[w]);
+    }
+    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);  // l 0: saw nothing
+    l *= f;
+    if (lane < PARTS)
+        factor[pair][lane] = f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
-        m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    float l = 0.0f, o[PER] = {};
-    for (int i = wave; i < parts; i += kJoinWaves) {
-        const float li = n.part_stat[2 * (at + i) + 1];
-        const float f = li == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(n.part_stat[2 * (at + i)] - m);
-        l += li * f;
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-            o[e] += n.part[(at + i) * D + PER * lane + e] * f;
-    }
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-        part[wave][PER * lane + e] = o[e];
-    if (lane == 0)
-        part_l[wave] = l;
+        l += __shfl_xor(l, d);
+    if (lane % 64 == 0)
+        wave_l[wave] = l;
     __syncthreads();
-    if (wave != 0)
+    const int g = lane / (D / 4), d4 = lane % (D / 4);
+    f32x4 o = {0, 0, 0, 0};
+    const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * (D / 4) + d4;
+#pragma unroll 4
+    for (int i = g; i < parts; i += GROUPS)
+        o += part[(int64_t)i * (D / 4)] * factor[pair][i];
+    sums[pair][g][d4] = o;
+    __syncthreads();
+    if (g != 0 || !mine)
         return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i)
+        o += sums[pair][i][d4];
     l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWaves; ++w)
-        l += part_l[w];
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *y = output_of(a, t, col) + PER * lane;
-    float r[PER] = {};
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-#pragma unroll
-        for (int w = 0; w < kJoinWaves; ++w)
-            r[e] += part[w][PER * lane + e];
-        r[e] *= inv;
-    }
-    if constexpr (PER == 2)
-        *reinterpret_cast<uint32_t *>(y) = pack_out(r[0], r[1], a.y_dtype);
-    else
-        y[0] = (uint16_t)pack_out(r[0], 0.0f, a.y_dtype);
+    for (int w = 0; w < WAVES; ++w)
+        l += wave_l[pair * WAVES + w];
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2 *>(output_of(a, t, col) + 4 * d4) =
+        uint2{pack_out(o.x, o.y, a.y_dtype), pack_out(o.z, o.w, a.y_dtype)};
 }
 
 // Columns of a (sequence, kv head) at most.
@@ -104,12 +113,16 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
     n.splits = 1;
     const int64_t pages = most_pages(a, cols);
     const int64_t units = n.tiles * (int64_t)a.kv.kv_heads * a.kv.batch;
-    // chunks of at least kMinPages pages, as many as give kWanted workgroups
-    const int64_t kMinPages = 16, kWanted = cols == kManyCols ? 512 : 2048;
-    if (pages > kMinPages && units < kWanted) {
-        int64_t splits = (kWanted + units - 1) / units;
-        const int64_t most = (pages + kMinPages - 1) / kMinPages;
+    // chunks of at least min_pages pages, as many as give `wanted` workgroups
+    const int64_t min_pages = 16, wanted = cols == kManyCols ? 512 : 2048;
+    n.waves = 4;
+    if (cols == kFewCols && units <= 256 && pages <= 64) {
+        n.waves = 8;
+    } else if (pages > min_pages && units < wanted) {
+        int64_t splits = (wanted + units - 1) / units;
+        const int64_t most = (pages + min_pages - 1) / min_pages;
         splits = splits < most ? splits : most;
+        splits = splits < kMaxSplits ? splits : kMaxSplits;
         n.pages = (int)((pages + splits - 1) / splits);
         n.splits = (int)((pages + n.pages - 1) / n.pages);
     }
@@ -129,14 +142,23 @@ size_t bytes_of(const Kv4AttentionArgs &a, const Kv4Launch &n)
                         : part_bytes(a, n) + round256((size_t)a.kv.rows * a.q_heads * n.splits * 2 * sizeof(float));
 }
 
+template <int D, int COLS>
+void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    const unsigned pairs = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
+    if (n.splits <= 16)
+        kv4_join_kernel<D, COLS, 1><<<(pairs + 3) / 4, 256, 0, stream>>>(a, n);
+    else
+        kv4_join_kernel<D, COLS, 4><<<pairs, 256, 0, stream>>>(a, n);
+}
+
 template <int D>
 void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    const unsigned grid = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
     if (tile_cols(a) == kManyCols)
-        kv4_join_kernel<D, kManyCols><<<grid, 64 * kJoinWaves, 0, stream>>>(a, n);
+        launch_join<D, kManyCols>(a, n, stream);
     else
-        kv4_join_kernel<D, kFewCols><<<grid, 64 * kJoinWaves, 0, stream>>>(a, n);
+        launch_join<D, kFewCols>(a, n, stream);
 }
 
 }  // namespace

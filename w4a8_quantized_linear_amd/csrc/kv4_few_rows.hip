@@ -27,15 +27,13 @@
 // (j, c) ends with the scores of tokens 4 j + i of column c in its registers
 // and they are, rounded and packed, the right operand of O^T += V^T P^T: no
 // transpose, no LDS for either product.  A wavefront takes whole 64-token pages
-// (every kWaves-th of the workgroup's), loads the next page's codes as soon as
+// (every 4th or 8th of the workgroup's), loads the next page's codes as soon as
 // it has used this one's, and the wavefronts' maxima, sums and outputs meet in LDS at the end.
 #include "kv4_attention.h"
 
 namespace cider {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kCols = kFewCols;
 
 // Maximum and sum over the 4 lanes (j = 0 .. 3) of a column.
@@ -233,26 +231,26 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
     }
 }
 
-template <int D, int GS>
-__global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+template <int D, int GS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int NM = D / 32;   // score products per 16 tokens
     constexpr int NG = D / GS;   // scales per token
     constexpr int NT = D / 16;   // output tiles
-    __shared__ __align__(16) float scales[kWaves][2][NG][kPageTokens];
-    __shared__ __align__(16) float part[kWaves][kCols][D + 4];
-    __shared__ float part_m[kWaves][kCols], part_l[kWaves][kCols];
+    __shared__ __align__(16) float scales[WAVES][2][NG][kPageTokens];
+    __shared__ __align__(16) float part[WAVES][kCols][D + 4];
+    __shared__ float part_m[WAVES][kCols], part_l[WAVES][kCols];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane % 16, j = lane / 16;
-    // heads fastest, then splits, tiles and sequences
+    // heads fastest, then sequences, splits and tiles
     unsigned id = blockIdx.x;
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
-    const int split = (int)(id % (unsigned)n.splits);
-    id /= (unsigned)n.splits;
-    const int tile = (int)(id % (unsigned)n.tiles), b = (int)(id / (unsigned)n.tiles);
+    const int b = (int)(id % (unsigned)a.kv.batch);
+    id /= (unsigned)a.kv.batch;
+    const int split = (int)(id % (unsigned)n.splits), tile = (int)(id / (unsigned)n.splits);
     Tile t;
     if (!tile_of<kCols>(a, b, head, tile, t))
         return;
@@ -324,15 +322,15 @@ __global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionA
         load_k<D, GS>(pg, block_of(n0), lane);
         load_v<D, GS>(pg, block_of(n0), lane);
     }
-    if (i + kWaves < end)
-        n1 = table[t.range.at(i + kWaves)];
-    for (; i < end; i += kWaves) {
+    if (i + WAVES < end)
+        n1 = table[t.range.at(i + WAVES)];
+    for (; i < end; i += WAVES) {
         int n2 = -1;
-        if (i + 2 * kWaves < end)
-            n2 = table[t.range.at(i + 2 * kWaves)];
+        if (i + 2 * WAVES < end)
+            n2 = table[t.range.at(i + 2 * WAVES)];
         // past the last page this one is loaded again (from the caches): a load
         // under a branch would cost its registers twice
-        const uint8_t *ahead = block_of(i + kWaves < end ? n1 : n0);
+        const uint8_t *ahead = block_of(i + WAVES < end ? n1 : n0);
         const bool there = (unsigned)n0 < (unsigned)a.kv.num_pages;
         const int t0 = t.range.at(i) * kPageTokens;
         const bool whole = t0 + kPageTokens - 1 <= t.p_lo &&
@@ -374,17 +372,17 @@ __global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionA
         part_l[wave][c] = st.l;
     }
     __syncthreads();
-    constexpr int PER = D / 16;  // elements per thread
-    const int oc = threadIdx.x / 16, d0 = threadIdx.x % 16 * PER;
+    constexpr int PER = kCols * D / (64 * WAVES);  // elements per thread
+    const int oc = threadIdx.x / (D / PER), d0 = threadIdx.x % (D / PER) * PER;
     const int ocol = t.tile * kCols + oc;
     if (ocol >= t.cols)
         return;
     float m = -__builtin_inff(), l = 0.0f, o[PER] = {};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         m = __builtin_fmaxf(m, part_m[w][oc]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         if (part_l[w][oc] == 0.0f)  // saw nothing
             continue;
         const float f = __builtin_amdgcn_exp2f(part_m[w][oc] - m);
@@ -396,8 +394,8 @@ __global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionA
     if (n.splits > 1 && t.range.count > n.pages) {
         const int64_t at = pair_of(a, t, ocol) * n.splits + split;
 #pragma unroll
-        for (int e = 0; e < PER; e += 4)
-            *reinterpret_cast<f32x4 *>(n.part + at * D + d0 + e) = f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
+        for (int e = 0; e < PER; ++e)
+            n.part[at * D + d0 + e] = o[e];
         if (d0 == 0) {
             n.part_stat[2 * at] = m;
             n.part_stat[2 * at + 1] = l;
@@ -412,22 +410,33 @@ __global__ __launch_bounds__(kThreads, 3) void kv4_few_rows_kernel(Kv4AttentionA
     uint16_t *y = output_of(a, t, ocol) + d0;
     if constexpr (PER == 8)
         *reinterpret_cast<uint4 *>(y) = uint4{w[0], w[1], w[2], w[3]};
-    else
+    else if constexpr (PER == 4)
         *reinterpret_cast<uint2 *>(y) = uint2{w[0], w[1]};
+    else
+        *reinterpret_cast<uint32_t *>(y) = w[0];
 }
 
 }  // namespace
 
-hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+template <int WAVES>
+static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_few_rows_kernel<64, 64><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<64, 64, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else if (a.kv.group_size == 64)
-        kv4_few_rows_kernel<128, 64><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 64, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else
-        kv4_few_rows_kernel<128, 128><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 128, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+}
+
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    if (n.waves == 8)
+        launch<8>(a, n, stream);
+    else
+        launch<4>(a, n, stream);
     return hipGetLastError();
 }
 

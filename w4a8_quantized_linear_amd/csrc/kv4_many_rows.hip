@@ -334,6 +334,23 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         fetch_v(share, n1);
         const int t0 = t.range.at(i) * kPageTokens;
 
+        // Operands come from LDS kAhead steps before they are used: the first of
+        // K's before the softmax begins, of V's in its last steps.
+        constexpr int kSteps = 2 * NK, kAhead = 2;  // score products, and as many of the outputs
+        static_assert(kSteps == 4 * NT, "");
+        uint4 kf[kAhead + 1], vf[kAhead + 1];
+        auto read_k = [&](int s) {
+            if (s < kSteps)
+                kf[s % (kAhead + 1)] = pk.code[k_tile(s)][k_step(s)][k_from[k_step(s) % 2]];
+        };
+        auto read_v = [&](int s) {
+            if (s < kSteps)
+                vf[s % (kAhead + 1)] = pv.code[s / (2 * NT)][s / NT % 2][s % NT][lane];
+        };
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+            read_k(s);
+
         // scores of page i less the running maximum
         const float m_sub = m_run == -inf ? 0.0f : m_run;
         float x[2][16];
@@ -394,13 +411,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
 
         // The weights of page i, one pair of tokens a step, each step with one
         // score product of page i + 1 in front of it: the matrix core works
-        // while the vector unit does.  LDS reads go out kAhead steps early, and
-        // the barriers keep the compiler from gathering the products.  (Past
+        // while the vector unit does.  The
+        // barriers keep the compiler from gathering the products.  (Past
         // the last page the products take what lies in the buffer; unused.)
         uint32_t w[2][NG][2][4];
         {
-            constexpr int kSteps = 2 * NK, kAhead = 2;
-            uint4 kf[kAhead + 1];
             float vs[2][NG], ratio[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -411,20 +426,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                     ratio[tt] = pk.ratio[32 * tt + slot];
             }
             float sum[2] = {0.0f, 0.0f};
-            auto read_step = [&](int s) {  // what step s needs
-                if (s < kSteps)
-                    kf[s % (kAhead + 1)] = pk.code[k_tile(s)][k_step(s)][k_from[k_step(s) % 2]];
-            };
-#pragma unroll
-            for (int s = 0; s < kAhead; ++s)
-                read_step(s);
             r[0] = f32x16{};
             r[1] = f32x16{};
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 r[k_tile(s)] = mfma(kf[s % (kAhead + 1)], q[k_step(s)], r[k_tile(s)]);
-                read_step(s + kAhead);
+                read_k(s + kAhead);
+                if (s >= kSteps - kAhead)
+                    read_v(s - (kSteps - kAhead));
                 // pairs of tokens of this step: one of 16 steps, two of 8
 #pragma unroll
                 for (int pair = s * 16 / kSteps; pair < (s + 1) * 16 / kSteps; ++pair) {
@@ -462,24 +472,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         // The outputs of page i, with the unpacking of what comes next between
         // them: K of page i + 2, V of page i + 1.
         {
-            constexpr int kSteps = 4 * NT, kAhead = 2;
             PageK<D, GS> &to_k = page_k[(i - begin) & 1];
             PageV<D, GS> &to_v = page_v[(i - begin + 1) & 1];
-            uint4 vf[kAhead + 1];
-            auto read_step = [&](int s) {
-                if (s < kSteps)
-                    vf[s % (kAhead + 1)] = pv.code[s / (2 * NT)][s / NT % 2][s % NT][lane];
-            };
-#pragma unroll
-            for (int s = 0; s < kAhead; ++s)
-                read_step(s);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const int tt = s / (2 * NT), y = s / NT % 2, z = s % NT;
                 const uint32_t(&o)[4] = w[tt][z * 32 / GS][y];
                 acc[z] = mfma(vf[s % (kAhead + 1)], __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]}), acc[z]);
-                read_step(s + kAhead);
+                read_v(s + kAhead);
                 if (s % 2 == 1) {
                     if (s < kSteps / 2)
                         stage_k_dword(to_k, share, s / 2);
