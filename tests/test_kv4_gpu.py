@@ -347,6 +347,34 @@ def test_bounds_of_the_device_arrays():
     assert base is not None
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_page_that_is_not_there_leaves_no_trace(rows):
+    """Whatever the cache's first page holds (the largest scales here), a page number outside the cache only
+    hides its tokens."""
+    s = Setup([300], [rows], 1, 128, 64, garbage="nan")
+    ref.fill(s.cache, s.table, s.lens, *s.values(1))
+    if s.table[0, 1] == 0 or 0 in s.table[0, 2:5]:   # page 0 is to be one that no token is in
+        free = next(n for n in range(s.num_pages) if n not in s.table[0, :5])
+        s.cache.data[[0, free]] = s.cache.data[[free, 0]]
+        s.table[0][s.table[0] == 0] = free
+    s.table[0, 1] = -7
+    s.cache.data[0, :, 64 * 128:] = np.tile(np.array([2.0 ** 100], np.float32).view(np.uint8), 256)
+    q = ref.to_bits(s.rng.standard_normal((rows, 4, 128)), 1)
+    got = ref.to_f64(attend(s, s.to_device(), q, 1, 0, 4, 0.1), 0)
+    # the same with the hidden tokens' keys far below all others
+    t = ref.Cache(s.cache.data.copy(), 128, 64)
+    pages = list(s.table[0, :5])
+    k, v = (t.values(i, [n if n >= 0 else pages[0] for n in pages]) for i in (0, 1))
+    for i in range(rows):
+        see = [u for u in range(300 - rows + i + 1) if u // 64 != 1]
+        for h in range(4):
+            x = 0.1 * (k[0][0][see] @ ref.to_f64(q[i, h], 1))
+            w = np.exp(x - x.max())
+            w /= w.sum()
+            want, size = w @ v[0][0][see], w @ (np.abs(v[0][0][see]) + 16 * v[1][0][see])
+            assert (np.abs(got[i, h] - want) <= 2.0 ** -9 * size + 2.0 ** -11 * np.abs(want)).all(), (i, h)
+
+
 def test_blocks_past_4_gib():
     import torch
     D, gs, H = 128, 64, 8

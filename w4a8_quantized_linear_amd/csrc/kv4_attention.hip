@@ -113,14 +113,21 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
     n.splits = 1;
     const int64_t pages = most_pages(a, cols);
     const int64_t units = n.tiles * (int64_t)a.kv.kv_heads * a.kv.batch;
-    // chunks of at least min_pages pages, as many as give `wanted` workgroups
-    const int64_t min_pages = 16, wanted = cols == kManyCols ? 512 : 2048;
+    // Chunks that make about two workgroups a compute unit, of 4 pages (one a
+    // wavefront) to kLongest: below that a chunk's fixed cost shows, above it the
+    // longest sequence of a ragged batch does.
+    constexpr int64_t kWanted = 512, kShortest = 4, kLongest = 32;
+    int64_t chunk = (units * pages / kWanted + 3) / 4 * 4;
+    chunk = chunk < kShortest ? kShortest : (chunk > kLongest ? kLongest : chunk);
+    const int64_t least = (pages + kMaxSplits - 1) / kMaxSplits;
+    chunk = chunk < least ? least : chunk;
     n.waves = 4;
-    if (cols == kFewCols && units <= 256 && pages <= 64) {
-        n.waves = 8;
-    } else if (pages > min_pages && units < wanted) {
-        int64_t splits = (wanted + units - 1) / units;
-        const int64_t most = (pages + min_pages - 1) / min_pages;
+    if (cols == kFewCols && pages > chunk) {
+        n.pages = (int)chunk;
+        n.splits = (int)((pages + chunk - 1) / chunk);
+    } else if (cols == kManyCols && pages > 16 && units < kWanted) {
+        int64_t splits = (kWanted + units - 1) / units;
+        const int64_t most = (pages + 15) / 16;
         splits = splits < most ? splits : most;
         splits = splits < kMaxSplits ? splits : kMaxSplits;
         n.pages = (int)((pages + splits - 1) / splits);

@@ -44,8 +44,9 @@ __device__ __forceinline__ float column_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// One page's codes as the lanes use them, and its scales by token (lane =
-// token).  K and V are loaded apart: the next page's K as soon as the scores
+// One page's codes as the lanes use them, and its scales: lane (j, n) holds
+// those of token 16 (n / 4) + 4 j + n % 4, so each row of 16 lanes has the
+// scales of its own 16 tokens and takes them by broadcast.  K and V are loaded apart: the next page's K as soon as the scores
 // have used this one's, its V after the outputs have, so one page's registers
 // serve and other wavefronts cover what is left of the latency.
 template <int D, int GS>
@@ -54,6 +55,8 @@ struct PageData {
     uint4 v[2][D / 64];
     float ks[D / GS], vs[D / GS];
 };
+
+__device__ __forceinline__ int scale_token(int lane) { return 16 * (lane / 4 % 4) + 4 * (lane / 16) + lane % 4; }
 
 template <int D, int GS>
 __device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block, int lane)
@@ -77,7 +80,7 @@ __device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block,
     const float *s = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
 #pragma unroll
     for (int g = 0; g < D / GS; ++g)
-        p.ks[g] = s[g * kPageTokens + (uint32_t)lane];
+        p.ks[g] = s[g * kPageTokens + (uint32_t)scale_token(lane)];
 }
 
 template <int D, int GS>
@@ -92,7 +95,7 @@ __device__ __forceinline__ void load_v(PageData<D, GS> &p, const uint8_t *block,
     const float *s = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
 #pragma unroll
     for (int g = 0; g < D / GS; ++g)
-        p.vs[g] = s[(D / GS + g) * kPageTokens + (uint32_t)lane];
+        p.vs[g] = s[(D / GS + g) * kPageTokens + (uint32_t)scale_token(lane)];
 }
 
 __device__ __forceinline__ half8 halves(uint32_t w) { return __builtin_bit_cast(half8, nibble_halves(w)); }
@@ -107,42 +110,26 @@ struct State {
     float zero[D / GS], qmul;
 };
 
-// A wavefront's slot for one page's scales by token.
-template <int D, int GS>
-using Scales = float[D / GS][kPageTokens];
-
-__device__ __forceinline__ void wave_lds_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Scores of a page: s[t][e] is token 16 t + 4 j + e of the lane's column.
 template <int D, int GS>
-__device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageData<D, GS> &pg,
-                                            Scales<D, GS> &scales, int lane, float (&s)[4][4])
+__device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageData<D, GS> &pg, float (&s)[4][4])
 {
     constexpr int NG = D / GS;
-    const int j = lane / 16;
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-        scales[g][lane] = pg.ks[g];
-    wave_lds_fence();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        f32x4 sum;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f32x4 r = {st.zero[g], st.zero[g], st.zero[g], st.zero[g]};
 #pragma unroll
             for (int m = g * GS / 32; m < (g + 1) * GS / 32; ++m)
                 r = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(pg.k[t][m]), st.q[m], r, 0, 0, 0);
-            const f32x4 ks = *reinterpret_cast<const f32x4 *>(&scales[g][16 * t + 4 * j]);
-            sum = g == 0 ? r * ks : sum + r * ks;
-        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            s[t][e] = sum[e];
+            for (int e = 0; e < 4; ++e) {
+                const float x = scaled(r[e], pg.ks[g], 4 * t + e);
+                s[t][e] = g == 0 ? x : s[t][e] + x;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all 4 tiles' operands at once would not fit the registers
     }
 }
 
@@ -150,17 +137,16 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
 // column sees the token (read where the page is not whole); last: the last token
 // of the page that any column of the tile sees (63 and more: all).
 template <int D, int GS>
-__device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg,
-                                             Scales<D, GS> &scales, int lane, float (&s)[4][4],
-                                             bool whole, uint32_t seen, int last)
+__device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
+                                             float (&s)[4][4], bool whole, uint32_t seen, int last)
 {
     constexpr int NG = D / GS, NT = D / 16;
     const float inf = __builtin_inff();
-    const int j = lane / 16;
-    // V's scales by token; the weights' exponents move up first
+    // V's scales; the weights' exponents move up first
+    float vs[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const float v = lane <= last ? pg.vs[g] : 0.0f;
+        const float v = scale_token(lane) <= last ? pg.vs[g] : 0.0f;
         if (__any(v >= ldexp_f(1.0f, st.v_exp[g]) && v < inf)) {
             const float top = wave_max(v < inf ? v : 0.0f);
             const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top));
@@ -174,9 +160,8 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
                 st.off[y] *= f;
         }
         // the 16 times larger codes belong to tokens 1 and 3 of each 4
-        scales[g][lane] = ldexp_f(v, 14 - st.v_exp[g] - (lane & 1 ? 4 : 0));
+        vs[g] = ldexp_f(v, 14 - st.v_exp[g] - (lane & 1 ? 4 : 0));
     }
-    wave_lds_fence();
     float top = s[0][0];
 #pragma unroll
     for (int n = 1; n < 16; ++n)
@@ -201,34 +186,41 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         st.l += x;
     }
     const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
+    uint32_t w[NG][2][4];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int B = 0; B < 2; ++B) {
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(&scales[g][32 * B + 4 * j]);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(&scales[g][32 * B + 16 + 4 * j]);
-            uint32_t w[4];
+        for (int B = 0; B < 2; ++B)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                w[e] = pack2<OUT_F16>(s[2 * B][e] * lo[e], s[2 * B + 1][e] * hi[e]);
-            if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+                w[g][B][e] = pack2<OUT_F16>(scaled(s[2 * B][e], vs[g], 8 * B + e),
+                                            scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e));
+    if (!whole) {  // a hidden token's weight is 0, its scale may be anything
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] &= ((seen >> (8 * B + e)) & 1u ? 0xFFFFu : 0u) |
-                            ((seen >> (8 * B + 4 + e)) & 1u ? 0xFFFF0000u : 0u);
+        for (int B = 0; B < 2; ++B)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t keep = ((seen >> (8 * B + e)) & 1u ? 0xFFFFu : 0u) |
+                                      ((seen >> (8 * B + 4 + e)) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    w[g][B][e] &= keep;
             }
-            const half8 weights = __builtin_bit_cast(half8, uint4{w[0], w[1], w[2], w[3]});
-#pragma unroll
-            for (int y = g * GS / 64; y < (g + 1) * GS / 64; ++y) {
-                const uint32_t u[4] = {pg.v[B][y].x, pg.v[B][y].y, pg.v[B][y].z, pg.v[B][y].w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(u[x]), weights,
-                                                                               st.acc[4 * y + x], 0, 0, 0);
-                st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights, st.off[y], 0, 0, 0);
-            }
-        }
     }
+#pragma unroll
+    for (int B = 0; B < 2; ++B)
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) {
+            const uint32_t(&o)[4] = w[y * 64 / GS][B];
+            const half8 weights = __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]});
+            const uint32_t u[4] = {pg.v[B][y].x, pg.v[B][y].y, pg.v[B][y].z, pg.v[B][y].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(u[x]), weights,
+                                                                           st.acc[4 * y + x], 0, 0, 0);
+            st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights, st.off[y], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 }
 
 template <int D, int GS, int WAVES>
@@ -237,7 +229,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
     constexpr int NM = D / 32;   // score products per 16 tokens
     constexpr int NG = D / GS;   // scales per token
     constexpr int NT = D / 16;   // output tiles
-    __shared__ __align__(16) float scales[WAVES][2][NG][kPageTokens];
     __shared__ __align__(16) float part[WAVES][kCols][D + 4];
     __shared__ float part_m[WAVES][kCols], part_l[WAVES][kCols];
 
@@ -264,18 +255,41 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
     const int row = valid ? col / t.G : 0;
     const int p = valid ? t.seq.kv - t.seq.n + row : -1;
 
+    // q is asked for first and used last: the first page's codes are on their
+    // way while it is scaled
+    uint4 qw[NM];
+    {
+        const uint16_t *q = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
+                            (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * j;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            qw[m] = *reinterpret_cast<const uint4 *>(q + 32 * m);
+    }
+    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
+    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
+    // a page number outside the cache is never followed: page 0 is loaded in
+    // its place and its tokens are left out
+    auto block_of = [&](int number) {
+        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+    };
+    // page numbers are read two pages ahead
+    PageData<D, GS> pg;
+    int i = begin + wave, n0 = -1, n1 = -1;
+    if (i < end) {
+        n0 = table[t.range.at(i)];
+        load_k<D, GS>(pg, block_of(n0), lane);
+        load_v<D, GS>(pg, block_of(n0), lane);
+    }
+    if (i + WAVES < end)
+        n1 = table[t.range.at(i + WAVES)];
+
     State<D, GS> st;
     {
         float x[NM][8], top = 0.0f;
-        const uint16_t *q = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
-                            (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * j;
-        uint4 w[NM];
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-            w[m] = *reinterpret_cast<const uint4 *>(q + 32 * m);
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            widen8(w[m], a.q_dtype, x[m]);
+            widen8(qw[m], a.q_dtype, x[m]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[m][e] = valid ? x[m][e] : 0.0f;
@@ -306,24 +320,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
         st.l = 0.0f;
     }
 
-    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
-    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
-    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
-    // a page number outside the cache is never followed: page 0 is loaded in
-    // its place and its tokens are left out
-    auto block_of = [&](int number) {
-        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
-    };
-    // page numbers are read two pages ahead
-    PageData<D, GS> pg;
-    int i = begin + wave, n0 = -1, n1 = -1;
-    if (i < end) {
-        n0 = table[t.range.at(i)];
-        load_k<D, GS>(pg, block_of(n0), lane);
-        load_v<D, GS>(pg, block_of(n0), lane);
-    }
-    if (i + WAVES < end)
-        n1 = table[t.range.at(i + WAVES)];
     for (; i < end; i += WAVES) {
         int n2 = -1;
         if (i + 2 * WAVES < end)
@@ -333,16 +329,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
         const uint8_t *ahead = block_of(i + WAVES < end ? n1 : n0);
         const bool there = (unsigned)n0 < (unsigned)a.kv.num_pages;
         const int t0 = t.range.at(i) * kPageTokens;
-        const bool whole = t0 + kPageTokens - 1 <= t.p_lo &&
+        const bool whole = there && t0 + kPageTokens - 1 <= t.p_lo &&
                            (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
         float s[4][4];
-        page_scores<D, GS>(st, pg, scales[wave][0], lane, s);
+        page_scores<D, GS>(st, pg, s);
         load_k<D, GS>(pg, ahead, lane);
         uint32_t seen = 0xFFFFu;
         if (!whole) {
             seen = 0;
             // bounds of the token's offset from the lane's first
-            const int at = t0 + 4 * j, upto = p - at, kept = a.sinks - at;
+            const int at = t0 + 4 * j, upto = there ? p - at : -1, kept = a.sinks - at;
             const int after = a.window == 0 ? -1 : p - a.window - at;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -352,8 +348,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
                 s[e / 4][e % 4] = see ? s[e / 4][e % 4] : -__builtin_inff();
             }
         }
-        if (there)
-            page_outputs<D, GS>(st, pg, scales[wave][1], lane, s, whole, seen, t.p_hi - t0);
+        page_outputs<D, GS>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
         load_v<D, GS>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;

@@ -54,34 +54,6 @@ struct PageV {
 // take them by a broadcast within the row (DPP), so a tile's scales cost one
 // 4-byte LDS read instead of four 16-byte ones.
 __device__ __forceinline__ int scale_slot(int t) { return t / 32 * 32 + t / 4 % 2 * 16 + t / 8 % 4 * 4 + t % 4; }
-template <int N>
-__device__ __forceinline__ float row_lane(float v)
-{
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
-}
-// x times the scale of the lane's token n of a tile.
-__device__ __forceinline__ float scaled(float x, float scales, int n)
-{
-    switch (n) {
-    case 0: return row_lane<0>(scales) * x;
-    case 1: return row_lane<1>(scales) * x;
-    case 2: return row_lane<2>(scales) * x;
-    case 3: return row_lane<3>(scales) * x;
-    case 4: return row_lane<4>(scales) * x;
-    case 5: return row_lane<5>(scales) * x;
-    case 6: return row_lane<6>(scales) * x;
-    case 7: return row_lane<7>(scales) * x;
-    case 8: return row_lane<8>(scales) * x;
-    case 9: return row_lane<9>(scales) * x;
-    case 10: return row_lane<10>(scales) * x;
-    case 11: return row_lane<11>(scales) * x;
-    case 12: return row_lane<12>(scales) * x;
-    case 13: return row_lane<13>(scales) * x;
-    case 14: return row_lane<14>(scales) * x;
-    default: return row_lane<15>(scales) * x;
-    }
-}
-
 // A thread's share of a page on its way.
 template <int D>
 struct Share {
@@ -265,11 +237,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
         const int x = vx + e;
         to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
     };
-    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<D> &s, float k_scale, int t0) {
+    // number, t0: the page's
+    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<D> &s, float k_scale, int number, int t0) {
         if (wave == 0)
             to.k_scale[scale_slot(lane)] = k_scale;
         if (wave >= 1 && wave <= NG) {
-            const float v = t0 + lane <= t.p_hi ? s.v_scale : 0.0f;
+            const bool held = t0 + lane <= t.p_hi && (unsigned)number < (unsigned)a.kv.num_pages;
+            const float v = held ? s.v_scale : 0.0f;
             const int e = __builtin_amdgcn_readfirstlane(
                 __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
             v_exp_run = e > v_exp_run ? e : v_exp_run;
@@ -303,7 +277,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
             stage_v_dword(page_v[0], share, m);
         }
         stage_k_scales(page_k[0], share);
-        stage_v_scales(page_v[0], share, k_scale_next, t.range.at(begin) * kPageTokens);
+        stage_v_scales(page_v[0], share, k_scale_next, n0, t.range.at(begin) * kPageTokens);
         fetch_k(share, n1);
 #pragma unroll
         for (int m = 0; m < D / 32; ++m)
@@ -489,7 +463,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            stage_v_scales(to_v, share, k_scale_next, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
+            stage_v_scales(to_v, share, k_scale_next, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
             stage_k_scales(to_k, share);
         }
         n0 = n1;
