@@ -159,6 +159,28 @@ def test_append_step_by_step_equals_append_at_once():
     assert np.array_equal(gu.to_host(steps.dcache), want)
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_scales_of_every_magnitude(dtype):
+    """Each finite 16-bit magnitude once as a group's largest value, the group's other values spread below it."""
+    r = np.random.default_rng(dtype)
+    top = np.arange(0, 0x7F80 if dtype else 0x7C00, dtype=np.uint16)
+    D, n = 64, len(top)
+    x = ref.to_f64(top, dtype)[:, None] * np.concatenate([[1.0], r.uniform(-1, 1, D - 1)])
+    x = ref.to_f64(ref.to_bits(x, dtype), dtype).reshape(n, 1, D)
+    s = Setup([n], [n], 1, D, 64, garbage="nan")
+    batch = s.to_device()
+    rows = gu.bits_to_dev(ref.to_bits(x, dtype).reshape(n, D))
+    cider.cider_kv4_append(batch, rows, rows, dtype, D, D)
+    u, sc = ref.quantize(x, 64)
+    c = ref.Cache(gu.to_host(s.dcache), D, 64)
+    pages = list(s.table[0, :-(-n // 64)])
+    with np.errstate(over="ignore"):
+        want = sc.astype(np.float64) * (u.astype(np.float64) - 8)
+    for which in (0, 1):
+        v, _ = c.values(which, pages)
+        assert np.array_equal(v[0, :n], want.reshape(n, D))
+
+
 def attend(s, batch, q, q_dtype, y_dtype, HQ, scale, window=0, sinks=0, workspace=True, stream=None):
     """q uint16 patterns [rows, HQ, D]; returns uint16 patterns, rows as they were where nothing is written."""
     import torch

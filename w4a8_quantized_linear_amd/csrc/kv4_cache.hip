@@ -90,12 +90,25 @@ __device__ __forceinline__ uint32_t run_max(uint32_t v)
     return v;
 }
 
+// a / 7 correctly rounded, a the magnitude of a 16-bit value: the product with
+// 1/7 and one correction by its exact remainder (right for every fp16 and, by
+// their mantissas, every bf16 value whose remainder does not underflow; the
+// others, 0 and infinity divide).
+__device__ __forceinline__ float seventh(float a)
+{
+    constexpr float kInv = 1.0f / 7.0f;
+    if (!(a >= 0x1p-90f && a < __builtin_inff()))
+        return a / quant_divisor<4>();
+    const float q = a * kInv;
+    return __builtin_fmaf(__builtin_fmaf(-7.0f, q, a), kInv, q);
+}
+
 // The int4 codes of 8 values, packed: quantize_chunk's, by fewer operations.
 // r = rint(x * rs) by adding and taking off 1.5 2^23, d = x * rs - r its
 // distance, and the nibbles u = r + 8 are put together as whole numbers in
 // fp32 (at most 16 bits, exact).  x * rs, exact inside the fused operations, is
-// within 2^-20 of the correctly rounded quotient x / s (|x / s| <= 7.5, rs off
-// by 2^-24 of itself), so where d stays 2^-14 away from a half the rounding is
+// within 2^-19 of the correctly rounded quotient x / s (|x / s| <= 7.5, rs, the
+// hardware's 1 / s, off by at most 2^-23 of itself), so where d stays 2^-14 away from a half the rounding is
 // the quotient's; a chunk with a value nearer to one, or of a group whose scale
 // is not a normal number (0, NaN and infinity too), divides.
 template <int DT>
@@ -164,10 +177,10 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4Args a, const u
     for (int i = 0; i < PT; ++i) {
         const int c8 = (tid + i * kThreads) % CH, t = (tid + i * kThreads) / CH, p = w.base + t;
         const int token = half * kSpan + t;
-        const float ks = widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(kx[i]))) / quant_divisor<4>();
-        const float vs = widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(vx[i]))) / quant_divisor<4>();
-        const uint32_t kq = int4_codes<DT>(kx[i], ks, 1.0f / ks);
-        vcode[t][c8] = int4_codes<DT>(vx[i], vs, 1.0f / vs);
+        const float ks = seventh(widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(kx[i]))));
+        const float vs = seventh(widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(vx[i]))));
+        const uint32_t kq = int4_codes<DT>(kx[i], ks, __builtin_amdgcn_rcpf(ks));
+        vcode[t][c8] = int4_codes<DT>(vx[i], vs, __builtin_amdgcn_rcpf(vs));
         if (p >= w.lo && p < w.hi) {
             kcode[token * CH + (c8 % 4) * (D / 32) + c8 / 4] = kq;
             if (c8 % (GS / 8) == 0) {
