@@ -113,20 +113,35 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
     n.splits = 1;
     const int64_t pages = most_pages(a, cols);
     const int64_t units = n.tiles * (int64_t)a.kv.kv_heads * a.kv.batch;
-    // Chunks that make about two workgroups a compute unit, of 4 pages (one a
-    // wavefront) to kLongest: below that a chunk's fixed cost shows, above it the
-    // longest sequence of a ragged batch does.
-    constexpr int64_t kWanted = 512, kShortest = 4, kLongest = 32;
-    int64_t chunk = (units * pages / kWanted + 3) / 4 * 4;
-    chunk = chunk < kShortest ? kShortest : (chunk > kLongest ? kLongest : chunk);
-    const int64_t least = (pages + kMaxSplits - 1) / kMaxSplits;
-    chunk = chunk < least ? least : chunk;
     n.waves = 4;
-    if (cols == kFewCols && pages > chunk) {
+    if (cols == kFewCols) {
+        // One workgroup per tile, or chunks and a second launch.  Measured (bf16,
+        // equal lengths; units = tiles of all heads and sequences): a page of 128
+        // elements takes a workgroup of 8 wavefronts 0.27 us; splitting costs 4 us
+        // and 1.9 ns for every page of all tiles on top.  8 / 64 units: 16 pages
+        // 9.6 / 10.0 us whole, 9.2 / 10.3 split; 64 pages 20.6 / 21.5 against 9.4 /
+        // 16.2; 256 units of 64 pages 31.7 against 36.3.  Past kWhole pages a
+        // ragged batch's longest sequence would be waited for.
+        constexpr int64_t kWhole = 80;
+        if (pages <= kWhole && pages * a.kv.head_dim * (2700 - 19 * (units < 1000 ? units : 1000)) <= 4 * 128 * 10000) {
+            // from two workgroups a compute unit on, more wavefronts in each only
+            // wait for one another (512 units of 16 pages: 21.9 us with 8, 16.4 with 4)
+            n.waves = units < 512 ? 8 : 4;
+            return n;
+        }
+        // Chunks that make about two workgroups a compute unit, of 4 pages (one a
+        // wavefront) to kLongest: below that a chunk's fixed cost shows (one
+        // sequence of 131072 tokens: 34 us in chunks of 32 pages, 42 of 8), above
+        // it the longest sequence of a ragged batch does.
+        constexpr int64_t kWanted = 512, kShortest = 4, kLongest = 32;
+        int64_t chunk = (units * pages / kWanted + 3) / 4 * 4;
+        chunk = chunk < kShortest ? kShortest : (chunk > kLongest ? kLongest : chunk);
+        const int64_t least = (pages + kMaxSplits - 1) / kMaxSplits;
+        chunk = chunk < least ? least : chunk;
         n.pages = (int)chunk;
         n.splits = (int)((pages + chunk - 1) / chunk);
-    } else if (cols == kManyCols && pages > 16 && units < kWanted) {
-        int64_t splits = (kWanted + units - 1) / units;
+    } else if (pages > 16 && units < 512) {
+        int64_t splits = (512 + units - 1) / units;
         const int64_t most = (pages + 15) / 16;
         splits = splits < most ? splits : most;
         splits = splits < kMaxSplits ? splits : kMaxSplits;

@@ -19,8 +19,14 @@
 // row's largest, then off by at most 2^-38 of it.  The weights e^(S - m) s_v
 // are fp32 rounded once to fp16 after scaling by a power of two that puts the
 // largest s_v seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the
-// largest possible weight, and sums of many weights average the error below
-// that of the 16-bit output.  Scores, maxima, sums and outputs are fp32.
+// largest possible weight.  That error is as large as an fp16 output's own
+// rounding (and far below a bf16 one's), so for fp16 outputs the weights go in
+// as two halves, hi + lo, 22 bits: 5 more products a 32-token, 64-element tile
+// and a few operations a weight, which cost little where the cache's bytes
+// bound the call and 6 % elsewhere (batch of 64 over up to 8192 tokens: 78.0 us
+// without, 82.4 with), and take the error against 64
+// bits from 2.9e-4 to 2.1e-4, the output's rounding alone.  Scores, maxima, sums
+// and outputs are fp32.
 //
 // Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
 // head, tokens the rows of S^T = K Q^T (v_mfma_f32_16x16x32_f16), so lane
@@ -136,7 +142,7 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
 // Their weights, and the outputs.  seen: bit 4 t + e set where the lane's
 // column sees the token (read where the page is not whole); last: the last token
 // of the page that any column of the tile sees (63 and more: all).
-template <int D, int GS>
+template <int D, int GS, bool FINE>
 __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
                                              float (&s)[4][4], bool whole, uint32_t seen, int last)
 {
@@ -186,15 +192,22 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         st.l += x;
     }
     const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
-    uint32_t w[NG][2][4];
+    constexpr int PARTS = FINE ? 2 : 1;  // hi, lo
+    uint32_t w[NG][2][PARTS][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int B = 0; B < 2; ++B)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[g][B][e] = pack2<OUT_F16>(scaled(s[2 * B][e], vs[g], 8 * B + e),
-                                            scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e));
+            for (int e = 0; e < 4; ++e) {
+                const float x = scaled(s[2 * B][e], vs[g], 8 * B + e);
+                const float y = scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e);
+                w[g][B][0][e] = pack2<OUT_F16>(x, y);
+                if constexpr (FINE) {
+                    const half2_t hi = __builtin_bit_cast(half2_t, w[g][B][0][e]);
+                    w[g][B][1][e] = pack2<OUT_F16>(x - (float)hi.x, y - (float)hi.y);
+                }
+            }
     if (!whole) {  // a hidden token's weight is 0, its scale may be anything
 #pragma unroll
         for (int B = 0; B < 2; ++B)
@@ -204,26 +217,37 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
                                       ((seen >> (8 * B + 4 + e)) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
-                    w[g][B][e] &= keep;
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i)
+                        w[g][B][i][e] &= keep;
             }
     }
 #pragma unroll
     for (int B = 0; B < 2; ++B)
 #pragma unroll
         for (int y = 0; y < D / 64; ++y) {
-            const uint32_t(&o)[4] = w[y * 64 / GS][B];
-            const half8 weights = __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]});
+            half8 weights[PARTS];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const uint32_t(&o)[4] = w[y * 64 / GS][B][i];
+                weights[i] = __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]});
+            }
             const uint32_t u[4] = {pg.v[B][y].x, pg.v[B][y].y, pg.v[B][y].z, pg.v[B][y].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(u[x]), weights,
-                                                                           st.acc[4 * y + x], 0, 0, 0);
-            st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights, st.off[y], 0, 0, 0);
+            for (int x = 0; x < 4; ++x) {
+                const half8 code = halves(u[x]);
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i)
+                    st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(code, weights[i], st.acc[4 * y + x], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i)
+                st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights[i], st.off[y], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
 }
 
-template <int D, int GS, int WAVES>
+template <int D, int GS, int WAVES, bool FINE>
 __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int NM = D / 32;   // score products per 16 tokens
@@ -348,7 +372,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
                 s[e / 4][e % 4] = see ? s[e / 4][e % 4] : -__builtin_inff();
             }
         }
-        page_outputs<D, GS>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
+        page_outputs<D, GS, FINE>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
         load_v<D, GS>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;
@@ -413,17 +437,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 
 }  // namespace
 
-template <int WAVES>
+template <int WAVES, bool FINE>
 static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_few_rows_kernel<64, 64, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<64, 64, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else if (a.kv.group_size == 64)
-        kv4_few_rows_kernel<128, 64, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 64, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else
-        kv4_few_rows_kernel<128, 128, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 128, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+}
+
+template <int WAVES>
+static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    if (a.y_dtype == DT_F16)
+        launch<WAVES, true>(a, n, stream);
+    else
+        launch<WAVES, false>(a, n, stream);
 }
 
 hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
