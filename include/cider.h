@@ -385,6 +385,12 @@ cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_
 size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
                                            int64_t window, int64_t sinks);
 
+/* Test hook: force the attention's column tiles for subsequent calls in this
+   process.  0 = automatic (by sizes), 16 = the few-row kernel, 128 or 256 = the
+   many-row kernel with that many (row, query head) pairs a tile; every setting
+   takes every shape.  Returns the previous setting, or -1 for an invalid value. */
+int cider_kv4_set_tiles(int columns);
+
 /* Test hook: force the product path for subsequent calls in this process.
    0 = automatic (M * K <= 65536 and M <= 8, or M <= 4 for int4 weights ->
    matrix-vector, else matrix cores),

@@ -113,6 +113,26 @@ def test_sizes():
     assert cider.cider_kv4_attention_workspace_bytes(None, 8, 0, 0) == 0
 
 
+def test_set_tiles():
+    assert cider.cider_kv4_set_tiles(128) == 0
+    assert cider.cider_kv4_set_tiles(256) == 128
+    assert cider.cider_kv4_set_tiles(16) == 256
+    for bad in (1, -16, 64, 512):
+        assert cider.cider_kv4_set_tiles(bad) == -1
+    assert cider.cider_kv4_set_tiles(0) == 16
+
+
+def test_workspace_follows_the_sizes():
+    """Enough for every split of a long cache, nothing for what is never split; more rows never need less per row."""
+    one = _batch(batch=1, rows=1, max_rows=1, max_kv_len=131072, max_pages=2048)
+    parts = cider.cider_kv4_attention_workspace_bytes(one, 32, 0, 0)
+    assert parts % 256 == 0 and 32 * 2 * (128 * 4 + 8) <= parts <= 32 * 256 * (128 * 4 + 8) + 512
+    short = _batch(batch=1, rows=1, max_rows=1, max_kv_len=64, max_pages=2048)
+    assert cider.cider_kv4_attention_workspace_bytes(short, 32, 0, 0) == 0
+    window = cider.cider_kv4_attention_workspace_bytes(one, 32, 128, 4)
+    assert window <= parts
+
+
 @pytest.mark.parametrize("D,gs", [(64, 64), (128, 64), (128, 128)])
 def test_reference_layout_is_one_to_one(D, gs):
     """Every nibble of a block's code bytes is one element of one token, and what is put in comes back."""

@@ -30,6 +30,10 @@ def _device():
 def _announce(request):
     gu.announce(request.node.nodeid)
     yield
+    cider.cider_kv4_set_tiles(0)
+
+
+TILES = [0, 16, 128, 256]   # automatic, and each kernel
 
 
 def i32(a):
@@ -198,20 +202,26 @@ def attend(s, batch, q, q_dtype, y_dtype, HQ, scale, window=0, sinks=0, workspac
     return got[:, :HQ * s.D].reshape(s.rows, HQ, s.D)
 
 
-def check(s, got, q, q_dtype, y_dtype, HQ, scale, window=0, sinks=0, only=None):
+def reference(s, q, q_dtype, HQ, scale, window=0, sinks=0):
+    """(outputs, bound) of every sequence."""
     q = ref.to_f64(q, q_dtype)
+    return [ref.attention(s.cache, s.table[b], kv, q[s.row_start[b]:s.row_start[b] + n], HQ // s.H, scale, window, sinks)
+            for b, (kv, n) in enumerate(zip(s.lens, s.n))]
+
+
+def compare(s, got, want, y_dtype):
     got = ref.to_f64(got, y_dtype)
-    for b, (kv, n) in enumerate(zip(s.lens, s.n)):
-        if only is not None and b not in only:
-            continue
-        at = slice(s.row_start[b], s.row_start[b] + n)
-        want, bound = ref.attention(s.cache, s.table[b], kv, q[at], HQ // s.H, scale, window, sinks)
-        assert np.isfinite(want).all()
-        step = 2.0 ** -8 if y_dtype == 1 else 2.0 ** -11
-        err = np.abs(got[at] - want)
-        ok = err <= bound + step * (np.abs(want) + bound) + 2.0 ** -25   # fp16's smallest step
+    step = 2.0 ** -8 if y_dtype == 1 else 2.0 ** -11
+    for b, (y, bound) in enumerate(want):
+        assert np.isfinite(y).all()
+        err = np.abs(got[s.row_start[b]:s.row_start[b] + s.n[b]] - y)
+        ok = err <= bound + step * (np.abs(y) + bound) + 2.0 ** -25   # fp16's smallest step
         assert ok.all(), "sequence %d: %d outside, worst %.3g of %.3g" % (
-            b, int((~ok).sum()), err[~ok].max(), np.abs(want).max())
+            b, int((~ok).sum()), err[~ok].max(), np.abs(y).max())
+
+
+def check(s, got, q, q_dtype, y_dtype, HQ, scale, window=0, sinks=0):
+    compare(s, got, reference(s, q, q_dtype, HQ, scale, window, sinks), y_dtype)
 
 
 ATTEND_CASES = [
@@ -238,28 +248,35 @@ ATTEND_CASES = [
 @pytest.mark.parametrize("D,gs", GEOMETRY)
 @pytest.mark.parametrize("lens,rows,H,HQ,window,sinks", ATTEND_CASES)
 def test_attention(lens, rows, H, HQ, window, sinks, D, gs):
+    """Each kernel, with and without a workspace, against the reference worked out once."""
     dtype = (len(lens) + HQ + D // 64 + gs // 64) % 2
     s = Setup(lens, rows, H, D, gs, seed=HQ, garbage="nan")
     ref.fill(s.cache, s.table, s.lens, *s.values(dtype))
     batch = s.to_device()
     q = ref.to_bits(s.rng.standard_normal((s.rows, HQ, D)) * 2, dtype)
     scale = 1 / np.sqrt(D)
-    for workspace in (True, False):
-        got = attend(s, batch, q, dtype, dtype, HQ, scale, window, sinks, workspace)
-        check(s, got, q, dtype, dtype, HQ, scale, window, sinks)
+    want = reference(s, q, dtype, HQ, scale, window, sinks)
+    for tiles in TILES:
+        cider.cider_kv4_set_tiles(tiles)
+        for workspace in (True, False):
+            compare(s, attend(s, batch, q, dtype, dtype, HQ, scale, window, sinks, workspace), want, dtype)
 
 
+@pytest.mark.parametrize("tiles", TILES)
 @pytest.mark.parametrize("q_dtype,y_dtype", [(0, 1), (1, 0)])
-def test_attention_types_are_independent(q_dtype, y_dtype):
+def test_attention_types_are_independent(q_dtype, y_dtype, tiles):
+    cider.cider_kv4_set_tiles(tiles)
     s = Setup([200, 77], [4, 1], 1, 128, 128, garbage="nan")
     ref.fill(s.cache, s.table, s.lens, *s.values(1))
     q = ref.to_bits(s.rng.standard_normal((s.rows, 4, 128)), q_dtype)
     check(s, attend(s, s.to_device(), q, q_dtype, y_dtype, 4, 0.11), q, q_dtype, y_dtype, 4, 0.11)
 
 
+@pytest.mark.parametrize("tiles", TILES)
 @pytest.mark.parametrize("rows", [1, 50])
-def test_attention_scores_and_scales_far_apart(rows):
+def test_attention_scores_and_scales_far_apart(rows, tiles):
     """A sharp softmax, values whose scales lie 2^20 apart, the large ones far back, tiny and huge bf16 queries."""
+    cider.cider_kv4_set_tiles(tiles)
     s = Setup([400, 150], [rows, 1], 1, 128, 64, garbage="nan")
     k, v = s.values(1)
     for b in range(2):
@@ -277,9 +294,11 @@ def test_attention_scores_and_scales_far_apart(rows):
     check(s, attend(s, s.to_device(), q, 1, 1, 4, 0.0883), q, 1, 1, 4, 0.0883)
 
 
+@pytest.mark.parametrize("tiles", TILES)
 @pytest.mark.parametrize("rows", [2, 40])
-def test_what_a_row_may_not_see_does_not_reach_it(rows):
+def test_what_a_row_may_not_see_does_not_reach_it(rows, tiles):
     """NaN and infinite keys and values behind the window and in front of the row, inside pages it does read."""
+    cider.cider_kv4_set_tiles(tiles)
     s = Setup([300], [rows], 2, 128, 64, garbage="nan")
     k, v = s.values(0)
     ref.fill(s.cache, s.table, s.lens, k, v)
@@ -305,7 +324,9 @@ def test_what_a_row_may_not_see_does_not_reach_it(rows):
             assert (np.abs(got[i] - want[0]) <= bound[0] + 2.0 ** -11 * (np.abs(want[0]) + bound[0]) + 2.0 ** -25).all(), i
 
 
-def test_a_query_with_nan_spoils_its_own_head_only():
+@pytest.mark.parametrize("tiles", TILES)
+def test_a_query_with_nan_spoils_its_own_head_only(tiles):
+    cider.cider_kv4_set_tiles(tiles)
     s = Setup([90], [3], 1, 64, 64, garbage="nan")
     ref.fill(s.cache, s.table, s.lens, *s.values(0))
     x = s.rng.standard_normal((3, 5, 64))
@@ -319,8 +340,10 @@ def test_a_query_with_nan_spoils_its_own_head_only():
     assert np.array_equal(got, good)
 
 
-def test_bounds_of_the_device_arrays():
+@pytest.mark.parametrize("tiles", TILES)
+def test_bounds_of_the_device_arrays(tiles):
     """Lengths, rows and pages outside the batch's bounds are clipped, left out or not followed."""
+    cider.cider_kv4_set_tiles(tiles)
     import torch
     D, gs, H, HQ = 128, 64, 1, 2
     s = Setup([130, 100, 64], [2, 2, 2], H, D, gs, garbage="nan", table_room=0)
@@ -369,10 +392,12 @@ def test_bounds_of_the_device_arrays():
     assert base is not None
 
 
+@pytest.mark.parametrize("tiles", TILES)
 @pytest.mark.parametrize("rows", [1, 40])
-def test_a_page_that_is_not_there_leaves_no_trace(rows):
+def test_a_page_that_is_not_there_leaves_no_trace(rows, tiles):
     """Whatever the cache's first page holds (the largest scales here), a page number outside the cache only
     hides its tokens."""
+    cider.cider_kv4_set_tiles(tiles)
     s = Setup([300], [rows], 1, 128, 64, garbage="nan")
     ref.fill(s.cache, s.table, s.lens, *s.values(1))
     if s.table[0, 1] == 0 or 0 in s.table[0, 2:5]:   # page 0 is to be one that no token is in
@@ -426,7 +451,9 @@ def test_blocks_past_4_gib():
     assert (big[:5] == 0x55).all().item()
 
 
-def test_same_bits_every_time_on_another_stream_and_from_a_graph():
+@pytest.mark.parametrize("tiles", TILES)
+def test_same_bits_every_time_on_another_stream_and_from_a_graph(tiles):
+    cider.cider_kv4_set_tiles(tiles)
     import torch
     D, gs, H, HQ = 128, 64, 2, 8
     s = Setup([2000, 900, 0], [1, 1, 1], H, D, gs, garbage="nan")

@@ -38,7 +38,7 @@ EXPORTS = (
     "cider_quantize_act_ex", "cider_gemm_ex", "cider_linear_ex", "cider_decode_linear",
     "cider_linear_ex_noalloc",
     "cider_kv4_cache_bytes", "cider_kv4_append", "cider_kv4_read", "cider_kv4_attention",
-    "cider_kv4_attention_workspace_bytes",
+    "cider_kv4_attention_workspace_bytes", "cider_kv4_set_tiles",
 )
 
 KV4_PAGE_TOKENS = 64
@@ -112,6 +112,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "cider_kv4_read": ([P, P, P, I, I64, I64, P], I),
         "cider_kv4_attention": ([P, P, I, I64, I64, ctypes.c_float, I64, I64, P, SZ, P, I, I64, P], I),
         "cider_kv4_attention_workspace_bytes": ([P, I64, I64, I64], SZ),
+        "cider_kv4_set_tiles": ([I], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -313,6 +314,10 @@ def cider_kv4_attention(b, q, q_dtype, ldq, q_heads, scale, window, sinks, works
 
 def cider_kv4_attention_workspace_bytes(b, q_heads, window, sinks) -> int:
     return int(load().cider_kv4_attention_workspace_bytes(_batch(b), q_heads, window, sinks))
+
+
+def cider_kv4_set_tiles(columns: int) -> int:
+    return int(load().cider_kv4_set_tiles(int(columns)))
 
 
 def cider_set_path(path: int) -> int:

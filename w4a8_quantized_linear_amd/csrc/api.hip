@@ -23,6 +23,7 @@ constexpr int64_t kMaxOperandBytes = int64_t(1) << 31;
 constexpr int64_t kDecodeMaxK = 32768;  // decode kernel: 16 activation chunks per thread, x [K] in LDS
 
 std::atomic<int> g_path{0};
+std::atomic<int> g_kv4_tiles{0};
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -462,6 +463,7 @@ cider::Kv4AttentionArgs kv4_attention_args(const cider_kv4_batch *b, int64_t q_h
     cider::Kv4AttentionArgs a{};
     a.kv = kv4_args(b);
     a.q_heads = (int)q_heads;
+    a.tiles = g_kv4_tiles.load(std::memory_order_relaxed);
     a.window = (int)(window < kMaxTokens ? window : 0);  // a window past every length hides nothing
     a.sinks = (int)(sinks < kMaxTokens ? sinks : kMaxTokens);
     return a;
@@ -744,6 +746,13 @@ size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_h
     if (check_kv4_attention(b, q_heads, window, sinks) != CIDER_OK || kv4_empty(b))
         return 0;
     return cider::kv4_attention_workspace(kv4_attention_args(b, q_heads, window, sinks));
+}
+
+int cider_kv4_set_tiles(int columns)
+{
+    if (columns != 0 && columns != 16 && columns != 128 && columns != 256)
+        return -1;
+    return g_kv4_tiles.exchange(columns);
 }
 
 int cider_set_path(int path)

@@ -156,6 +156,7 @@ struct Kv4AttentionArgs {
     int q_dtype, y_dtype, q_heads;
     float scale;
     int window, sinks;  // window 0: none
+    int tiles;          // columns of a tile (16, 128, 256), 0: by sizes (test hook)
 };
 // Scratch with which the call splits as far as it would, and the call itself
 // (less scratch, or none: fewer splits).

@@ -82,6 +82,7 @@ __device__ __forceinline__ float scaled(float x, float scales, int n)
 
 // What a launch adds to the call's arguments.
 struct Kv4Launch {
+    int cols;          // columns of a tile
     int tiles;         // column tiles of the longest sequence
     int splits;        // workgroups that a tile's pages may be dealt to
     int pages;         // pages of one of them (splits > 1)
@@ -200,8 +201,8 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b, int dtype)
     return dtype == DT_BF16 ? pack2<OUT_BF16>(a, b) : pack2<OUT_F16>(a, b);
 }
 
-// The kernels, one launch each: columns tiles of 16 (few rows) and of 128.
-constexpr int kFewCols = 16, kManyCols = 128;
+// The kernels, one launch each: tiles of 16 columns (few rows), of 128 or 256.
+constexpr int kFewCols = 16;
 hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
 hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
 

@@ -102,19 +102,42 @@ int64_t most_pages(const Kv4AttentionArgs &a, int cols)
     return seen < all ? seen : all;
 }
 
-// Columns of the tiles of the kernel that takes the call.
-int tile_cols(const Kv4AttentionArgs &a) { return most_columns(a) > 48 ? kManyCols : kFewCols; }
+// Tiles of `cols` columns over all heads and sequences.
+int64_t units_of(const Kv4AttentionArgs &a, int cols)
+{
+    return tiles_of(a, cols) * (int64_t)a.kv.kv_heads * a.kv.batch;
+}
+
+// Columns of the tiles, by sizes (measured; G = 4, 8 kv heads of 128):
+//   the few-row kernel keeps up to 64 columns (64 columns, 8 sequences of 16384
+//   tokens: 110 us against 107), and while all its tiles see no more than 24576
+//   pages together (128 columns over 4096 tokens, 1 / 4 / 8 sequences: 17 / 28 /
+//   49 us against 24 / 38 / 48; 512 columns over 1024, 4 / 8 sequences: 30 / 51
+//   against 40 / 43): the other one spends 2 us a page on a tile of any fill;
+//   then 128 columns, two workgroups a compute unit, or, for one long sequence,
+//   256 and one: half the unpacking per column (2048 rows over 16384 tokens
+//   647 -> 615 us, 4096 of 4096 182 -> 169), but coarser where tiles end at
+//   different times (ragged prompts 232 -> 246, 8000 rows with a window of 1024
+//   222 -> 243).
+int columns_of(const Kv4AttentionArgs &a)
+{
+    if (a.tiles)
+        return a.tiles;
+    if (most_columns(a) <= 64 || units_of(a, kFewCols) * most_pages(a, kFewCols) <= 24576)
+        return kFewCols;
+    const int64_t units = units_of(a, 256);
+    return a.kv.batch == 1 && a.window == 0 && units >= 128 && units <= 512 && most_pages(a, 256) >= 64 ? 256 : 128;
+}
 
 Kv4Launch plan(const Kv4AttentionArgs &a)
 {
     Kv4Launch n{};
-    const int cols = tile_cols(a);
-    n.tiles = (int)tiles_of(a, cols);
+    n.cols = columns_of(a);
+    n.tiles = (int)tiles_of(a, n.cols);
     n.splits = 1;
-    const int64_t pages = most_pages(a, cols);
-    const int64_t units = n.tiles * (int64_t)a.kv.kv_heads * a.kv.batch;
     n.waves = 4;
-    if (cols == kFewCols) {
+    const int64_t pages = most_pages(a, n.cols), units = units_of(a, n.cols);
+    if (n.cols == kFewCols) {
         // One workgroup per tile, or chunks and a second launch.  Measured (bf16,
         // equal lengths; units = tiles of all heads and sequences): a page of 128
         // elements takes a workgroup of 8 wavefronts 0.27 us; splitting costs 4 us
@@ -139,15 +162,23 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
         const int64_t least = (pages + kMaxSplits - 1) / kMaxSplits;
         chunk = chunk < least ? least : chunk;
         n.pages = (int)chunk;
-        n.splits = (int)((pages + chunk - 1) / chunk);
-    } else if (pages > 16 && units < 512) {
-        int64_t splits = (512 + units - 1) / units;
-        const int64_t most = (pages + 15) / 16;
-        splits = splits < most ? splits : most;
+    } else {
+        // Two workgroups a compute unit (one of 256 columns) as long as a chunk
+        // keeps 16 pages, one down to 4 (128 rows over 16384 tokens, 64 tiles: 8
+        // chunks 69 us, 4 81; 4 sequences of 1024, 256 tiles of 16 pages: whole 43
+        // us, halved 58).
+        auto chunks = [&](int64_t wanted, int64_t least) {
+            const int64_t by_units = (wanted + units - 1) / units, by_pages = (pages + least - 1) / least;
+            return by_units < by_pages ? by_units : by_pages;
+        };
+        const int64_t two = chunks(n.cols == 256 ? 256 : 512, 16), one = chunks(256, 4);
+        int64_t splits = two > one ? two : one;
         splits = splits < kMaxSplits ? splits : kMaxSplits;
+        if (splits < 2)
+            return n;
         n.pages = (int)((pages + splits - 1) / splits);
-        n.splits = (int)((pages + n.pages - 1) / n.pages);
     }
+    n.splits = (int)((pages + n.pages - 1) / n.pages);
     return n;
 }
 
@@ -177,10 +208,12 @@ void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stre
 template <int D>
 void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (tile_cols(a) == kManyCols)
-        launch_join<D, kManyCols>(a, n, stream);
-    else
+    if (n.cols == kFewCols)
         launch_join<D, kFewCols>(a, n, stream);
+    else if (n.cols == 128)
+        launch_join<D, 128>(a, n, stream);
+    else
+        launch_join<D, 256>(a, n, stream);
 }
 
 }  // namespace
@@ -200,8 +233,8 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size
         n.part = static_cast<float *>(workspace);
         n.part_stat = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a, n));
     }
-    const hipError_t e = tile_cols(a) == kManyCols ? launch_kv4_many_rows(a, n, stream)
-                                                   : launch_kv4_few_rows(a, n, stream);
+    const hipError_t e = n.cols == kFewCols ? launch_kv4_few_rows(a, n, stream)
+                                            : launch_kv4_many_rows(a, n, stream);
     if (e != hipSuccess || n.splits < 2)
         return e;
     if (a.kv.head_dim == 64)

@@ -20,10 +20,7 @@
 namespace cider {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kWaveCols = kManyCols / kWaves;
-static_assert(kWaveCols == 32, "a wavefront's columns are one matrix operand");
+constexpr int kWaveCols = 32;  // one matrix operand
 
 // The running maximum may lie this far (in units of log2) below the true one
 // before it is moved: weights reach 2^kSlack, and the outputs are rescaled in
@@ -54,10 +51,10 @@ struct PageV {
 // take them by a broadcast within the row (DPP), so a tile's scales cost one
 // 4-byte LDS read instead of four 16-byte ones.
 __device__ __forceinline__ int scale_slot(int t) { return t / 32 * 32 + t / 4 % 2 * 16 + t / 8 % 4 * 4 + t % 4; }
-// A thread's share of a page on its way.
-template <int D>
+// A thread's share of a page on its way: ND dwords of K and of V.
+template <int ND>
 struct Share {
-    uint32_t k[D / 32], v[D / 32];
+    uint32_t k[ND], v[ND];
     float k_scale[2], v_scale;  // by token: wavefront 0 K's groups, wavefront 1 + g V's group g
 };
 
@@ -70,6 +67,8 @@ __device__ __forceinline__ void load_dwords(uint32_t (&w)[N], const uint8_t *at)
         w[1] = x.y;
         w[2] = x.z;
         w[3] = x.w;
+    } else if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(at);
     } else {
         const uint2 x = *reinterpret_cast<const uint2 *>(at);
         w[0] = x.x;
@@ -93,33 +92,39 @@ __device__ __forceinline__ f32x16 mfma(uint4 x, half8 y, f32x16 z)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, x), y, z, 0, 0, 0);
 }
 
-template <int D, int GS>
-__global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+template <int D, int GS, int COLS>
+__global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int NG = D / GS;   // scales per token
     constexpr int NK = D / 16;   // score products per 32 tokens
     constexpr int NT = D / 32;   // output tiles
+    constexpr int WAVES = COLS / kWaveCols, TEAMS = WAVES / 4;
+    constexpr int ND = D / 32 / TEAMS;  // dwords of K and of V that a thread unpacks
+    static_assert(TEAMS == 1 || TEAMS == 2, "teams of 256 threads take a page's code runs");
     __shared__ PageK<D, GS> page_k[2];
     __shared__ PageV<D, GS> page_v[2];
-    __shared__ float tile_top[kWaves];
+    __shared__ float tile_top[WAVES];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane % 32, h = lane / 32;
     const float inf = __builtin_inff();
-    // heads fastest (one kv head's pages stay in one XCD's L2), then splits and
-    // tiles, the last ones, which see most, first; sequences slowest: dealt in
-    // turn, workgroups of sequences of different lengths fall into step with the
-    // order in which an XCD fills its shader engines, and all long ones of a batch of 4
-    // land on one (ragged prompts up to 4096 rows: 617 us against 250)
+    // heads fastest (one kv head's pages stay in one XCD's L2), then sequences,
+    // splits and tiles, the last tiles, which see most, first.  Sequences are
+    // dealt in another order for every tile: in one fixed order a batch of 4
+    // falls into step with the 4 shader engines that an XCD fills in turn, and
+    // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
+    // 617 us against 232)
     unsigned id = blockIdx.x;
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
+    const unsigned turn = id % (unsigned)a.kv.batch;
+    id /= (unsigned)a.kv.batch;
     const int split = (int)(id % (unsigned)n.splits);
-    id /= (unsigned)n.splits;
-    const int tile = n.tiles - 1 - (int)(id % (unsigned)n.tiles), b = (int)(id / (unsigned)n.tiles);
+    const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
+    const int b = (int)((turn + (unsigned)tile) % (unsigned)a.kv.batch);
     Tile t;
-    if (!tile_of<kManyCols>(a, b, head, tile, t))
+    if (!tile_of<COLS>(a, b, head, tile, t))
         return;
     const int begin = n.splits > 1 ? split * n.pages : 0;
     if (split > 0 && begin >= t.range.count)
@@ -127,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
 
     const int first = t.seq.kv - t.seq.n;  // position of row 0
-    const int col0 = t.tile * kManyCols + wave * kWaveCols;
+    const int col0 = t.tile * COLS + wave * kWaveCols;
     const int col = col0 + c;
     const bool valid = col < t.cols;
     const int row = valid ? col / t.G : 0;
@@ -137,21 +142,62 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     const int w_last = col0 + kWaveCols <= t.cols ? col0 + kWaveCols - 1 : t.cols - 1;
     const int w_hi = col0 < t.cols ? first + w_last / t.G : -1;
 
+    // q is asked for first and used last: the first pages' codes are on their
+    // way while it is scaled
+    uint4 qw[NK];
+    {
+        const uint16_t *at = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
+                             (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * h;
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+            qw[k] = *reinterpret_cast<const uint4 *>(at + 16 * k);
+    }
+    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
+    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
+    // a page number outside the cache is never followed: page 0 is loaded in
+    // its place and its tokens are left out
+    auto block_of = [&](int number) {
+        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+    };
+    auto fetch_k = [&](Share<ND> &s, int number) {
+        const uint8_t *block = block_of(number);
+        load_dwords(s.k, block + (uint32_t)(tid % 256 * (D / 8) + tid / 256 * 4 * ND));
+        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            s.k_scale[g] = scales[g * kPageTokens + (uint32_t)lane];
+    };
+    auto fetch_v = [&](Share<ND> &s, int number) {
+        const uint8_t *block = block_of(number);
+        load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)(tid % 256 * (D / 8) + tid / 256 * 4 * ND));
+        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+        s.v_scale = (scales + (NG + (wave == 2 && NG == 2 ? 1 : 0)) * kPageTokens)[(uint32_t)lane];
+    };
+    // page numbers: of page i + 1 (V) and i + 2 (K); read one step ahead
+    Share<ND> share, share1;
+    const int last_page = end - 1;
+    auto number_of = [&](int i) { return table[t.range.at(i < last_page ? i : last_page)]; };
+    f32x16 r[2];
+    int n0 = -1, n1 = -1, n2 = -1;
+    if (begin < end) {
+        n0 = number_of(begin);
+        n1 = number_of(begin + 1);
+        n2 = number_of(begin + 2);
+        fetch_k(share, n0);
+        fetch_v(share, n0);
+        fetch_k(share1, n1);
+    }
+
     // q: one power of two for the whole tile, so that the scores' factor goes
     // into K's scales once a page
     half8 q[NK];
     float qmul;
     {
         float x[NK][8], top = 0.0f;
-        const uint16_t *at = a.q + (int64_t)(t.seq.row0 + row) * a.ldq +
-                             (int64_t)(t.h * t.G + (valid ? col % t.G : 0)) * D + 8 * h;
-        uint4 w[NK];
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-            w[k] = *reinterpret_cast<const uint4 *>(at + 16 * k);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-            widen8(w[k], a.q_dtype, x[k]);
+            widen8(qw[k], a.q_dtype, x[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[k][e] = valid ? x[k][e] : 0.0f;
@@ -164,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
             tile_top[wave] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < WAVES; ++w)
             top = __builtin_fmaxf(top, tile_top[w]);
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
         qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
@@ -184,43 +230,21 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     for (int g = 0; g < NG; ++g)
         v_exp[g] = -100;
 
-    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
-    const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
-    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
-    // a page number outside the cache is never followed: page 0 is loaded in
-    // its place and its tokens are left out
-    auto block_of = [&](int number) {
-        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
-    };
-    auto fetch_k = [&](Share<D> &s, int number) {
-        const uint8_t *block = block_of(number);
-        load_dwords(s.k, block + (uint32_t)tid * (D / 8));
-        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-            s.k_scale[g] = scales[g * kPageTokens + (uint32_t)lane];
-    };
-    auto fetch_v = [&](Share<D> &s, int number) {
-        const uint8_t *block = block_of(number);
-        load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)tid * (D / 8));
-        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
-        s.v_scale = (scales + (NG + (wave == 2 && NG == 2 ? 1 : 0)) * kPageTokens)[(uint32_t)lane];
-    };
     // where a thread's operands go, and where a lane finds its own: K's slots
     // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
     // hit different banks
     const int slot = 16 * h + lane % 16;  // of the lane's own scale in a tile's
-    const int kt = tid / 4, kj = tid % 4;
+    const int kt = tid % 256 / 4, kj = tid % 4, km = tid / 256 * ND;
     const int k_to = ((kj % 2) * 32 + kt % 32) ^ (2 * kj);
     const int k_from[2] = {lane ^ (2 * h), lane ^ (4 + 2 * h)};
-    const int unit = D == 128 ? tid : tid / 2;
-    const int vx = D == 128 ? 0 : 2 * (tid % 2);
+    const int unit = D == 128 ? tid % 256 : tid % 256 / 2;
+    const int vx = (D == 128 ? 0 : 2 * (tid % 2)) + tid / 256 * ND;
     const int vc = unit % 16, vj = unit / 16 % 4, vg = unit / 64 % (D / 64), vb = unit / (64 * (D / 64));
     float k_scale_next = 0.0f;  // wavefront 0: of the page whose K was staged last
-    auto stage_k_dword = [&](PageK<D, GS> &to, const Share<D> &s, int m) {
-        to.code[kt / 32][2 * m + kj / 2][k_to] = code_halves(s.k[m]);
+    auto stage_k_dword = [&](PageK<D, GS> &to, const Share<ND> &s, int m) {
+        to.code[kt / 32][2 * (km + m) + kj / 2][k_to] = code_halves(s.k[m]);
     };
-    auto stage_k_scales = [&](PageK<D, GS> &to, const Share<D> &s) {
+    auto stage_k_scales = [&](PageK<D, GS> &to, const Share<ND> &s) {
         if (NG == 1) {
             k_scale_next = s.k_scale[0] * qmul;
         } else {
@@ -233,12 +257,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                 to.ratio[scale_slot(lane)] = s.k_scale[0] / last;
         }
     };
-    auto stage_v_dword = [&](PageV<D, GS> &to, const Share<D> &s, int e) {
+    auto stage_v_dword = [&](PageV<D, GS> &to, const Share<ND> &s, int e) {
         const int x = vx + e;
         to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
     };
     // number, t0: the page's
-    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<D> &s, float k_scale, int number, int t0) {
+    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<ND> &s, float k_scale, int number, int t0) {
         if (wave == 0)
             to.k_scale[scale_slot(lane)] = k_scale;
         if (wave >= 1 && wave <= NG) {
@@ -259,30 +283,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
     auto k_tile = [](int s) { return s / SG % 2; };
     auto k_step = [](int s) { return s / (2 * SG) * SG + s % SG; };
 
-    // page numbers: of page i + 1 (V) and i + 2 (K); read one step ahead
-    Share<D> share;
-    const int last_page = end - 1;
-    auto number_of = [&](int i) { return table[t.range.at(i < last_page ? i : last_page)]; };
-    f32x16 r[2];
-    int n0 = -1, n1 = -1, n2 = -1;
     if (begin < end) {
-        n0 = number_of(begin);
-        n1 = number_of(begin + 1);
-        n2 = number_of(begin + 2);
-        fetch_k(share, n0);
-        fetch_v(share, n0);
 #pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
+        for (int m = 0; m < ND; ++m) {
             stage_k_dword(page_k[0], share, m);
             stage_v_dword(page_v[0], share, m);
+            stage_k_dword(page_k[1], share1, m);
         }
         stage_k_scales(page_k[0], share);
         stage_v_scales(page_v[0], share, k_scale_next, n0, t.range.at(begin) * kPageTokens);
-        fetch_k(share, n1);
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m)
-            stage_k_dword(page_k[1], share, m);
-        stage_k_scales(page_k[1], share);
+        stage_k_scales(page_k[1], share1);
     }
     __syncthreads();
     if (begin < end) {
@@ -455,11 +465,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
                 const uint32_t(&o)[4] = w[tt][z * 32 / GS][y];
                 acc[z] = mfma(vf[s % (kAhead + 1)], __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]}), acc[z]);
                 read_v(s + kAhead);
-                if (s % 2 == 1) {
-                    if (s < kSteps / 2)
-                        stage_k_dword(to_k, share, s / 2);
+                constexpr int EVERY = kSteps / (2 * ND);
+                if (s % EVERY == EVERY - 1) {
+                    if (s / EVERY < ND)
+                        stage_k_dword(to_k, share, s / EVERY);
                     else
-                        stage_v_dword(to_v, share, s / 2 - kSteps / 4);
+                        stage_v_dword(to_v, share, s / EVERY - ND);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -507,16 +518,25 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_many_rows_kernel(Kv4Attention
 
 }  // namespace
 
-hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+template <int COLS>
+static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_many_rows_kernel<64, 64><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_many_rows_kernel<64, 64, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
     else if (a.kv.group_size == 64)
-        kv4_many_rows_kernel<128, 64><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_many_rows_kernel<128, 64, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
     else
-        kv4_many_rows_kernel<128, 128><<<grid, kThreads, 0, stream>>>(a, n);
+        kv4_many_rows_kernel<128, 128, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
+}
+
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    if (n.cols == 256)
+        launch<256>(a, n, stream);
+    else
+        launch<128>(a, n, stream);
     return hipGetLastError();
 }
 
