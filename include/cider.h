@@ -363,7 +363,9 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
                         window 0: every t <= p)
      S[t] = scale * sum_d q[d] * K[t, d],  P[t] = exp(S[t] - max S)
      y[d] = sum_t P[t] * V[t, d] / sum_t P[t];  no visible t: y = 0
-   with K, V the values the codes stand for, sums and softmax in fp32.  The
+   with K, V the values the codes stand for, sums and softmax in fp32 (scores
+   are to stay finite there; a row that meets NaN or infinity where it may look
+   gives NaN, and what it may not see never reaches it).  The
    rows' own tokens must have been appended before.  q, y:
    [rows][q_heads][head_dim] of types q_dtype, y_dtype, row strides ldq, ldy.
    scale finite and positive; window, sinks >= 0 (the first `sinks` tokens stay

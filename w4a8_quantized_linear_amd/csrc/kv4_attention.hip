@@ -179,6 +179,8 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
         n.pages = (int)((pages + splits - 1) / splits);
     }
     n.splits = (int)((pages + n.pages - 1) / n.pages);
+    if (units * n.splits >= int64_t(1) << 31)  // a launch counts workgroups in 32 bits
+        n.splits = 1;
     return n;
 }
 

@@ -23,8 +23,8 @@
 // rounding (and far below a bf16 one's), so for fp16 outputs the weights go in
 // as two halves, hi + lo, 22 bits: 5 more products a 32-token, 64-element tile
 // and a few operations a weight, which cost little where the cache's bytes
-// bound the call and 6 % elsewhere (batch of 64 over up to 8192 tokens: 78.0 us
-// without, 82.4 with), and take the error against 64
+// bound the call and 6 % elsewhere (batch of 64 over up to 8192 tokens: 72.5 us
+// without, 77.5 with), and take the error against 64
 // bits from 2.9e-4 to 2.1e-4, the output's rounding alone.  Scores, maxima, sums
 // and outputs are fp32.
 //
@@ -64,7 +64,21 @@ struct PageData {
 
 __device__ __forceinline__ int scale_token(int lane) { return 16 * (lane / 4 % 4) + 4 * (lane / 16) + lane % 4; }
 
-template <int D, int GS>
+// ONCE: the call's columns of a kv head are one tile, so each page is read
+// once and goes past the caches (batch of 64 over up to 8192 tokens 78.2 -> 72.5
+// us, 256 of 4096 215 -> 200, 6.1 TB/s; with 3 and more tiles it costs 3 - 12 %).
+template <typename T, bool ONCE>
+__device__ __forceinline__ T load_codes(const uint8_t *p)
+{
+    typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) / 4)));
+    const words *w = reinterpret_cast<const words *>(p);
+    if constexpr (ONCE)
+        return __builtin_bit_cast(T, __builtin_nontemporal_load(w));
+    else
+        return __builtin_bit_cast(T, *w);
+}
+
+template <int D, int GS, bool ONCE>
 __device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block, int lane)
 {
 #pragma unroll
@@ -72,13 +86,13 @@ __device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block,
         const uint8_t *at = block + 16 * t * (D / 2);
         const uint32_t off = lane % 16 * (D / 2) + lane / 16 * (D / 8);
         if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(at + off);
+            const uint4 w = load_codes<uint4, ONCE>(at + off);
             p.k[t][0] = w.x;
             p.k[t][1] = w.y;
             p.k[t][2] = w.z;
             p.k[t][3] = w.w;
         } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(at + off);
+            const uint2 w = load_codes<uint2, ONCE>(at + off);
             p.k[t][0] = w.x;
             p.k[t][1] = w.y;
         }
@@ -89,15 +103,14 @@ __device__ __forceinline__ void load_k(PageData<D, GS> &p, const uint8_t *block,
         p.ks[g] = s[g * kPageTokens + (uint32_t)scale_token(lane)];
 }
 
-template <int D, int GS>
+template <int D, int GS, bool ONCE>
 __device__ __forceinline__ void load_v(PageData<D, GS> &p, const uint8_t *block, int lane)
 {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
-            p.v[b][g] = *reinterpret_cast<const uint4 *>(block + kv4_v_offset(D) +
-                                                         (b * (D / 64) + g) * 1024 + (uint32_t)lane * 16);
+            p.v[b][g] = load_codes<uint4, ONCE>(block + kv4_v_offset(D) + (b * (D / 64) + g) * 1024 + (uint32_t)lane * 16);
     const float *s = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
 #pragma unroll
     for (int g = 0; g < D / GS; ++g)
@@ -247,7 +260,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         }
 }
 
-template <int D, int GS, int WAVES, bool FINE>
+template <int D, int GS, int WAVES, bool FINE, bool ONCE>
 __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int NM = D / 32;   // score products per 16 tokens
@@ -302,8 +315,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
     int i = begin + wave, n0 = -1, n1 = -1;
     if (i < end) {
         n0 = table[t.range.at(i)];
-        load_k<D, GS>(pg, block_of(n0), lane);
-        load_v<D, GS>(pg, block_of(n0), lane);
+        load_k<D, GS, ONCE>(pg, block_of(n0), lane);
+        load_v<D, GS, ONCE>(pg, block_of(n0), lane);
     }
     if (i + WAVES < end)
         n1 = table[t.range.at(i + WAVES)];
@@ -357,7 +370,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
                            (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
         float s[4][4];
         page_scores<D, GS>(st, pg, s);
-        load_k<D, GS>(pg, ahead, lane);
+        load_k<D, GS, ONCE>(pg, ahead, lane);
         uint32_t seen = 0xFFFFu;
         if (!whole) {
             seen = 0;
@@ -373,7 +386,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
             }
         }
         page_outputs<D, GS, FINE>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
-        load_v<D, GS>(pg, ahead, lane);
+        load_v<D, GS, ONCE>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;
     }
@@ -437,26 +450,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 
 }  // namespace
 
-template <int WAVES, bool FINE>
+template <int WAVES, bool FINE, bool ONCE>
 static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_few_rows_kernel<64, 64, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else if (a.kv.group_size == 64)
-        kv4_few_rows_kernel<128, 64, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
     else
-        kv4_few_rows_kernel<128, 128, WAVES, FINE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
 }
 
 template <int WAVES>
 static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     if (a.y_dtype == DT_F16)
-        launch<WAVES, true>(a, n, stream);
+        n.tiles == 1 ? launch<WAVES, true, true>(a, n, stream) : launch<WAVES, true, false>(a, n, stream);
     else
-        launch<WAVES, false>(a, n, stream);
+        n.tiles == 1 ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
 }
 
 hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
