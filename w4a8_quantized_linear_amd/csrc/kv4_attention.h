@@ -87,6 +87,7 @@ struct Kv4Launch {
     int splits;        // workgroups that a tile's pages may be dealt to
     int pages;         // pages of one of them (splits > 1)
     int waves;         // wavefronts of a few-row workgroup, 4 or 8
+    bool once;         // few rows: pages are read by one tile and are more than the last-level cache keeps
     float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
     float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
 };
@@ -105,34 +106,76 @@ __device__ __forceinline__ uint4 nibble_halves(uint32_t w)
 // -8 2^-24 and -128 2^-24: the codes' offset in the same order.
 constexpr uint32_t kOffset = 0x80088008u, kOffset16 = 0x80808080u;
 
-// Elements 8 i .. 8 i + 7 of a 16-bit row as fp32.
-__device__ __forceinline__ void widen8(uint4 w, int dtype, float (&x)[8])
+// A lane's share of a query row: N chunks of 8 values.  For finite values the
+// magnitudes order as their bit patterns; a chunk with NaN or infinity (no
+// scale is taken from those: they would push other columns' values out of
+// fp16) is looked at value by value.
+template <int DT, int N>
+__device__ __forceinline__ float query_top(const uint4 (&w)[N])
+{
+    constexpr uint32_t kInf = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t m = chunk_absmax_bits(w[i]);
+        top = m > top ? m : top;
+    }
+    if (top >= kInf) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t m = (e & 1 ? u[e / 2] >> 16 : u[e / 2]) & 0x7FFFu;
+                top = m < kInf && m > top ? m : top;
+            }
+        }
+    }
+    return widen_bits<DT>(top);
+}
+template <int N>
+__device__ __forceinline__ float query_top(const uint4 (&w)[N], int dtype)
+{
+    return dtype == DT_BF16 ? query_top<DT_BF16>(w) : query_top<DT_F16>(w);
+}
+
+// 8 query values times 2^shift as an operand against nibble_halves: in the
+// order 0 4 1 5 2 6 3 7, those of the odd nibbles divided by 16.
+template <int DT>
+__device__ __forceinline__ half8 query_operand(uint4 w, int shift)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // values e and e + 4
+        const int by = e & 1 ? shift - 4 : shift;
+        const uint32_t lo = e & 1 ? u[e / 2] >> 16 : u[e / 2], hi = e & 1 ? u[e / 2 + 2] >> 16 : u[e / 2 + 2];
+        o[e] = pack2<OUT_F16>(ldexp_f(widen_bits<DT>(lo), by), ldexp_f(widen_bits<DT>(hi), by));
+    }
+    return __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]});
+}
+template <int N>
+__device__ __forceinline__ void query_operands(const uint4 (&w)[N], int dtype, int shift, half8 (&op)[N])
+{
     if (dtype == DT_BF16) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = widen_bits<DT_BF16>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+        for (int i = 0; i < N; ++i)
+            op[i] = query_operand<DT_BF16>(w[i], shift);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = widen_bits<DT_F16>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+        for (int i = 0; i < N; ++i)
+            op[i] = query_operand<DT_F16>(w[i], shift);
     }
 }
 
-// 8 query values times 2^shift as an operand against nibble_halves; returns
-// the operand's sum with the divided elements counted in full.
-__device__ __forceinline__ float query_operand(const float (&x)[8], int shift, half8 &op)
+// The sum of an operand's values, the divided ones counted in full.
+__device__ __forceinline__ float operand_sum(half8 op, float sum)
 {
-    float sum = 0.0f;
+    const half2_t one = {(_Float16)1, (_Float16)1}, sixteen = {(_Float16)16, (_Float16)16};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int n = e / 2 + 4 * (e & 1);  // 0 4 1 5 2 6 3 7
-        const bool sixteenth = (e >> 1) & 1;
-        const _Float16 v = (_Float16)ldexp_f(x[n], sixteenth ? shift - 4 : shift);
-        op[e] = v;
-        sum += sixteenth ? 16.0f * (float)v : (float)v;
-    }
+    for (int e = 0; e < 4; ++e)
+        sum = __builtin_amdgcn_fdot2(half2_t{op[2 * e], op[2 * e + 1]}, e & 1 ? sixteen : one, sum, false);
     return sum;
 }
 

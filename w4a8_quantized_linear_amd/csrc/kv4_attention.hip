@@ -138,6 +138,8 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
     n.waves = 4;
     const int64_t pages = most_pages(a, n.cols), units = units_of(a, n.cols);
     if (n.cols == kFewCols) {
+        n.once = n.tiles == 1 &&
+                 units * pages * kv4_block_bytes(a.kv.head_dim, a.kv.group_size) >= int64_t(128) << 20;
         // One workgroup per tile, or chunks and a second launch.  Measured (bf16,
         // equal lengths; units = tiles of all heads and sequences): a page of 128
         // elements takes a workgroup of 8 wavefronts 0.27 us; splitting costs 4 us

@@ -65,8 +65,11 @@ struct PageData {
 __device__ __forceinline__ int scale_token(int lane) { return 16 * (lane / 4 % 4) + 4 * (lane / 16) + lane % 4; }
 
 // ONCE: the call's columns of a kv head are one tile, so each page is read
-// once and goes past the caches (batch of 64 over up to 8192 tokens 78.2 -> 72.5
-// us, 256 of 4096 215 -> 200, 6.1 TB/s; with 3 and more tiles it costs 3 - 12 %).
+// once, and the pages are more than half the 256 MB last-level cache: they go
+// past the caches (batch of 64 over up to 8192 tokens 78.2 -> 72.5 us, 256 of
+// 4096 215 -> 200, 6.1 TB/s; with 3 and more tiles it costs 3 - 12 %, as it does
+// for a small cache that was read a moment ago, 64 sequences of 1024: 18.4 ->
+// 20.3).
 template <typename T, bool ONCE>
 __device__ __forceinline__ T load_codes(const uint8_t *p)
 {
@@ -323,25 +326,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 
     State<D, GS> st;
     {
-        float x[NM][8], top = 0.0f;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            widen8(qw[m], a.q_dtype, x[m]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[m][e] = valid ? x[m][e] : 0.0f;
-                top = __builtin_fmaxf(top, __builtin_fabsf(x[m][e]));
-            }
-        }
-        top = column_max(top);
+        for (int m = 0; m < NM; ++m)
+            qw[m] = valid ? qw[m] : uint4{0, 0, 0, 0};
+        const float top = column_max(query_top(qw, a.q_dtype));
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
         st.qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
+        query_operands(qw, a.q_dtype, shift, st.q);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
             st.zero[g] = 0.0f;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
-            st.zero[m * 32 / GS] += query_operand(x[m], shift, st.q[m]);
+            st.zero[m * 32 / GS] = operand_sum(st.q[m], st.zero[m * 32 / GS]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             st.zero[g] = column_sum(st.zero[g]) * -0x1p-21f;
@@ -467,9 +464,9 @@ template <int WAVES>
 static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     if (a.y_dtype == DT_F16)
-        n.tiles == 1 ? launch<WAVES, true, true>(a, n, stream) : launch<WAVES, true, false>(a, n, stream);
+        n.once ? launch<WAVES, true, true>(a, n, stream) : launch<WAVES, true, false>(a, n, stream);
     else
-        n.tiles == 1 ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
+        n.once ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
 }
 
 hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)

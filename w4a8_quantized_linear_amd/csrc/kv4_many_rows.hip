@@ -194,18 +194,10 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     half8 q[NK];
     float qmul;
     {
-        float x[NK][8], top = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            widen8(qw[k], a.q_dtype, x[k]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[k][e] = valid ? x[k][e] : 0.0f;
-                const float size = __builtin_fabsf(x[k][e]);
-                top = __builtin_fmaxf(top, size < inf ? size : 0.0f);
-            }
-        }
-        top = wave_max(top);
+        for (int k = 0; k < NK; ++k)
+            qw[k] = valid ? qw[k] : uint4{0, 0, 0, 0};
+        float top = wave_max(query_top(qw, a.q_dtype));
         if (lane == 0)
             tile_top[wave] = top;
         __syncthreads();
@@ -214,9 +206,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             top = __builtin_fmaxf(top, tile_top[w]);
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
         qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-            (void)query_operand(x[k], shift, q[k]);
+        query_operands(qw, a.q_dtype, shift, q);
     }
 
     f32x16 acc[NT];
