@@ -300,6 +300,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             r[tt] = mfma(page_k[0].code[tt][k][k_from[k % 2]], q[k], r[tt]);
         }
     }
+    __syncthreads();  // the first step unpacks the third page's K to where the first one's was
     for (int i = begin; i < end; ++i) {
         const PageV<D, GS> &pv = page_v[(i - begin) & 1];
         const PageK<D, GS> &pk = page_k[(i - begin + 1) & 1];
