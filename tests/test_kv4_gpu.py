@@ -295,6 +295,17 @@ def test_attention_scores_and_scales_far_apart(rows, tiles):
 
 
 @pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("rows", [1, 50])
+def test_attention_scores_that_vanish(rows, tiles):
+    """Queries and a scale so small that their product with every key is 0 in 32 bits: the mean of what is seen."""
+    cider.cider_kv4_set_tiles(tiles)
+    s = Setup([400, 150], [rows, 1], 1, 64, 64, garbage="nan")
+    ref.fill(s.cache, s.table, s.lens, *s.values(1))
+    q = ref.to_bits(s.rng.standard_normal((s.rows, 4, 64)) * 2.0 ** -125, 1)
+    check(s, attend(s, s.to_device(), q, 1, 1, 4, 1e-30, 90, 2), q, 1, 1, 4, 1e-30, 90, 2)
+
+
+@pytest.mark.parametrize("tiles", TILES)
 @pytest.mark.parametrize("rows", [2, 40])
 def test_what_a_row_may_not_see_does_not_reach_it(rows, tiles):
     """NaN and infinite keys and values behind the window and in front of the row, inside pages it does read."""

@@ -179,6 +179,32 @@ __device__ __forceinline__ float operand_sum(half8 op, float sum)
     return sum;
 }
 
+// Masks.  A lane's tokens lie at offsets STRIDE (e / 4) + e % 4 from its first
+// one, which rises with e: those in front of an offset are the low bits of a
+// word, so a page's mask takes a few operations, not some for every token.
+template <int STRIDE>
+__device__ __forceinline__ uint32_t tokens_below(int offset)
+{
+    const int u = offset < 0 ? 0 : (offset > kPageTokens ? kPageTokens : offset);
+    const int n = 4 * (u / STRIDE) + (u % STRIDE < 4 ? u % STRIDE : 4);
+    return n >= 32 ? ~0u : (1u << n) - 1u;
+}
+// The tokens that a column at position p sees, the lane's first at position at.
+template <int STRIDE>
+__device__ __forceinline__ uint32_t tokens_seen(int p, int at, int window, int sinks)
+{
+    uint32_t seen = tokens_below<STRIDE>(p + 1 - at);
+    if (window > 0)
+        seen &= ~tokens_below<STRIDE>(p - window + 1 - at) | tokens_below<STRIDE>(sinks - at);
+    return seen;
+}
+// A score, or minus infinity where bit e of the mask is 0.
+__device__ __forceinline__ float seen_score(float s, uint32_t seen, int e)
+{
+    const uint32_t keep = (uint32_t)((int32_t)(seen << (31 - e)) >> 31);
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, s) & keep) | (0xFF800000u & ~keep));
+}
+
 // The pages that a tile of columns sees: [0, sink_pages) and [first, end).
 struct PageRange {
     int sink_pages, first, count;

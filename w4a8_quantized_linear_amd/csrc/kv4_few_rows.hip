@@ -224,7 +224,13 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
                     w[g][B][1][e] = pack2<OUT_F16>(x - (float)hi.x, y - (float)hi.y);
                 }
             }
-    if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+    // a hidden token's weight is 0, and times a scale that is not finite it would
+    // not stay so
+    bool odd = false;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        odd |= !(__builtin_fabsf(vs[g]) < inf);
+    if (!whole && __any(odd)) {
 #pragma unroll
         for (int B = 0; B < 2; ++B)
 #pragma unroll
@@ -331,7 +337,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
             qw[m] = valid ? qw[m] : uint4{0, 0, 0, 0};
         const float top = column_max(query_top(qw, a.q_dtype));
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
-        st.qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
+        // above 0: a hidden token's score, minus infinity, times 0 would be NaN
+        st.qmul = __builtin_fmaxf(ldexp_f(a.scale * kLog2e, 24 - shift), 0x1p-149f);
         query_operands(qw, a.q_dtype, shift, st.q);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
@@ -370,17 +377,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
         load_k<D, GS, ONCE>(pg, ahead, lane);
         uint32_t seen = 0xFFFFu;
         if (!whole) {
-            seen = 0;
-            // bounds of the token's offset from the lane's first
-            const int at = t0 + 4 * j, upto = there ? p - at : -1, kept = a.sinks - at;
-            const int after = a.window == 0 ? -1 : p - a.window - at;
+            seen = there ? tokens_seen<16>(p, t0 + 4 * j, a.window, a.sinks) : 0u;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int tok = 16 * (e / 4) + e % 4;
-                const bool see = tok <= upto && (tok > after || tok < kept);
-                seen |= (uint32_t)see << e;
-                s[e / 4][e % 4] = see ? s[e / 4][e % 4] : -__builtin_inff();
-            }
+            for (int e = 0; e < 16; ++e)
+                s[e / 4][e % 4] = seen_score(s[e / 4][e % 4], seen, e);
         }
         page_outputs<D, GS, FINE>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
         load_v<D, GS, ONCE>(pg, ahead, lane);

@@ -340,18 +340,10 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                            (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
         uint32_t seen = ~0u;
         if (!whole) {
-            seen = 0;
-            // bounds of the token's offset from the lane's first
-            const int at = t0 + 4 * h, kept = a.sinks - at;
-            const int upto = (unsigned)n0 < (unsigned)a.kv.num_pages ? p - at : -1;
-            const int after = a.window == 0 ? -1 : p - a.window - at;
+            seen = (unsigned)n0 < (unsigned)a.kv.num_pages ? tokens_seen<8>(p, t0 + 4 * h, a.window, a.sinks) : 0u;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int tok = 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4;
-                const bool see = tok <= upto && (tok > after || tok < kept);
-                seen |= (uint32_t)see << e;
-                x[e / 16][e % 16] = see ? x[e / 16][e % 16] : -inf;
-            }
+            for (int e = 0; e < 32; ++e)
+                x[e / 16][e % 16] = seen_score(x[e / 16][e % 16], seen, e);
         }
         float top = x[0][0];
 #pragma unroll
@@ -390,6 +382,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         // barriers keep the compiler from gathering the products.  (Past
         // the last page the products take what lies in the buffer; unused.)
         uint32_t w[2][NG][2][4];
+        bool masked = false;
         {
             float vs[2][NG], ratio[2];
 #pragma unroll
@@ -399,6 +392,17 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                     vs[tt][g] = pv.scale[g][32 * tt + slot];
                 if (NG == 2)
                     ratio[tt] = pk.ratio[32 * tt + slot];
+            }
+            // a hidden token's weight is 0, and times a scale that is not finite
+            // it would not stay so
+            if (!whole) {
+                bool odd = false;
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        odd |= !(__builtin_fabsf(vs[tt][g]) < inf);
+                masked = __any(odd);
             }
             float sum[2] = {0.0f, 0.0f};
             r[0] = f32x16{};
@@ -433,7 +437,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             }
             l_run += sum[0] + sum[1];
         }
-        if (!whole) {  // a hidden token's weight is 0, its scale may be anything
+        if (masked) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
 #pragma unroll
