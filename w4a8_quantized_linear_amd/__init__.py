@@ -1,7 +1,8 @@
 """Python binding of libcider.so, the MI355X (gfx950) fused quantized linear
 layer: per-token INT8 activation quantization, INT8 x INT8 -> INT32 product on
 the matrix cores, fused dequantization to fp16 (W8A8 per channel, W8A8 per
-group of 64 / 128, W4A8 with packed int4 weights).
+group of 64 / 128, W4A8 with packed int4 weights), and of its 4-bit paged
+key/value cache with attention over it (the cider_kv4_ functions).
 
 This module only marshals arguments: every function has the name and the
 argument order of the C function declared in include/cider.h, takes device
