@@ -16,8 +16,8 @@
 //
 // Two LDS buffers each for K and V, one barrier a page: while the weights of
 // page i are worked out the scores of page i + 1 are multiplied, and between
-// the products of page i's outputs K of page i + 2 and V of page i + 1, loaded
-// at the step's start, are unpacked.
+// the products of page i's outputs those scores are scaled and K of page i + 2
+// and V of page i + 1, loaded at the step's start, are unpacked.
 //
 // Rounding.  q is scaled by one power of two for the whole tile (its largest
 // magnitude to [2^13, 2^14)), so the score's factor goes into K's scales once a
@@ -57,13 +57,13 @@ constexpr int kTop = 11;
 template <int D, int GS>
 struct PageK {
     uint4 code[2][D / 16][64];  // [32-token tile][16-element step][lane]
-    float ratio[kPageTokens];   // groups of 64 in 128: the first group's scale over the second one's
+    float scale[kPageTokens];   // of the scores, to units of log2: the last group's scale times q's factor
+    float ratio[kPageTokens];   // groups of 64 in 128: the first group's scale over the last one's
 };  // scales stand at scale_slot(token)
 template <int D, int GS>
 struct PageV {
     uint4 code[2][2][D / 32][64];     // [32-token tile][16-token step][32-element tile][lane]
     float scale[D / GS][kPageTokens];
-    float k_scale[kPageTokens];       // of the scores, to units of log2: K's last group's scale times q's factor
     int exp[D / GS];                  // V's scales are 2^(kTop - exp) times as large
 };
 
@@ -251,21 +251,21 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     const int unit = D == 128 ? tid % 256 : tid % 256 / 2;
     const int vx = (D == 128 ? 0 : 2 * (tid % 2)) + tid / 256 * ND;
     const int vc = unit % 16, vj = unit / 16 % 4, vg = unit / 64 % (D / 64), vb = unit / (64 * (D / 64));
-    float k_scale_next = 0.0f;  // wavefront 0: of the page whose K was staged last
     auto stage_k_dword = [&](PageK<D, GS> &to, const Share<ND> &s, int m) {
         to.code[kt / 32][2 * (km + m) + kj / 2][k_to] = code_halves(s.k[m]);
     };
     auto stage_k_scales = [&](PageK<D, GS> &to, const Share<ND> &s) {
+        if (wave != 0)
+            return;
         if (NG == 1) {
-            k_scale_next = s.k_scale[0] * qmul;
+            to.scale[scale_slot(lane)] = s.k_scale[0] * qmul;
         } else {
             // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
             // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
             const float low = __builtin_fmaxf(s.k_scale[0] * 0x1p-60f, 0x1p-149f);
             const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
-            k_scale_next = last * qmul;
-            if (wave == 0)
-                to.ratio[scale_slot(lane)] = s.k_scale[0] / last;
+            to.scale[scale_slot(lane)] = last * qmul;
+            to.ratio[scale_slot(lane)] = s.k_scale[0] / last;
         }
     };
     auto stage_v_dword = [&](PageV<D, GS> &to, const Share<ND> &s, int e) {
@@ -273,9 +273,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
     };
     // number, t0: the page's
-    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<ND> &s, float k_scale, int number, int t0) {
-        if (wave == 0)
-            to.k_scale[scale_slot(lane)] = k_scale;
+    auto stage_v_scales = [&](PageV<D, GS> &to, const Share<ND> &s, int number, int t0) {
         if (wave >= 1 && wave <= NG) {
             const bool held = t0 + lane <= t.p_hi && (unsigned)number < (unsigned)a.kv.num_pages;
             const float v = held ? s.v_scale : 0.0f;
@@ -302,10 +300,12 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             stage_k_dword(page_k[1], share1, m);
         }
         stage_k_scales(page_k[0], share);
-        stage_v_scales(page_v[0], share, k_scale_next, n0, t.range.at(begin) * kPageTokens);
+        stage_v_scales(page_v[0], share, n0, t.range.at(begin) * kPageTokens);
         stage_k_scales(page_k[1], share1);
     }
     __syncthreads();
+    // scores of the page in turn less the running maximum, and the lane's largest
+    float x[2][16], top = 0.0f;
     if (begin < end) {
 #pragma unroll
         for (int s = 0; s < 2 * NK; ++s) {
@@ -319,6 +319,15 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                     r[tt][e] = scaled(r[tt][e], ratio, e);
             }
             r[tt] = mfma(page_k[0].code[tt][k][k_from[k % 2]], q[k], r[tt]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const float ks = page_k[0].scale[32 * tt + slot];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                x[tt][e] = scaled(r[tt][e], ks, e);
+                top = e + tt == 0 ? x[tt][e] : __builtin_fmaxf(top, x[tt][e]);
+            }
         }
     }
     __syncthreads();  // the first step unpacks the third page's K to where the first one's was
@@ -347,16 +356,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         for (int s = 0; s < kAhead; ++s)
             read_k(s);
 
-        // scores of page i less the running maximum
-        const float m_sub = m_run == -inf ? 0.0f : m_run;
-        float x[2][16];
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            const float ks = pv.k_scale[32 * tt + slot];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[tt][e] = scaled(r[tt][e], ks, e) - m_sub;
-        }
+        const float m_old = m_run == -inf ? 0.0f : m_run;  // what x is less by
         const bool whole = t0 + kPageTokens - 1 <= w_lo && (unsigned)n0 < (unsigned)a.kv.num_pages &&
                            (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
         uint32_t seen = ~0u;
@@ -365,17 +365,17 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 x[e / 16][e % 16] = seen_score(x[e / 16][e % 16], seen, e);
-        }
-        float top = x[0][0];
+            top = x[0][0];
 #pragma unroll
-        for (int e = 1; e < 32; ++e)
-            top = __builtin_fmaxf(top, x[e / 16][e % 16]);
+            for (int e = 1; e < 32; ++e)
+                top = __builtin_fmaxf(top, x[e / 16][e % 16]);
+        }
         if (__any(top > (m_run == -inf ? -inf : kSlack))) {
             top = max_lane32(top);
             const float up = top > 0.0f || m_run == -inf ? top : 0.0f;  // of the maximum
             if (up != -inf) {
                 const float f = m_run == -inf ? 0.0f : __builtin_amdgcn_exp2f(-up);
-                m_run = m_sub + up;
+                m_run = m_old + up;
                 l_run *= f;
 #pragma unroll
                 for (int y = 0; y < NT; ++y)
@@ -404,10 +404,12 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         // the last page the products take what lies in the buffer; unused.)
         uint32_t w[2][NG][2][4];
         bool masked = false;
+        float ks[2];  // K's scales of page i + 1
         {
             float vs[2][NG], ratio[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
+                ks[tt] = pk.scale[32 * tt + slot];
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     vs[tt][g] = pv.scale[g][32 * tt + slot];
@@ -469,9 +471,11 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                 }
         }
 
-        // The outputs of page i, with the unpacking of what comes next between
-        // them: K of page i + 2, V of page i + 1.
+        // The outputs of page i, with vector work of what comes next between
+        // them: the scaling of page i + 1's scores and their maximum, the
+        // unpacking of K of page i + 2 and V of page i + 1.
         {
+            const float m_sub = m_run == -inf ? 0.0f : m_run;
             PageK<D, GS> &to_k = page_k[(i - begin) & 1];
             PageV<D, GS> &to_v = page_v[(i - begin + 1) & 1];
             __builtin_amdgcn_sched_barrier(0);
@@ -481,6 +485,11 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                 const uint32_t(&o)[4] = w[tt][z * 32 / GS][y];
                 acc[z] = mfma(vf[s % (kAhead + 1)], __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]}), acc[z]);
                 read_v(s + kAhead);
+#pragma unroll
+                for (int e = s * 32 / kSteps; e < (s + 1) * 32 / kSteps; ++e) {
+                    x[e / 16][e % 16] = scaled(r[e / 16][e % 16], ks[e / 16], e % 16) - m_sub;
+                    top = e == 0 ? x[0][0] : __builtin_fmaxf(top, x[e / 16][e % 16]);
+                }
                 constexpr int EVERY = kSteps / (2 * ND);
                 if (s % EVERY == EVERY - 1) {
                     if (s / EVERY < ND)
@@ -490,7 +499,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            stage_v_scales(to_v, share, k_scale_next, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
+            stage_v_scales(to_v, share, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
             stage_k_scales(to_k, share);
         }
         n0 = n1;
