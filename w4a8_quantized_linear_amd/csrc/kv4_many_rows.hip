@@ -42,6 +42,7 @@ namespace cider {
 namespace {
 
 constexpr int kWaveCols = 32;  // one matrix operand
+constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw 32-bit buffer
 
 // The running maximum may lie this far (in units of log2) below the true one
 // before it is moved: weights reach 2^kSlack, and the outputs are rescaled in
@@ -79,19 +80,21 @@ struct Share {
     float k_scale[2], v_scale;  // by token: wavefront 0 K's groups, wavefront 1 + g V's group g
 };
 
+// Loads of a block go through a buffer descriptor made from its address: one
+// offset register for all pages and no vector arithmetic for a page's address.
 template <int N>
-__device__ __forceinline__ void load_dwords(uint32_t (&w)[N], const uint8_t *at)
+__device__ __forceinline__ void load_dwords(uint32_t (&w)[N], __amdgpu_buffer_rsrc_t block, uint32_t off, uint32_t base)
 {
     if constexpr (N == 4) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        const uint4 x = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(block, off, base, 0));
         w[0] = x.x;
         w[1] = x.y;
         w[2] = x.z;
         w[3] = x.w;
     } else if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(at);
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_raw_buffer_load_b32(block, off, base, 0));
     } else {
-        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(block, off, base, 0));
         w[0] = x.x;
         w[1] = x.y;
     }
@@ -175,40 +178,42 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     }
     const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
     const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
-    const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
+    const uint32_t page_bytes = (uint32_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
     // a page number outside the cache is never followed: page 0 is loaded in
     // its place and its tokens are left out
     auto block_of = [&](int number) {
-        return heads + ((unsigned)number < (unsigned)a.kv.num_pages ? number : 0) * page_bytes;
+        const uint32_t in = (unsigned)number < (unsigned)a.kv.num_pages ? (uint32_t)number : 0u;
+        return __builtin_amdgcn_make_buffer_rsrc((void *)(heads + (uint64_t)in * page_bytes), (short)0,
+                                                 kv4_block_bytes(D, GS), kRsrcWord3);
     };
-    auto fetch_k = [&](Share<ND> &s, int number) {
-        const uint8_t *block = block_of(number);
-        load_dwords(s.k, block + (uint32_t)(tid % 256 * (D / 8) + tid / 256 * 4 * ND));
-        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
+    const uint32_t code_off = tid % 256 * (D / 8) + tid / 256 * 4 * ND, scale_off = lane * 4;
+    auto fetch_k = [&](Share<ND> &s, __amdgpu_buffer_rsrc_t block) {
+        load_dwords(s.k, block, code_off, 0);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-            s.k_scale[g] = scales[g * kPageTokens + (uint32_t)lane];
+            s.k_scale[g] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                block, scale_off, kv4_scale_offset(D) + 4 * kPageTokens * g, 0));
     };
-    auto fetch_v = [&](Share<ND> &s, int number) {
-        const uint8_t *block = block_of(number);
-        load_dwords(s.v, block + kv4_v_offset(D) + (uint32_t)(tid % 256 * (D / 8) + tid / 256 * 4 * ND));
-        const float *scales = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
-        s.v_scale = (scales + (NG + (wave == 2 && NG == 2 ? 1 : 0)) * kPageTokens)[(uint32_t)lane];
+    auto fetch_v = [&](Share<ND> &s, __amdgpu_buffer_rsrc_t block) {
+        load_dwords(s.v, block, code_off, kv4_v_offset(D));
+        s.v_scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+            block, scale_off, kv4_scale_offset(D) + 4 * kPageTokens * (NG + (wave == 2 && NG == 2 ? 1 : 0)), 0));
     };
     // page numbers: of page i + 1 (V) and i + 2 (K); read one step ahead
     Share<ND> share, share1;
     const int last_page = end - 1;
-    auto number_of = [&](int i) { return table[t.range.at(i < last_page ? i : last_page)]; };
+    auto number_of = [&](int i) { return table[(uint32_t)t.range.at(i < last_page ? i : last_page)]; };
     f32x16 r[2];
     int n0 = -1, n1 = -1, n2 = -1;
     if (begin < end) {
         n0 = number_of(begin);
         n1 = number_of(begin + 1);
         n2 = number_of(begin + 2);
-        fetch_k(share, n0);
-        fetch_v(share, n0);
-        fetch_k(share1, n1);
+        fetch_k(share, block_of(n0));
+        fetch_v(share, block_of(n0));
+        fetch_k(share1, block_of(n1));
     }
+    __amdgpu_buffer_rsrc_t v_block = block_of(n1);  // of page i + 1
 
     // q: one power of two for the whole tile, so that the scores' factor goes
     // into K's scales once a page
@@ -265,7 +270,9 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             const float low = __builtin_fmaxf(s.k_scale[0] * 0x1p-60f, 0x1p-149f);
             const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
             to.scale[scale_slot(lane)] = last * qmul;
-            to.ratio[scale_slot(lane)] = s.k_scale[0] / last;
+            // (a division without its last bits: 2^-22)
+            const float rest = __builtin_amdgcn_rcpf(__builtin_amdgcn_frexp_mantf(last));
+            to.ratio[scale_slot(lane)] = ldexp_f(s.k_scale[0] * rest, -__builtin_amdgcn_frexp_expf(last));
         }
     };
     auto stage_v_dword = [&](PageV<D, GS> &to, const Share<ND> &s, int e) {
@@ -334,9 +341,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     for (int i = begin; i < end; ++i) {
         const PageV<D, GS> &pv = page_v[(i - begin) & 1];
         const PageK<D, GS> &pk = page_k[(i - begin + 1) & 1];
-        const int n3 = number_of(i + 3);
-        fetch_k(share, n2);
-        fetch_v(share, n1);
+        int n3 = -1;
         const int t0 = t.range.at(i) * kPageTokens;
 
         // Operands come from LDS kAhead steps before they are used: the first of
@@ -355,6 +360,14 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
 #pragma unroll
         for (int s = 0; s < kAhead; ++s)
             read_k(s);
+        float vs[2][NG];  // V's scales and their exponents
+        int vs_exp[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            vs_exp[g] = pv.exp[g];
+            vs[0][g] = pv.scale[g][slot];
+            vs[1][g] = pv.scale[g][32 + slot];
+        }
 
         const float m_old = m_run == -inf ? 0.0f : m_run;  // what x is less by
         const bool whole = t0 + kPageTokens - 1 <= w_lo && (unsigned)n0 < (unsigned)a.kv.num_pages &&
@@ -387,7 +400,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const int e = __builtin_amdgcn_readfirstlane(pv.exp[g]);
+            const int e = __builtin_amdgcn_readfirstlane(vs_exp[g]);
             if (e != v_exp[g]) {
                 const float f = ldexp_f(1.0f, v_exp[g] - e);
 #pragma unroll
@@ -406,13 +419,10 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         bool masked = false;
         float ks[2];  // K's scales of page i + 1
         {
-            float vs[2][NG], ratio[2];
+            float ratio[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 ks[tt] = pk.scale[32 * tt + slot];
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    vs[tt][g] = pv.scale[g][32 * tt + slot];
                 if (NG == 2)
                     ratio[tt] = pk.ratio[32 * tt + slot];
             }
@@ -435,6 +445,12 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             for (int s = 0; s < kSteps; ++s) {
                 r[k_tile(s)] = mfma(kf[s % (kAhead + 1)], q[k_step(s)], r[k_tile(s)]);
                 read_k(s + kAhead);
+                if (s == 0) {  // what is unpacked in this step's second half
+                    n3 = number_of(i + 3);
+                    fetch_v(share, v_block);
+                    v_block = block_of(n2);
+                    fetch_k(share, v_block);
+                }
                 if (s >= kSteps - kAhead)
                     read_v(s - (kSteps - kAhead));
                 // pairs of tokens of this step: one of 16 steps, two of 8
@@ -497,10 +513,12 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                     else
                         stage_v_dword(to_v, share, s / EVERY - ND);
                 }
+                if (s == kSteps / 2) {  // a chain of a few operations in one wavefront each
+                    stage_v_scales(to_v, share, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
+                    stage_k_scales(to_k, share);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            stage_v_scales(to_v, share, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
-            stage_k_scales(to_k, share);
         }
         n0 = n1;
         n1 = n2;
