@@ -357,9 +357,6 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             if (s < kSteps)
                 vf[s % (kAhead + 1)] = pv.code[s / (2 * NT)][s / NT % 2][s % NT][lane];
         };
-#pragma unroll
-        for (int s = 0; s < kAhead; ++s)
-            read_k(s);
         float vs[2][NG];  // V's scales and their exponents
         int vs_exp[NG];
 #pragma unroll
@@ -369,6 +366,9 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             vs[1][g] = pv.scale[g][32 + slot];
         }
 
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+            read_k(s);
         const float m_old = m_run == -inf ? 0.0f : m_run;  // what x is less by
         const bool whole = t0 + kPageTokens - 1 <= w_lo && (unsigned)n0 < (unsigned)a.kv.num_pages &&
                            (a.window == 0 || t0 > w_hi - a.window || t0 + kPageTokens <= a.sinks);
@@ -437,6 +437,19 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                         odd |= !(__builtin_fabsf(vs[tt][g]) < inf);
                 masked = __any(odd);
             }
+            // exponentials are taken a step before their use, which waits for them else
+            constexpr int kPairs = 16 / kSteps;
+            auto power = [&](int pair) {
+                if (pair < 16) {
+                    float &lo = x[pair / 8][4 * (pair / 4 % 2) + pair % 4];
+                    float &hi = x[pair / 8][8 + 4 * (pair / 4 % 2) + pair % 4];
+                    lo = __builtin_amdgcn_exp2f(lo);
+                    hi = __builtin_amdgcn_exp2f(hi);
+                }
+            };
+#pragma unroll
+            for (int pair = 0; pair < kPairs; ++pair)
+                power(pair);
             float sum[2] = {0.0f, 0.0f};
             r[0] = f32x16{};
             r[1] = f32x16{};
@@ -457,8 +470,8 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
 #pragma unroll
                 for (int pair = s * 16 / kSteps; pair < (s + 1) * 16 / kSteps; ++pair) {
                     const int tt = pair / 8, y = pair / 4 % 2, e = pair % 4;
-                    const float lo = __builtin_amdgcn_exp2f(x[tt][4 * y + e]);
-                    const float hi = __builtin_amdgcn_exp2f(x[tt][8 + 4 * y + e]);
+                    const float lo = x[tt][4 * y + e], hi = x[tt][8 + 4 * y + e];
+                    power(pair + kPairs);
                     sum[0] += lo;
                     sum[1] += hi;
 #pragma unroll
