@@ -112,15 +112,15 @@ int64_t units_of(const Kv4AttentionArgs &a, int cols)
 
 // Columns of the tiles, by sizes (measured; G = 4, 8 kv heads of 128):
 //   the few-row kernel keeps up to 64 columns (64 columns, 8 sequences of 16384
-//   tokens: 110 us against 107), and while all its tiles see no more than 24576
-//   pages together (128 columns over 4096 tokens, 1 / 4 / 8 sequences: 17 / 28 /
-//   49 us against 24 / 38 / 48; 512 columns over 1024, 4 / 8 sequences: 30 / 51
-//   against 40 / 43): the other one spends 2 us a page on a tile of any fill;
+//   tokens: 108 us against 104), and while all its tiles see no more than 24576
+//   pages together (128 columns over 4096 tokens, 1 / 4 / 8 sequences: 17 / 27 /
+//   49 us against 22 / 33 / 48; 512 columns over 1024, 4 / 8 sequences: 29 / 49
+//   against 38 / 39): the other one spends 2 us a page on a tile of any fill;
 //   then 128 columns, two workgroups a compute unit, or, for one long sequence,
 //   256 and one: half the unpacking per column (2048 rows over 16384 tokens
-//   647 -> 615 us, 4096 of 4096 182 -> 169), but coarser where tiles end at
-//   different times (ragged prompts 232 -> 246, 8000 rows with a window of 1024
-//   222 -> 243).
+//   619 -> 585 us, 4096 of 4096 186 -> 179), but coarser where tiles end at
+//   different times (ragged prompts 219 -> 234, 8000 rows with a window of 1024
+//   205 -> 226).
 int columns_of(const Kv4AttentionArgs &a)
 {
     if (a.tiles)
@@ -168,9 +168,9 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
         n.pages = (int)chunk;
     } else {
         // Two workgroups a compute unit (one of 256 columns) as long as a chunk
-        // keeps 16 pages, one down to 4 (128 rows over 16384 tokens, 64 tiles: 8
-        // chunks 69 us, 4 81; 4 sequences of 1024, 256 tiles of 16 pages: whole 43
-        // us, halved 58).
+        // keeps 16 pages, one down to 4 (128 rows over 16384 tokens, 32 tiles: 16
+        // chunks 72 us, 8 75; 8 sequences of 1024, 256 tiles of 16 pages: whole 39
+        // us, halved 57).
         auto chunks = [&](int64_t wanted, int64_t least) {
             const int64_t by_units = (wanted + units - 1) / units, by_pages = (pages + least - 1) / least;
             return by_units < by_pages ? by_units : by_pages;

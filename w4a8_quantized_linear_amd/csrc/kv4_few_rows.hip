@@ -135,7 +135,7 @@ __device__ __forceinline__ half8 halves(uint32_t w) { return __builtin_bit_cast(
 template <int D, int GS>
 struct State {
     f32x4 acc[D / 16], off[D / 64];
-    float m, l;          // in units of q's scaled scores
+    float m, l;          // m in units of log2
     int v_exp[D / GS];   // 2^v_exp is above every finite s_v seen
     half8 q[D / 32];
     float zero[D / GS], qmul;
@@ -164,12 +164,23 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
     }
 }
 
-// Their weights, and the outputs.  seen: bit 4 t + e set where the lane's
-// column sees the token (read where the page is not whole); last: the last token
-// of the page that any column of the tile sees (63 and more: all).
+__device__ __forceinline__ float largest(const float (&s)[4][4])
+{
+    float top = s[0][0];
+#pragma unroll
+    for (int n = 1; n < 16; ++n)
+        top = __builtin_fmaxf(top, s[n / 4][n % 4]);
+    return top;
+}
+
+// Their weights, and the outputs.  top: the largest score; seen: bit 4 t + e
+// set where the lane's column sees the token (read where the page is not
+// whole); last: the last token of the page that any column of the tile sees
+// (63 and more: all).
 template <int D, int GS, bool FINE>
 __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
-                                             float (&s)[4][4], bool whole, uint32_t seen, int last)
+                                             float (&s)[4][4], float top, bool whole, uint32_t seen,
+                                             int last)
 {
     constexpr int NG = D / GS, NT = D / 16;
     const float inf = __builtin_inff();
@@ -179,8 +190,8 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
     for (int g = 0; g < NG; ++g) {
         const float v = scale_token(lane) <= last ? pg.vs[g] : 0.0f;
         if (__any(v >= ldexp_f(1.0f, st.v_exp[g]) && v < inf)) {
-            const float top = wave_max(v < inf ? v : 0.0f);
-            const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top));
+            const int e = __builtin_amdgcn_readfirstlane(
+                __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
             const float f = ldexp_f(1.0f, st.v_exp[g] - e);
             st.v_exp[g] = e;
 #pragma unroll
@@ -193,14 +204,10 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         // the 16 times larger codes belong to tokens 1 and 3 of each 4
         vs[g] = ldexp_f(v, 14 - st.v_exp[g] - (lane & 1 ? 4 : 0));
     }
-    float top = s[0][0];
-#pragma unroll
-    for (int n = 1; n < 16; ++n)
-        top = __builtin_fmaxf(top, s[n / 4][n % 4]);
-    const float m_new = __builtin_fmaxf(st.m, column_max(top));
+    const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.qmul);
     const float m_sub = m_new == -inf ? 0.0f : m_new;
     if (__any(m_new > st.m)) {
-        const float f = __builtin_amdgcn_exp2f((st.m - m_sub) * st.qmul);
+        const float f = __builtin_amdgcn_exp2f(st.m - m_sub);
         st.l *= f;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -213,7 +220,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
         float &x = s[n / 4][n % 4];
-        x = __builtin_amdgcn_exp2f((x - m_sub) * st.qmul);
+        x = __builtin_amdgcn_exp2f(__builtin_fmaf(x, st.qmul, -m_sub));
         st.l += x;
     }
     const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
@@ -225,8 +232,10 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         for (int B = 0; B < 2; ++B)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = scaled(s[2 * B][e], vs[g], 8 * B + e);
-                const float y = scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e);
+                float x = scaled(s[2 * B][e], vs[g], 8 * B + e);
+                float y = scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e);
+                if constexpr (FINE)  // kept from being computed twice, by the subtraction below too
+                    asm("" : "+v"(x), "+v"(y));
                 w[g][B][0][e] = pack2<OUT_F16>(x, y);
                 if constexpr (FINE) {
                     const half2_t hi = __builtin_bit_cast(half2_t, w[g][B][0][e]);
@@ -385,13 +394,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
         page_scores<D, GS>(st, pg, s);
         load_k<D, GS, ONCE>(pg, ahead, lane);
         uint32_t seen = 0xFFFFu;
+        float top = largest(s);
         if (!whole) {
             seen = there ? tokens_seen<16>(p, t0 + 4 * j, a.window, a.sinks) : 0u;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 s[e / 4][e % 4] = seen_score(s[e / 4][e % 4], seen, e);
+            top = largest(s);
         }
-        page_outputs<D, GS, FINE>(st, pg, lane, s, whole, seen, there ? t.p_hi - t0 : -1);
+        page_outputs<D, GS, FINE>(st, pg, lane, s, top, whole, seen, there ? t.p_hi - t0 : -1);
         load_v<D, GS, ONCE>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;
@@ -405,8 +416,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
         *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) = o;
     }
     if (j == 0) {
-        // in units of log2, so that parts compare without the column's qmul
-        part_m[wave][c] = st.m == -__builtin_inff() ? st.m : st.m * st.qmul;
+        part_m[wave][c] = st.m;
         part_l[wave][c] = st.l;
     }
     __syncthreads();

@@ -27,15 +27,18 @@
 // of it the output's rounding.  (Two halves, as for few rows, would double the
 // second product, which is not hidden here.)
 //
-// What bounds it: instruction issue.  A wavefront takes 410 instructions a page
-// (D 128 in groups of 64), 32 of them products; counters show the matrix cores
-// busy 31 % of the time and the vector units 53 %, and a probe of nothing but
-// such products and multiply-adds, two wavefronts on a SIMD, shows hardly any
-// overlap of the two: about 32 cycles a product and 2.6 an instruction, of
-// which this loop reaches 88 %.  Measured: 2048 rows over 16384 tokens 631 us,
-// 816 TFLOP/s (groups of 128: 560 us, 920); 4 ragged prompts of up to 4096
-// rows, groups of 128, 227 us, 790; 8000 rows with a window of 1024 214 us, 590
-// (18 pages a tile do not hide a tile's beginning and end, 9 us of 65).
+// What bounds it: the vector units.  A wavefront takes about 365 vector
+// instructions a page (D 128 in groups of 64), which cost 4.4 cycles of its SIMD
+// each (8.3 an exponential) while products run, 1730 in all; the 32 products,
+// 32 cycles each, go under them.  Counters for 2048 rows over 16384 tokens: the
+// vector units are busy 65 % of the time, the matrix cores 40 %, either 81 %; the
+// rest is the page's barrier and results waited for.  So the work was moved, not
+// only cut: scaling under the outputs' products, loads and unpacking between
+// products, exponentials a step early (647 -> 580 us with the 256 columns).
+// Measured: 2048 rows over 16384 tokens 580 us, 890 TFLOP/s (groups of 128: 513,
+// 1005); 4 ragged prompts of up to 4096 rows, groups of 128, 220 us, 815; 8000
+// rows with a window of 1024 205 us, 615 (18 pages a tile do not hide a tile's
+// beginning and end, 9 us of 60).
 #include "kv4_attention.h"
 
 namespace cider {
