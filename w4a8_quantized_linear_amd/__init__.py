@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_PKG, "libcider.so")
@@ -54,6 +55,9 @@ class CiderError(RuntimeError):
         super().__init__("%s failed: %s (status %d)" % (what, cider_status_str(status), status))
 
 
+_KV4_BATCH = struct.Struct("4Q8qi4x")  # cider_kv4_batch's fields
+
+
 class cider_kv4_batch(ctypes.Structure):
     """The batch of a cider_kv4_* call (the struct of include/cider.h): a paged
     4-bit key/value cache, its page table, and the rows and lengths of each
@@ -65,8 +69,10 @@ class cider_kv4_batch(ctypes.Structure):
 
     def __init__(self, cache, pages, row_start, kv_len, batch, rows, max_rows, max_kv_len, max_pages,
                  num_pages, kv_heads, head_dim, group_size):
-        super().__init__(_ptr(cache), _ptr(pages), _ptr(row_start), _ptr(kv_len), batch, rows, max_rows,
-                         max_kv_len, max_pages, num_pages, kv_heads, head_dim, group_size)
+        # written in one piece: 13 assignments cost 0.35 us more, a tenth of a launch
+        _KV4_BATCH.pack_into(self, 0, _ptr(cache) or 0, _ptr(pages) or 0, _ptr(row_start) or 0, _ptr(kv_len) or 0,
+                             batch, rows, max_rows, max_kv_len, max_pages, num_pages, kv_heads, head_dim,
+                             group_size)
         self._tensors = (cache, pages, row_start, kv_len)
 
 
@@ -124,11 +130,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
 _raw_stream = None
@@ -139,8 +146,8 @@ def _current_stream() -> int | None:
     torch.cuda.current_stream() builds costs 2.7 us a call, as much as a
     launch, so the handle is asked for directly where torch offers that."""
     global _raw_stream
-    import torch
     if _raw_stream is None:
+        import torch
         if not torch.cuda.is_available():
             return None
         get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
