@@ -11,8 +11,10 @@
 // tokens are what shares a dword of V codes, so every dword of the cache has
 // one writer in a call and a partly filled one is read, patched and written
 // back without atomics.  Both directions move 16 bytes per lane on the 16-bit
-// side (a head of a row is one contiguous run) and dwords on the cache side;
-// V's codes cross from token-major to element-major through LDS.
+// side (a head of a row is one contiguous run) and dwords on the cache side.
+// Wavefront j has the 8 tokens 16 b + 4 j + i that share dwords of V, so V's
+// codes change between token-major and element-major order in registers, by
+// exchanges across the wavefront: 14 operations for 128 dwords, no LDS.
 //
 // What bounds them: bytes.  The append of 6 ragged prompts of up to 4096 rows
 // (8 heads of 128, 70 MB) takes 22.6 us, 3.1 TB/s, of 65536 rows 4.1 TB/s, where
@@ -144,23 +146,167 @@ __device__ __forceinline__ uint32_t int4_codes(uint4 v, float s, float rs)
     return half[0] | half[1] << 16;
 }
 
+// Where a lane's chunks (8 elements each) are: chunk column and, per register,
+// token of the span.  D 128: 16 columns, i = lane / 16, b the register; D 64: 8
+// columns, b = lane / 32, i = lane / 8 % 4.
+template <int D>
+__device__ __forceinline__ int token_of(int lane, int j, int reg)
+{
+    return D == 128 ? 16 * reg + 4 * j + lane / 16 : lane / 32 * 16 + 4 * j + lane / 8 % 4;
+}
+
+// Exchanges between registers and lane halves (rows of 16): the first's upper
+// half (odd rows) against the second's lower half (even rows).  The second
+// operand is made another value in the compiler's eyes: given one value twice
+// it takes both results for equal.
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
+{
+    asm("" : "+v"(b));
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b)
+{
+    asm("" : "+v"(b));
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+
+// V's codes between orders, the same steps in reverse order both ways.  Tokens:
+// w[b] holds a chunk's 8 elements of the lane's token.  Dwords: w holds, per
+// element, the wavefront's 8 tokens; the lane's dwords lie together at
+// dword_of.
+//   halves  elements 0 - 3 and 4 - 7 of the two b   <->  lane bit 5
+//   pairs   within them                             <->  lane bit 4
+//   nibbles of a pair                               <->  the register (D 128) or lane bit 3 (D 64)
+// and, D 128, two dwords that are neighbours in the cache (x, x + 1; lanes l and
+// l ^ 2) into one lane.
+constexpr uint32_t kLowHalves = 0x05040100u, kHighHalves = 0x07060302u;  // byte selectors of v_perm
+constexpr uint32_t kEvenBytes = 0x06020400u, kOddBytes = 0x07030501u;
+constexpr uint32_t kLowNibbles = 0x0F0F0F0Fu;
+
+template <int D>
+__device__ __forceinline__ int dword_of(int lane, int j)
+{
+    if constexpr (D == 128) {
+        const int c8 = lane % 16, c = c8 % 2 * 8 + lane / 32 * 4 + lane / 16 % 2 * 2 + c8 / 2 % 2;
+        return ((c8 / 8 * 4 + j) * 16 + c) * 4 + c8 / 4 % 2 * 2;
+    } else {
+        const int c8 = lane % 8, c = c8 % 2 * 8 + lane / 32 * 4 + lane / 16 % 2 * 2 + lane / 8 % 2;
+        return (j * 16 + c) * 4 + c8 / 2;
+    }
+}
+
+__device__ __forceinline__ void neighbours(uint32_t (&w)[2], int lane)
+{
+    const bool odd = lane & 2;
+    const uint32_t got = dpp<0x4E>(odd ? w[0] : w[1]);  // quad_perm [2,3,0,1]
+    w[0] = odd ? got : w[0];
+    w[1] = odd ? w[1] : got;
+}
+__device__ __forceinline__ void nibbles(uint32_t (&w)[2])
+{
+    const uint32_t a = w[0], b = w[1];
+    w[0] = (a & kLowNibbles) | ((b << 4) & ~kLowNibbles);
+    w[1] = ((a >> 4) & kLowNibbles) | (b & ~kLowNibbles);
+}
+__device__ __forceinline__ void select(uint32_t (&w)[2], uint32_t first, uint32_t second)
+{
+    const uint32_t a = w[0], b = w[1];
+    w[0] = __builtin_amdgcn_perm(b, a, first);
+    w[1] = __builtin_amdgcn_perm(b, a, second);
+}
+__device__ __forceinline__ void nibbles(uint32_t (&w)[1], int lane)
+{
+    const uint32_t a = w[0], b = dpp<0x128>(a);  // row_ror:8, the lane 8 away
+    w[0] = lane & 8 ? ((b >> 4) & kLowNibbles) | (a & ~kLowNibbles)
+                    : (a & kLowNibbles) | ((b << 4) & ~kLowNibbles);
+}
+__device__ __forceinline__ void pairs(uint32_t (&w)[1], int lane)
+{
+    uint32_t a = w[0], b = a;
+    swap16(a, b);
+    w[0] = __builtin_amdgcn_perm(b, a, lane & 16 ? kOddBytes : kEvenBytes);
+}
+__device__ __forceinline__ void half_words(uint32_t (&w)[1], int lane)
+{
+    uint32_t a = w[0], b = a;
+    swap32(a, b);
+    w[0] = __builtin_amdgcn_perm(b, a, lane & 32 ? kHighHalves : kLowHalves);
+}
+__device__ __forceinline__ void tokens_to_dwords(uint32_t (&w)[2], int lane)
+{
+    select(w, kLowHalves, kHighHalves);
+    swap32(w[0], w[1]);
+    select(w, kEvenBytes, kOddBytes);
+    swap16(w[0], w[1]);
+    nibbles(w);
+    neighbours(w, lane);
+}
+__device__ __forceinline__ void dwords_to_tokens(uint32_t (&w)[2], int lane)
+{
+    neighbours(w, lane);
+    nibbles(w);
+    swap16(w[0], w[1]);
+    select(w, kEvenBytes, kOddBytes);
+    swap32(w[0], w[1]);
+    select(w, kLowHalves, kHighHalves);
+}
+__device__ __forceinline__ void tokens_to_dwords(uint32_t (&w)[1], int lane)
+{
+    half_words(w, lane);
+    pairs(w, lane);
+    nibbles(w, lane);
+}
+__device__ __forceinline__ void dwords_to_tokens(uint32_t (&w)[1], int lane)
+{
+    nibbles(w, lane);
+    pairs(w, lane);
+    half_words(w, lane);
+}
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t (&w)[N], const uint32_t *at)
+{
+    if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *at;
+    }
+}
+
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4Args a, const uint16_t *k,
                                                               const uint16_t *v, int64_t ldk,
                                                               int64_t ldv, int spans)
 {
-    constexpr int CH = D / 8;                     // 8-value chunks of a token
-    constexpr int PT = kSpan * CH / kThreads;     // chunks per thread
-    constexpr int WT = 4 * D / kThreads;          // V dwords per thread
-    __shared__ uint32_t vcode[kSpan][CH];
+    constexpr int CH = D / 8;   // 8-value chunks of a token
+    constexpr int PT = D / 64;  // chunks of K and of V, and V dwords, per thread
     Place w;
     if (!place_of(a, spans, w))
         return;
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x % 64, c8 = lane % CH;
+    const int j = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+    uint32_t mask = 0;  // of a V dword's tokens, those of this call
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int p = w.base + e / 4 * 16 + 4 * j + e % 4;
+        mask |= (p >= w.lo && p < w.hi ? 15u : 0u) << (4 * e);
+    }
+    if (mask == 0)
+        return;
     uint4 kx[PT], vx[PT];
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-        const int c8 = (tid + i * kThreads) % CH, p = w.base + (tid + i * kThreads) / CH;
+        const int p = w.base + token_of<D>(lane, j, i);
         kx[i] = vx[i] = uint4{0, 0, 0, 0};
         if (p >= w.lo && p < w.hi) {
             kx[i] = nt_load(k + (p + w.shift) * ldk + w.h * D + c8 * 8);
@@ -171,25 +317,21 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4Args a, const u
     if (!block)
         return;
     const int half = (w.base / kSpan) & 1;  // which 32 tokens of the page
-    const bool full = w.lo == w.base && w.hi == w.base + kSpan;
     float *kscale = reinterpret_cast<float *>(block + kv4_scale_offset(D));
     float *vscale = kscale + kPageTokens * (D / GS);
     uint32_t *kcode = reinterpret_cast<uint32_t *>(block);
-    uint32_t *vout = reinterpret_cast<uint32_t *>(block + kv4_v_offset(D)) + half * 4 * D;
-    uint32_t old[WT];  // what a partly filled span keeps
-    if (!full) {
-#pragma unroll
-        for (int i = 0; i < WT; ++i)
-            old[i] = vout[tid + i * kThreads];
-    }
+    uint32_t *vout = reinterpret_cast<uint32_t *>(block + kv4_v_offset(D)) + half * 4 * D + dword_of<D>(lane, j);
+    uint32_t old[PT] = {};  // what a partly filled dword keeps
+    if (mask != ~0u)
+        load_dwords(old, vout);
+    uint32_t vcode[PT];
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-        const int c8 = (tid + i * kThreads) % CH, t = (tid + i * kThreads) / CH, p = w.base + t;
-        const int token = half * kSpan + t;
+        const int t = token_of<D>(lane, j, i), p = w.base + t, token = half * kSpan + t;
         const float ks = seventh(widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(kx[i]))));
         const float vs = seventh(widen_bits<DT>(run_max<GS / 8>(chunk_absmax_bits(vx[i]))));
         const uint32_t kq = int4_codes<DT>(kx[i], ks, __builtin_amdgcn_rcpf(ks));
-        vcode[t][c8] = int4_codes<DT>(vx[i], vs, __builtin_amdgcn_rcpf(vs));
+        vcode[i] = int4_codes<DT>(vx[i], vs, __builtin_amdgcn_rcpf(vs));
         if (p >= w.lo && p < w.hi) {
             kcode[token * CH + (c8 % 4) * (D / 32) + c8 / 4] = kq;
             if (c8 % (GS / 8) == 0) {
@@ -198,29 +340,14 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4Args a, const u
             }
         }
     }
-    __syncthreads();
+    tokens_to_dwords(vcode, lane);
 #pragma unroll
-    for (int i = 0; i < WT; ++i) {
-        const int n = tid + i * kThreads;
-        const int x = n & 3, c = (n >> 2) & 15, j = (n >> 6) & 3, d = (n >> 8) * 64 + x * 16 + c;
-        uint32_t word = 0, mask = ~0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int t = (e >> 2) * 16 + 4 * j + (e & 3);
-            word |= ((vcode[t][d >> 3] >> (4 * (d & 7))) & 15u) << (4 * e);
-        }
-        if (!full) {
-            mask = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int p = w.base + (e >> 2) * 16 + 4 * j + (e & 3);
-                mask |= (p >= w.lo && p < w.hi ? 15u : 0u) << (4 * e);
-            }
-            word = (old[i] & ~mask) | (word & mask);
-        }
-        if (mask)
-            vout[n] = word;
-    }
+    for (int i = 0; i < PT; ++i)
+        vcode[i] = (old[i] & ~mask) | (vcode[i] & mask);
+    if constexpr (PT == 2)
+        *reinterpret_cast<uint2 *>(vout) = uint2{vcode[0], vcode[1]};
+    else
+        *vout = vcode[0];
 }
 
 // 8 codes (nibble e: value e) as 16-bit values scaled by s.
@@ -240,45 +367,32 @@ template <int D, int GS, int DT>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Args a, uint16_t *k, uint16_t *v,
                                                             int64_t ldk, int64_t ldv, int spans)
 {
-    constexpr int CH = D / 8;
-    constexpr int PT = kSpan * CH / kThreads;
-    constexpr int WT = 4 * D / kThreads;
-    __shared__ uint32_t vword[4 * D];
+    constexpr int CH = D / 8, PT = D / 64;
     Place w;
     if (!place_of(a, spans, w))
         return;
     const uint8_t *block = block_of<D, GS>(a, w);
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x % 64, c8 = lane % CH;
+    const int j = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
     const int half = (w.base / kSpan) & 1;
-    if (block) {
-        const uint32_t *vin = reinterpret_cast<const uint32_t *>(block + kv4_v_offset(D)) + half * 4 * D;
-#pragma unroll
-        for (int i = 0; i < WT; ++i)
-            vword[tid + i * kThreads] = vin[tid + i * kThreads];
-    }
-    __syncthreads();
+    const uint32_t *kcode = reinterpret_cast<const uint32_t *>(block);
     const float *kscale = reinterpret_cast<const float *>(block + kv4_scale_offset(D));
     const float *vscale = kscale + kPageTokens * (D / GS);
-    const uint32_t *kcode = reinterpret_cast<const uint32_t *>(block);
+    uint32_t vcode[PT] = {};
+    if (block)
+        load_dwords(vcode, reinterpret_cast<const uint32_t *>(block + kv4_v_offset(D)) + half * 4 * D +
+                               dword_of<D>(lane, j));
+    dwords_to_tokens(vcode, lane);
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-        const int c8 = (tid + i * kThreads) % CH, t = (tid + i * kThreads) / CH, p = w.base + t;
-        const int token = half * kSpan + t;
+        const int t = token_of<D>(lane, j, i), p = w.base + t, token = half * kSpan + t;
         if (p < w.lo || p >= w.hi)
             continue;
         uint4 kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
         if (p >= 0 && block) {
             const int s = c8 / (GS / 8) * kPageTokens + token;
             kv = values_of<DT>(kcode[token * CH + (c8 % 4) * (D / 32) + c8 / 4], kscale[s]);
-            const int shift = 4 * ((t >> 4) * 4 + (t & 3)), j = (t >> 2) & 3;
-            uint32_t codes = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = c8 * 8 + e;
-                const int n = (((d >> 6) * 4 + j) * 16 + (d & 15)) * 4 + ((d >> 4) & 3);
-                codes |= ((vword[n] >> shift) & 15u) << (4 * e);
-            }
-            vv = values_of<DT>(codes, vscale[s]);
+            vv = values_of<DT>(vcode[i], vscale[s]);
         }
         nt_store(k + (p + w.shift) * ldk + w.h * D + c8 * 8, kv);
         nt_store(v + (p + w.shift) * ldv + w.h * D + c8 * 8, vv);
