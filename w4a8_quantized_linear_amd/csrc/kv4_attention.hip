@@ -202,24 +202,20 @@ size_t bytes_of(const Kv4AttentionArgs &a, const Kv4Launch &n)
 }
 
 template <int D, int COLS>
-void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned pairs = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
     if (n.splits <= 16)
-        kv4_join_kernel<D, COLS, 1><<<(pairs + 3) / 4, 256, 0, stream>>>(a, n);
-    else
-        kv4_join_kernel<D, COLS, 4><<<pairs, 256, 0, stream>>>(a, n);
+        return kv4_launch(kv4_join_kernel<D, COLS, 1>, (pairs + 3) / 4, 256, stream, a, n);
+    return kv4_launch(kv4_join_kernel<D, COLS, 4>, pairs, 256, stream, a, n);
 }
 
 template <int D>
-void launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     if (n.cols == kFewCols)
-        launch_join<D, kFewCols>(a, n, stream);
-    else if (n.cols == 128)
-        launch_join<D, 128>(a, n, stream);
-    else
-        launch_join<D, 256>(a, n, stream);
+        return launch_join<D, kFewCols>(a, n, stream);
+    return n.cols == 128 ? launch_join<D, 128>(a, n, stream) : launch_join<D, 256>(a, n, stream);
 }
 
 }  // namespace
@@ -243,11 +239,7 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size
                                             : launch_kv4_many_rows(a, n, stream);
     if (e != hipSuccess || n.splits < 2)
         return e;
-    if (a.kv.head_dim == 64)
-        launch_join<64>(a, n, stream);
-    else
-        launch_join<128>(a, n, stream);
-    return hipGetLastError();
+    return a.kv.head_dim == 64 ? launch_join<64>(a, n, stream) : launch_join<128>(a, n, stream);
 }
 
 }  // namespace cider

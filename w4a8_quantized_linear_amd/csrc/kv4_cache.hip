@@ -426,8 +426,7 @@ hipError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, const uint16_t
     const int spans = spans_of(a);
     const unsigned grid = (unsigned)spans * (unsigned)a.kv_heads * (unsigned)a.batch;
     return with_geometry(a, dtype, [&](auto D, auto GS, auto DT) {
-        kv4_append_kernel<D(), GS(), DT()><<<grid, kThreads, 0, stream>>>(a, k, v, ldk, ldv, spans);
-        return hipGetLastError();
+        return kv4_launch(kv4_append_kernel<D(), GS(), DT()>, grid, kThreads, stream, a, k, v, ldk, ldv, spans);
     });
 }
 
@@ -437,8 +436,7 @@ hipError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, int dtype
     const int spans = spans_of(a);
     const unsigned grid = (unsigned)spans * (unsigned)a.kv_heads * (unsigned)a.batch;
     return with_geometry(a, dtype, [&](auto D, auto GS, auto DT) {
-        kv4_read_kernel<D(), GS(), DT()><<<grid, kThreads, 0, stream>>>(a, k, v, ldk, ldv, spans);
-        return hipGetLastError();
+        return kv4_launch(kv4_read_kernel<D(), GS(), DT()>, grid, kThreads, stream, a, k, v, ldk, ldv, spans);
     });
 }
 

@@ -467,34 +467,28 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 }  // namespace
 
 template <int WAVES, bool FINE, bool ONCE>
-static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
-    else if (a.kv.group_size == 64)
-        kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
-    else
-        kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE><<<grid, 64 * WAVES, 0, stream>>>(a, n);
+        return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
+    if (a.kv.group_size == 64)
+        return kv4_launch(kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
+    return kv4_launch(kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
 }
 
 template <int WAVES>
-static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     if (a.y_dtype == DT_F16)
-        n.once ? launch<WAVES, true, true>(a, n, stream) : launch<WAVES, true, false>(a, n, stream);
-    else
-        n.once ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
+        return n.once ? launch<WAVES, true, true>(a, n, stream) : launch<WAVES, true, false>(a, n, stream);
+    return n.once ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
 }
 
 hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (n.waves == 8)
-        launch<8>(a, n, stream);
-    else
-        launch<4>(a, n, stream);
-    return hipGetLastError();
+    return n.waves == 8 ? launch<8>(a, n, stream) : launch<4>(a, n, stream);
 }
 
 }  // namespace cider

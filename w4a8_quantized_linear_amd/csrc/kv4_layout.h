@@ -29,6 +29,22 @@ __host__ __device__ constexpr int kv4_block_bytes(int D, int GS)
 __host__ __device__ constexpr int kv4_v_offset(int D) { return kPageTokens * D / 2; }
 __host__ __device__ constexpr int kv4_scale_offset(int D) { return kPageTokens * D; }
 
+// Launches a kernel and returns the launch's own status.  (The triple-bracket
+// form stores the configuration first and takes it back: 0.23 us of the 2.4 that
+// a launch costs the host, which is what bounds the smallest calls.)
+template <typename... P, typename... A>
+inline hipError_t kv4_launch(void (*kernel)(P...), unsigned grid, unsigned threads, hipStream_t stream, A... args)
+{
+    return [&](P... p) {
+        void *at[] = {&p...};
+        const hipError_t e =
+            hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), at, 0, stream);
+        if (e != hipSuccess)
+            (void)hipGetLastError();  // returned, and not left for another call to find
+        return e;
+    }(args...);
+}
+
 // Rows of one sequence in a call: its first row, their count (0 where the row
 // range is not inside the call's) and the tokens in the cache, clipped to the
 // batch's bounds.

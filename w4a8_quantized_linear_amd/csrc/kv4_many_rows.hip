@@ -578,25 +578,20 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
 }  // namespace
 
 template <int COLS>
-static void launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        kv4_many_rows_kernel<64, 64, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
-    else if (a.kv.group_size == 64)
-        kv4_many_rows_kernel<128, 64, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
-    else
-        kv4_many_rows_kernel<128, 128, COLS><<<grid, COLS * 2, 0, stream>>>(a, n);
+        return kv4_launch(kv4_many_rows_kernel<64, 64, COLS>, grid, COLS * 2, stream, a, n);
+    if (a.kv.group_size == 64)
+        return kv4_launch(kv4_many_rows_kernel<128, 64, COLS>, grid, COLS * 2, stream, a, n);
+    return kv4_launch(kv4_many_rows_kernel<128, 128, COLS>, grid, COLS * 2, stream, a, n);
 }
 
 hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (n.cols == 256)
-        launch<256>(a, n, stream);
-    else
-        launch<128>(a, n, stream);
-    return hipGetLastError();
+    return n.cols == 256 ? launch<256>(a, n, stream) : launch<128>(a, n, stream);
 }
 
 }  // namespace cider
