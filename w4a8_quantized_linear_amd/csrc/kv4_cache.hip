@@ -17,12 +17,12 @@
 // exchanges across the wavefront: 14 operations for 128 dwords, no LDS.
 //
 // What bounds them: bytes.  The append of 6 ragged prompts of up to 4096 rows
-// (8 heads of 128, 70 MB) takes 22.6 us, 3.1 TB/s, of 65536 rows 4.1 TB/s, where
-// its arithmetic (58 % of the vector units' time) still shows next to a plain
+// (8 heads of 128, 70 MB) takes 22.1 us, 3.2 TB/s, of 65536 rows 4.3 TB/s, where
+// its arithmetic (56 % of the vector units' time) still shows next to a plain
 // copy's 4.85; the read of 8 sequences of up to 8192 (223 MB, three quarters of
 // it written) 33.5 us, 6.6 TB/s.  One token is the launch and three loads in a
 // row (lengths, then row and page number, then the codes that share its words):
-// append 5.0 us, read 2.6.
+// append 4.7 us, read 2.7.
 #include <type_traits>
 
 #include "kv4_layout.h"
