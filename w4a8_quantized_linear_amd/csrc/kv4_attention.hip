@@ -16,49 +16,96 @@ namespace {
 
 constexpr int kMaxSplits = 256;
 
-// WAVES wavefronts per (row, query head), 4 / WAVES pairs per workgroup.  A
-// part's factor is computed once, by the lane of its number; then groups of
-// D / 4 lanes add up the parts, 16 bytes a lane.  A chain of three loads
-// (lengths, statistics, parts): 3.8 us for 32 pairs of 4 parts, 4.6 for 32 of 64
-// and 4.8 for 2048 of up to 4, the launch included.
-template <int D, int COLS, int WAVES>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttentionArgs a, Kv4Launch n)
+// The (row, query head) pair of a number, and the parts it has (0: none, its
+// workgroup wrote the output itself or the pair is not there).
+template <int COLS>
+__device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int64_t id, Tile &t, int &col)
 {
-    constexpr int PAIRS = 4 / WAVES, LANES = 64 * WAVES, GROUPS = LANES / (D / 4);
-    constexpr int PARTS = WAVES == 1 ? 64 : kMaxSplits;  // per pair at most
-    __shared__ float factor[PAIRS][PARTS];
-    __shared__ f32x4 sums[PAIRS][GROUPS][D / 4];
-    __shared__ float wave_m[4], wave_l[4];
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int pair = wave / WAVES, lane = (int)threadIdx.x % LANES;
     const int64_t cols = (int64_t)a.kv.max_rows * (a.q_heads / a.kv.kv_heads);
-    const int64_t id = (int64_t)blockIdx.x * PAIRS + pair;
-    const int col = (int)(id % cols);
+    col = (int)(id % cols);
     const int64_t bh = id / cols;
-    Tile t;
     const bool mine = bh < (int64_t)a.kv.kv_heads * a.kv.batch &&
                       tile_of<COLS>(a, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, t) &&
                       col < t.cols && t.range.count > n.pages;
-    const int parts = mine ? (t.range.count + n.pages - 1) / n.pages : 0;
-    const int64_t at = mine ? pair_of(a, t, col) * n.splits : 0;
+    return mine ? (t.range.count + n.pages - 1) / n.pages : 0;
+}
+
+__device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Tile &t, int col, int d4, f32x4 o, float l)
+{
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2 *>(output_of(a, t, col) + 4 * d4) =
+        uint2{pack_out(o.x, o.y, a.y_dtype), pack_out(o.z, o.w, a.y_dtype)};
+}
+
+// At most PARTS parts: D / 4 lanes a pair, each with 4 elements of every part.
+// All loads are on their way at once.
+template <int D, int COLS, int PARTS>
+__global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    constexpr int LANES = D / 4;
+    Tile t;
+    int col;
+    const int parts = parts_of<COLS>(a, n, (int64_t)blockIdx.x * (256 / LANES) + (int)threadIdx.x / LANES, t, col);
+    if (parts == 0)
+        return;
+    const int d4 = (int)threadIdx.x % LANES;
+    const int64_t at = pair_of(a, t, col) * n.splits;
+    const float2 *stat = reinterpret_cast<const float2 *>(n.part_stat) + at;
+    const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * LANES + d4;
+    float2 ml[PARTS];  // maximum, sum
+    f32x4 v[PARTS];
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        ml[i] = stat[i < parts ? i : 0];
+        v[i] = part[(i < parts ? i : 0) * LANES];
+    }
+    float m = ml[0].x, l = 0.0f;
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i)
+        m = __builtin_fmaxf(m, ml[i].x);
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const float f = i >= parts || ml[i].y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml[i].x - m);  // 0: saw nothing
+        l += f == 0.0f ? 0.0f : ml[i].y * f;
+        o += f == 0.0f ? f32x4{0, 0, 0, 0} : v[i] * f;
+    }
+    write_joined(a, t, col, d4, o, l);
+}
+
+// Up to 256 parts: a workgroup per pair.  A part's factor is computed once, by
+// the lane of its number; then groups of D / 4 lanes add up the parts, 16 bytes a
+// lane.  A chain of three loads (lengths, statistics, parts): 4.6 us for 32 pairs
+// of 64 parts, the launch included.
+template <int D, int COLS>
+__global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    constexpr int GROUPS = 256 / (D / 4);
+    __shared__ float factor[kMaxSplits];
+    __shared__ f32x4 sums[GROUPS][D / 4];
+    __shared__ float wave_m[4], wave_l[4];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x;
+    Tile t;
+    int col;
+    const int parts = parts_of<COLS>(a, n, blockIdx.x, t, col);
+    if (parts == 0)
+        return;
+    const int64_t at = pair_of(a, t, col) * n.splits;
     float m = -__builtin_inff(), l = 0.0f;
     if (lane < parts) {
         m = n.part_stat[2 * (at + lane)];
         l = n.part_stat[2 * (at + lane) + 1];
     }
     float top = wave_max(m);
-    if constexpr (WAVES > 1) {
-        if (lane % 64 == 0)
-            wave_m[wave] = top;
-        __syncthreads();
+    if (lane % 64 == 0)
+        wave_m[wave] = top;
+    __syncthreads();
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            top = __builtin_fmaxf(top, wave_m[w]);
-    }
+    for (int w = 0; w < 4; ++w)
+        top = __builtin_fmaxf(top, wave_m[w]);
     const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);  // l 0: saw nothing
     l *= f;
-    if (lane < PARTS)
-        factor[pair][lane] = f;
+    factor[lane] = f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         l += __shfl_xor(l, d);
@@ -70,21 +117,19 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttentionArgs a, Kv4La
     const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * (D / 4) + d4;
 #pragma unroll 4
     for (int i = g; i < parts; i += GROUPS)
-        o += part[(int64_t)i * (D / 4)] * factor[pair][i];
-    sums[pair][g][d4] = o;
+        o += part[(int64_t)i * (D / 4)] * factor[i];
+    sums[g][d4] = o;
     __syncthreads();
-    if (g != 0 || !mine)
+    if (g != 0)
         return;
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i)
-        o += sums[pair][i][d4];
+        o += sums[i][d4];
     l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-        l += wave_l[pair * WAVES + w];
-    o *= l == 0.0f ? 0.0f : 1.0f / l;
-    *reinterpret_cast<uint2 *>(output_of(a, t, col) + 4 * d4) =
-        uint2{pack_out(o.x, o.y, a.y_dtype), pack_out(o.z, o.w, a.y_dtype)};
+    for (int w = 0; w < 4; ++w)
+        l += wave_l[w];
+    write_joined(a, t, col, d4, o, l);
 }
 
 // Columns of a (sequence, kv head) at most.
@@ -205,9 +250,12 @@ template <int D, int COLS>
 hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned pairs = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
+    constexpr unsigned PAIRS = 256 / (D / 4);
+    if (n.splits <= 4)
+        return kv4_launch(kv4_join_few_kernel<D, COLS, 4>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
     if (n.splits <= 16)
-        return kv4_launch(kv4_join_kernel<D, COLS, 1>, (pairs + 3) / 4, 256, stream, a, n);
-    return kv4_launch(kv4_join_kernel<D, COLS, 4>, pairs, 256, stream, a, n);
+        return kv4_launch(kv4_join_few_kernel<D, COLS, 16>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
+    return kv4_launch(kv4_join_many_kernel<D, COLS>, pairs, 256, stream, a, n);
 }
 
 template <int D>
