@@ -155,22 +155,69 @@ int64_t units_of(const Kv4AttentionArgs &a, int cols)
     return tiles_of(a, cols) * (int64_t)a.kv.kv_heads * a.kv.batch;
 }
 
-// Columns of the tiles, by sizes (measured; G = 4, 8 kv heads of 128):
-//   the few-row kernel keeps up to 64 columns (64 columns, 8 sequences of 16384
-//   tokens: 108 us against 104), and while all its tiles see no more than 24576
-//   pages together (128 columns over 4096 tokens, 1 / 4 / 8 sequences: 17 / 27 /
-//   49 us against 22 / 33 / 48; 512 columns over 1024, 4 / 8 sequences: 29 / 49
-//   against 38 / 39): the other one spends 2 us a page on a tile of any fill;
-//   then 128 columns, two workgroups a compute unit, or, for one long sequence,
-//   256 and one: half the unpacking per column (2048 rows over 16384 tokens
-//   619 -> 585 us, 4096 of 4096 186 -> 179), but coarser where tiles end at
-//   different times (ragged prompts 219 -> 234, 8000 rows with a window of 1024
-//   205 -> 226).
+// Pages that a tile sees on average: a prompt's rows see what lies before them.
+double mean_pages(const Kv4AttentionArgs &a, int cols)
+{
+    const double mean = (a.kv.max_kv_len - 0.5 * a.kv.max_rows) / kPageTokens + 0.5, most = (double)most_pages(a, cols);
+    return mean < most ? mean : most;
+}
+
+// Times in us, fitted to calls of 64 to 4096 rows over 256 to 16384 tokens, 2 to 8
+// kv heads, G 1 to 7, within about 15 % each.
+//
+// The few-row kernel: a tile costs its beginning and its pages.
+double few_rows_time(const Kv4AttentionArgs &a)
+{
+    return 8 + (a.kv.head_dim == 64 ? 0.57 : 1.0) * (double)units_of(a, kFewCols) *
+                   (0.0068 + 0.00104 * mean_pages(a, kFewCols));
+}
+
+// The other one, 128 columns, a tile's pages in `splits` chunks: beginnings, of
+// which 512 run at a time; then the longest chunk, 1.85 us a page of 128 elements
+// for a workgroup alone on its compute unit and 2.1 for one of two, or all pages
+// at 2.4 us with 512 at work and what the longest tile has over the mean; then
+// the parts' way through memory and the second launch.
+double many_rows_time(const Kv4AttentionArgs &a, int64_t splits)
+{
+    const double units = (double)units_of(a, 128), pages = (double)most_pages(a, 128), mean = mean_pages(a, 128);
+    const double rounds = units * splits / 512;
+    const double longest = (rounds > 0.5 ? 2.1 : 1.85) * pages / splits;
+    const double all = units * mean * 2.4 / 512 + 1.8 * (pages - mean) / splits;
+    const double join = splits < 2 ? 0 : 4 + units * 128 * splits * a.kv.head_dim * 8 / 5e6;
+    return 3 + 5 * (rounds > 1 ? rounds : 1) + (a.kv.head_dim == 64 ? 0.7 : 1.0) * (longest > all ? longest : all) + join;
+}
+
+// Chunks of a tile of 128 columns: as many as make the call shortest, of 4 pages
+// and more; as many as run at once, or a half, a quarter of that, which fills the
+// compute units evenly.  (4096 rows, 448 tiles of 64 pages: whole 97
+// us, halved 125; 512 rows over 4096, 128 tiles of 64: whole 117, in four 69; 128
+// over 16384, 32 of 256: 8 chunks 75, 16 72.)
+int64_t many_rows_splits(const Kv4AttentionArgs &a)
+{
+    const int64_t units = units_of(a, 128), pages = most_pages(a, 128);
+    int64_t best = 1, most = 512 / units;
+    most = most < pages / 4 ? most : pages / 4;
+    most = most < kMaxSplits ? most : kMaxSplits;
+    for (int64_t s = most; s >= 2; s /= 2)
+        if (many_rows_time(a, s) < many_rows_time(a, best))
+            best = s;
+    return best;
+}
+
+// Columns of the tiles.  Up to 64 columns take the few-row kernel: it is bound by
+// the pages' bytes there.  Past that the kernel that the estimates above prefer
+// (prompts of 1 x 512 / 2 x 512 / 4 x 512 rows, 8 kv heads of 128, G 4: 17 / 30 /
+// 51 us against 24 / 26 / 31; of 2 x 1024 and 4 x 1024, 2 heads of 64, G 7: 23 /
+// 40 against 29 / 31; 2048 rows with a window of 256: 54 against 30).
+// One long sequence takes 256 columns, one workgroup a compute unit: half the
+// unpacking per column (2048 rows over 16384 tokens 619 -> 585 us, 4096 of 4096
+// 186 -> 179), but coarser where tiles end at different times (ragged prompts 219
+// -> 234, 8000 rows with a window of 1024 205 -> 226).
 int columns_of(const Kv4AttentionArgs &a)
 {
     if (a.tiles)
         return a.tiles;
-    if (most_columns(a) <= 64 || units_of(a, kFewCols) * most_pages(a, kFewCols) <= 24576)
+    if (most_columns(a) <= 64 || few_rows_time(a) <= many_rows_time(a, many_rows_splits(a)))
         return kFewCols;
     const int64_t units = units_of(a, 256);
     return a.kv.batch == 1 && a.window == 0 && units >= 128 && units <= 512 && most_pages(a, 256) >= 64 ? 256 : 128;
@@ -212,17 +259,9 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
         chunk = chunk < least ? least : chunk;
         n.pages = (int)chunk;
     } else {
-        // Two workgroups a compute unit (one of 256 columns) as long as a chunk
-        // keeps 16 pages, one down to 4 (128 rows over 16384 tokens, 32 tiles: 16
-        // chunks 72 us, 8 75; 8 sequences of 1024, 256 tiles of 16 pages: whole 39
-        // us, halved 57).
-        auto chunks = [&](int64_t wanted, int64_t least) {
-            const int64_t by_units = (wanted + units - 1) / units, by_pages = (pages + least - 1) / least;
-            return by_units < by_pages ? by_units : by_pages;
-        };
-        const int64_t two = chunks(n.cols == 256 ? 256 : 512, 16), one = chunks(256, 4);
-        int64_t splits = two > one ? two : one;
-        splits = splits < kMaxSplits ? splits : kMaxSplits;
+        // 256 columns: one workgroup a compute unit, chunks of 16 pages and more
+        const int64_t most = 256 / units < pages / 16 ? 256 / units : pages / 16;
+        const int64_t splits = n.cols == 128 ? many_rows_splits(a) : (most < kMaxSplits ? most : kMaxSplits);
         if (splits < 2)
             return n;
         n.pages = (int)((pages + splits - 1) / splits);
@@ -253,7 +292,7 @@ hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_
     constexpr unsigned PAIRS = 256 / (D / 4);
     if (n.splits <= 4)
         return kv4_launch(kv4_join_few_kernel<D, COLS, 4>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
-    if (n.splits <= 16)
+    if (n.splits <= 16 && pairs >= 2048)
         return kv4_launch(kv4_join_few_kernel<D, COLS, 16>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
     return kv4_launch(kv4_join_many_kernel<D, COLS>, pairs, 256, stream, a, n);
 }
