@@ -38,7 +38,8 @@ __device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Ti
 }
 
 // At most PARTS parts: D / 4 lanes a pair, each with 4 elements of every part.
-// All loads are on their way at once.
+// All loads are on their way at once: a chain of two (lengths, then statistics
+// and parts), 2.9 us for 32 pairs of 4 parts, 4.6 for 2048, the launch included.
 template <int D, int COLS, int PARTS>
 __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
@@ -290,6 +291,9 @@ hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_
 {
     const unsigned pairs = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
     constexpr unsigned PAIRS = 256 / (D / 4);
+    // 5 to 16 parts: a workgroup per pair while there are few pairs (256 of 16
+    // parts: the call 16.3 us, 17.0 by lanes; 4096 of 16 and 8192 of 8: 75 and 125
+    // us, 71 and 114 by lanes)
     if (n.splits <= 4)
         return kv4_launch(kv4_join_few_kernel<D, COLS, 4>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
     if (n.splits <= 16 && pairs >= 2048)
