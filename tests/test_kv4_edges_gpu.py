@@ -1,0 +1,164 @@
+"""The 4-bit key/value cache where its calls meet their limits: the joins of
+split caches (every one of them, with pairs of none, one and all parts, and
+with NaN in a part), workspaces smaller than asked for, finite values of any
+size where a row may not look, values and queries at the ends of bf16's range,
+rows of one tile that are far apart, and launches past 2^24 workgroups."""
+import numpy as np
+import pytest
+
+import w4a8_quantized_linear_amd as cider
+from tests import gpu_util as gu
+from tests import kv4_reference as ref
+from tests.test_kv4_gpu import Setup, attend, compare, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    assert cider.cider_is_available(), "libcider.so reports no usable gfx950 device"
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    gu.announce(request.node.nodeid)
+    yield
+    cider.cider_kv4_set_tiles(0)
+
+
+# ---------------------------------------------------------------- joins
+
+# (tiles, sequences, rows of each, kv heads, query heads, bound on the lengths, parts, pairs): the parts and pairs
+# choose the join: up to 4 parts, up to 16 with 2048 pairs and more, any number
+JOINS = {
+    "few columns, 4 parts": (0, 64, 1, 2, 4, 8192, 4, 256),
+    "few columns, 10 parts": (0, 64, 1, 2, 32, 20480, 10, 2048),
+    "few columns, 8 parts of few pairs": (0, 4, 1, 2, 4, 2048, 8, 16),
+    "few columns, 32 parts": (0, 1, 1, 2, 4, 8192, 32, 4),
+    "128 columns, up to 4 parts": (128, 1, 64, 1, 2, 1024, (2, 4), 128),
+    "128 columns, up to 16 parts": (128, 1, 64, 8, 32, 4096, (5, 16), 2048),
+    "128 columns, many parts": (128, 1, 64, 1, 2, 8192, (5, 128), 128),
+    "256 columns, 4 parts": (256, 1, 64, 1, 4, 4096, 4, 256),
+    "256 columns, 8 parts": (256, 1, 128, 4, 16, 8192, 8, 2048),
+    "256 columns, 8 parts of few pairs": (256, 1, 64, 1, 4, 8192, 8, 256),
+}
+
+
+def join_batch(name, D, gs, lens, seed=0):
+    """The setup and batch of a join's case; how many parts and pages a part the call takes.  The workspace holds
+    4 D + 8 bytes for every row, query head and part, each kind rounded up to 256."""
+    tiles, batch, rows, H, HQ, bound, parts, pairs = JOINS[name]
+    cider.cider_kv4_set_tiles(tiles)
+    lens = (list(lens) + [5] * batch)[:batch]
+    s = Setup(lens, [rows] * batch, H, D, gs, seed=seed, garbage="nan")
+    pages = bound // 64
+    table = np.full((batch, pages), 2 ** 31 - 1, np.int32)
+    width = min(pages, s.table.shape[1])
+    table[:, :width] = s.table[:, :width]
+    s.table, s.max_pages = table, pages
+    want = parts if isinstance(parts, tuple) else (parts, parts)
+
+    def batch_of():
+        b = s.to_device(max_kv_len=bound)
+        n = cider.cider_kv4_attention_workspace_bytes(b, HQ, 0, 0)
+        got = n // (s.rows * HQ * (4 * D + 8))
+        assert rows * HQ * batch == pairs and want[0] <= got <= want[1], (got, want)
+        return b, -(-pages // got)
+
+    return s, batch_of, HQ
+
+
+@pytest.mark.parametrize("D,gs", [(64, 64), (128, 64)])
+@pytest.mark.parametrize("name", JOINS)
+def test_joins(name, D, gs):
+    """Sequences that end in their first, a middle and the last part, one token into a part, and without tokens."""
+    bound, rows = JOINS[name][5], JOINS[name][2]
+    lens = [bound] if rows > 1 else [bound // 2 + 1, bound, 0, 1, 64, bound // 4, bound // 4 + 1, bound - 70]
+    s, batch_of, HQ = join_batch(name, D, gs, lens)
+    dtype = D // 64 % 2
+    ref.fill(s.cache, s.table, s.lens, *s.values(dtype))
+    b, _ = batch_of()
+    x = s.rng.standard_normal((s.rows, HQ, D))
+    q = ref.to_bits(x, dtype)
+    scale = 1 / np.sqrt(D)
+    got = attend(s, b, q, dtype, dtype, HQ, scale)
+    if rows == 1:
+        compare(s, got, reference(s, q, dtype, HQ, scale), dtype)
+        return
+    qf = ref.to_f64(q, dtype)
+    step = 2.0 ** -8 if dtype == 1 else 2.0 ** -11
+    for i in (0, 1, 31, 62, rows - 1):   # (the reference would take minutes for every row)
+        y, bound_y = ref.attention(s.cache, s.table[0], s.lens[0] - rows + i + 1, qf[i:i + 1], HQ // s.H, scale, 0, 0)
+        err = np.abs(ref.to_f64(got[i:i + 1], dtype) - y)
+        assert (err <= bound_y + step * (np.abs(y) + bound_y) + 2.0 ** -25).all(), (i, err.max())
+
+
+def spoil(s, t, which, bits, heads=slice(None)):
+    """Every scale of K (0) or V (1) of token t of sequence 0 becomes the fp32 number of that pattern."""
+    D, gs = s.D, s.gs
+    block = s.cache.data[s.table[0, t // 64]]
+    for g in range(D // gs):
+        at = 64 * D + which * 256 * (D // gs) + 4 * (g * 64 + t % 64)
+        block[heads, at:at + 4] = np.array([bits], np.uint32).view(np.uint8)
+
+
+@pytest.mark.parametrize("which", ["K", "V", "V, weight vanishes"])
+@pytest.mark.parametrize("name", JOINS)
+def test_nan_in_a_part_of_its_own_reaches_the_row(name, which):
+    """The newest token alone in its part: NaN keys there leave the part without a maximum, and NaN values count
+    even where the part's factor is 0."""
+    D, gs = 128, 64
+    rows = JOINS[name][2]
+    s, batch_of, HQ = join_batch(name, D, gs, [3])   # for the size of a part
+    _, pages = batch_of()
+    kv = (2 if JOINS[name][5] >= 3 * 64 * pages else 1) * pages * 64 + 1
+    s, batch_of, HQ = join_batch(name, D, gs, [kv])
+    k, v = s.values(0)
+    x = s.rng.standard_normal((s.rows, HQ, D))
+    if which == "V, weight vanishes":
+        x = np.abs(x) + 0.5
+        k[0][0] = 40.0    # the first token takes all the weight
+        k[0][-1] = -40.0
+    ref.fill(s.cache, s.table, s.lens, k, v)
+    q = ref.to_bits(x, 0)
+    clean = attend(s, batch_of()[0], q, 0, 0, HQ, 0.1)
+    spoil(s, kv - 1, 0 if which == "K" else 1, 0x7FC00000, heads=slice(0, 1))
+    got = attend(s, batch_of()[0], q, 0, 0, HQ, 0.1)
+    G, last = HQ // s.H, rows - 1
+    assert np.isnan(ref.to_f64(got[last, :G], 0)).all()
+    got[last, :G] = clean[last, :G]
+    assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("name", JOINS)
+def test_workspace_smaller_than_asked_for(name):
+    """Fewer, longer parts; nothing behind the bytes that were given is written."""
+    import torch
+    D, gs = 128, 128
+    bound, rows = JOINS[name][5], JOINS[name][2]
+    s, batch_of, HQ = join_batch(name, D, gs, [min(bound, 3000), 700])
+    ref.fill(s.cache, s.table, s.lens, *s.values(1))
+    b, _ = batch_of()
+    q = ref.to_bits(s.rng.standard_normal((s.rows, HQ, D)), 1)
+    few = sorted({0, min(1, s.rows - 1), s.rows - 1})
+    qf = ref.to_f64(q, 1)
+    want = []
+    for i in few:
+        at = i if rows == 1 else 0
+        kv = s.lens[0] - rows + i + 1 if rows > 1 else s.lens[at]
+        want.append(ref.attention(s.cache, s.table[at], kv, qf[i:i + 1], HQ // s.H, 0.09, 0, 0))
+    full = cider.cider_kv4_attention_workspace_bytes(b, HQ, 0, 0)
+    qd = gu.bits_to_dev(q.reshape(s.rows, -1))
+    guard = 1 << 16
+    for nbytes in (full, full - 1, full // 2, full // 2 - 256, full // 4, full // 8, 300, 1):
+        ws = torch.full((full + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+        y = torch.full((s.rows, HQ * D), 99, dtype=torch.int16, device="cuda")
+        cider.cider_kv4_attention(b, qd, 1, HQ * D, HQ, 0.09, 0, 0, ws, nbytes, y, 1, HQ * D)
+        assert (ws[nbytes:] == 0xA5).all().item(), nbytes
+        got = ref.to_f64(gu.bits_to_host(y).reshape(s.rows, HQ, D), 1)
+        for i, (w, bound_y) in zip(few, want):
+            assert (np.abs(got[i] - w[0]) <= bound_y[0] + 2.0 ** -8 * (np.abs(w[0]) + bound_y[0])).all(), (nbytes, i)

@@ -67,9 +67,12 @@ __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, K
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        const float f = i >= parts || ml[i].y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml[i].x - m);  // 0: saw nothing
-        l += f == 0.0f ? 0.0f : ml[i].y * f;
-        o += f == 0.0f ? f32x4{0, 0, 0, 0} : v[i] * f;
+        // only what is not there or saw nothing (sum 0) stays out: NaN in a part is
+        // the result's NaN though its factor be 0
+        const bool there = i < parts && ml[i].y != 0.0f;
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - m);
+        l += there ? ml[i].y * f : 0.0f;
+        o += there ? v[i] * f : f32x4{0, 0, 0, 0};
     }
     write_joined(a, t, col, d4, o, l);
 }
