@@ -1,15 +1,14 @@
 """The 4-bit key/value cache where its calls meet their limits: the joins of
 split caches (every one of them, with pairs of none, one and all parts, and
-with NaN in a part), workspaces smaller than asked for, finite values of any
-size where a row may not look, values and queries at the ends of bf16's range,
-rows of one tile that are far apart, and launches past 2^24 workgroups."""
+with NaN in a part), workspaces smaller than asked for and finite values of any
+size where a row may not look."""
 import numpy as np
 import pytest
 
 import w4a8_quantized_linear_amd as cider
 from tests import gpu_util as gu
 from tests import kv4_reference as ref
-from tests.test_kv4_gpu import Setup, attend, compare, reference
+from tests.test_kv4_gpu import GEOMETRY, TILES, Setup, attend, compare, i32, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -162,3 +161,79 @@ def test_workspace_smaller_than_asked_for(name):
         got = ref.to_f64(gu.bits_to_host(y).reshape(s.rows, HQ, D), 1)
         for i, (w, bound_y) in zip(few, want):
             assert (np.abs(got[i] - w[0]) <= bound_y[0] + 2.0 ** -8 * (np.abs(w[0]) + bound_y[0])).all(), (nbytes, i)
+
+
+# ---------------------------------------------------------------- what a row may not see
+
+def bits_of(x):
+    return int(np.array([x], np.float32).view(np.uint32)[0])
+
+
+HUGE = [2.0 ** 24, 2.0 ** 40, 2.0 ** 100, 2.0 ** 120, float(np.finfo(np.float32).max)]
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("huge", HUGE)
+@pytest.mark.parametrize("rows,window,sinks", [(1, 50, 6), (2, 0, 0), (2, 50, 6), (5, 3, 0), (40, 0, 0), (40, 50, 6),
+                                               (100, 64, 70)])
+def test_finite_scales_that_a_row_may_not_see_change_nothing(rows, window, sinks, huge, tiles):
+    """Scales of any size behind the window, after the sinks and in front of a row, in pages that it does read:
+    the row's bits are those of a cache without them."""
+    cider.cider_kv4_set_tiles(tiles)
+    for dtype, (D, gs) in zip((0, 1, 1), GEOMETRY):
+        s = Setup([300], [rows], 2, D, gs, garbage="nan")
+        ref.fill(s.cache, s.table, s.lens, *s.values(dtype))
+        q = ref.to_bits(s.rng.standard_normal((s.rows, 6, D)), dtype)
+        clean = attend(s, s.to_device(), q, dtype, dtype, 6, 0.1, window, sinks)
+        plain = s.cache.data.copy()
+        for base in {0, rows - 1}:   # everything that the first row, or the last, may not see
+            hidden = ~ref.visible(300 - rows + base, 300, window, sinks)
+            bad = [t for t in (20, 200, 230, 262, 288, 299) if hidden[t]]
+            s.cache.data = plain.copy()
+            for t in bad:
+                for which in (0, 1):
+                    spoil(s, t, which, bits_of(huge))
+            got = attend(s, s.to_device(), q, dtype, dtype, 6, 0.1, window, sinks)
+            for i in range(rows):
+                if not ref.visible(300 - rows + i, 300, window, sinks)[bad].any():
+                    assert np.array_equal(got[i], clean[i]), (base, i)
+
+
+@pytest.mark.parametrize("tiles", TILES)
+def test_a_later_token_far_larger(tiles):
+    """Two rows, the second token's values 2^40 times the first's: the first row is the first token's values."""
+    import torch
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([2], [2], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        v[0][1] *= 2.0 ** 40
+        b = s.to_device()
+        kd, vd = (gu.bits_to_dev(ref.to_bits(x[0], 1).reshape(2, -1)) for x in (k, v))
+        cider.cider_kv4_append(b, kd, vd, 1, D, D)
+        back = torch.empty((2, 2, D), dtype=torch.int16, device="cuda")
+        cider.cider_kv4_read(b, back[0], back[1], 1, D, D)
+        q = ref.to_bits(s.rng.standard_normal((2, 1, D)), 1)
+        got = attend(s, b, q, 1, 1, 1, 0.1)
+        assert np.array_equal(got[0, 0], gu.bits_to_host(back[1])[0])
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("window,sinks,power", [(0, 0, 0.7), (5, 0, -0.7), (5, 0, 0.7), (9, 2, -0.5), (0, 0, -0.7)])
+def test_every_row_has_values_of_its_own_size(window, sinks, power, tiles):
+    """Values that grow or shrink by a power of two every token or two, whole prompts: no row may lose bits to what
+    another row of its tile sees.  (A head's halves apart too.)"""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([100, 61], [100, 7], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        for x in v:
+            x *= 2.0 ** np.floor(power * np.arange(len(x)))[:, None, None]
+            x[:, :, :D // 2] *= 2.0 ** np.floor(5 * np.sin(np.arange(len(x))))[:, None, None]
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        q = ref.to_bits(s.rng.standard_normal((s.rows, 3, D)), 1)
+        want = reference(s, q, 1, 3, 0.1, window, sinks)
+        got = ref.to_f64(attend(s, s.to_device(), q, 1, 1, 3, 0.1, window, sinks), 1)
+        for b, (y, bound) in enumerate(want):
+            err = np.abs(got[s.row_start[b]:s.row_start[b] + s.n[b]] - y)
+            assert (err <= bound + 2.0 ** -8 * (np.abs(y) + bound)).all(), (D, gs, b)

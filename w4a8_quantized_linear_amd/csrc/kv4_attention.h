@@ -179,6 +179,75 @@ __device__ __forceinline__ float operand_sum(half8 op, float sum)
     return sum;
 }
 
+// Exponents of V's scales.  Weights go to the matrix cores in fp16, times V's
+// scale and a power of two that puts the largest s_v that the column has seen
+// just under fp16's end; its outputs are in those units.  The exponent is the
+// column's own: a token that the column does not see (behind its window, in front
+// of its row) must not move it, or a large value there would flush the column's
+// weights.  Powers of two are exact, so a column's result has the same bits
+// whatever its neighbours see.  Most often all columns of a wavefront have seen
+// scales of one exponent, and the power of two goes into the scales, once a page;
+// where they stand apart every weight takes its column's difference.
+constexpr int kNoScale = -200;  // nothing seen; below the exponent of every fp32 number
+constexpr int kSpread = 200;    // columns are kept this close, so that every product is a normal number: one
+                                // that sees values 2^200 below another's of its wavefront loses bits
+
+// One group's exponents, the same in every lane; a column's own (2^own is above
+// every finite s_v that it has seen) is kept by the kernel.
+struct ScaleExponents {
+    int all;    // the columns' own, or the middle of them where they stand apart
+    int reach;  // the least of own: scales below 2^reach move nothing
+    bool same;  // every lane's own is `all`
+    bool apart; // columns that have seen a scale stand apart
+
+    __device__ __forceinline__ void clear()
+    {
+        all = kNoScale;
+        reach = -149;
+        same = true;
+        apart = false;
+    }
+
+    // A page's scales are below 2^top where the lane's column sees them; returns the
+    // column's new exponent.  valid: there is such a column.
+    __device__ __forceinline__ int raise(int own, int top, bool valid)
+    {
+        int now = top > own ? top : own;
+        const int first = __builtin_amdgcn_readfirstlane(now);
+        if (__all(!valid || now == first)) {
+            all = first;
+            reach = first < -149 ? -149 : first;
+            same = true;
+            apart = false;
+            return first;
+        }
+        const int hi = __builtin_amdgcn_readfirstlane((int)wave_max((float)(valid ? now : kNoScale)));
+        int lo = -__builtin_amdgcn_readfirstlane((int)wave_max(valid && now > kNoScale ? -(float)now : -1000.0f));
+        reach = -__builtin_amdgcn_readfirstlane((int)wave_max(valid ? -(float)now : -1000.0f));
+        lo = lo > hi ? hi : lo;
+        reach = reach > hi ? hi : reach;
+        if (lo < hi - kSpread)
+            lo = hi - kSpread;
+        now = !valid ? hi : (now > kNoScale && now < lo ? lo : now);
+        same = reach == hi;
+        apart = lo != hi;
+        all = (hi + lo) >> 1;
+        reach = reach < -149 ? -149 : reach;
+        return now;
+    }
+    // The same where `same` holds and every column sees the page's scales.
+    __device__ __forceinline__ int raise_all(int top)
+    {
+        top = __builtin_amdgcn_readfirstlane(top);
+        all = top > all ? top : all;
+        reach = all < -149 ? -149 : all;
+        return all;
+    }
+};
+// The power of two that a column's weights are short of when they are worked out
+// for all; a column that has seen no scale has no weights.
+__device__ __forceinline__ int scale_shift(int all, int own) { return own == kNoScale ? 0 : all - own; }
+
 // Masks.  A lane's tokens lie at offsets STRIDE (e / 4) + e % 4 from its first
 // one, which rises with e: those in front of an offset are the low bits of a
 // word, so a page's mask takes a few operations, not some for every token.
@@ -198,23 +267,65 @@ __device__ __forceinline__ uint32_t tokens_seen(int p, int at, int window, int s
         seen &= ~tokens_below<STRIDE>(p - window + 1 - at) | tokens_below<STRIDE>(sinks - at);
     return seen;
 }
+__device__ __forceinline__ uint32_t seen_bits(uint32_t seen, int e) { return (uint32_t)((int32_t)(seen << (31 - e)) >> 31); }
 // A score, or minus infinity where bit e of the mask is 0.
 __device__ __forceinline__ float seen_score(float s, uint32_t seen, int e)
 {
-    const uint32_t keep = (uint32_t)((int32_t)(seen << (31 - e)) >> 31);
+    const uint32_t keep = seen_bits(seen, e);
     return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, s) & keep) | (0xFF800000u & ~keep));
+}
+// The largest of 16 N tokens' scales (a row of lanes holds 16), 0 for those whose
+// bit is 0: the scales go round the row, the lane's bits with them.  A loop, not 16
+// copies: it is taken rarely, and its mere length would cost the code around it
+// 5 % (registers, instruction fetches).
+template <int N>
+__device__ __forceinline__ float seen_largest(const float (&scales)[N], uint32_t seen, int lane)
+{
+    float top = 0.0f, s[N];
+    uint32_t bits[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        s[t] = scales[t];
+        bits[t] = (seen >> 16 * t & 0xFFFFu) * 0x10001u >> lane % 16;
+    }
+#pragma unroll 1
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                const uint32_t u = __builtin_bit_cast(uint32_t, s[t]) & seen_bits(bits[t], i);
+                top = __builtin_fmaxf(top, __builtin_bit_cast(float, u));
+                s[t] = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, s[t]), 0x12F, 0xF, 0xF, true));
+            }
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            bits[t] >>= 4;
+    }
+    return top;
+}
+__device__ __forceinline__ int scale_exponent(float largest)
+{
+    return largest > 0.0f ? __builtin_amdgcn_frexp_expf(largest) : kNoScale;
 }
 
 // The pages that a tile of columns sees: [0, sink_pages) and [first, end).
 struct PageRange {
     int sink_pages, first, count;
+    int lead;  // pages before the first one that lies inside every column's window
     __device__ __forceinline__ int at(int i) const { return i < sink_pages ? i : first + i - sink_pages; }
+    // From there on, the ones before it last: what every column sees comes first.
+    __device__ __forceinline__ int at_turned(int i) const
+    {
+        i += lead;
+        return at(i < count ? i : i - count);
+    }
 };
 
 // Columns at positions p_lo .. p_hi; count 0 where p_hi < 0.
 __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, int sinks)
 {
-    PageRange r = {0, 0, 0};
+    PageRange r = {0, 0, 0, 0};
     if (p_hi < 0)
         return r;
     const int end = p_hi / kPageTokens + 1;
@@ -224,6 +335,10 @@ __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, 
     const int kept_pages = (kept + kPageTokens - 1) / kPageTokens;
     r.sink_pages = kept_pages < r.first ? kept_pages : r.first;
     r.count = r.sink_pages + end - r.first;
+    if (window > 0 && p_hi >= window) {
+        const int lead = r.sink_pages + (p_hi - window) / kPageTokens + 1 - r.first;
+        r.lead = lead < r.count ? lead : 0;
+    }
     return r;
 }
 
@@ -252,6 +367,18 @@ __device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, int b, int h,
     t.p_hi = first + last / t.G;
     t.range = pages_seen(t.p_lo, t.p_hi, a.window, a.sinks);
     return true;
+}
+
+// Whether some column of the tile sees a token.
+__device__ __forceinline__ bool tile_sees(const Kv4AttentionArgs &a, const Tile &t, int token)
+{
+    return token <= t.p_hi && (a.window == 0 || token > t.p_lo - a.window || token < a.sinks);
+}
+
+// Whether every one does.
+__device__ __forceinline__ bool tile_shares(const Kv4AttentionArgs &a, const Tile &t, int token)
+{
+    return token <= t.p_lo && (a.window == 0 || token > t.p_hi - a.window || token < a.sinks);
 }
 
 // Where column `col` of a tile's result goes: 16-bit outputs, or one split's

@@ -16,16 +16,18 @@
 //
 // Rounding.  q is scaled per row by a power of two to a largest magnitude in
 // [2^13, 2^14) and held in fp16: exact unless an element is below 2^-23 of the
-// row's largest, then off by at most 2^-38 of it.  The weights e^(S - m) s_v
-// are fp32 rounded once to fp16 after scaling by a power of two that puts the
-// largest s_v seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the
-// largest possible weight.  That error is as large as an fp16 output's own
-// rounding (and far below a bf16 one's), so for fp16 outputs the weights go in
-// as two halves, hi + lo, 22 bits: twice the products of V and some operations
-// a weight, which cost little where the cache's bytes bound the call and 6 %
-// elsewhere (batch of 64 over up to 8192 tokens: 72.5 us without, 77.5 with),
-// and take the error against 64 bits from 2.9e-4 to 2.1e-4, the output's
-// rounding alone.  Scores, maxima, sums and outputs are fp32.
+// row's largest, then off by at most 2^-34 of it (operands of the odd nibbles are
+// stored divided by 16).  The weights e^(S - m) s_v are fp32 rounded once to fp16
+// after scaling by a power of two that puts the largest s_v that the column has
+// seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the largest possible
+// weight, 2^-24 for the tokens of odd nibbles.  What the column does not see has no
+// part in that power of two (ScaleExponents).  That error is as large as an fp16
+// output's own rounding (and far below a bf16 one's), so for fp16 outputs the
+// weights go in as two halves, hi + lo, 22 bits: twice the products of V and some
+// operations a weight, which cost little where the cache's bytes bound the call and
+// 6 % elsewhere (batch of 64 over up to 8192 tokens: 72.5 us without, 77.5 with),
+// and take the error against 64 bits from 2.9e-4 to 2.1e-4, the output's rounding
+// alone.  Scores, maxima, sums and outputs are fp32.
 //
 // Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
 // head, tokens the rows of S^T = K Q^T (v_mfma_f32_16x16x32_f16), so lane
@@ -135,8 +137,9 @@ __device__ __forceinline__ half8 halves(uint32_t w) { return __builtin_bit_cast(
 template <int D, int GS>
 struct State {
     f32x4 acc[D / 16], off[D / 64];
-    float m, l;          // m in units of log2
-    int v_exp[D / GS];   // 2^v_exp is above every finite s_v seen
+    float m, l;  // m in units of log2
+    int own[D / GS];  // exponents of V's scales, the column's and the wavefront's
+    ScaleExponents exps[D / GS];
     half8 q[D / 32];
     float zero[D / GS], qmul;
 };
@@ -173,27 +176,90 @@ __device__ __forceinline__ float largest(const float (&s)[4][4])
     return top;
 }
 
+// The outputs' products of tokens 32 B .. 32 B + 31 and elements 64 y .. 64 y + 63.
+template <int D, int GS, int PARTS>
+__device__ __forceinline__ void output_products(State<D, GS> &st, uint4 codes, int y, const uint32_t (&w)[PARTS][4])
+{
+    const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
+    half8 weights[PARTS];
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+        weights[i] = __builtin_bit_cast(half8, uint4{w[i][0], w[i][1], w[i][2], w[i][3]});
+    const uint32_t u[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const half8 code = halves(u[x]);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+            st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(code, weights[i], st.acc[4 * y + x], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+        st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights[i], st.off[y], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Two weights rounded to fp16, as one part or as hi + lo.
+template <int PARTS>
+__device__ __forceinline__ void round_weights(float x, float y, int e, uint32_t (&w)[PARTS][4])
+{
+    if constexpr (PARTS == 2)  // kept from being computed twice, by the subtraction below too
+        asm("" : "+v"(x), "+v"(y));
+    w[0][e] = pack2<OUT_F16>(x, y);
+    if constexpr (PARTS == 2) {
+        const half2_t hi = __builtin_bit_cast(half2_t, w[0][e]);
+        w[1][e] = pack2<OUT_F16>(x - (float)hi.x, y - (float)hi.y);
+    }
+}
+
 // Their weights, and the outputs.  top: the largest score; seen: bit 4 t + e
-// set where the lane's column sees the token (read where the page is not
-// whole); last: the last token of the page that any column of the tile sees
-// (63 and more: all).
-template <int D, int GS, bool FINE>
+// set where the lane's column sees the token (read where the page is not whole);
+// whole: every column sees every token; held, common: some column of the tile,
+// or every one, sees the token of the lane's scales; valid: the lane has a column.
+// ONE: the tile is one row.
+template <int D, int GS, bool FINE, bool ONE>
 __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
                                              float (&s)[4][4], float top, bool whole, uint32_t seen,
-                                             int last)
+                                             bool held, bool common, bool valid)
 {
-    constexpr int NG = D / GS, NT = D / 16;
+    constexpr int NG = D / GS, NT = D / 16, PARTS = FINE ? 2 : 1;
     const float inf = __builtin_inff();
-    // V's scales; the weights' exponents move up first
+    // V's scales; the columns' exponents move up first
     float vs[NG];
+    bool above = false, apart = false;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const float v = scale_token(lane) <= last ? pg.vs[g] : 0.0f;
-        if (__any(v >= ldexp_f(1.0f, st.v_exp[g]) && v < inf)) {
-            const int e = __builtin_amdgcn_readfirstlane(
-                __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
-            const float f = ldexp_f(1.0f, st.v_exp[g] - e);
-            st.v_exp[g] = e;
+        vs[g] = held ? pg.vs[g] : 0.0f;
+        above |= vs[g] >= ldexp_f(1.0f, st.exps[g].reach) && vs[g] < inf;
+    }
+    if (__any(above)) {
+        float v[NG];
+        int now[NG];
+        bool alike = true;  // and the exponents were
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            v[g] = vs[g] < inf ? vs[g] : 0.0f;
+            now[g] = __builtin_amdgcn_readfirstlane(scale_exponent(wave_max(v[g])));
+            alike &= st.exps[g].same;
+        }
+        if (!ONE && !whole) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                alike &= __builtin_amdgcn_readfirstlane(scale_exponent(wave_max(common ? v[g] : 0.0f))) == now[g];
+        }
+        if (ONE || __builtin_expect(alike, 1)) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                now[g] = st.exps[g].raise_all(now[g]);
+        } else {
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                now[g] = st.exps[g].raise(st.own[g], scale_exponent(column_max(seen_largest({v[g]}, seen, lane))), valid);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float f = ldexp_f(1.0f, st.own[g] - now[g]);
+            st.own[g] = now[g];
 #pragma unroll
             for (int x = g * GS / 16; x < (g + 1) * GS / 16; ++x)
                 st.acc[x] *= f;
@@ -201,8 +267,12 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
             for (int y = g * GS / 64; y < (g + 1) * GS / 64; ++y)
                 st.off[y] *= f;
         }
-        // the 16 times larger codes belong to tokens 1 and 3 of each 4
-        vs[g] = ldexp_f(v, 14 - st.v_exp[g] - (lane & 1 ? 4 : 0));
+    }
+    // the 16 times larger codes belong to tokens 1 and 3 of each 4
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        vs[g] = ldexp_f(vs[g], 14 - st.exps[g].all - (lane & 1 ? 4 : 0));
+        apart |= !ONE && st.exps[g].apart;
     }
     const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.qmul);
     const float m_sub = m_new == -inf ? 0.0f : m_new;
@@ -223,25 +293,23 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         x = __builtin_amdgcn_exp2f(__builtin_fmaf(x, st.qmul, -m_sub));
         st.l += x;
     }
-    const half8 offset = __builtin_bit_cast(half8, uint4{kOffset, kOffset16, kOffset, kOffset16});
-    constexpr int PARTS = FINE ? 2 : 1;  // hi, lo
     uint32_t w[NG][2][PARTS][4];
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g) {
+        if (__builtin_expect(apart, 0)) {
+            const int by = scale_shift(st.exps[g].all, st.own[g]) -
+                           (g == 0 ? 0 : scale_shift(st.exps[g - 1].all, st.own[g - 1]));
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+                s[n / 4][n % 4] = ldexp_f(s[n / 4][n % 4], by);
+        }
 #pragma unroll
         for (int B = 0; B < 2; ++B)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = scaled(s[2 * B][e], vs[g], 8 * B + e);
-                float y = scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e);
-                if constexpr (FINE)  // kept from being computed twice, by the subtraction below too
-                    asm("" : "+v"(x), "+v"(y));
-                w[g][B][0][e] = pack2<OUT_F16>(x, y);
-                if constexpr (FINE) {
-                    const half2_t hi = __builtin_bit_cast(half2_t, w[g][B][0][e]);
-                    w[g][B][1][e] = pack2<OUT_F16>(x - (float)hi.x, y - (float)hi.y);
-                }
-            }
+            for (int e = 0; e < 4; ++e)
+                round_weights<PARTS>(scaled(s[2 * B][e], vs[g], 8 * B + e), scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e),
+                                     e, w[g][B]);
+    }
     // a hidden token's weight is 0, and times a scale that is not finite it would
     // not stay so
     bool odd = false;
@@ -265,30 +333,18 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
     for (int B = 0; B < 2; ++B)
 #pragma unroll
-        for (int y = 0; y < D / 64; ++y) {
-            half8 weights[PARTS];
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                const uint32_t(&o)[4] = w[y * 64 / GS][B][i];
-                weights[i] = __builtin_bit_cast(half8, uint4{o[0], o[1], o[2], o[3]});
-            }
-            const uint32_t u[4] = {pg.v[B][y].x, pg.v[B][y].y, pg.v[B][y].z, pg.v[B][y].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const half8 code = halves(u[x]);
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i)
-                    st.acc[4 * y + x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(code, weights[i], st.acc[4 * y + x], 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i)
-                st.off[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset, weights[i], st.off[y], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int y = 0; y < D / 64; ++y)
+            output_products<D, GS, PARTS>(st, pg.v[B][y], y, w[y * 64 / GS][B]);
 }
 
-template <int D, int GS, int WAVES, bool FINE, bool ONCE>
-__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+// ONE: every sequence has one row at most, so a tile's columns see the same tokens
+// and the exponents of V's scales are one for all of them: none of what keeps them
+// apart is in the way of a decoding step (64 sequences of up to 8192 tokens: 98 us
+// with it, for its registers, 71 without).  With more rows 2 wavefronts a SIMD are
+// enough to be given registers for (64 x 2 rows over 4000 tokens 57.7 us, 62 with 3
+// and what spills).
+template <int D, int GS, int WAVES, bool FINE, bool ONCE, bool ONE>
+__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int NM = D / 32;   // score products per 16 tokens
     constexpr int NG = D / GS;   // scales per token
@@ -367,7 +423,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             st.zero[g] = column_sum(st.zero[g]) * -0x1p-21f;
-            st.v_exp[g] = -100;
+            st.exps[g].clear();
+            st.own[g] = kNoScale;
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -402,7 +459,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
                 s[e / 4][e % 4] = seen_score(s[e / 4][e % 4], seen, e);
             top = largest(s);
         }
-        page_outputs<D, GS, FINE>(st, pg, lane, s, top, whole, seen, there ? t.p_hi - t0 : -1);
+        const bool held = whole || (there && tile_sees(a, t, t0 + scale_token(lane)));
+        const bool common = whole || tile_shares(a, t, t0 + scale_token(lane));
+        page_outputs<D, GS, FINE, ONE>(st, pg, lane, s, top, whole, seen, held, common, valid && p >= 0);
         load_v<D, GS, ONCE>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;
@@ -412,7 +471,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
     st.l = column_sum(st.l);
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-        const f32x4 o = (st.acc[x] + st.off[x / 4]) * ldexp_f(1.0f, st.v_exp[x * 16 / GS] + 10);
+        const f32x4 o = (st.acc[x] + st.off[x / 4]) * ldexp_f(1.0f, st.own[x * 16 / GS] + 10);
         *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) = o;
     }
     if (j == 0) {
@@ -466,16 +525,22 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : 3) void kv4_few
 
 }  // namespace
 
-template <int WAVES, bool FINE, bool ONCE>
+template <int WAVES, bool FINE, bool ONCE, bool ONE>
 static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
                           (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
-        return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
+        return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
     if (a.kv.group_size == 64)
-        return kv4_launch(kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
-    return kv4_launch(kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE>, grid, 64 * WAVES, stream, a, n);
+        return kv4_launch(kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
+    return kv4_launch(kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
+}
+
+template <int WAVES, bool FINE, bool ONCE>
+static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    return a.kv.max_rows == 1 ? launch<WAVES, FINE, ONCE, true>(a, n, stream) : launch<WAVES, FINE, ONCE, false>(a, n, stream);
 }
 
 template <int WAVES>

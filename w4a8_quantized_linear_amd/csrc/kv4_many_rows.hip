@@ -21,11 +21,12 @@
 //
 // Rounding.  q is scaled by one power of two for the whole tile (its largest
 // magnitude to [2^13, 2^14)), so the score's factor goes into K's scales once a
-// page; what is below 2^-23 of the tile's largest is off by at most 2^-38 of
-// it.  The weights are rounded once to fp16, 11 significant bits down to 2^-25
-// of the largest: the error against 64 bits is 2.9e-4 with fp16 outputs, 2.1e-4
-// of it the output's rounding.  (Two halves, as for few rows, would double the
-// second product, which is not hidden here.)
+// page; what is below 2^-23 of the tile's largest is off by at most 2^-34 of it
+// (operands of the odd nibbles are stored divided by 16).  The weights are rounded
+// once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for the
+// tokens of odd nibbles: the error against 64 bits is 2.9e-4 with fp16 outputs,
+// 2.1e-4 of it the output's rounding.  (Two halves, as for few rows, would double
+// the second product, which is not hidden here.)
 //
 // What bounds it: the vector units.  A wavefront takes about 365 vector
 // instructions a page (D 128 in groups of 64), which cost 4.4 cycles of its SIMD
@@ -47,13 +48,16 @@ namespace {
 constexpr int kWaveCols = 32;  // one matrix operand
 constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw 32-bit buffer
 
-// The running maximum may lie this far (in units of log2) below the true one
-// before it is moved: weights reach 2^kSlack, and the outputs are rescaled in
-// few pages instead of nearly all (with 32 columns some column has a new
-// maximum in most pages).  kTop leaves fp16 the room: weights times V's scale
-// stay below 2^(kTop + kSlack) = 2^14.
-constexpr float kSlack = 3.0f;
+// The running maximum may lie kSlack (in units of log2) below the true one before
+// it is moved, and the exponent of V's scales kLag: the outputs are rescaled in few
+// pages instead of nearly all (with 32 columns some column has a new maximum in
+// most pages).  A column's moves are its own, whatever its neighbours see.  kTop
+// leaves fp16 the room: weights times V's scale stay below 2^(kTop + kSlack + kLag),
+// 61147.
+constexpr float kSlack = 2.9f;
+constexpr int kLag = 2;
 constexpr int kTop = 11;
+constexpr int kLeastExp = -126;  // of scales that are not normal numbers
 
 // One page's K and V in LDS.  They are used one step apart (the scores of page
 // i + 1 are computed while page i's weights are), so each has its own pair of
@@ -120,7 +124,23 @@ __device__ __forceinline__ f32x16 mfma(uint4 x, half8 y, f32x16 z)
 }
 
 template <int D, int GS, int COLS>
-__global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+struct Lds {
+    PageK<D, GS> page_k[2];
+    PageV<D, GS> page_v[2];
+    float tile_top[COLS / kWaveCols];
+    int own[D / GS][COLS];  // where columns stand apart: the exponents of V's scales
+    int stand_apart[2];     // by a page's number: some wavefront's columns do
+};
+
+// One tile's share of pages.  All columns of a wavefront have seen V's scales of
+// one exponent, and the power of two is staged with them; where a page that only
+// some of them see has larger ones than all before it, they stand apart, and every
+// weight takes its column's difference, 32 instructions a group and page more.
+// APART does that.  Without it the workgroup, all wavefronts together, leaves off
+// there and returns false.
+template <int D, int GS, int COLS, bool APART>
+__device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const Kv4Launch &n, Lds<D, GS, COLS> &lds,
+                                               const Tile &t, int b, int split, int begin, int end, const int tid)
 {
     constexpr int NG = D / GS;   // scales per token
     constexpr int NK = D / 16;   // score products per 32 tokens
@@ -128,36 +148,13 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     constexpr int WAVES = COLS / kWaveCols, TEAMS = WAVES / 4;
     constexpr int ND = D / 32 / TEAMS;  // dwords of K and of V that a thread unpacks
     static_assert(TEAMS == 1 || TEAMS == 2, "teams of 256 threads take a page's code runs");
-    __shared__ PageK<D, GS> page_k[2];
-    __shared__ PageV<D, GS> page_v[2];
-    __shared__ float tile_top[WAVES];
+    PageK<D, GS>(&page_k)[2] = lds.page_k;
+    PageV<D, GS>(&page_v)[2] = lds.page_v;
 
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane % 32, h = lane / 32;
     const float inf = __builtin_inff();
-    // heads fastest (one kv head's pages stay in one XCD's L2), then sequences,
-    // splits and tiles, the last tiles, which see most, first.  Sequences are
-    // dealt in another order for every tile: in one fixed order a batch of 4
-    // falls into step with the 4 shader engines that an XCD fills in turn, and
-    // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
-    // 617 us against 232)
-    unsigned id = blockIdx.x;
-    const int head = (int)(id % (unsigned)a.kv.kv_heads);
-    id /= (unsigned)a.kv.kv_heads;
-    const unsigned turn = id % (unsigned)a.kv.batch;
-    id /= (unsigned)a.kv.batch;
-    const int split = (int)(id % (unsigned)n.splits);
-    const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
-    const int b = (int)((turn + (unsigned)tile) % (unsigned)a.kv.batch);
-    Tile t;
-    if (!tile_of<COLS>(a, b, head, tile, t))
-        return;
-    const int begin = n.splits > 1 ? split * n.pages : 0;
-    if (split > 0 && begin >= t.range.count)
-        return;
-    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
-
     const int first = t.seq.kv - t.seq.n;  // position of row 0
     const int col0 = t.tile * COLS + wave * kWaveCols;
     const int col = col0 + c;
@@ -205,7 +202,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     // page numbers: of page i + 1 (V) and i + 2 (K); read one step ahead
     Share<ND> share, share1;
     const int last_page = end - 1;
-    auto number_of = [&](int i) { return table[(uint32_t)t.range.at(i < last_page ? i : last_page)]; };
+    auto number_of = [&](int i) { return table[(uint32_t)t.range.at_turned(i < last_page ? i : last_page)]; };
     f32x16 r[2];
     int n0 = -1, n1 = -1, n2 = -1;
     if (begin < end) {
@@ -228,11 +225,13 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             qw[k] = valid ? qw[k] : uint4{0, 0, 0, 0};
         float top = wave_max(query_top(qw, a.q_dtype));
         if (lane == 0)
-            tile_top[wave] = top;
+            lds.tile_top[wave] = top;
+        if (tid < 2)
+            lds.stand_apart[tid] = 0;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WAVES; ++w)
-            top = __builtin_fmaxf(top, tile_top[w]);
+            top = __builtin_fmaxf(top, lds.tile_top[w]);
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
         qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
         query_operands(qw, a.q_dtype, shift, q);
@@ -243,11 +242,23 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     for (int x = 0; x < NT; ++x)
         acc[x] = f32x16{};
     float m_run = -inf, l_run = 0.0f;
-    int v_exp[NG];       // of the outputs so far
-    int v_exp_run = -100;  // of the wavefront that writes V's scales
+    int v_exp[NG];             // of the outputs so far,
+    ScaleExponents exps[NG];   // where columns stand apart these and lds.own
+    const int own_at = wave * kWaveCols + c;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-        v_exp[g] = -100;
+    for (int g = 0; g < NG; ++g) {
+        if constexpr (APART) {
+            exps[g].clear();
+            lds.own[g][own_at] = kNoScale;
+        } else {
+            v_exp[g] = kLeastExp;
+        }
+    }
+    // of the wavefront that writes V's scales: 2^v_exp_run is above those that some
+    // column of the tile saw so far, up to 2^kMostStaged, past which small ones
+    // would not stay normal numbers
+    constexpr int kMostStaged = 60, kPast = 4096;  // added where a page has larger ones
+    int v_exp_run = kLeastExp;
 
     // where a thread's operands go, and where a lane finds its own: K's slots
     // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
@@ -282,18 +293,22 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         const int x = vx + e;
         to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
     };
+    const int held_from = a.window > 0 ? t.p_lo - a.window + 1 : 0;  // the first token in some column's window
     // number, t0: the page's
     auto stage_v_scales = [&](PageV<D, GS> &to, const Share<ND> &s, int number, int t0) {
         if (wave >= 1 && wave <= NG) {
-            const bool held = t0 + lane <= t.p_hi && (unsigned)number < (unsigned)a.kv.num_pages;
+            const int token = t0 + lane;
+            const bool held = (unsigned)number < (unsigned)a.kv.num_pages && token <= t.p_hi &&
+                              (token >= held_from || token < a.sinks);
             const float v = held ? s.v_scale : 0.0f;
-            const int e = __builtin_amdgcn_readfirstlane(
-                __builtin_amdgcn_frexp_expf(wave_max(v < inf ? v : 0.0f)));
-            v_exp_run = e > v_exp_run ? e : v_exp_run;
+            int e = (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, wave_max(v < inf ? v : 0.0f))) >> 23) + kLeastExp;
+            const bool past = e > kMostStaged + kLag;
+            e = e < kMostStaged ? e : kMostStaged;
+            v_exp_run = e > v_exp_run + kLag ? e : v_exp_run;
             // the 16 times larger codes belong to tokens 1 and 3 of each 4
             to.scale[wave - 1][scale_slot(lane)] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
             if (lane == 0)
-                to.exp[wave - 1] = v_exp_run;
+                to.exp[wave - 1] = past ? v_exp_run + kPast : v_exp_run;
         }
     };
     // the K operands of step s of a page: steps go through both tiles' first
@@ -310,7 +325,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             stage_k_dword(page_k[1], share1, m);
         }
         stage_k_scales(page_k[0], share);
-        stage_v_scales(page_v[0], share, n0, t.range.at(begin) * kPageTokens);
+        stage_v_scales(page_v[0], share, n0, t.range.at_turned(begin) * kPageTokens);
         stage_k_scales(page_k[1], share1);
     }
     __syncthreads();
@@ -341,11 +356,16 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         }
     }
     __syncthreads();  // the first step unpacks the third page's K to where the first one's was
+    int t1 = t.range.at_turned(begin) * kPageTokens;  // the next page's first token
+    int stop = 0;  // columns stand apart: known a page later, when the word has come from LDS
     for (int i = begin; i < end; ++i) {
+        if (!APART && stop)
+            return false;
         const PageV<D, GS> &pv = page_v[(i - begin) & 1];
         const PageK<D, GS> &pk = page_k[(i - begin + 1) & 1];
         int n3 = -1;
-        const int t0 = t.range.at(i) * kPageTokens;
+        const int t0 = t1;
+        t1 = t.range.at_turned(i + 1 < end ? i + 1 : i) * kPageTokens;
 
         // Operands come from LDS kAhead steps before they are used: the first of
         // K's before the softmax begins, of V's in its last steps.
@@ -360,7 +380,8 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             if (s < kSteps)
                 vf[s % (kAhead + 1)] = pv.code[s / (2 * NT)][s / NT % 2][s % NT][lane];
         };
-        float vs[2][NG];  // V's scales and their exponents
+        const int stood_apart = lds.stand_apart[(i - begin + 1) & 1];  // in the page before
+        float vs[2][NG];  // V's scales and the page's exponents
         int vs_exp[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -388,7 +409,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         }
         if (__any(top > (m_run == -inf ? -inf : kSlack))) {
             top = max_lane32(top);
-            const float up = top > 0.0f || m_run == -inf ? top : 0.0f;  // of the maximum
+            const float up = top > kSlack || m_run == -inf ? top : 0.0f;  // of the column's own maximum
             if (up != -inf) {
                 const float f = m_run == -inf ? 0.0f : __builtin_amdgcn_exp2f(-up);
                 m_run = m_old + up;
@@ -401,15 +422,43 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                     x[e / 16][e % 16] -= up;
             }
         }
+        stop = __builtin_amdgcn_readfirstlane(stood_apart);
+        int by[NG];  // what a column's weights are short of
+        if constexpr (!APART) {
+            // the exponents move with pages that every column sees
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int e = __builtin_amdgcn_readfirstlane(vs_exp[g]);
-            if (e != v_exp[g]) {
-                const float f = ldexp_f(1.0f, v_exp[g] - e);
+            for (int g = 0; g < NG; ++g) {
+                const int e = __builtin_amdgcn_readfirstlane(vs_exp[g]);
+                if (e != v_exp[g]) {
+                    if (!whole || e > kPast / 2)
+                        lds.stand_apart[(i - begin) & 1] = 1;
+                    const float f = ldexp_f(1.0f, v_exp[g] - e);
+#pragma unroll
+                    for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
+                        acc[y] *= f;
+                    v_exp[g] = e;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int staged = vs_exp[g] > kPast / 2 ? vs_exp[g] - kPast : vs_exp[g], was = lds.own[g][own_at];
+                float v[2];  // as they are
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) {
+                    v[tt] = ldexp_f(vs[tt][g], staged - kTop + (lane & 1 ? 4 : 0));
+                    v[tt] = v[tt] < inf ? v[tt] : 0.0f;
+                }
+                const int e = scale_exponent(max_lane32(seen_largest(v, seen, lane)));
+                const int now = exps[g].raise(was, e > was + kLag ? e : was, p >= 0);
+                lds.own[g][own_at] = now;
+                by[g] = scale_shift(exps[g].all, now);
+                const float f = ldexp_f(1.0f, was - now);
 #pragma unroll
                 for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
                     acc[y] *= f;
-                v_exp[g] = e;
+                vs[0][g] = ldexp_f(vs[0][g], staged - exps[g].all);
+                vs[1][g] = ldexp_f(vs[1][g], staged - exps[g].all);
             }
         }
 
@@ -479,7 +528,8 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                     sum[1] += hi;
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
-                        w[tt][g][y][e] = pack2<OUT_F16>(scaled(lo, vs[tt][g], 4 * y + e), scaled(hi, vs[tt][g], 8 + 4 * y + e));
+                        w[tt][g][y][e] = pack2<OUT_F16>(scaled(APART ? ldexp_f(lo, by[g]) : lo, vs[tt][g], 4 * y + e),
+                                                        scaled(APART ? ldexp_f(hi, by[g]) : hi, vs[tt][g], 8 + 4 * y + e));
                 }
                 // between a tile's groups its products are scaled, a quarter a step
                 if (NG == 2 && s >= SG && s < 3 * SG) {
@@ -530,7 +580,7 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
                         stage_v_dword(to_v, share, s / EVERY - ND);
                 }
                 if (s == kSteps / 2) {  // a chain of a few operations in one wavefront each
-                    stage_v_scales(to_v, share, n1, t.range.at(i + 1 < end ? i + 1 : i) * kPageTokens);
+                    stage_v_scales(to_v, share, n1, t1);
                     stage_k_scales(to_k, share);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -542,15 +592,19 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         __syncthreads();
     }
 
+    if (!APART && begin < end && (stop || __builtin_amdgcn_readfirstlane(lds.stand_apart[(end - begin - 1) & 1])))
+        return false;
+
     // lane (h, c) holds elements 32 x + 8 i + 4 h .. + 3 of column c
     l_run += __shfl_xor(l_run, 32);
     if (!valid)
-        return;
+        return true;
+    auto exp_of = [&](int g) { return APART ? lds.own[g][own_at] : v_exp[g]; };
     if (n.splits > 1 && t.range.count > n.pages) {
         const int64_t at = pair_of(a, t, col) * n.splits + split;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            const float f = ldexp_f(1.0f, v_exp[x * 32 / GS] + 24 - kTop);
+            const float f = ldexp_f(1.0f, exp_of(x * 32 / GS) + 24 - kTop);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) =
@@ -560,19 +614,61 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
             n.part_stat[2 * at] = m_run;
             n.part_stat[2 * at + 1] = l_run;
         }
-        return;
+        return true;
     }
     const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
     uint16_t *y = output_of(a, t, col) + 4 * h;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-        const float f = ldexp_f(inv, v_exp[x * 32 / GS] + 24 - kTop);
+        const float f = ldexp_f(inv, exp_of(x * 32 / GS) + 24 - kTop);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint2 *>(y + 32 * x + 8 * i) =
                 uint2{pack_out(acc[x][4 * i] * f, acc[x][4 * i + 1] * f, a.y_dtype),
                       pack_out(acc[x][4 * i + 2] * f, acc[x][4 * i + 3] * f, a.y_dtype)};
     }
+    return true;
+}
+
+template <int D, int GS, int COLS>
+__global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    __shared__ Lds<D, GS, COLS> lds;
+    // heads fastest (one kv head's pages stay in one XCD's L2), then sequences,
+    // splits and tiles, the last tiles, which see most, first.  Sequences are
+    // dealt in another order for every tile: in one fixed order a batch of 4
+    // falls into step with the 4 shader engines that an XCD fills in turn, and
+    // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
+    // 617 us against 232)
+    unsigned id = blockIdx.x;
+    const int head = (int)(id % (unsigned)a.kv.kv_heads);
+    id /= (unsigned)a.kv.kv_heads;
+    const unsigned turn = id % (unsigned)a.kv.batch;
+    id /= (unsigned)a.kv.batch;
+    const int split = (int)(id % (unsigned)n.splits);
+    const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
+    const int b = (int)((turn + (unsigned)tile) % (unsigned)a.kv.batch);
+    Tile t;
+    if (!tile_of<COLS>(a, b, head, tile, t))
+        return;
+    const int begin = n.splits > 1 ? split * n.pages : 0;
+    if (split > 0 && begin >= t.range.count)
+        return;
+    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+
+    // a tile that begins with a page that not all its columns see (a prompt's first
+    // rows) goes the long way at once
+    const int t0 = begin < end ? t.range.at_turned(begin) * kPageTokens : 0;
+    const bool alike = t0 + kPageTokens - 1 <= t.p_lo && (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
+    int tid = threadIdx.x;
+    if (alike && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
+        return;
+    // From the beginning, nothing of the first way kept: whatever both had in common
+    // would cost that one its registers (2048 rows over 16384 tokens 588 us; with a
+    // block for such pages in its loop 613, with a copy of the loop in place 2580).
+    __syncthreads();
+    asm volatile("" : "+v"(tid));
+    many_rows_tile<D, GS, COLS, true>(a, n, lds, t, b, split, begin, end, tid);
 }
 
 }  // namespace
