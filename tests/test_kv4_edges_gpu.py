@@ -1,7 +1,7 @@
 """The 4-bit key/value cache where its calls meet their limits: the joins of
 split caches (every one of them, with pairs of none, one and all parts, and
-with NaN in a part), workspaces smaller than asked for and finite values of any
-size where a row may not look."""
+with NaN in a part), workspaces smaller than asked for, finite values of any
+size where a row may not look, and values at the ends of bf16's range."""
 import numpy as np
 import pytest
 
@@ -237,3 +237,41 @@ def test_every_row_has_values_of_its_own_size(window, sinks, power, tiles):
         for b, (y, bound) in enumerate(want):
             err = np.abs(got[s.row_start[b]:s.row_start[b] + s.n[b]] - y)
             assert (err <= bound + 2.0 ** -8 * (np.abs(y) + bound)).all(), (D, gs, b)
+
+
+# ---------------------------------------------------------------- the ends of the range
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("kv,rows,HQ", [(1, 1, 1), (70, 1, 4), (70, 70, 4), (4097, 1, 4), (4100, 8, 40)])
+def test_values_at_the_end_of_bf16(kv, rows, HQ, tiles):
+    """Values of 1.75 2^126, all alike, beside elements of 0: the outputs are those values and 0 within the
+    reference's bound, though a sum of the tokens' would not be finite."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([kv], [rows], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        v[0][:] = 0
+        v[0][:, :, ::3] = 1.75 * 2.0 ** 126
+        v[0][:, :, ::6] *= -1
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        q = ref.to_bits(s.rng.standard_normal((s.rows, HQ, D)), 1)
+        got = attend(s, s.to_device(), q, 1, 1, HQ, 0.1)
+        assert np.isfinite(ref.to_f64(got, 1)).all()
+        compare(s, got, reference(s, q, 1, HQ, 0.1), 1)
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_values_at_the_other_end_of_bf16(rows, tiles):
+    """Values around 2^-118: their scales are as exact as any, and so are the outputs."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([200], [rows], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        v[0] *= 2.0 ** -118
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        q = ref.to_bits(s.rng.standard_normal((s.rows, 2, D)), 1)
+        (y, bound), = reference(s, q, 1, 2, 0.1)
+        err = np.abs(ref.to_f64(attend(s, s.to_device(), q, 1, 1, 2, 0.1), 1) - y)
+        # 2^-134: half of bf16's smallest step
+        assert (err <= bound + 2.0 ** -8 * (np.abs(y) + bound) + 2.0 ** -134).all()

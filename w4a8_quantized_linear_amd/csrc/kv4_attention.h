@@ -89,10 +89,24 @@ struct Kv4Launch {
     int waves;         // wavefronts of a few-row workgroup, 4 or 8
     bool once;         // few rows: pages are read by one tile and are more than the last-level cache keeps
     float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
+                       // times 2^-sum_bits(pages),
     float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
 };
 
 __device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
+__device__ __forceinline__ f32x4 ldexp_f(f32x4 x, int e)
+{
+    return f32x4{ldexp_f(x.x, e), ldexp_f(x.y, e), ldexp_f(x.z, e), ldexp_f(x.w, e)};
+}
+
+// A sum of weights over so many pages is below 2^sum_bits (a weight below 2^3): sums
+// of values are kept this much smaller, or those of many large ones would not be
+// finite.
+__device__ __forceinline__ int sum_bits(int pages) { return 9 + 32 - __builtin_clz(pages | 1); }
+
+// 1 / l of a sum of weights (0, or about 1 and more), 2^-23 off at most; 0 where
+// nothing was seen.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(l); }
 
 // The 8 nibbles of a dword as fp16 operands u 2^-24, in the order 0 4 1 5 2 6
 // 3 7; elements 2, 3, 6, 7 of the result (nibbles 1, 5, 3, 7) are 16 times as

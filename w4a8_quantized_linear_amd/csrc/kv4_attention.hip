@@ -5,8 +5,9 @@
 // Splitting.  The kernels give a workgroup one tile of columns of one kv head
 // and some of the pages that the tile sees.  With few sequences and rows that
 // leaves compute units idle, so a tile's pages are cut into equal chunks, one
-// workgroup each; a chunk's unscaled outputs (fp32), maximum and sum go to the
-// workspace, and a second small launch joins them in chunk order:
+// workgroup each; a chunk's unscaled outputs (fp32, small by a power of two so that
+// sums of many large values are finite), maximum and sum go to the workspace, and a
+// second small launch joins them in chunk order:
 //   m = max m_i, y = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
 // Chunk boundaries depend on the sizes of the call alone, not on timing.
 #include "kv4_attention.h"
@@ -30,9 +31,8 @@ __device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Laun
     return mine ? (t.range.count + n.pages - 1) / n.pages : 0;
 }
 
-__device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Tile &t, int col, int d4, f32x4 o, float l)
+__device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Tile &t, int col, int d4, f32x4 o)
 {
-    o *= l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2 *>(output_of(a, t, col) + 4 * d4) =
         uint2{pack_out(o.x, o.y, a.y_dtype), pack_out(o.z, o.w, a.y_dtype)};
 }
@@ -64,17 +64,20 @@ __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, K
 #pragma unroll
     for (int i = 1; i < PARTS; ++i)
         m = __builtin_fmaxf(m, ml[i].x);
-    f32x4 o = {0, 0, 0, 0};
+    // only what is not there or saw nothing (sum 0) stays out: NaN in a part is the
+    // result's NaN though its factor be 0
+    float f[PARTS];
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        // only what is not there or saw nothing (sum 0) stays out: NaN in a part is
-        // the result's NaN though its factor be 0
-        const bool there = i < parts && ml[i].y != 0.0f;
-        const float f = __builtin_amdgcn_exp2f(ml[i].x - m);
-        l += there ? ml[i].y * f : 0.0f;
-        o += there ? v[i] * f : f32x4{0, 0, 0, 0};
+        f[i] = i < parts && ml[i].y != 0.0f ? __builtin_amdgcn_exp2f(ml[i].x - m) : 0.0f;
+        l += ml[i].y * f[i];
     }
-    write_joined(a, t, col, d4, o, l);
+    const float inv = ldexp_f(reciprocal(l), sum_bits(n.pages));
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+        o += v[i] * (f[i] * inv);
+    write_joined(a, t, col, d4, o);
 }
 
 // Up to 256 parts: a workgroup per pair.  A part's factor is computed once, by
@@ -116,12 +119,17 @@ __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, 
     if (lane % 64 == 0)
         wave_l[wave] = l;
     __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        l += wave_l[w];
+    const float inv = ldexp_f(reciprocal(l), sum_bits(n.pages));
     const int g = lane / (D / 4), d4 = lane % (D / 4);
     f32x4 o = {0, 0, 0, 0};
     const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * (D / 4) + d4;
 #pragma unroll 4
     for (int i = g; i < parts; i += GROUPS)
-        o += part[(int64_t)i * (D / 4)] * factor[i];
+        o += part[(int64_t)i * (D / 4)] * (factor[i] * inv);
     sums[g][d4] = o;
     __syncthreads();
     if (g != 0)
@@ -129,11 +137,7 @@ __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, 
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i)
         o += sums[i][d4];
-    l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-        l += wave_l[w];
-    write_joined(a, t, col, d4, o, l);
+    write_joined(a, t, col, d4, o);
 }
 
 // Columns of a (sequence, kv head) at most.

@@ -469,11 +469,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
 
     // the wavefronts' parts: lane (j, c) holds elements 16 x + 4 j .. + 3 of column c
     st.l = column_sum(st.l);
+    const int less = sum_bits(n.splits > 1 ? n.pages : t.range.count);
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-        const f32x4 o = (st.acc[x] + st.off[x / 4]) * ldexp_f(1.0f, st.own[x * 16 / GS] + 10);
-        *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) = o;
-    }
+    for (int x = 0; x < NT; ++x)
+        *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) =
+            ldexp_f(st.acc[x] + st.off[x / 4], st.own[x * 16 / GS] + 10 - less);
     if (j == 0) {
         part_m[wave][c] = st.m;
         part_l[wave][c] = st.l;
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         }
         return;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = ldexp_f(reciprocal(l), less);
     uint32_t w[PER / 2];
 #pragma unroll
     for (int e = 0; e < PER; e += 2)

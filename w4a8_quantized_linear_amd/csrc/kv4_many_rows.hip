@@ -600,33 +600,35 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
     if (!valid)
         return true;
     auto exp_of = [&](int g) { return APART ? lds.own[g][own_at] : v_exp[g]; };
+    // taken to their units last: a power of two by itself would not be finite for the
+    // largest
+    auto result = [&](int x, int i, float f, int e) {
+        return ldexp_f(f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]} * f,
+                       exp_of(x * 32 / GS) + 24 - kTop - e);
+    };
     if (n.splits > 1 && t.range.count > n.pages) {
         const int64_t at = pair_of(a, t, col) * n.splits + split;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            const float f = ldexp_f(1.0f, exp_of(x * 32 / GS) + 24 - kTop);
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) =
-                    f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]} * f;
-        }
+                *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) = result(x, i, 1.0f, sum_bits(n.pages));
         if (h == 0) {
             n.part_stat[2 * at] = m_run;
             n.part_stat[2 * at + 1] = l_run;
         }
         return true;
     }
-    const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+    const float inv = reciprocal(l_run);
     uint16_t *y = output_of(a, t, col) + 4 * h;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-        const float f = ldexp_f(inv, exp_of(x * 32 / GS) + 24 - kTop);
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 o = result(x, i, inv, 0);
             *reinterpret_cast<uint2 *>(y + 32 * x + 8 * i) =
-                uint2{pack_out(acc[x][4 * i] * f, acc[x][4 * i + 1] * f, a.y_dtype),
-                      pack_out(acc[x][4 * i + 2] * f, acc[x][4 * i + 3] * f, a.y_dtype)};
-    }
+                uint2{pack_out(o.x, o.y, a.y_dtype), pack_out(o.z, o.w, a.y_dtype)};
+        }
     return true;
 }
 
