@@ -1,7 +1,8 @@
 """The 4-bit key/value cache where its calls meet their limits: the joins of
 split caches (every one of them, with pairs of none, one and all parts, and
 with NaN in a part), workspaces smaller than asked for, finite values of any
-size where a row may not look, and values at the ends of bf16's range."""
+size where a row may not look, values at the ends of bf16's range and scores of any
+size."""
 import numpy as np
 import pytest
 
@@ -275,3 +276,30 @@ def test_values_at_the_other_end_of_bf16(rows, tiles):
         err = np.abs(ref.to_f64(attend(s, s.to_device(), q, 1, 1, 2, 0.1), 1) - y)
         # 2^-134: half of bf16's smallest step
         assert (err <= bound + 2.0 ** -8 * (np.abs(y) + bound) + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("power", [12, 24, 40, 70])
+def test_scores_of_any_size(power, rows, tiles):
+    """Scores of 2^power and more: where the largest stands out by 2^-12 of itself it takes all the weight."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([200], [rows], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        pages = list(s.table[0, :4])
+        q = ref.to_bits(s.rng.standard_normal((s.rows, 5, D)) * 2.0 ** power, 1)
+        (kk, _), (vv, _) = s.cache.values(0, pages), s.cache.values(1, pages)
+        got = ref.to_f64(attend(s, s.to_device(), q, 1, 1, 5, 0.5), 1)
+        assert np.isfinite(got).all()
+        tried = 0
+        for i in range(rows):
+            for h in range(5):
+                x = 0.5 * (kk[0][:201 - rows + i] @ ref.to_f64(q[i, h], 1))
+                top = x.argmax()
+                second = np.delete(x, top).max()
+                if x[top] - second >= max(2.0 ** -12 * x[top], 40):
+                    tried += 1
+                    assert (np.abs(got[i, h] - vv[0][top]) <= 2.0 ** -8 * np.abs(vv[0][top]) + 2.0 ** -11).all()
+        assert tried >= rows

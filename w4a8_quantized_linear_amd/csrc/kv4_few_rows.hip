@@ -141,14 +141,20 @@ struct State {
     int own[D / GS];  // exponents of V's scales, the column's and the wavefront's
     ScaleExponents exps[D / GS];
     half8 q[D / 32];
-    float zero[D / GS], qmul;
+    float zero[D / GS];
+    float k_factor, q_factor;  // of the scores, to units of log2: on K's scales; the row's, a power of two
 };
 
-// Scores of a page: s[t][e] is token 16 t + 4 j + e of the lane's column.
+// Scores of a page, short of the row's factor: s[t][e] is token 16 t + 4 j + e of
+// the lane's column.
 template <int D, int GS>
 __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageData<D, GS> &pg, float (&s)[4][4])
 {
     constexpr int NG = D / GS;
+    float ks[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        ks[g] = pg.ks[g] * st.k_factor;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -159,7 +165,7 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
                 r = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(pg.k[t][m]), st.q[m], r, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = scaled(r[e], pg.ks[g], 4 * t + e);
+                const float x = scaled(r[e], ks[g], 4 * t + e);
                 s[t][e] = g == 0 ? x : s[t][e] + x;
             }
         }
@@ -274,7 +280,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         vs[g] = ldexp_f(vs[g], 14 - st.exps[g].all - (lane & 1 ? 4 : 0));
         apart |= !ONE && st.exps[g].apart;
     }
-    const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.qmul);
+    const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.q_factor);
     const float m_sub = m_new == -inf ? 0.0f : m_new;
     if (__any(m_new > st.m)) {
         const float f = __builtin_amdgcn_exp2f(st.m - m_sub);
@@ -290,7 +296,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
         float &x = s[n / 4][n % 4];
-        x = __builtin_amdgcn_exp2f(__builtin_fmaf(x, st.qmul, -m_sub));
+        x = __builtin_amdgcn_exp2f(__builtin_fmaf(x, st.q_factor, -m_sub));
         st.l += x;
     }
     uint32_t w[NG][2][PARTS][4];
@@ -411,8 +417,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
             qw[m] = valid ? qw[m] : uint4{0, 0, 0, 0};
         const float top = column_max(query_top(qw, a.q_dtype));
         const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
-        // above 0: a hidden token's score, minus infinity, times 0 would be NaN
-        st.qmul = __builtin_fmaxf(ldexp_f(a.scale * kLog2e, 24 - shift), 0x1p-149f);
+        // the row's factor is a power of two, exact: with a rounded product the maximum
+        // of large scores would lie below one of them by more than fp32's exponents.
+        // 2^12 of the operands' 2^24 go to K's scales, which keeps it a number for any q
+        st.k_factor = ldexp_f(a.scale * kLog2e, 12);
+        st.q_factor = ldexp_f(1.0f, 12 - shift);
         query_operands(qw, a.q_dtype, shift, st.q);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
