@@ -1,8 +1,8 @@
 """The 4-bit key/value cache where its calls meet their limits: the joins of
 split caches (every one of them, with pairs of none, one and all parts, and
 with NaN in a part), workspaces smaller than asked for, finite values of any
-size where a row may not look, values at the ends of bf16's range and scores of any
-size."""
+size where a row may not look, values at the ends of bf16's range, scores of any
+size, and rows of one tile that are far apart."""
 import numpy as np
 import pytest
 
@@ -303,3 +303,21 @@ def test_scores_of_any_size(power, rows, tiles):
                     tried += 1
                     assert (np.abs(got[i, h] - vv[0][top]) <= 2.0 ** -8 * np.abs(vv[0][top]) + 2.0 ** -11).all()
         assert tried >= rows
+
+
+@pytest.mark.parametrize("tiles", TILES)
+def test_rows_of_a_tile_do_not_share_their_queries_size(tiles):
+    """Rows that are not there hold anything, 2^100 here; one row that is there holds 2^40; the others are as exact
+    as alone."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([30, 120], [40, 30], 2, D, gs, garbage="nan")
+        ref.fill(s.cache, s.table, s.lens, *s.values(1))
+        x = s.rng.standard_normal((s.rows, 4, D))
+        x[:10] *= 2.0 ** 100
+        x[50, 1] *= 2.0 ** 40
+        x[60:63] *= 2.0 ** -40
+        q = ref.to_bits(x, 1)
+        want = reference(s, q, 1, 4, 0.1)
+        want[1][1][10, 1] = np.inf   # scores of 2^40 are known to 2^22: no bound for that one
+        compare(s, attend(s, s.to_device(), q, 1, 1, 4, 0.1), want, 1)

@@ -57,28 +57,30 @@ __device__ __forceinline__ float row_lane(float v)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
 }
-// x times the value of lane N of the row; n is a constant after unrolling.
-__device__ __forceinline__ float scaled(float x, float scales, int n)
+// The same for a constant after unrolling.
+__device__ __forceinline__ float row_value(float v, int n)
 {
     switch (n) {
-    case 0: return row_lane<0>(scales) * x;
-    case 1: return row_lane<1>(scales) * x;
-    case 2: return row_lane<2>(scales) * x;
-    case 3: return row_lane<3>(scales) * x;
-    case 4: return row_lane<4>(scales) * x;
-    case 5: return row_lane<5>(scales) * x;
-    case 6: return row_lane<6>(scales) * x;
-    case 7: return row_lane<7>(scales) * x;
-    case 8: return row_lane<8>(scales) * x;
-    case 9: return row_lane<9>(scales) * x;
-    case 10: return row_lane<10>(scales) * x;
-    case 11: return row_lane<11>(scales) * x;
-    case 12: return row_lane<12>(scales) * x;
-    case 13: return row_lane<13>(scales) * x;
-    case 14: return row_lane<14>(scales) * x;
-    default: return row_lane<15>(scales) * x;
+    case 0: return row_lane<0>(v);
+    case 1: return row_lane<1>(v);
+    case 2: return row_lane<2>(v);
+    case 3: return row_lane<3>(v);
+    case 4: return row_lane<4>(v);
+    case 5: return row_lane<5>(v);
+    case 6: return row_lane<6>(v);
+    case 7: return row_lane<7>(v);
+    case 8: return row_lane<8>(v);
+    case 9: return row_lane<9>(v);
+    case 10: return row_lane<10>(v);
+    case 11: return row_lane<11>(v);
+    case 12: return row_lane<12>(v);
+    case 13: return row_lane<13>(v);
+    case 14: return row_lane<14>(v);
+    default: return row_lane<15>(v);
     }
 }
+// x times the value of lane n of the row.
+__device__ __forceinline__ float scaled(float x, float scales, int n) { return row_value(scales, n) * x; }
 
 // What a launch adds to the call's arguments.
 struct Kv4Launch {

@@ -19,10 +19,12 @@
 // the products of page i's outputs those scores are scaled and K of page i + 2
 // and V of page i + 1, loaded at the step's start, are unpacked.
 //
-// Rounding.  q is scaled by one power of two for the whole tile (its largest
-// magnitude to [2^13, 2^14)), so the score's factor goes into K's scales once a
-// page; what is below 2^-23 of the tile's largest is off by at most 2^-34 of it
-// (operands of the odd nibbles are stored divided by 16).  The weights are rounded
+// Rounding.  q is scaled by a power of two and held in fp16: exact unless an element
+// is below 2^-17 of its row's largest, then off by at most 2^-28 of it.  One power
+// for the whole tile (its largest magnitude to [2^13, 2^14)), so that the scores'
+// factor goes into K's scales once a page, where all rows are within kReach bits of
+// one another; else each row's own, which meets the products' sums.  The weights are
+// rounded
 // once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for the
 // tokens of odd nibbles: the error against 64 bits is 2.9e-4 with fp16 outputs,
 // 2.1e-4 of it the output's rounding.  (Two halves, as for few rows, would double
@@ -57,6 +59,7 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw 32-bit buffer
 constexpr float kSlack = 2.9f;
 constexpr int kLag = 2;
 constexpr int kTop = 11;
+constexpr int kReach = 7;
 constexpr int kLeastExp = -126;  // of scales that are not normal numbers
 
 // One page's K and V in LDS.  They are used one step apart (the scores of page
@@ -65,7 +68,7 @@ constexpr int kLeastExp = -126;  // of scales that are not normal numbers
 template <int D, int GS>
 struct PageK {
     uint4 code[2][D / 16][64];  // [32-token tile][16-element step][lane]
-    float scale[kPageTokens];   // of the scores, to units of log2: the last group's scale times q's factor
+    float scale[kPageTokens];   // of the scores, to units of log2: the last group's times k_factor
     float ratio[kPageTokens];   // groups of 64 in 128: the first group's scale over the last one's
 };  // scales stand at scale_slot(token)
 template <int D, int GS>
@@ -127,17 +130,18 @@ template <int D, int GS, int COLS>
 struct Lds {
     PageK<D, GS> page_k[2];
     PageV<D, GS> page_v[2];
-    float tile_top[COLS / kWaveCols];
+    float tile_top[COLS / kWaveCols], tile_low[COLS / kWaveCols];  // of the rows' largest magnitudes
     int own[D / GS][COLS];  // where columns stand apart: the exponents of V's scales
     int stand_apart[2];     // by a page's number: some wavefront's columns do
 };
 
-// One tile's share of pages.  All columns of a wavefront have seen V's scales of
-// one exponent, and the power of two is staged with them; where a page that only
-// some of them see has larger ones than all before it, they stand apart, and every
-// weight takes its column's difference, 32 instructions a group and page more.
-// APART does that.  Without it the workgroup, all wavefronts together, leaves off
-// there and returns false.
+// One tile's share of pages.  Its rows' queries are of about one size, all columns
+// of a wavefront have seen V's scales of one exponent, and the powers of two of both
+// are staged with the page's scales.  Where that is not so (a page that only some
+// columns see has larger values than all before it, rows 2^kReach apart) the columns
+// stand apart: every score takes its row's factor and every weight its column's
+// difference, 32 instructions a group and page more.  APART does that.  Without it
+// the workgroup, all wavefronts together, leaves off there and returns false.
 template <int D, int GS, int COLS, bool APART>
 __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const Kv4Launch &n, Lds<D, GS, COLS> &lds,
                                                const Tile &t, int b, int split, int begin, int end, const int tid)
@@ -215,26 +219,40 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
     }
     __amdgpu_buffer_rsrc_t v_block = block_of(n1);  // of page i + 1
 
-    // q: one power of two for the whole tile, so that the scores' factor goes
-    // into K's scales once a page
     half8 q[NK];
-    float qmul;
+    float k_factor, q_factor = 1.0f;  // of the scores, to units of log2: on K's scales, on the row
     {
 #pragma unroll
         for (int k = 0; k < NK; ++k)
-            qw[k] = valid ? qw[k] : uint4{0, 0, 0, 0};
-        float top = wave_max(query_top(qw, a.q_dtype));
-        if (lane == 0)
-            lds.tile_top[wave] = top;
-        if (tid < 2)
-            lds.stand_apart[tid] = 0;
-        __syncthreads();
+            qw[k] = p >= 0 ? qw[k] : uint4{0, 0, 0, 0};
+        float top = max_lane32(query_top(qw, a.q_dtype));
+        if constexpr (APART) {
+            k_factor = ldexp_f(a.scale * kLog2e, 12);
+            const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
+            q_factor = ldexp_f(1.0f, 12 - shift);
+            query_operands(qw, a.q_dtype, shift, q);
+        } else {
+            float low = -wave_max(top == 0.0f ? -inf : -top);
+            top = wave_max(top);
+            if (lane == 0) {
+                lds.tile_top[wave] = top;
+                lds.tile_low[wave] = low;
+            }
+            if (tid < 2)
+                lds.stand_apart[tid] = 0;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            top = __builtin_fmaxf(top, lds.tile_top[w]);
-        const int shift = 14 - __builtin_amdgcn_frexp_expf(top);
-        qmul = ldexp_f(a.scale * kLog2e, 24 - shift);
-        query_operands(qw, a.q_dtype, shift, q);
+            for (int w = 0; w < WAVES; ++w) {
+                top = __builtin_fmaxf(top, lds.tile_top[w]);
+                low = __builtin_fminf(low, lds.tile_low[w]);
+            }
+            const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top));
+            if (low < ldexp_f(1.0f, e - kReach) || e > 64)
+                return false;
+            const int shift = 14 - e;
+            k_factor = ldexp_f(a.scale * kLog2e, 24 - shift);
+            query_operands(qw, a.q_dtype, shift, q);
+        }
     }
 
     f32x16 acc[NT];
@@ -277,13 +295,13 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         if (wave != 0)
             return;
         if (NG == 1) {
-            to.scale[scale_slot(lane)] = s.k_scale[0] * qmul;
+            to.scale[scale_slot(lane)] = s.k_scale[0] * k_factor;
         } else {
             // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
             // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
             const float low = __builtin_fmaxf(s.k_scale[0] * 0x1p-60f, 0x1p-149f);
             const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
-            to.scale[scale_slot(lane)] = last * qmul;
+            to.scale[scale_slot(lane)] = last * k_factor;
             // (a division without its last bits: 2^-22)
             const float rest = __builtin_amdgcn_rcpf(__builtin_amdgcn_frexp_mantf(last));
             to.ratio[scale_slot(lane)] = ldexp_f(s.k_scale[0] * rest, -__builtin_amdgcn_frexp_expf(last));
@@ -350,7 +368,7 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
             const float ks = page_k[0].scale[32 * tt + slot];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                x[tt][e] = scaled(r[tt][e], ks, e);
+                x[tt][e] = scaled(APART ? r[tt][e] * q_factor : r[tt][e], ks, e);
                 top = e + tt == 0 ? x[tt][e] : __builtin_fmaxf(top, x[tt][e]);
             }
         }
@@ -569,7 +587,9 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
                 read_v(s + kAhead);
 #pragma unroll
                 for (int e = s * 32 / kSteps; e < (s + 1) * 32 / kSteps; ++e) {
-                    x[e / 16][e % 16] = scaled(r[e / 16][e % 16], ks[e / 16], e % 16) - m_sub;
+                    const float s = APART ? r[e / 16][e % 16] * q_factor : r[e / 16][e % 16];
+                    // (fused both ways, which makes them agree to the last bit)
+                    x[e / 16][e % 16] = __builtin_fmaf(row_value(ks[e / 16], e % 16), s, -m_sub);
                     top = e == 0 ? x[0][0] : __builtin_fmaxf(top, x[e / 16][e % 16]);
                 }
                 constexpr int EVERY = kSteps / (2 * ND);
