@@ -321,3 +321,22 @@ def test_rows_of_a_tile_do_not_share_their_queries_size(tiles):
         want = reference(s, q, 1, 4, 0.1)
         want[1][1][10, 1] = np.inf   # scores of 2^40 are known to 2^22: no bound for that one
         compare(s, attend(s, s.to_device(), q, 1, 1, 4, 0.1), want, 1)
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("first", [50, 56, 57, 58, 60, 100])
+@pytest.mark.parametrize("up", [1, 2, 3, 4, 5])
+def test_values_and_scores_that_grow_from_page_to_page(up, first, tiles):
+    """Scales of 2^first, then 2^up times those with scores a little higher, which a running maximum may lag
+    behind."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([4 * 64], [50], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        v[0][:] = np.sign(v[0]) * 7 * 2.0 ** first
+        v[0][64:] *= 2.0 ** up
+        k[0][:64] = 0
+        k[0][64:] = 1.94 / (0.1 * D)   # 2.8 in units of log2
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        q = ref.to_bits(np.ones((s.rows, 3, D)), 1)
+        compare(s, attend(s, s.to_device(), q, 1, 1, 3, 0.1), reference(s, q, 1, 3, 0.1), 1)

@@ -319,10 +319,10 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
             const bool held = (unsigned)number < (unsigned)a.kv.num_pages && token <= t.p_hi &&
                               (token >= held_from || token < a.sinks);
             const float v = held ? s.v_scale : 0.0f;
-            int e = (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, wave_max(v < inf ? v : 0.0f))) >> 23) + kLeastExp;
-            const bool past = e > kMostStaged + kLag;
-            e = e < kMostStaged ? e : kMostStaged;
-            v_exp_run = e > v_exp_run + kLag ? e : v_exp_run;
+            const int e = (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, wave_max(v < inf ? v : 0.0f))) >> 23) + kLeastExp;
+            if (e > v_exp_run + kLag)
+                v_exp_run = e < kMostStaged ? e : kMostStaged;
+            const bool past = e > v_exp_run + kLag;
             // the 16 times larger codes belong to tokens 1 and 3 of each 4
             to.scale[wave - 1][scale_slot(lane)] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
             if (lane == 0)
