@@ -340,3 +340,41 @@ def test_values_and_scores_that_grow_from_page_to_page(up, first, tiles):
         ref.fill(s.cache, s.table, s.lens, k, v)
         q = ref.to_bits(np.ones((s.rows, 3, D)), 1)
         compare(s, attend(s, s.to_device(), q, 1, 1, 3, 0.1), reference(s, q, 1, 3, 0.1), 1)
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_queries_at_the_end_of_bf16(rows, tiles):
+    """Queries around 2^122 with keys around 2^-121, next to ordinary ones."""
+    cider.cider_kv4_set_tiles(tiles)
+    for D, gs in GEOMETRY:
+        s = Setup([150, 90], [rows, 1], 1, D, gs, garbage="nan")
+        k, v = s.values(1)
+        k[0] *= 2.0 ** -121
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        x = s.rng.standard_normal((s.rows, 2, D))
+        x[:rows] *= 2.0 ** 122
+        q = ref.to_bits(x, 1)
+        compare(s, attend(s, s.to_device(), q, 1, 1, 2, 0.3), reference(s, q, 1, 2, 0.3), 1)
+
+
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("power", [35, 55])
+def test_keys_whose_halves_are_far_apart(power, rows, tiles):
+    """K's groups 2^(2 power) apart, queries in either half alone, so that the scores matter."""
+    cider.cider_kv4_set_tiles(tiles)
+    for big in (0, 1):
+        s = Setup([130], [rows], 1, 128, 64, garbage="nan")
+        k, v = s.values(1)
+        halves = [slice(0, 64), slice(64, 128)]
+        k[0][:, :, halves[big]] *= 2.0 ** power
+        k[0][:, :, halves[1 - big]] *= 2.0 ** -power
+        ref.fill(s.cache, s.table, s.lens, k, v)
+        x = s.rng.standard_normal((s.rows, 4, 128))
+        x[:, :2, halves[big]] = 0
+        x[:, :2, halves[1 - big]] *= 2.0 ** power
+        x[:, 2:, halves[1 - big]] = 0
+        x[:, 2:, halves[big]] *= 2.0 ** -power
+        q = ref.to_bits(x, 1)
+        compare(s, attend(s, s.to_device(), q, 1, 1, 4, 0.1), reference(s, q, 1, 4, 0.1), 1)

@@ -298,8 +298,9 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
             to.scale[scale_slot(lane)] = s.k_scale[0] * k_factor;
         } else {
             // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
-            // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under 2^60
-            const float low = __builtin_fmaxf(s.k_scale[0] * 0x1p-60f, 0x1p-149f);
+            // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under
+            // 2^120, which r0, below 2, leaves finite
+            const float low = __builtin_fmaxf(s.k_scale[0] * (s.k_scale[1] == 0.0f ? 0x1p-60f : 0x1p-120f), 0x1p-149f);
             const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
             to.scale[scale_slot(lane)] = last * k_factor;
             // (a division without its last bits: 2^-22)
