@@ -2,7 +2,7 @@
 split caches (every one of them, with pairs of none, one and all parts, and
 with NaN in a part), workspaces smaller than asked for, finite values of any
 size where a row may not look, values at the ends of bf16's range, scores of any
-size, and rows of one tile that are far apart."""
+size, rows of one tile that are far apart, and launches past 2^24 workgroups."""
 import numpy as np
 import pytest
 
@@ -378,3 +378,69 @@ def test_keys_whose_halves_are_far_apart(power, rows, tiles):
         x[:, 2:, halves[big]] *= 2.0 ** -power
         q = ref.to_bits(x, 1)
         compare(s, attend(s, s.to_device(), q, 1, 1, 4, 0.1), reference(s, q, 1, 4, 0.1), 1)
+
+
+# ---------------------------------------------------------------- launches past 2^24 workgroups
+
+def test_append_and_read_with_wide_bounds():
+    """1024 sequences of up to 65536 rows and 8 heads: 16.8 million workgroups, nearly all without work."""
+    import torch
+    D, gs, H, batch, bound = 64, 64, 8, 1024, 65536
+    s = Setup([70, 3], [2, 3], H, D, gs, garbage="nan")
+    k, v = s.values(0)
+    starts = np.full(batch + 1, 5, np.int32)
+    starts[0] = 0
+    starts[1:batch] = 2
+    lens = np.zeros(batch, np.int32)
+    lens[0], lens[-1] = 70, 3
+    table = np.zeros((batch, bound // 64), np.int32)
+    table[0, :2], table[-1, :1] = s.table[0, :2], s.table[1, :1]
+    d = torch.from_numpy(s.cache.data.copy()).cuda()
+    b = cider.cider_kv4_batch(d, i32(table), i32(starts), i32(lens), batch, bound, bound, bound, bound // 64,
+                              s.num_pages, H, D, gs)
+    kr, vr = (np.concatenate([x[0][68:], x[1]]) for x in (k, v))
+    kd, vd = (gu.bits_to_dev(ref.to_bits(x, 0).reshape(5, -1)) for x in (kr, vr))
+    cider.cider_kv4_append(b, kd, vd, 0, H * D, H * D)
+    for seq, kv, n in ((0, 70, 2), (1, 3, 3)):
+        for t in range(kv - n, kv):
+            for which, x in ((0, k), (1, v)):
+                s.cache.put(s.table[seq, t // 64], t % 64, which, *ref.quantize(x[seq][t], gs))
+    assert np.array_equal(gu.to_host(d), s.cache.data)
+    out = torch.zeros((2, 5, H * D), dtype=torch.int16, device="cuda")
+    cider.cider_kv4_read(b, out[0], out[1], 0, H * D, H * D)
+    for x, got in ((kr, out[0]), (vr, out[1])):
+        u, sc = ref.quantize(x, gs)
+        want = np.repeat(sc, gs, -1) * (u.astype(np.float32) - 8)
+        assert np.array_equal(gu.bits_to_host(got), ref.to_bits(want, 0).reshape(5, -1))
+
+
+@pytest.mark.parametrize("tiles,batch,kv_heads,q_heads,pages,rows", [
+    (16, 4096, 64, 64, 2048, 1),      # a split launch of 2^24 workgroups
+    (16, 16384, 64, 1024, 544, 1),    # and its join
+    (128, 16384, 64, 64, 4, 2046),    # tiles of many columns, whole
+])
+def test_attention_with_wide_bounds(tiles, batch, kv_heads, q_heads, pages, rows):
+    import torch
+    cider.cider_kv4_set_tiles(tiles)
+    D, gs = 64, 64
+    n = min(rows, 3)
+    s = Setup([200, 67], [n, 1], kv_heads, D, gs, garbage="nan")
+    ref.fill(s.cache, s.table, s.lens, *s.values(0))
+    s.to_device()
+    starts = np.full(batch + 1, n + 1, np.int32)
+    starts[0] = 0
+    starts[1:batch] = n
+    lens = np.zeros(batch, np.int32)
+    lens[0], lens[-1] = s.lens
+    table = torch.zeros((batch, pages), dtype=torch.int32, device="cuda")
+    table[0, :4], table[-1, :2] = i32(s.table[0, :4]), i32(s.table[1, :2])
+    rows = max(rows, n + 1)
+    b = cider.cider_kv4_batch(s.dcache, table, i32(starts), i32(lens), batch, rows, rows if n > 1 else 1, pages * 64,
+                              pages, s.num_pages, kv_heads, D, gs)
+    q = ref.to_bits(s.rng.standard_normal((n + 1, q_heads, D)), 0)
+    qd = gu.bits_to_dev(q.reshape(n + 1, -1))
+    y = torch.zeros((n + 1, q_heads * D), dtype=torch.int16, device="cuda")
+    nbytes = cider.cider_kv4_attention_workspace_bytes(b, q_heads, 0, 0)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+    cider.cider_kv4_attention(b, qd, 0, q_heads * D, q_heads, 0.1, 0, 0, ws, nbytes, y, 0, q_heads * D)
+    compare(s, gu.bits_to_host(y).reshape(n + 1, q_heads, D), reference(s, q, 0, q_heads, 0.1), 0)

@@ -422,8 +422,8 @@ cider_status check_kv4_rows(const cider_kv4_batch *b, const void *k, const void 
     if (!dtype_ok(dtype) || ldk < width || ldv < width)
         return CIDER_ERR_INVALID_ARG;
     // one workgroup per head and 32-token block that a sequence may touch
-    if (b->batch * b->kv_heads > kMaxInt ||
-        (b->max_rows / 32 + 2) > kMaxInt / (b->batch * b->kv_heads + 1))
+    const int64_t heads = b->batch * b->kv_heads;
+    if (heads > kMaxInt || (heads > 0 && b->max_rows / 32 + 2 > kMaxInt / heads))
         return CIDER_ERR_UNSUPPORTED_SHAPE;
     if (kv4_empty(b))
         return CIDER_OK;
@@ -452,7 +452,8 @@ cider_status check_kv4_attention(const cider_kv4_batch *b, int64_t q_heads, int6
         return CIDER_ERR_UNSUPPORTED_SHAPE;
     // launches count workgroups in 32 bits: at most one per (row, query head) pair of the longest sequence
     const int64_t pairs = (b->max_rows < b->rows ? b->max_rows : b->rows) * (q_heads / b->kv_heads);
-    if (b->batch * b->kv_heads > kMaxInt || (pairs + 1) > kMaxInt / (b->batch * b->kv_heads + 1))
+    const int64_t heads = b->batch * b->kv_heads;
+    if (heads > kMaxInt || (heads > 0 && pairs > kMaxInt / heads))
         return CIDER_ERR_UNSUPPORTED_SHAPE;
     return CIDER_OK;
 }

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, K
     constexpr int LANES = D / 4;
     Tile t;
     int col;
-    const int parts = parts_of<COLS>(a, n, (int64_t)blockIdx.x * (256 / LANES) + (int)threadIdx.x / LANES, t, col);
+    const int parts = parts_of<COLS>(a, n, (int64_t)kv4_workgroup() * (256 / LANES) + (int)threadIdx.x / LANES, t, col);
     if (parts == 0)
         return;
     const int d4 = (int)threadIdx.x % LANES;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x;
     Tile t;
     int col;
-    const int parts = parts_of<COLS>(a, n, blockIdx.x, t, col);
+    const int parts = parts_of<COLS>(a, n, kv4_workgroup(), t, col);
     if (parts == 0)
         return;
     const int64_t at = pair_of(a, t, col) * n.splits;

@@ -56,11 +56,13 @@ struct Place {
 
 __device__ __forceinline__ bool place_of(const Kv4Args &a, int spans, Place &w)
 {
-    unsigned id = blockIdx.x;
+    unsigned id = kv4_workgroup();
     w.h = (int)(id % (unsigned)a.kv_heads);
     id /= (unsigned)a.kv_heads;
     const int span = (int)(id % (unsigned)spans);
     w.b = (int)(id / (unsigned)spans);
+    if (w.b >= a.batch)
+        return false;
     const Kv4Sequence s = kv4_sequence(a, w.b);
     const int first = s.kv - s.n;
     w.base = (first & ~(kSpan - 1)) + span * kSpan;  // rounds down below 0 too

@@ -362,7 +362,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane % 16, j = lane / 16;
     // heads fastest, then sequences, splits and tiles
-    unsigned id = blockIdx.x;
+    unsigned id = kv4_workgroup();
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
     const int b = (int)(id % (unsigned)a.kv.batch);

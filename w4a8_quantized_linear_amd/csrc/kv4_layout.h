@@ -29,7 +29,13 @@ __host__ __device__ constexpr int kv4_block_bytes(int D, int GS)
 __host__ __device__ constexpr int kv4_v_offset(int D) { return kPageTokens * D / 2; }
 __host__ __device__ constexpr int kv4_scale_offset(int D) { return kPageTokens * D; }
 
-// Launches a kernel and returns the launch's own status.  (The triple-bracket
+// Workgroups are counted over x and y: a launch holds less than 2^32 threads along
+// x, 2^23 workgroups of 512, and calls with wide bounds have more.
+constexpr unsigned kMostX = 1u << 22;
+__device__ __forceinline__ unsigned kv4_workgroup() { return blockIdx.y * kMostX + blockIdx.x; }
+
+// Launches a kernel on that many workgroups at least (those past `grid` are to
+// return) and returns the launch's own status.  (The triple-bracket
 // form stores the configuration first and takes it back: 0.23 us of the 2.4 that
 // a launch costs the host, which is what bounds the smallest calls.)
 template <typename... P, typename... A>
@@ -38,7 +44,8 @@ inline hipError_t kv4_launch(void (*kernel)(P...), unsigned grid, unsigned threa
     return [&](P... p) {
         void *at[] = {&p...};
         const hipError_t e =
-            hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), at, 0, stream);
+            hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid < kMostX ? grid : kMostX, (grid + kMostX - 1) / kMostX),
+                            dim3(threads), at, 0, stream);
         if (e != hipSuccess)
             (void)hipGetLastError();  // returned, and not left for another call to find
         return e;

@@ -663,13 +663,15 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     // falls into step with the 4 shader engines that an XCD fills in turn, and
     // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
     // 617 us against 232)
-    unsigned id = blockIdx.x;
+    unsigned id = kv4_workgroup();
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
     const unsigned turn = id % (unsigned)a.kv.batch;
     id /= (unsigned)a.kv.batch;
     const int split = (int)(id % (unsigned)n.splits);
     const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
+    if (tile < 0)
+        return;
     const int b = (int)((turn + (unsigned)tile) % (unsigned)a.kv.batch);
     Tile t;
     if (!tile_of<COLS>(a, b, head, tile, t))
