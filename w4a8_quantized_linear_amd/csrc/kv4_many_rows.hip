@@ -461,21 +461,24 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         } else {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const int staged = vs_exp[g] > kPast / 2 ? vs_exp[g] - kPast : vs_exp[g], was = lds.own[g][own_at];
-                float v[2];  // as they are
+                const int said = __builtin_amdgcn_readfirstlane(vs_exp[g]);
+                const int staged = said > kPast / 2 ? said - kPast : said, was = lds.own[g][own_at];
+                if (said > exps[g].reach) {  // else the page is within the lag of every column's
+                    float v[2];              // as they are
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    v[tt] = ldexp_f(vs[tt][g], staged - kTop + (lane & 1 ? 4 : 0));
-                    v[tt] = v[tt] < inf ? v[tt] : 0.0f;
+                    for (int tt = 0; tt < 2; ++tt) {
+                        v[tt] = ldexp_f(vs[tt][g], staged - kTop + (lane & 1 ? 4 : 0));
+                        v[tt] = v[tt] < inf ? v[tt] : 0.0f;
+                    }
+                    const int e = scale_exponent(max_lane32(seen_largest(v, seen, lane)));
+                    const int now = exps[g].raise(was, e > was + kLag ? e : was, p >= 0);
+                    lds.own[g][own_at] = now;
+                    const float f = ldexp_f(1.0f, was - now);
+#pragma unroll
+                    for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
+                        acc[y] *= f;
                 }
-                const int e = scale_exponent(max_lane32(seen_largest(v, seen, lane)));
-                const int now = exps[g].raise(was, e > was + kLag ? e : was, p >= 0);
-                lds.own[g][own_at] = now;
-                by[g] = scale_shift(exps[g].all, now);
-                const float f = ldexp_f(1.0f, was - now);
-#pragma unroll
-                for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
-                    acc[y] *= f;
+                by[g] = scale_shift(exps[g].all, lds.own[g][own_at]);
                 vs[0][g] = ldexp_f(vs[0][g], staged - exps[g].all);
                 vs[1][g] = ldexp_f(vs[1][g], staged - exps[g].all);
             }
