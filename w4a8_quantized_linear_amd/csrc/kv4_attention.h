@@ -50,6 +50,40 @@ __device__ __forceinline__ float wave_max(float v)
     return max_lane32(max_lane16(v));
 }
 
+// Maxima of two 16-bit halves at once: over a row of 16 lanes, with the row next to
+// it, with the other half of the wavefront.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
+{
+    typedef unsigned short halves __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(halves, a), __builtin_bit_cast(halves, b)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_halves_dpp(uint32_t v)
+{
+    return max_halves(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t max_halves_row(uint32_t v)
+{
+    v = max_halves_dpp<0xB1>(v);
+    v = max_halves_dpp<0x4E>(v);
+    v = max_halves_dpp<0x141>(v);
+    return max_halves_dpp<0x140>(v);
+}
+__device__ __forceinline__ uint32_t max_halves_lane16(uint32_t u)
+{
+    uint32_t w = u;
+    asm("" : "+v"(w));
+    const auto r = __builtin_amdgcn_permlane16_swap(u, w, false, false);
+    return max_halves(r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t max_halves_lane32(uint32_t u)
+{
+    uint32_t w = u;
+    asm("" : "+v"(w));
+    const auto r = __builtin_amdgcn_permlane32_swap(u, w, false, false);
+    return max_halves(r[0], r[1]);
+}
+
 // Lane N's value in each row of 16 lanes: a broadcast that the instruction
 // which uses it does itself (DPP).
 template <int N>
@@ -205,59 +239,48 @@ __device__ __forceinline__ float operand_sum(half8 op, float sum)
 // scales of one exponent, and the power of two goes into the scales, once a page;
 // where they stand apart every weight takes its column's difference.
 constexpr int kNoScale = -200;  // nothing seen; below the exponent of every fp32 number
-constexpr int kSpread = 200;    // columns are kept this close, so that every product is a normal number: one
-                                // that sees values 2^200 below another's of its wavefront loses bits
+constexpr int kExpBias = 512;   // makes 16-bit halves of exponents
+// Where columns stand apart the scales are taken 2^kMiddle up and the columns are
+// kept within kSpread, so that every product is a normal number: one that sees
+// values 2^kSpread below another's of its wavefront loses bits.
+constexpr int kMiddle = 60, kSpread = 180;
+
+__device__ __forceinline__ int scale_exponent(float s)
+{
+    return s > 0.0f && s < __builtin_inff() ? __builtin_amdgcn_frexp_expf(s) : kNoScale;
+}
 
 // One group's exponents, the same in every lane; a column's own (2^own is above
 // every finite s_v that it has seen) is kept by the kernel.
 struct ScaleExponents {
-    int all;    // the columns' own, or the middle of them where they stand apart
-    int reach;  // the least of own: scales below 2^reach move nothing
+    int all;    // what the scales are taken to
+    int reach;  // the least of own, as a power of two that is a number: scales below 2^reach move nothing
     bool same;  // every lane's own is `all`
-    bool apart; // columns that have seen a scale stand apart
 
-    __device__ __forceinline__ void clear()
+    __device__ __forceinline__ void set(int top)
     {
-        all = kNoScale;
-        reach = -149;
+        all = reach = top < -149 ? -149 : top;
         same = true;
-        apart = false;
     }
-
     // A page's scales are below 2^top where the lane's column sees them; returns the
-    // column's new exponent.  valid: there is such a column.
+    // column's new exponent.  valid: there is such a column.  LANES: 16, or 32.
+    template <int LANES>
     __device__ __forceinline__ int raise(int own, int top, bool valid)
     {
-        int now = top > own ? top : own;
-        const int first = __builtin_amdgcn_readfirstlane(now);
-        if (__all(!valid || now == first)) {
-            all = first;
-            reach = first < -149 ? -149 : first;
-            same = true;
-            apart = false;
-            return first;
+        const int now = top > own ? top : own;
+        uint32_t u = valid ? (uint32_t)(now + kExpBias) << 16 | (uint32_t)(kExpBias - now) : 0u;
+        u = max_halves_row(u);
+        if constexpr (LANES == 32)
+            u = max_halves_lane16(u);
+        u = __builtin_amdgcn_readfirstlane(u);
+        const int hi = u ? (int)(u >> 16) - kExpBias : all, lo = u ? kExpBias - (int)(u & 0xFFFFu) : hi;
+        set(hi);
+        if (lo != hi) {
+            all = hi - kMiddle;
+            reach = lo < -149 ? -149 : lo;
+            same = false;
         }
-        const int hi = __builtin_amdgcn_readfirstlane((int)wave_max((float)(valid ? now : kNoScale)));
-        int lo = -__builtin_amdgcn_readfirstlane((int)wave_max(valid && now > kNoScale ? -(float)now : -1000.0f));
-        reach = -__builtin_amdgcn_readfirstlane((int)wave_max(valid ? -(float)now : -1000.0f));
-        lo = lo > hi ? hi : lo;
-        reach = reach > hi ? hi : reach;
-        if (lo < hi - kSpread)
-            lo = hi - kSpread;
-        now = !valid ? hi : (now > kNoScale && now < lo ? lo : now);
-        same = reach == hi;
-        apart = lo != hi;
-        all = (hi + lo) >> 1;
-        reach = reach < -149 ? -149 : reach;
-        return now;
-    }
-    // The same where `same` holds and every column sees the page's scales.
-    __device__ __forceinline__ int raise_all(int top)
-    {
-        top = __builtin_amdgcn_readfirstlane(top);
-        all = top > all ? top : all;
-        reach = all < -149 ? -149 : all;
-        return all;
+        return !valid ? hi : (now > kNoScale && now < hi - kSpread ? hi - kSpread : now);
     }
 };
 // The power of two that a column's weights are short of when they are worked out
@@ -290,18 +313,17 @@ __device__ __forceinline__ float seen_score(float s, uint32_t seen, int e)
     const uint32_t keep = seen_bits(seen, e);
     return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, s) & keep) | (0xFF800000u & ~keep));
 }
-// The largest of 16 N tokens' scales (a row of lanes holds 16), 0 for those whose
-// bit is 0: the scales go round the row, the lane's bits with them.  A loop, not 16
-// copies: it is taken rarely, and its mere length would cost the code around it
-// 5 % (registers, instruction fetches).
+// The largest, by halves, of what 16 N tokens have (a row of lanes holds 16), 0
+// for those whose bit is 0: it goes round the row, the lane's bits with it.  A loop,
+// not 16 copies: it is taken rarely, and its mere length would cost the code around
+// it 5 % (registers, instruction fetches).
 template <int N>
-__device__ __forceinline__ float seen_largest(const float (&scales)[N], uint32_t seen, int lane)
+__device__ __forceinline__ uint32_t seen_largest(const uint32_t (&halves)[N], uint32_t seen, int lane)
 {
-    float top = 0.0f, s[N];
-    uint32_t bits[N];
+    uint32_t top = 0, s[N], bits[N];
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-        s[t] = scales[t];
+        s[t] = halves[t];
         bits[t] = (seen >> 16 * t & 0xFFFFu) * 0x10001u >> lane % 16;
     }
 #pragma unroll 1
@@ -310,9 +332,8 @@ __device__ __forceinline__ float seen_largest(const float (&scales)[N], uint32_t
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int t = 0; t < N; ++t) {
-                const uint32_t u = __builtin_bit_cast(uint32_t, s[t]) & seen_bits(bits[t], i);
-                top = __builtin_fmaxf(top, __builtin_bit_cast(float, u));
-                s[t] = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, s[t]), 0x12F, 0xF, 0xF, true));
+                top = max_halves(top, s[t] & seen_bits(bits[t], i));
+                s[t] = (uint32_t)__builtin_amdgcn_mov_dpp((int)s[t], 0x12F, 0xF, 0xF, true);
             }
 #pragma unroll
         for (int t = 0; t < N; ++t)
@@ -320,9 +341,11 @@ __device__ __forceinline__ float seen_largest(const float (&scales)[N], uint32_t
     }
     return top;
 }
-__device__ __forceinline__ int scale_exponent(float largest)
+// The exponent in a half; 0 there is none.
+__device__ __forceinline__ int half_exponent(uint32_t halves, int g)
 {
-    return largest > 0.0f ? __builtin_amdgcn_frexp_expf(largest) : kNoScale;
+    const int e = (int)(halves >> 16 * g & 0xFFFFu);
+    return e ? e - kExpBias : kNoScale;
 }
 
 // The pages that a tile of columns sees: [0, sink_pages) and [first, end).

@@ -19,14 +19,14 @@
 // row's largest, then off by at most 2^-34 of it (operands of the odd nibbles are
 // stored divided by 16).  The weights e^(S - m) s_v are fp32 rounded once to fp16
 // after scaling by a power of two that puts the largest s_v that the column has
-// seen into [2^13, 2^14): 11 significant bits down to 2^-28 of the largest possible
-// weight, 2^-24 for the tokens of odd nibbles.  What the column does not see has no
+// seen into [2^13, 2^15): 11 significant bits down to 2^-27 of the largest possible
+// weight, 2^-23 for the tokens of odd nibbles.  What the column does not see has no
 // part in that power of two (ScaleExponents).  That error is as large as an fp16
 // output's own rounding (and far below a bf16 one's), so for fp16 outputs the
 // weights go in as two halves, hi + lo, 22 bits: twice the products of V and some
 // operations a weight, which cost little where the cache's bytes bound the call and
 // 6 % elsewhere (batch of 64 over up to 8192 tokens: 72.5 us without, 77.5 with),
-// and take the error against 64 bits from 2.9e-4 to 2.1e-4, the output's rounding
+// and take the error against 64 bits from 2.9e-4 to 2.0e-4, the output's rounding
 // alone.  Scores, maxima, sums and outputs are fp32.
 //
 // Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
@@ -39,19 +39,27 @@
 // LDS at the end.
 //
 // What bounds it.  A page's 8 to 10 KB feed 16 columns, so with enough pages
-// the bytes do: 64 sequences of up to 8192 tokens (341 MB) in 66 us, 5.1 TB/s;
-// one of 131072 (143 MB) in 27.6, 5.2; 256 of 4096 in 200, 6.1, the rate at
+// the bytes do: 64 sequences of up to 8192 tokens (341 MB) in 70 us, 4.9 TB/s;
+// one of 131072 (143 MB) in 28, 5.1; 256 of 4096 in 200, 6.1, the rate at
 // which a plain reading kernel streams here.  A call of few pages is a chain of
 // loads (lengths, page number, page: 0.8 us each) and the parts' meeting, 6.6 us
 // for one sequence of 1001; with 2 to 3 tiles a head and pages in the caches
 // (16 sequences of up to 3001, 35 columns: 13.7 us) the vector instructions of
 // a page, 1.2 us for two wavefronts on a SIMD.
+#include <type_traits>
+
 #include "kv4_attention.h"
 
 namespace cider {
 namespace {
 
 constexpr int kCols = kFewCols;
+
+// With several rows the exponent of V's scales may lie this far below a column's
+// largest before it is moved (weights stay below 2^15, and fp16 holds 2^16): else one
+// page in twenty that not all of a tile's rows see would move it for some of them
+// alone, the long way.
+constexpr int kLag = 1;
 
 // Maximum and sum over the 4 lanes (j = 0 .. 3) of a column.
 __device__ __forceinline__ float column_max(float v) { return max_lane32(max_lane16(v)); }
@@ -138,8 +146,9 @@ template <int D, int GS>
 struct State {
     f32x4 acc[D / 16], off[D / 64];
     float m, l;  // m in units of log2
-    int own[D / GS];  // exponents of V's scales, the column's and the wavefront's
-    ScaleExponents exps[D / GS];
+    ScaleExponents exps[D / GS];  // of V's scales; where columns stand apart (not same) each has
+    int *own;                     // its own, a group's 16 apart
+    __device__ __forceinline__ int exponent(int g) const { return exps[g].same ? exps[g].all : own[16 * g]; }
     half8 q[D / 32];
     float zero[D / GS];
     float k_factor, q_factor;  // of the scores, to units of log2: on K's scales; the row's, a power of two
@@ -236,49 +245,57 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         vs[g] = held ? pg.vs[g] : 0.0f;
-        above |= vs[g] >= ldexp_f(1.0f, st.exps[g].reach) && vs[g] < inf;
+        above |= vs[g] >= ldexp_f(1.0f, st.exps[g].reach + (ONE ? 0 : kLag)) && vs[g] < inf;
     }
     if (__any(above)) {
-        float v[NG];
-        int now[NG];
-        bool alike = true;  // and the exponents were
+        uint32_t e = 0;  // exponents of the lane's token, a half each
+        bool alike = true;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            v[g] = vs[g] < inf ? vs[g] : 0.0f;
-            now[g] = __builtin_amdgcn_readfirstlane(scale_exponent(wave_max(v[g])));
+            e |= (uint32_t)(scale_exponent(vs[g]) + kExpBias) << 16 * g;
             alike &= st.exps[g].same;
         }
-        if (!ONE && !whole) {
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                alike &= __builtin_amdgcn_readfirstlane(scale_exponent(wave_max(common ? v[g] : 0.0f))) == now[g];
-        }
-        if (ONE || __builtin_expect(alike, 1)) {
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                now[g] = st.exps[g].raise_all(now[g]);
-        } else {
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                now[g] = st.exps[g].raise(st.own[g], scale_exponent(column_max(seen_largest({v[g]}, seen, lane))), valid);
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float f = ldexp_f(1.0f, st.own[g] - now[g]);
-            st.own[g] = now[g];
+        auto largest = [](uint32_t u) {
+            return (uint32_t)__builtin_amdgcn_readfirstlane(max_halves_lane32(max_halves_lane16(max_halves_row(u))));
+        };
+        const uint32_t most = largest(e);
+        const uint32_t all = ONE || whole ? most : largest(common ? e : 0u);
+        auto rescale = [&](int g, float f) {
 #pragma unroll
             for (int x = g * GS / 16; x < (g + 1) * GS / 16; ++x)
                 st.acc[x] *= f;
 #pragma unroll
             for (int y = g * GS / 64; y < (g + 1) * GS / 64; ++y)
                 st.off[y] *= f;
+        };
+        // up to the largest that every column sees
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int top = half_exponent(all, g), was = st.exps[g].all;
+            if (ONE || st.exps[g].same) {
+                const int now = top > was + (ONE ? 0 : kLag) ? top : was;
+                rescale(g, ldexp_f(1.0f, was - now));
+                st.exps[g].set(now);
+                alike &= half_exponent(most, g) <= now + kLag;
+            }
+        }
+        if (!ONE && __builtin_expect(!alike, 0)) {  // then to what each does
+            const uint32_t own = max_halves_lane32(max_halves_lane16(seen_largest({e}, seen, lane)));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int top = half_exponent(all, g), e = half_exponent(own, g), was = st.exponent(g);
+                const int next = top > was + kLag ? top : was;
+                const int then = st.exps[g].template raise<16>(was, e > next + kLag ? e : next, valid);
+                st.own[16 * g] = then;
+                rescale(g, ldexp_f(1.0f, was - then));
+            }
         }
     }
     // the 16 times larger codes belong to tokens 1 and 3 of each 4
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         vs[g] = ldexp_f(vs[g], 14 - st.exps[g].all - (lane & 1 ? 4 : 0));
-        apart |= !ONE && st.exps[g].apart;
+        apart |= !ONE && !st.exps[g].same;
     }
     const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.q_factor);
     const float m_sub = m_new == -inf ? 0.0f : m_new;
@@ -300,22 +317,27 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
         st.l += x;
     }
     uint32_t w[NG][2][PARTS][4];
+    auto weigh = [&](auto is_apart) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if (__builtin_expect(apart, 0)) {
-            const int by = scale_shift(st.exps[g].all, st.own[g]) -
-                           (g == 0 ? 0 : scale_shift(st.exps[g - 1].all, st.own[g - 1]));
+        for (int g = 0; g < NG; ++g) {
+            const int by = is_apart() ? scale_shift(st.exps[g].all, st.exponent(g)) : 0;
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
-                s[n / 4][n % 4] = ldexp_f(s[n / 4][n % 4], by);
+            for (int B = 0; B < 2; ++B)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[2 * B][e], y = s[2 * B + 1][e];
+                    if constexpr (is_apart()) {
+                        x = ldexp_f(x, by);
+                        y = ldexp_f(y, by);
+                    }
+                    round_weights<PARTS>(scaled(x, vs[g], 8 * B + e), scaled(y, vs[g], 8 * B + 4 + e), e, w[g][B]);
+                }
         }
-#pragma unroll
-        for (int B = 0; B < 2; ++B)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                round_weights<PARTS>(scaled(s[2 * B][e], vs[g], 8 * B + e), scaled(s[2 * B + 1][e], vs[g], 8 * B + 4 + e),
-                                     e, w[g][B]);
-    }
+    };
+    if (__builtin_expect(apart, 0))
+        weigh(std::true_type{});
+    else
+        weigh(std::false_type{});
     // a hidden token's weight is 0, and times a scale that is not finite it would
     // not stay so
     bool odd = false;
@@ -357,6 +379,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
     constexpr int NT = D / 16;   // output tiles
     __shared__ __align__(16) float part[WAVES][kCols][D + 4];
     __shared__ float part_m[WAVES][kCols], part_l[WAVES][kCols];
+    __shared__ int own[ONE ? 1 : WAVES][NG][kCols];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -411,6 +434,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         n1 = table[t.range.at(i + WAVES)];
 
     State<D, GS> st;
+    st.own = &own[ONE ? 0 : wave][0][c];
     {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -432,8 +456,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             st.zero[g] = column_sum(st.zero[g]) * -0x1p-21f;
-            st.exps[g].clear();
-            st.own[g] = kNoScale;
+            st.exps[g].set(kNoScale);
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -482,7 +505,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
 #pragma unroll
     for (int x = 0; x < NT; ++x)
         *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) =
-            ldexp_f(st.acc[x] + st.off[x / 4], st.own[x * 16 / GS] + 10 - less);
+            ldexp_f(st.acc[x] + st.off[x / 4], st.exponent(x * 16 / GS) + 10 - less);
     if (j == 0) {
         part_m[wave][c] = st.m;
         part_l[wave][c] = st.l;

@@ -266,7 +266,7 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if constexpr (APART) {
-            exps[g].clear();
+            exps[g].set(kNoScale);
             lds.own[g][own_at] = kNoScale;
         } else {
             v_exp[g] = kLeastExp;
@@ -459,28 +459,39 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
                 }
             }
         } else {
+            bool look = false;  // else the page is within the lag of every column's
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const int said = __builtin_amdgcn_readfirstlane(vs_exp[g]);
-                const int staged = said > kPast / 2 ? said - kPast : said, was = lds.own[g][own_at];
-                if (said > exps[g].reach) {  // else the page is within the lag of every column's
-                    float v[2];              // as they are
+                vs_exp[g] = __builtin_amdgcn_readfirstlane(vs_exp[g]);
+                look |= vs_exp[g] > exps[g].reach;
+                vs_exp[g] -= vs_exp[g] > kPast / 2 ? kPast : 0;
+            }
+            if (look) {
+                uint32_t e[2] = {0, 0};  // exponents of the lane's two tokens, a half for a group
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) {
-                        v[tt] = ldexp_f(vs[tt][g], staged - kTop + (lane & 1 ? 4 : 0));
-                        v[tt] = v[tt] < inf ? v[tt] : 0.0f;
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const float v = ldexp_f(vs[tt][g], vs_exp[g] - kTop + (lane & 1 ? 4 : 0));  // as it is
+                        e[tt] |= (uint32_t)(scale_exponent(v) + kExpBias) << 16 * g;
                     }
-                    const int e = scale_exponent(max_lane32(seen_largest(v, seen, lane)));
-                    const int now = exps[g].raise(was, e > was + kLag ? e : was, p >= 0);
+                const uint32_t largest = max_halves_lane32(seen_largest(e, seen, lane));
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int was = lds.own[g][own_at], top = half_exponent(largest, g);
+                    const int now = exps[g].template raise<32>(was, top > was + kLag ? top : was, p >= 0);
                     lds.own[g][own_at] = now;
                     const float f = ldexp_f(1.0f, was - now);
 #pragma unroll
                     for (int y = g * GS / 32; y < (g + 1) * GS / 32; ++y)
                         acc[y] *= f;
                 }
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
                 by[g] = scale_shift(exps[g].all, lds.own[g][own_at]);
-                vs[0][g] = ldexp_f(vs[0][g], staged - exps[g].all);
-                vs[1][g] = ldexp_f(vs[1][g], staged - exps[g].all);
+                vs[0][g] = ldexp_f(vs[0][g], vs_exp[g] - exps[g].all);
+                vs[1][g] = ldexp_f(vs[1][g], vs_exp[g] - exps[g].all);
             }
         }
 
