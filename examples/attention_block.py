@@ -7,7 +7,8 @@ a batch of prompts first, then decoding steps replayed from a HIP graph.
 
 Sizes are those of the benchmark's decoder stack (hidden 4096, 32 query heads
 and 8 key/value heads of 128: QKV 6144 x 4096, O 4096 x 4096); weights are
-random.  Prints the time of the prompt pass and of a decoding step, and how far
+random.  Positions are not encoded: a model that rotates q and k does so with an
+operation of its own between the product and the append.  Prints the time of the prompt pass and of a decoding step, and how far
 the block's attention is from 16-bit attention over the same keys and values
 (what 4 bits cost)."""
 from __future__ import annotations

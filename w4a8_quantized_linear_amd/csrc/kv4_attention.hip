@@ -171,7 +171,10 @@ double mean_pages(const Kv4AttentionArgs &a, int cols)
 }
 
 // Times in us, fitted to calls of 64 to 4096 rows over 256 to 16384 tokens, 2 to 8
-// kv heads, G 1 to 7, within about 15 % each.
+// kv heads, G 1 to 7.  Over 68 of them the many-row one is 28 % below to 19 % above
+// what is measured, the few-row one 38 % below to 40 % above, far off only where the
+// other kernel is far ahead or behind: the choice by them is within 3 % of the best
+// in 61, within 11 % in all.
 //
 // The few-row kernel: a tile costs its beginning and its pages.
 double few_rows_time(const Kv4AttentionArgs &a)
@@ -197,9 +200,9 @@ double many_rows_time(const Kv4AttentionArgs &a, int64_t splits)
 
 // Chunks of a tile of 128 columns: as many as make the call shortest, of 4 pages
 // and more; as many as run at once, or a half, a quarter of that, which fills the
-// compute units evenly.  (4096 rows, 448 tiles of 64 pages: whole 97
-// us, halved 125; 512 rows over 4096, 128 tiles of 64: whole 117, in four 69; 128
-// over 16384, 32 of 256: 8 chunks 75, 16 72.)
+// compute units evenly.  (4096 rows, 448 tiles of 64 pages: whole 96
+// us, halved 125; 512 rows over 4096, 128 tiles of 64: whole 125, in four 70; 128
+// over 16384, 32 of 256: 8 chunks 75, 16 73.)
 int64_t many_rows_splits(const Kv4AttentionArgs &a)
 {
     const int64_t units = units_of(a, 128), pages = most_pages(a, 128);
@@ -214,13 +217,16 @@ int64_t many_rows_splits(const Kv4AttentionArgs &a)
 
 // Columns of the tiles.  Up to 64 columns take the few-row kernel: it is bound by
 // the pages' bytes there.  Past that the kernel that the estimates above prefer
-// (prompts of 1 x 512 / 2 x 512 / 4 x 512 rows, 8 kv heads of 128, G 4: 17 / 30 /
-// 51 us against 24 / 26 / 31; of 2 x 1024 and 4 x 1024, 2 heads of 64, G 7: 23 /
-// 40 against 29 / 31; 2048 rows with a window of 256: 54 against 30).
+// (prompts of 1 x 512 / 2 x 512 / 4 x 512 rows, 8 kv heads of 128, G 4: 20 / 35 /
+// 65 us against 25 / 27 / 32; of 2 x 1024 and 4 x 1024, 2 heads of 64, G 7: 23 /
+// 40 against 30 / 32; 2048 rows with a window of 256: 78 against 31).
 // One long sequence takes 256 columns, one workgroup a compute unit: half the
-// unpacking per column (2048 rows over 16384 tokens 619 -> 585 us, 4096 of 4096
-// 186 -> 179), but coarser where tiles end at different times (ragged prompts 219
-// -> 234, 8000 rows with a window of 1024 205 -> 226).
+// unpacking per column (2048 rows over 16384 tokens 631 -> 595 us, 4096 of 4096
+// 205 -> 200), but coarser where tiles end at different times (ragged prompts 229
+// -> 246, 8000 rows with a window of 1024 212 -> 235).  Of several sequences the
+// launch knows only the longest's bounds: equal ones mostly gain (2 x 2048 rows over
+// 8192 tokens 581 -> 557, 4 x 1024 623 -> 589, but 2 x 4096 of 4096 335 -> 342),
+// ragged ones lose more.
 int columns_of(const Kv4AttentionArgs &a)
 {
     if (a.tiles)

@@ -24,23 +24,25 @@
 // for the whole tile (its largest magnitude to [2^13, 2^14)), so that the scores'
 // factor goes into K's scales once a page, where all rows are within kReach bits of
 // one another; else each row's own, which meets the products' sums.  The weights are
-// rounded
-// once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for the
-// tokens of odd nibbles: the error against 64 bits is 2.9e-4 with fp16 outputs,
-// 2.1e-4 of it the output's rounding.  (Two halves, as for few rows, would double
-// the second product, which is not hidden here.)
+// rounded once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for
+// the tokens of odd nibbles, by an exponent that only tokens the column sees have a
+// part in: the error against 64 bits is 2.9e-4 with fp16 outputs, 2.1e-4 of it the
+// output's rounding.  (Two halves, as for few rows, would double the second product,
+// which is not hidden here.)
 //
 // What bounds it: the vector units.  A wavefront takes about 365 vector
 // instructions a page (D 128 in groups of 64), which cost 4.4 cycles of its SIMD
-// each (8.3 an exponential) while products run, 1730 in all; the 32 products,
-// 32 cycles each, go under them.  Counters for 2048 rows over 16384 tokens: the
-// vector units are busy 65 % of the time, the matrix cores 40 %, either 81 %; the
-// rest is the page's barrier and results waited for.  So the work was moved, not
-// only cut: scaling under the outputs' products, loads and unpacking between
-// products, exponentials a step early (647 -> 580 us with the 256 columns).
-// Measured: 2048 rows over 16384 tokens 580 us, 890 TFLOP/s (groups of 128: 513,
-// 1005); 4 ragged prompts of up to 4096 rows, groups of 128, 220 us, 815; 8000
-// rows with a window of 1024 205 us, 615 (18 pages a tile do not hide a tile's
+// each (8.3 an exponential) while products run, 1730 in all, next to 32 products of
+// 32 cycles: two wavefronts of a SIMD, 240 pages each on average, 830 thousand
+// cycles or about 390 us for 2048 rows over 16384 tokens.  Counters for that call:
+// of a wavefront's life the vector units work 64 %, the matrix cores 38 %, either
+// 80 %; the rest is the page's barrier and results waited for.  So the work was
+// moved, not only cut: scaling under the outputs' products, loads and unpacking
+// between products, exponentials a step early (a tenth of the call with the 256
+// columns).
+// Measured: 2048 rows over 16384 tokens 603 us, 855 TFLOP/s (groups of 128: 539,
+// 956); 4 ragged prompts of up to 4096 rows, groups of 128, 230 us, 779; 8000
+// rows with a window of 1024 214 us, 589 (18 pages a tile do not hide a tile's
 // beginning and end, 9 us of 60).
 #include "kv4_attention.h"
 
@@ -703,8 +705,9 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     if (alike && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
         return;
     // From the beginning, nothing of the first way kept: whatever both had in common
-    // would cost that one its registers (2048 rows over 16384 tokens 588 us; with a
-    // block for such pages in its loop 613, with a copy of the loop in place 2580).
+    // would cost that one its registers (2048 rows over 16384 tokens 603 us; with a
+    // block for such pages in its loop 4 % more, with a copy of the loop in place four
+    // times as much).
     __syncthreads();
     asm volatile("" : "+v"(tid));
     many_rows_tile<D, GS, COLS, true>(a, n, lds, t, b, split, begin, end, tid);
