@@ -19,9 +19,10 @@
 // row's largest, then off by at most 2^-34 of it (operands of the odd nibbles are
 // stored divided by 16).  The weights e^(S - m) s_v are fp32 rounded once to fp16
 // after scaling by a power of two that puts the largest s_v that the column has
-// seen into [2^13, 2^15): 11 significant bits down to 2^-27 of the largest possible
-// weight, 2^-23 for the tokens of odd nibbles.  What the column does not see has no
-// part in that power of two (ScaleExponents).  That error is as large as an fp16
+// seen into [2^13, 2^14), of several rows into [2^11, 2^15): 11 significant bits down
+// to 2^-27 (2^-25) of the largest possible weight, 2^-23 (2^-21) for the tokens of
+// odd nibbles.  What the column does not see has no part in that power of two
+// (ScaleExponents).  That error is as large as an fp16
 // output's own rounding (and far below a bf16 one's), so for fp16 outputs the
 // weights go in as two halves, hi + lo, 22 bits: twice the products of V and some
 // operations a weight, which cost little where the cache's bytes bound the call and
@@ -55,11 +56,20 @@ namespace {
 
 constexpr int kCols = kFewCols;
 
-// With several rows the exponent of V's scales may lie this far below a column's
-// largest before it is moved (weights stay below 2^15, and fp16 holds 2^16): else one
-// page in twenty that not all of a tile's rows see would move it for some of them
-// alone, the long way.
-constexpr int kLag = 1;
+// Which columns a workgroup has.  One: every sequence has one row at most, so all
+// columns see the same tokens and the exponents of V's scales are one for all of
+// them.  Alike: of several rows, which have met scales of one exponent so far.  Apart:
+// of several rows, each column with its own.
+enum class Columns { One, Alike, Apart };
+
+// With several rows the exponent of V's scales may lie kLag below a column's largest
+// before it is moved: else one page in twenty that not all of a tile's rows see would
+// move it for some of them alone.  kTop: scales go into the weights 2^(kTop - exponent)
+// times as large, which stay below 2^15 (fp16 holds 2^16).
+template <Columns KIND>
+constexpr int kLag = KIND == Columns::One ? 0 : 3;
+template <Columns KIND>
+constexpr int kTop = KIND == Columns::One ? 14 : 12;
 
 // Maximum and sum over the 4 lanes (j = 0 .. 3) of a column.
 __device__ __forceinline__ float column_max(float v) { return max_lane32(max_lane16(v)); }
@@ -148,7 +158,11 @@ struct State {
     float m, l;  // m in units of log2
     ScaleExponents exps[D / GS];  // of V's scales; where columns stand apart (not same) each has
     int *own;                     // its own, a group's 16 apart
-    __device__ __forceinline__ int exponent(int g) const { return exps[g].same ? exps[g].all : own[16 * g]; }
+    template <Columns KIND>
+    __device__ __forceinline__ int exponent(int g) const
+    {
+        return KIND != Columns::Apart || exps[g].same ? exps[g].all : own[16 * g];
+    }
     half8 q[D / 32];
     float zero[D / GS];
     float k_factor, q_factor;  // of the scores, to units of log2: on K's scales; the row's, a power of two
@@ -174,8 +188,8 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
                 r = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(pg.k[t][m]), st.q[m], r, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = scaled(r[e], ks[g], 4 * t + e);
-                s[t][e] = g == 0 ? x : s[t][e] + x;
+                s[t][e] = g == 0 ? scaled(r[e], ks[g], 4 * t + e)
+                                 : __builtin_fmaf(row_value(ks[g], 4 * t + e), r[e], s[t][e]);
             }
         }
         __builtin_amdgcn_sched_barrier(0);  // all 4 tiles' operands at once would not fit the registers
@@ -231,35 +245,32 @@ __device__ __forceinline__ void round_weights(float x, float y, int e, uint32_t 
 // set where the lane's column sees the token (read where the page is not whole);
 // whole: every column sees every token; held, common: some column of the tile,
 // or every one, sees the token of the lane's scales; valid: the lane has a column.
-// ONE: the tile is one row.
-template <int D, int GS, bool FINE, bool ONE>
-__device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
+// False, and the state is spoilt, where columns that were alike no longer are.
+template <int D, int GS, bool FINE, Columns KIND>
+__device__ __forceinline__ bool page_outputs(State<D, GS> &st, const PageData<D, GS> &pg, int lane,
                                              float (&s)[4][4], float top, bool whole, uint32_t seen,
                                              bool held, bool common, bool valid)
 {
-    constexpr int NG = D / GS, NT = D / 16, PARTS = FINE ? 2 : 1;
+    constexpr int NG = D / GS, NT = D / 16, PARTS = FINE ? 2 : 1, LAG = kLag<KIND>;
     const float inf = __builtin_inff();
     // V's scales; the columns' exponents move up first
     float vs[NG];
-    bool above = false, apart = false;
+    bool above = false, alike = true, apart = false;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         vs[g] = held ? pg.vs[g] : 0.0f;
-        above |= vs[g] >= ldexp_f(1.0f, st.exps[g].reach + (ONE ? 0 : kLag)) && vs[g] < inf;
+        above |= vs[g] >= ldexp_f(1.0f, st.exps[g].reach + LAG) && vs[g] < inf;
     }
     if (__any(above)) {
         uint32_t e = 0;  // exponents of the lane's token, a half each
-        bool alike = true;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NG; ++g)
             e |= (uint32_t)(scale_exponent(vs[g]) + kExpBias) << 16 * g;
-            alike &= st.exps[g].same;
-        }
         auto largest = [](uint32_t u) {
             return (uint32_t)__builtin_amdgcn_readfirstlane(max_halves_lane32(max_halves_lane16(max_halves_row(u))));
         };
         const uint32_t most = largest(e);
-        const uint32_t all = ONE || whole ? most : largest(common ? e : 0u);
+        const uint32_t all = KIND == Columns::One || whole ? most : largest(common ? e : 0u);
         auto rescale = [&](int g, float f) {
 #pragma unroll
             for (int x = g * GS / 16; x < (g + 1) * GS / 16; ++x)
@@ -272,20 +283,22 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const int top = half_exponent(all, g), was = st.exps[g].all;
-            if (ONE || st.exps[g].same) {
-                const int now = top > was + (ONE ? 0 : kLag) ? top : was;
+            if (KIND == Columns::Apart && !st.exps[g].same) {
+                alike = false;
+            } else {
+                const int now = top > was + LAG ? top : was;
                 rescale(g, ldexp_f(1.0f, was - now));
                 st.exps[g].set(now);
-                alike &= half_exponent(most, g) <= now + kLag;
+                alike &= half_exponent(most, g) <= now + LAG;
             }
         }
-        if (!ONE && __builtin_expect(!alike, 0)) {  // then to what each does
+        if (KIND == Columns::Apart && !alike) {  // then to what each does
             const uint32_t own = max_halves_lane32(max_halves_lane16(seen_largest({e}, seen, lane)));
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const int top = half_exponent(all, g), e = half_exponent(own, g), was = st.exponent(g);
-                const int next = top > was + kLag ? top : was;
-                const int then = st.exps[g].template raise<16>(was, e > next + kLag ? e : next, valid);
+                const int top = half_exponent(all, g), e = half_exponent(own, g), was = st.template exponent<KIND>(g);
+                const int next = top > was + LAG ? top : was;
+                const int then = st.exps[g].template raise<16>(was, e > next + LAG ? e : next, valid);
                 st.own[16 * g] = then;
                 rescale(g, ldexp_f(1.0f, was - then));
             }
@@ -294,8 +307,8 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
     // the 16 times larger codes belong to tokens 1 and 3 of each 4
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        vs[g] = ldexp_f(vs[g], 14 - st.exps[g].all - (lane & 1 ? 4 : 0));
-        apart |= !ONE && !st.exps[g].same;
+        vs[g] = ldexp_f(vs[g], kTop<KIND> - st.exps[g].all - (lane & 1 ? 4 : 0));
+        apart |= KIND == Columns::Apart && !st.exps[g].same;
     }
     const float m_new = __builtin_fmaxf(st.m, column_max(top) * st.q_factor);
     const float m_sub = m_new == -inf ? 0.0f : m_new;
@@ -320,7 +333,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
     auto weigh = [&](auto is_apart) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const int by = is_apart() ? scale_shift(st.exps[g].all, st.exponent(g)) : 0;
+            const int by = is_apart() ? scale_shift(st.exps[g].all, st.template exponent<KIND>(g)) : 0;
 #pragma unroll
             for (int B = 0; B < 2; ++B)
 #pragma unroll
@@ -334,7 +347,7 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
                 }
         }
     };
-    if (__builtin_expect(apart, 0))
+    if (apart)
         weigh(std::true_type{});
     else
         weigh(std::false_type{});
@@ -363,42 +376,22 @@ __device__ __forceinline__ void page_outputs(State<D, GS> &st, const PageData<D,
 #pragma unroll
         for (int y = 0; y < D / 64; ++y)
             output_products<D, GS, PARTS>(st, pg.v[B][y], y, w[y * 64 / GS][B]);
+    return KIND != Columns::Alike || alike;
 }
 
-// ONE: every sequence has one row at most, so a tile's columns see the same tokens
-// and the exponents of V's scales are one for all of them: none of what keeps them
-// apart is in the way of a decoding step (64 sequences of up to 8192 tokens: 98 us
-// with it, for its registers, 71 without).  With more rows 2 wavefronts a SIMD are
-// enough to be given registers for (64 x 2 rows over 4000 tokens 57.7 us, 62 with 3
-// and what spills).
-template <int D, int GS, int WAVES, bool FINE, bool ONCE, bool ONE>
-__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+// A wavefront's pages, every WAVES-th of begin .. end - 1 from its own number on, and
+// its part of the outputs (element stride 1, columns D + 4 apart), maxima and sums.
+// False where columns that were alike no longer are: nothing is written then.
+template <int D, int GS, int WAVES, bool FINE, bool ONCE, Columns KIND>
+__device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, const Tile &t, int b, int begin,
+                                           int end, int wave, const int lane, int *own, float (*part)[D + 4],
+                                           float *part_m, float *part_l)
 {
     constexpr int NM = D / 32;   // score products per 16 tokens
     constexpr int NG = D / GS;   // scales per token
     constexpr int NT = D / 16;   // output tiles
-    __shared__ __align__(16) float part[WAVES][kCols][D + 4];
-    __shared__ float part_m[WAVES][kCols], part_l[WAVES][kCols];
-    __shared__ int own[ONE ? 1 : WAVES][NG][kCols];
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr bool LATE = KIND == Columns::Apart;  // K's next page: registers first
     const int c = lane % 16, j = lane / 16;
-    // heads fastest, then sequences, splits and tiles
-    unsigned id = kv4_workgroup();
-    const int head = (int)(id % (unsigned)a.kv.kv_heads);
-    id /= (unsigned)a.kv.kv_heads;
-    const int b = (int)(id % (unsigned)a.kv.batch);
-    id /= (unsigned)a.kv.batch;
-    const int split = (int)(id % (unsigned)n.splits), tile = (int)(id / (unsigned)n.splits);
-    Tile t;
-    if (!tile_of<kCols>(a, b, head, tile, t))
-        return;
-    const int begin = n.splits > 1 ? split * n.pages : 0;
-    if (split > 0 && begin >= t.range.count)
-        return;
-    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
-
     const int col = t.tile * kCols + c;
     const bool valid = col < t.cols;
     const int row = valid ? col / t.G : 0;
@@ -434,7 +427,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         n1 = table[t.range.at(i + WAVES)];
 
     State<D, GS> st;
-    st.own = &own[ONE ? 0 : wave][0][c];
+    st.own = own + c;
     {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -468,7 +461,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         st.l = 0.0f;
     }
 
-    for (; i < end; i += WAVES) {
+    bool alike = true;
+    for (; alike && i < end; i += WAVES) {
         int n2 = -1;
         if (i + 2 * WAVES < end)
             n2 = table[t.range.at(i + 2 * WAVES)];
@@ -481,7 +475,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
                            (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
         float s[4][4];
         page_scores<D, GS>(st, pg, s);
-        load_k<D, GS, ONCE>(pg, ahead, lane);
+        if constexpr (!LATE)
+            load_k<D, GS, ONCE>(pg, ahead, lane);
         uint32_t seen = 0xFFFFu;
         float top = largest(s);
         if (!whole) {
@@ -493,22 +488,69 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         }
         const bool held = whole || (there && tile_sees(a, t, t0 + scale_token(lane)));
         const bool common = whole || tile_shares(a, t, t0 + scale_token(lane));
-        page_outputs<D, GS, FINE, ONE>(st, pg, lane, s, top, whole, seen, held, common, valid && p >= 0);
+        alike = page_outputs<D, GS, FINE, KIND>(st, pg, lane, s, top, whole, seen, held, common, valid && p >= 0);
+        if constexpr (LATE)
+            load_k<D, GS, ONCE>(pg, ahead, lane);
         load_v<D, GS, ONCE>(pg, ahead, lane);
         n0 = n1;
         n1 = n2;
     }
 
-    // the wavefronts' parts: lane (j, c) holds elements 16 x + 4 j .. + 3 of column c
+    if (KIND == Columns::Alike && !alike)
+        return false;
+    // lane (j, c) holds elements 16 x + 4 j .. + 3 of column c
     st.l = column_sum(st.l);
     const int less = sum_bits(n.splits > 1 ? n.pages : t.range.count);
 #pragma unroll
     for (int x = 0; x < NT; ++x)
-        *reinterpret_cast<f32x4 *>(&part[wave][c][16 * x + 4 * j]) =
-            ldexp_f(st.acc[x] + st.off[x / 4], st.exponent(x * 16 / GS) + 10 - less);
+        *reinterpret_cast<f32x4 *>(&part[c][16 * x + 4 * j]) =
+            ldexp_f(st.acc[x] + st.off[x / 4], st.template exponent<KIND>(x * 16 / GS) + 24 - kTop<KIND> - less);
     if (j == 0) {
-        part_m[wave][c] = st.m;
-        part_l[wave][c] = st.l;
+        part_m[c] = st.m;
+        part_l[c] = st.l;
+    }
+    return true;
+}
+
+// ONE: one row a sequence at most.  Of several rows a wavefront whose columns no longer
+// are alike (a page that only some of them see has far larger values than all before
+// it) begins again with a copy of its loop that keeps them apart: what that takes stays
+// out of the way of the others (512 rows of a prompt 17.3 us, 19.6 with both in one
+// loop; a batch of 64 over up to 8192 tokens, one row each, 71 and 98).  Pages read
+// past the caches want the registers of 2 wavefronts a SIMD rather than a third
+// (64 x 2 rows over 4000 tokens 56.0 us, 57.6 with 3), others the third.
+template <int D, int GS, int WAVES, bool FINE, bool ONCE, bool ONE>
+__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ? 3 : 2)) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
+{
+    __shared__ __align__(16) float part[WAVES][kCols][D + 4];
+    __shared__ float part_m[WAVES][kCols], part_l[WAVES][kCols];
+    __shared__ int own[ONE ? 1 : WAVES][D / GS][kCols];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // heads fastest, then sequences, splits and tiles
+    unsigned id = kv4_workgroup();
+    const int head = (int)(id % (unsigned)a.kv.kv_heads);
+    id /= (unsigned)a.kv.kv_heads;
+    const int b = (int)(id % (unsigned)a.kv.batch);
+    id /= (unsigned)a.kv.batch;
+    const int split = (int)(id % (unsigned)n.splits), tile = (int)(id / (unsigned)n.splits);
+    Tile t;
+    if (!tile_of<kCols>(a, b, head, tile, t))
+        return;
+    const int begin = n.splits > 1 ? split * n.pages : 0;
+    if (split > 0 && begin >= t.range.count)
+        return;
+    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+
+    int lane = threadIdx.x & 63;
+    if constexpr (ONE) {
+        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::One>(a, n, t, b, begin, end, wave, lane, nullptr, part[wave], part_m[wave],
+                                                           part_l[wave]);
+    } else if (!wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Alike>(a, n, t, b, begin, end, wave, lane, nullptr, part[wave],
+                                                                     part_m[wave], part_l[wave])) {
+        asm volatile("" : "+v"(lane));  // nothing of the first way kept
+        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Apart>(a, n, t, b, begin, end, wave, lane, own[wave][0], part[wave],
+                                                             part_m[wave], part_l[wave]);
     }
     __syncthreads();
     constexpr int PER = kCols * D / (64 * WAVES);  // elements per thread
@@ -541,7 +583,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE ? 3 : 2)) 
         }
         return;
     }
-    const float inv = ldexp_f(reciprocal(l), less);
+    const float inv = ldexp_f(reciprocal(l), sum_bits(n.splits > 1 ? n.pages : t.range.count));
     uint32_t w[PER / 2];
 #pragma unroll
     for (int e = 0; e < PER; e += 2)
