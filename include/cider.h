@@ -374,7 +374,7 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
    (norm of the difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off
    for few rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
    1.7e-3, which is that rounding.  Where rows
-   that stand within 256 (row, head) pairs see values more than 2^180 apart, the
+   that stand within 256 (row, head) pairs see values more than 2^130 apart, the
    smaller ones lose bits, and so do a token's keys whose two groups have scales
    more than 2^120 apart.  The rows' own tokens must have been appended before.
    q, y:

@@ -240,6 +240,29 @@ def test_every_row_has_values_of_its_own_size(window, sinks, power, tiles):
             assert (err <= bound + 2.0 ** -8 * (np.abs(y) + bound)).all(), (D, gs, b)
 
 
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 0), (40, 4), (100, 0), (100, 70)])
+def test_one_larger_token_moves_only_the_rows_that_see_it(window, sinks, tiles):
+    """A prompt whose rows see one page by halves or no page together, one token's values 2 to 2^30 times the others':
+    rows that see it are within the bound, the others keep their bits."""
+    cider.cider_kv4_set_tiles(tiles)
+    for dtype, (D, gs) in zip((0, 1, 1), GEOMETRY):
+        for token, by in ((0, 4), (0, 2 ** 30), (3, 8), (64, 16), (130, 2), (130, 32), (199, 64), (150, 2 ** 30)):
+            by = min(by, 2 ** 12) if dtype == 0 else by
+            s = Setup([200], [200], 1, D, gs, garbage="nan")
+            k, v = s.values(dtype)
+            ref.fill(s.cache, s.table, s.lens, k, v)
+            q = ref.to_bits(s.rng.standard_normal((s.rows, 3, D)), dtype)
+            clean = attend(s, s.to_device(), q, dtype, dtype, 3, 0.1, window, sinks)
+            v[0][token] *= by
+            ref.fill(s.cache, s.table, s.lens, k, v)
+            got = attend(s, s.to_device(), q, dtype, dtype, 3, 0.1, window, sinks)
+            compare(s, got, reference(s, q, dtype, 3, 0.1, window, sinks), dtype)
+            for i in range(200):
+                if not ref.visible(i, 200, window, sinks)[token]:
+                    assert np.array_equal(got[i], clean[i]), (D, gs, token, by, i)
+
+
 # ---------------------------------------------------------------- the ends of the range
 
 @pytest.mark.parametrize("tiles", TILES)

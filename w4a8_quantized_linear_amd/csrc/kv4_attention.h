@@ -351,7 +351,7 @@ __device__ __forceinline__ int half_exponent(uint32_t halves, int g)
 // The pages that a tile of columns sees: [0, sink_pages) and [first, end).
 struct PageRange {
     int sink_pages, first, count;
-    int lead;  // pages before the first one that lies inside every column's window
+    int lead;  // pages before the first one that lies inside every column's window, or that has tokens of all
     __device__ __forceinline__ int at(int i) const { return i < sink_pages ? i : first + i - sink_pages; }
     // From there on, the ones before it last: what every column sees comes first.
     __device__ __forceinline__ int at_turned(int i) const
@@ -375,7 +375,10 @@ __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, 
     r.sink_pages = kept_pages < r.first ? kept_pages : r.first;
     r.count = r.sink_pages + end - r.first;
     if (window > 0 && p_hi >= window) {
-        const int lead = r.sink_pages + (p_hi - window) / kPageTokens + 1 - r.first;
+        int page = (p_hi - window) / kPageTokens + 1;
+        if (page * kPageTokens > p_lo && page > r.first)
+            --page;
+        const int lead = r.sink_pages + page - r.first;
         r.lead = lead < r.count ? lead : 0;
     }
     return r;

@@ -24,7 +24,7 @@
 // for the whole tile (its largest magnitude to [2^13, 2^14)), so that the scores'
 // factor goes into K's scales once a page, where all rows are within kReach bits of
 // one another; else each row's own, which meets the products' sums.  The weights are
-// rounded once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for
+// rounded once to fp16, 11 significant bits down to 2^-24 of the largest, 2^-20 for
 // the tokens of odd nibbles, by an exponent that only tokens the column sees have a
 // part in: the error against 64 bits is 2.9e-4 with fp16 outputs, 2.1e-4 of it the
 // output's rounding.  (Two halves, as for few rows, would double the second product,
@@ -57,10 +57,11 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw 32-bit buffer
 // pages instead of nearly all (with 32 columns some column has a new maximum in
 // most pages).  A column's moves are its own, whatever its neighbours see.  kTop
 // leaves fp16 the room: weights times V's scale stay below 2^(kTop + kSlack + kLag),
-// 61147.
+// 61147.  (A kLag of 2 sends a batch's first tiles, whose columns share few tokens, the
+// long way: 8 prompts of 64 rows 20.1 us, 11.1 with 3.)
 constexpr float kSlack = 2.9f;
-constexpr int kLag = 2;
-constexpr int kTop = 11;
+constexpr int kLag = 3;
+constexpr int kTop = 10;
 constexpr int kReach = 7;
 constexpr int kLeastExp = -126;  // of scales that are not normal numbers
 
@@ -78,6 +79,7 @@ struct PageV {
     uint4 code[2][2][D / 32][64];     // [32-token tile][16-token step][32-element tile][lane]
     float scale[D / GS][kPageTokens];
     int exp[D / GS];                  // V's scales are 2^(kTop - exp) times as large
+    int base[D / GS];                 // the exponent that tokens of all columns have led to
 };
 
 // Scales by token.  Lane (h, c) needs those of the 16 tokens 8 i + 4 h + f of a
@@ -137,13 +139,14 @@ struct Lds {
     int stand_apart[2];     // by a page's number: some wavefront's columns do
 };
 
-// One tile's share of pages.  Its rows' queries are of about one size, all columns
-// of a wavefront have seen V's scales of one exponent, and the powers of two of both
-// are staged with the page's scales.  Where that is not so (a page that only some
-// columns see has larger values than all before it, rows 2^kReach apart) the columns
-// stand apart: every score takes its row's factor and every weight its column's
-// difference, 32 instructions a group and page more.  APART does that.  Without it
-// the workgroup, all wavefronts together, leaves off there and returns false.
+// One tile's share of pages.  Its rows' queries are of about one size, V's scales
+// are taken to the exponent that tokens of all its columns have led to, and the powers
+// of two of both are staged with the page's scales.  Where that is not enough (tokens
+// that only some columns see have scales 2^kLag times larger, rows 2^kReach apart) the
+// columns stand apart: every score takes its row's factor and every weight its
+// column's difference, 32 instructions a group and page more.  APART does that.
+// Without it the workgroup, all wavefronts together, leaves off there and returns
+// false.
 template <int D, int GS, int COLS, bool APART>
 __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const Kv4Launch &n, Lds<D, GS, COLS> &lds,
                                                const Tile &t, int b, int split, int begin, int end, const int tid)
@@ -274,10 +277,10 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
             v_exp[g] = kLeastExp;
         }
     }
-    // of the wavefront that writes V's scales: 2^v_exp_run is above those that some
-    // column of the tile saw so far, up to 2^kMostStaged, past which small ones
+    // of the wavefront that writes V's scales: 2^(v_exp_run + kLag) is above those that
+    // every column of the tile saw so far, up to 2^kMostStaged, past which small ones
     // would not stay normal numbers
-    constexpr int kMostStaged = 60, kPast = 4096;  // added where a page has larger ones
+    constexpr int kMostStaged = 60, kPast = 4096;  // added where some column sees larger ones
     int v_exp_run = kLeastExp;
 
     // where a thread's operands go, and where a lane finds its own: K's slots
@@ -314,22 +317,32 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         const int x = vx + e;
         to.code[vb][vj / 2][2 * vg + x / 2][(vj % 2) * 32 + 16 * (x % 2) + vc] = code_halves(s.v[e]);
     };
-    const int held_from = a.window > 0 ? t.p_lo - a.window + 1 : 0;  // the first token in some column's window
+    // the first tokens in some column's window, and in every one's
+    const int held_from = a.window > 0 ? t.p_lo - a.window + 1 : 0;
+    const int shared_from = a.window > 0 ? t.p_hi - a.window + 1 : 0;
     // number, t0: the page's
     auto stage_v_scales = [&](PageV<D, GS> &to, const Share<ND> &s, int number, int t0) {
         if (wave >= 1 && wave <= NG) {
             const int token = t0 + lane;
             const bool held = (unsigned)number < (unsigned)a.kv.num_pages && token <= t.p_hi &&
                               (token >= held_from || token < a.sinks);
+            const bool shared = token <= t.p_lo && (token >= shared_from || token < a.sinks);
             const float v = held ? s.v_scale : 0.0f;
-            const int e = (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, wave_max(v < inf ? v : 0.0f))) >> 23) + kLeastExp;
-            if (e > v_exp_run + kLag)
-                v_exp_run = e < kMostStaged ? e : kMostStaged;
-            const bool past = e > v_exp_run + kLag;
+            // the upper halves of the largest that some column sees, and that all do
+            const uint32_t u = __builtin_bit_cast(uint32_t, v < inf ? v : 0.0f);
+            const uint32_t top = __builtin_amdgcn_readfirstlane(
+                max_halves_lane32(max_halves_lane16(max_halves_row((u & 0xFFFF0000u) | (shared ? u >> 16 : 0u)))));
+            const int most = (int)(top >> 23) + kLeastExp, all = (int)((top & 0xFFFFu) >> 7) + kLeastExp;
+            if (all > v_exp_run + kLag)
+                v_exp_run = all < kMostStaged ? all : kMostStaged;
+            const bool past = most > v_exp_run + kLag;
+            const int exp = !past ? v_exp_run : (most < kMostStaged ? most : kMostStaged);
             // the 16 times larger codes belong to tokens 1 and 3 of each 4
-            to.scale[wave - 1][scale_slot(lane)] = ldexp_f(v, kTop - v_exp_run - (lane & 1 ? 4 : 0));
-            if (lane == 0)
-                to.exp[wave - 1] = past ? v_exp_run + kPast : v_exp_run;
+            to.scale[wave - 1][scale_slot(lane)] = ldexp_f(v, kTop - exp - (lane & 1 ? 4 : 0));
+            if (lane == 0) {
+                to.exp[wave - 1] = past ? exp + kPast : exp;
+                to.base[wave - 1] = v_exp_run;
+            }
         }
     };
     // the K operands of step s of a page: steps go through both tiles' first
@@ -446,12 +459,12 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         stop = __builtin_amdgcn_readfirstlane(stood_apart);
         int by[NG];  // what a column's weights are short of
         if constexpr (!APART) {
-            // the exponents move with pages that every column sees
+            // the exponents move with what every column sees
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const int e = __builtin_amdgcn_readfirstlane(vs_exp[g]);
                 if (e != v_exp[g]) {
-                    if (!whole || e > kPast / 2)
+                    if (e > kPast / 2)
                         lds.stand_apart[(i - begin) & 1] = 1;
                     const float f = ldexp_f(1.0f, v_exp[g] - e);
 #pragma unroll
@@ -462,10 +475,12 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
             }
         } else {
             bool look = false;  // else the page is within the lag of every column's
+            int base[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 vs_exp[g] = __builtin_amdgcn_readfirstlane(vs_exp[g]);
-                look |= vs_exp[g] > exps[g].reach;
+                base[g] = __builtin_amdgcn_readfirstlane(pv.base[g]);
+                look |= vs_exp[g] > kPast / 2 || base[g] > exps[g].reach;
                 vs_exp[g] -= vs_exp[g] > kPast / 2 ? kPast : 0;
             }
             if (look) {
@@ -481,7 +496,8 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const int was = lds.own[g][own_at], top = half_exponent(largest, g);
-                    const int now = exps[g].template raise<32>(was, top > was + kLag ? top : was, p >= 0);
+                    const int next = base[g] > was ? base[g] : was;
+                    const int now = exps[g].template raise<32>(was, top > next + kLag ? top : next, p >= 0);
                     lds.own[g][own_at] = now;
                     const float f = ldexp_f(1.0f, was - now);
 #pragma unroll
@@ -697,10 +713,11 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         return;
     const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
 
-    // a tile that begins with a page that not all its columns see (a prompt's first
-    // rows) goes the long way at once
+    // a tile that begins with a page of which its columns share no token goes the long
+    // way at once
     const int t0 = begin < end ? t.range.at_turned(begin) * kPageTokens : 0;
-    const bool alike = t0 + kPageTokens - 1 <= t.p_lo && (a.window == 0 || t0 > t.p_hi - a.window || t0 + kPageTokens <= a.sinks);
+    const bool alike = t0 <= t.p_lo && (a.window == 0 || t0 < a.sinks ||
+                                        (t0 + kPageTokens > t.p_hi - a.window + 1 && t.p_lo > t.p_hi - a.window));
     int tid = threadIdx.x;
     if (alike && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
         return;
