@@ -351,7 +351,7 @@ __device__ __forceinline__ int half_exponent(uint32_t halves, int g)
 // The pages that a tile of columns sees: [0, sink_pages) and [first, end).
 struct PageRange {
     int sink_pages, first, count;
-    int lead;  // pages before the first one that lies inside every column's window, or that has tokens of all
+    int lead;  // pages before the first one that lies inside every column's window
     __device__ __forceinline__ int at(int i) const { return i < sink_pages ? i : first + i - sink_pages; }
     // From there on, the ones before it last: what every column sees comes first.
     __device__ __forceinline__ int at_turned(int i) const
@@ -375,10 +375,7 @@ __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, 
     r.sink_pages = kept_pages < r.first ? kept_pages : r.first;
     r.count = r.sink_pages + end - r.first;
     if (window > 0 && p_hi >= window) {
-        int page = (p_hi - window) / kPageTokens + 1;
-        if (page * kPageTokens > p_lo && page > r.first)
-            --page;
-        const int lead = r.sink_pages + page - r.first;
+        const int lead = r.sink_pages + (p_hi - window) / kPageTokens + 1 - r.first;
         r.lead = lead < r.count ? lead : 0;
     }
     return r;
@@ -409,6 +406,31 @@ __device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, int b, int h,
     t.p_hi = first + last / t.G;
     t.range = pages_seen(t.p_lo, t.p_hi, a.window, a.sinks);
     return true;
+}
+
+// The tile's first position is its newest token that all columns may see (false: their
+// windows share none): the columns' exponents start of V's scales there, so that a page
+// which only some of them see finds them alike.  Of a tile that sees pages; 0 where
+// there is none.
+__device__ __forceinline__ bool tile_has_first(const Kv4AttentionArgs &a, const Tile &t)
+{
+    return t.p_lo >= 0 && (a.window == 0 || t.p_lo > t.p_hi - a.window || t.p_lo < a.sinks);
+}
+template <int D, int GS>
+__device__ __forceinline__ void first_scales(const Kv4AttentionArgs &a, const Tile &t, const int32_t *table, float (&s)[D / GS])
+{
+    // loaded in any case, from memory that is there, and taken or not: nothing waits
+    const int token = t.p_lo > 0 ? t.p_lo : 0, number = table[token / kPageTokens];
+    const bool there = (unsigned)number < (unsigned)a.kv.num_pages;
+    const uint8_t *block = a.kv.cache + ((int64_t)(there ? number : 0) * a.kv.kv_heads + t.h) * kv4_block_bytes(D, GS);
+    // one address for all lanes: constant to the launch, so that a scalar load serves
+    typedef const __attribute__((address_space(4))) float scalar_float;
+    const scalar_float *v = (const scalar_float *)reinterpret_cast<const float *>(block + kv4_scale_offset(D)) +
+                            D / GS * kPageTokens + token % kPageTokens;
+    const bool taken = there && tile_has_first(a, t);
+#pragma unroll
+    for (int g = 0; g < D / GS; ++g)
+        s[g] = taken ? v[g * kPageTokens] : 0.0f;
 }
 
 // Whether some column of the tile sees a token.

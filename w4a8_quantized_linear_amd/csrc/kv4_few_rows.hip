@@ -64,8 +64,9 @@ enum class Columns { One, Alike, Apart };
 
 // With several rows the exponent of V's scales may lie kLag below a column's largest
 // before it is moved: else one page in twenty that not all of a tile's rows see would
-// move it for some of them alone.  kTop: scales go into the weights 2^(kTop - exponent)
-// times as large, which stay below 2^15 (fp16 holds 2^16).
+// move it for some of them alone.  (It starts of a token that all see: 16 x 5 rows with
+// a window of 1000 11.9 us without, 8.5 with.)  kTop: scales go into the weights
+// 2^(kTop - exponent) times as large, which stay below 2^15 (fp16 holds 2^16).
 template <Columns KIND>
 constexpr int kLag = KIND == Columns::One ? 0 : 3;
 template <Columns KIND>
@@ -418,8 +419,11 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
     // page numbers are read two pages ahead
     PageData<D, GS> pg;
     int i = begin + wave, n0 = -1, n1 = -1;
+    float first[NG] = {};
     if (i < end) {
         n0 = table[t.range.at(i)];
+        if constexpr (KIND != Columns::One)
+            first_scales<D, GS>(a, t, table, first);
         load_k<D, GS, ONCE>(pg, block_of(n0), lane);
         load_v<D, GS, ONCE>(pg, block_of(n0), lane);
     }
@@ -449,7 +453,8 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             st.zero[g] = column_sum(st.zero[g]) * -0x1p-21f;
-            st.exps[g].set(kNoScale);
+            const int e = __builtin_amdgcn_readfirstlane(scale_exponent(first[g]));
+            st.exps[g].set(KIND == Columns::One ? kNoScale : e);
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -515,7 +520,7 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
 // ONE: one row a sequence at most.  Of several rows a wavefront whose columns no longer
 // are alike (a page that only some of them see has far larger values than all before
 // it) begins again with a copy of its loop that keeps them apart: what that takes stays
-// out of the way of the others (512 rows of a prompt 17.3 us, 19.6 with both in one
+// out of the way of the others (512 rows of a prompt 17.9 us, 19.6 with both in one
 // loop; a batch of 64 over up to 8192 tokens, one row each, 71 and 98).  Pages read
 // past the caches want the registers of 2 wavefronts a SIMD rather than a third
 // (64 x 2 rows over 4000 tokens 56.0 us, 57.6 with 3), others the third.

@@ -282,6 +282,13 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
     // would not stay normal numbers
     constexpr int kMostStaged = 60, kPast = 4096;  // added where some column sees larger ones
     int v_exp_run = kLeastExp;
+    if (wave >= 1 && wave <= NG && begin < end) {
+        float first[NG];
+        first_scales<D, GS>(a, t, table, first);
+        const float v = first[NG == 2 ? wave - 1 : 0];
+        const int e = (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v > 0.0f && v < inf ? v : 0.0f)) >> 23) + kLeastExp;
+        v_exp_run = e < kMostStaged ? e : kMostStaged;
+    }
 
     // where a thread's operands go, and where a lane finds its own: K's slots
     // are exchanged by j so that the 8 lanes of one write cycle (2 tokens, 4 j)
@@ -713,13 +720,9 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
         return;
     const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
 
-    // a tile that begins with a page of which its columns share no token goes the long
-    // way at once
-    const int t0 = begin < end ? t.range.at_turned(begin) * kPageTokens : 0;
-    const bool alike = t0 <= t.p_lo && (a.window == 0 || t0 < a.sinks ||
-                                        (t0 + kPageTokens > t.p_hi - a.window + 1 && t.p_lo > t.p_hi - a.window));
+    // a tile whose columns share no token goes the long way at once
     int tid = threadIdx.x;
-    if (alike && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
+    if (tile_has_first(a, t) && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
         return;
     // From the beginning, nothing of the first way kept: whatever both had in common
     // would cost that one its registers (2048 rows over 16384 tokens 603 us; with a
