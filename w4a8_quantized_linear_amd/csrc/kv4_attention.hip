@@ -171,10 +171,10 @@ double mean_pages(const Kv4AttentionArgs &a, int cols)
 }
 
 // Times in us, fitted to calls of 64 to 4096 rows over 256 to 16384 tokens, 2 to 8
-// kv heads, G 1 to 7.  Over 68 of them the many-row one is 28 % below to 19 % above
-// what is measured, the few-row one 38 % below to 40 % above, far off only where the
+// kv heads, G 1 to 7.  Over 68 of them the many-row one is 29 % below to 16 % above
+// what is measured, the few-row one 36 % below to 49 % above, far off mostly where the
 // other kernel is far ahead or behind: the choice by them is within 3 % of the best
-// in 61, within 11 % in all.
+// in 59, within 15 % in all.
 //
 // The few-row kernel: a tile costs its beginning and its pages.
 double few_rows_time(const Kv4AttentionArgs &a)
@@ -217,9 +217,9 @@ int64_t many_rows_splits(const Kv4AttentionArgs &a)
 
 // Columns of the tiles.  Up to 64 columns take the few-row kernel: it is bound by
 // the pages' bytes there.  Past that the kernel that the estimates above prefer
-// (prompts of 1 x 512 / 2 x 512 / 4 x 512 rows, 8 kv heads of 128, G 4: 20 / 35 /
-// 65 us against 25 / 27 / 32; of 2 x 1024 and 4 x 1024, 2 heads of 64, G 7: 23 /
-// 40 against 30 / 32; 2048 rows with a window of 256: 78 against 31).
+// (prompts of 1 x 512 / 2 x 512 / 4 x 512 rows, 8 kv heads of 128, G 4: 19 / 30 /
+// 52 us against 26 / 28 / 33; of 2 x 1024 and 4 x 1024, 2 heads of 64, G 7: 23 /
+// 39 against 31 / 34; 2048 rows with a window of 256: 56 against 32).
 // One long sequence takes 256 columns, one workgroup a compute unit: half the
 // unpacking per column (2048 rows over 16384 tokens 631 -> 595 us, 4096 of 4096
 // 205 -> 200), but coarser where tiles end at different times (ragged prompts 229

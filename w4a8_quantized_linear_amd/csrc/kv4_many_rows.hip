@@ -35,14 +35,14 @@
 // each (8.3 an exponential) while products run, 1730 in all, next to 32 products of
 // 32 cycles: two wavefronts of a SIMD, 240 pages each on average, 830 thousand
 // cycles or about 390 us for 2048 rows over 16384 tokens.  Counters for that call:
-// of a wavefront's life the vector units work 64 %, the matrix cores 38 %, either
+// of a wavefront's life the vector units work 65 %, the matrix cores 38 %, either
 // 80 %; the rest is the page's barrier and results waited for.  So the work was
 // moved, not only cut: scaling under the outputs' products, loads and unpacking
 // between products, exponentials a step early (a tenth of the call with the 256
 // columns).
 // Measured: 2048 rows over 16384 tokens 603 us, 855 TFLOP/s (groups of 128: 539,
-// 956); 4 ragged prompts of up to 4096 rows, groups of 128, 230 us, 779; 8000
-// rows with a window of 1024 214 us, 589 (18 pages a tile do not hide a tile's
+// 956); 4 ragged prompts of up to 4096 rows, groups of 128, 231 us, 776; 8000
+// rows with a window of 1024 217 us, 581 (18 pages a tile do not hide a tile's
 // beginning and end, 9 us of 60).
 #include "kv4_attention.h"
 
