@@ -369,8 +369,9 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
    it may not see never reaches it).  For the two products q, times a power of
    two of its row or of rows of about one size, and P times V's scales, times a
    power of two of the row, are fp16: elements of q down to 2^-17 of their row's
-   largest lose nothing, smaller ones 2^-28 of that at most; the weights keep 11
-   significant bits, 22 for few rows with fp16 outputs.  Against 64 bits
+   largest lose nothing, smaller ones 2^-28 of that at most; the weights P
+   s_v (P up to 1) keep 11 significant bits, 22 for few rows with fp16 outputs, down
+   to 2^-21 of the largest scale s_v of V that the row sees, and lose them below.  Against 64 bits
    (norm of the difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off
    for few rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
    1.7e-3, which is that rounding.  Where rows

@@ -24,7 +24,7 @@
 // for the whole tile (its largest magnitude to [2^13, 2^14)), so that the scores'
 // factor goes into K's scales once a page, where all rows are within kReach bits of
 // one another; else each row's own, which meets the products' sums.  The weights are
-// rounded once to fp16, 11 significant bits down to 2^-24 of the largest, 2^-20 for
+// rounded once to fp16, 11 significant bits down to 2^-25 of the largest, 2^-21 for
 // the tokens of odd nibbles, by an exponent that only tokens the column sees have a
 // part in: the error against 64 bits is 2.9e-4 with fp16 outputs, 2.1e-4 of it the
 // output's rounding.  (Two halves, as for few rows, would double the second product,
@@ -59,9 +59,9 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw 32-bit buffer
 // leaves fp16 the room: weights times V's scale stay below 2^(kTop + kSlack + kLag),
 // 61147.  (A kLag of 2 sends a batch's first tiles, whose columns share few tokens, the
 // long way: 8 prompts of 64 rows 20.1 us, 11.1 with 3.)
-constexpr float kSlack = 2.9f;
+constexpr float kSlack = 1.9f;
 constexpr int kLag = 3;
-constexpr int kTop = 10;
+constexpr int kTop = 11;
 constexpr int kReach = 7;
 constexpr int kLeastExp = -126;  // of scales that are not normal numbers
 
