@@ -364,21 +364,21 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
      S[t] = scale * sum_d q[d] * K[t, d],  P[t] = exp(S[t] - max S)
      y[d] = sum_t P[t] * V[t, d] / sum_t P[t];  no visible t: y = 0
    with K, V the values the codes stand for; scores, softmax and sums in fp32
-   (scale * |K| and scale * |q| * |K| of the largest elements are to stay below
-   2^118; a row that meets NaN or infinity where it may look gives NaN, and what
-   it may not see never reaches it).  For the two products q, times a power of
-   two of its row or of rows of about one size, and P times V's scales, times a
-   power of two of the row, are fp16: elements of q down to 2^-17 of their row's
-   largest lose nothing, smaller ones 2^-28 of that at most; the weights P
-   s_v (P up to 1) keep 11 significant bits, 22 for few rows with fp16 outputs, down
-   to 2^-21 of the largest scale s_v of V that the row sees, and lose them below.  Against 64 bits
-   (norm of the difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off
-   for few rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
-   1.7e-3, which is that rounding.  Where rows
-   that stand within 256 (row, head) pairs see values more than 2^130 apart, the
-   smaller ones lose bits, and so do a token's keys whose two groups have scales
-   more than 2^120 apart.  The rows' own tokens must have been appended before.
-   q, y:
+   (scale * |K| and scale * |q| * |K| of the largest elements are to stay
+   below 2^118; a row that meets NaN or infinity where it may look gives NaN,
+   and what it may not see never reaches it). For the two products q, times a
+   power of two of its row or of rows of about one size, and P times V's
+   scales, times a power of two of the row, are fp16: elements of q down to
+   2^-17 of their row's largest lose nothing, smaller ones 2^-28 of that at
+   most; the weights keep 11 significant bits, 22 for few rows with fp16
+   outputs, as long as P times V's scale, P being up to 1, is above 2^-21 of
+   the largest of V's scales that the row sees. Against 64 bits (norm of the
+   difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off for few
+   rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
+   1.7e-3, which is that rounding. Where rows that stand within 256 (row,
+   head) pairs see values more than 2^130 apart, the smaller ones lose bits,
+   and so do a token's keys whose two groups have scales more than 2^120
+   apart. The rows' own tokens must have been appended before. q, y:
    [rows][q_heads][head_dim] of types q_dtype, y_dtype, row strides ldq, ldy.
    scale finite and positive; window, sinks >= 0 (the first `sinks` tokens stay
    visible behind a window).  One row per sequence is a decoding step, a few
