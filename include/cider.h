@@ -351,6 +351,45 @@ size_t cider_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_d
 cider_status cider_kv4_append(const cider_kv4_batch *b, const void *k, const void *v, int dtype,
                               int64_t ldk, int64_t ldv, void *stream);
 
+/* Norm and rotation of a batch's queries and keys, on the keys' way into the
+   cache.  For a head x of a row, r = 1 / sqrt(mean_d x_d^2 + eps):
+     n_d = x_d * r * weight_d            (weight null: n = x)
+   the first rot_dim elements of n form pairs (a, b), pair i being elements
+   (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved; each turns by the
+   table's (c, s) = cos_sin[position][i]:
+     a' = a * c - b * s,   b' = b * c + a * s
+   and the elements past rot_dim stay.  What a model does to its angles
+   (stretching, frequencies, a factor on both) is in the table, and what it adds
+   to its weights in the weights.  position is the row's p, or positions[0][row];
+   with several axes (time, height and width of images and video) pair i takes
+   positions[pair_axis[i]][row].  A position outside the table is taken as the
+   nearer end. */
+typedef struct {
+    const float *cos_sin;       /* device, [table_len][rot_dim / 2][2]; not read if rot_dim is 0 */
+    const int32_t *positions;   /* device, [axes][rows], or null if axes is 1 */
+    const float *q_weight;      /* device, [head_dim], or null: no norm of q */
+    const float *k_weight;      /* the same of k */
+    const uint8_t *pair_axis;   /* host, [rot_dim / 2], each below axes; not read if axes is 1 */
+    int64_t table_len, rot_dim; /* rot_dim a multiple of 16 up to head_dim */
+    int64_t axes;               /* 1 to 4 */
+    int interleaved;
+    float eps;                  /* positive; not looked at without weights */
+} cider_rotation;
+
+/* cider_kv4_append with norm and rotation in the same pass: q' rounded once to
+   dtype into q_out, k' (evaluated in 64 bits and rounded once to fp32, so that
+   its codes do not depend on the order of operations) and v quantized into the
+   cache as cider_kv4_append does.  q, q_out: [rows][q_heads][head_dim] with row
+   strides ldq, ldq_out; q_out may be q itself with the same stride (a fused QKV
+   product's columns turned in place), else it overlaps nothing.  q_heads is a
+   multiple of kv_heads; 0: only keys and values.  q_out is written with zeros
+   for rows that are not there, and a row whose page is not in the cache has its
+   q' all the same.  Row ranges, lengths and pages are bounded as above. */
+cider_status cider_kv4_append_rotated(const cider_kv4_batch *b, const cider_rotation *rotation,
+                                      const void *q, const void *k, const void *v, int dtype,
+                                      int64_t ldq, int64_t ldk, int64_t ldv, int64_t q_heads,
+                                      void *q_out, int64_t ldq_out, void *stream);
+
 /* Reads the cached values of the batch's rows back: the fp32 product s * (u - 8) rounded
    to dtype (n_b = kv_len[b] reads a whole sequence).  k, v:
    [rows][kv_heads][head_dim] with row strides ldk, ldv. */

@@ -40,7 +40,7 @@ EXPORTS = (
     "cider_quantize_act_ex", "cider_gemm_ex", "cider_linear_ex", "cider_decode_linear",
     "cider_linear_ex_noalloc",
     "cider_kv4_cache_bytes", "cider_kv4_append", "cider_kv4_read", "cider_kv4_attention",
-    "cider_kv4_attention_workspace_bytes", "cider_kv4_set_tiles",
+    "cider_kv4_attention_workspace_bytes", "cider_kv4_set_tiles", "cider_kv4_append_rotated",
 )
 
 KV4_PAGE_TOKENS = 64
@@ -74,6 +74,33 @@ class cider_kv4_batch(ctypes.Structure):
                              batch, rows, max_rows, max_kv_len, max_pages, num_pages, kv_heads, head_dim,
                              group_size)
         self._tensors = (cache, pages, row_start, kv_len)
+
+
+_ROTATION = struct.Struct("5Q3qif")  # cider_rotation's fields
+
+
+class cider_rotation(ctypes.Structure):
+    """Norm weights and rotation of cider_kv4_append_rotated (the struct of
+    include/cider.h).  pair_axis: bytes, or any row of whole numbers, one
+    below `axes` for each pair; None with one axis.  Tensors and pair_axis are kept
+    alive as long as the object is, so a program makes one for each step's
+    positions, or one for all where the cache's positions serve."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("cos_sin", "positions", "q_weight", "k_weight", "pair_axis")] +
+                [(n, ctypes.c_int64) for n in ("table_len", "rot_dim", "axes")] +
+                [("interleaved", ctypes.c_int), ("eps", ctypes.c_float)])
+
+    def __init__(self, cos_sin, table_len, rot_dim, interleaved=False, positions=None, axes=1, pair_axis=None,
+                 q_weight=None, k_weight=None, eps=1e-6):
+        axis = 0
+        if pair_axis is not None and axes > 1:
+            if not isinstance(pair_axis, bytes):
+                pair_axis = bytes(int(i) for i in pair_axis)
+            if len(pair_axis) != rot_dim // 2:
+                raise ValueError("pair_axis has %d entries, rot_dim / 2 is %d" % (len(pair_axis), rot_dim // 2))
+            axis = ctypes.cast(pair_axis, ctypes.c_void_p).value or 0
+        _ROTATION.pack_into(self, 0, _ptr(cos_sin) or 0, _ptr(positions) or 0, _ptr(q_weight) or 0,
+                            _ptr(k_weight) or 0, axis, table_len, rot_dim, axes, bool(interleaved), eps)
+        self._kept = (cos_sin, positions, q_weight, k_weight, pair_axis)
 
 
 _lib: ctypes.CDLL | None = None
@@ -117,6 +144,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "cider_kv4_cache_bytes": ([I64, I64, I64, I], SZ),
         "cider_kv4_append": ([P, P, P, I, I64, I64, P], I),
         "cider_kv4_read": ([P, P, P, I, I64, I64, P], I),
+        "cider_kv4_append_rotated": ([P, P, P, P, P, I, I64, I64, I64, I64, P, I64, P], I),
         "cider_kv4_attention": ([P, P, I, I64, I64, ctypes.c_float, I64, I64, P, SZ, P, I, I64, P], I),
         "cider_kv4_attention_workspace_bytes": ([P, I64, I64, I64], SZ),
         "cider_kv4_set_tiles": ([I], I),
@@ -305,6 +333,13 @@ def _batch(b):
 def cider_kv4_append(b, k, v, dtype, ldk, ldv, stream=None, check=True):
     st = load().cider_kv4_append(_batch(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
     return _ret(st, "cider_kv4_append", check)
+
+
+def cider_kv4_append_rotated(b, rotation, q, k, v, dtype, ldq, ldk, ldv, q_heads, q_out, ldq_out, stream=None,
+                             check=True):
+    st = load().cider_kv4_append_rotated(_batch(b), _batch(rotation), _ptr(q), _ptr(k), _ptr(v), dtype, ldq, ldk,
+                                         ldv, q_heads, _ptr(q_out), ldq_out, _stream(stream))
+    return _ret(st, "cider_kv4_append_rotated", check)
 
 
 def cider_kv4_read(b, k, v, dtype, ldk, ldv, stream=None, check=True):

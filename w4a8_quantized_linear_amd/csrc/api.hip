@@ -440,6 +440,52 @@ cider_status check_kv4_rows(const cider_kv4_batch *b, const void *k, const void 
     return CIDER_OK;
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes, scalars and the host array of a rotation (no device pointer is followed).
+cider_status check_rotation(const cider_rotation *r, int64_t head_dim)
+{
+    if (!r || r->rot_dim < 0)
+        return CIDER_ERR_INVALID_ARG;
+    if (r->rot_dim % 16 != 0 || r->rot_dim > head_dim)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    if ((r->q_weight || r->k_weight) && !(r->eps > 0.0f && std::isfinite(r->eps)))  // NaN fails too
+        return CIDER_ERR_INVALID_ARG;
+    if (r->rot_dim == 0)
+        return CIDER_OK;
+    if (r->table_len < 1 || r->axes < 1 || !r->cos_sin)
+        return CIDER_ERR_INVALID_ARG;
+    if (r->table_len > kMaxTokens || r->axes > cider::kMostAxes)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    if (r->axes > 1) {
+        if (!r->positions || !r->pair_axis)
+            return CIDER_ERR_INVALID_ARG;
+        for (int64_t i = 0; i < r->rot_dim / 2; ++i)
+            if (r->pair_axis[i] >= r->axes)
+                return CIDER_ERR_INVALID_ARG;
+    }
+    return CIDER_OK;
+}
+
+cider::Kv4Rotation rotation_args(const cider_rotation *r)
+{
+    cider::Kv4Rotation a{};
+    a.q_weight = r->q_weight;
+    a.k_weight = r->k_weight;
+    a.eps = r->eps;
+    a.rot_dim = (int)r->rot_dim;
+    if (r->rot_dim == 0)
+        return a;
+    a.table = reinterpret_cast<const float2 *>(r->cos_sin);
+    a.positions = r->positions;
+    a.table_len = (int)r->table_len;
+    a.axes = (int)r->axes;
+    a.interleaved = r->interleaved != 0;
+    for (int64_t i = 0; r->axes > 1 && i < r->rot_dim / 2; ++i)
+        a.pair_axis[i / 32] |= (uint64_t)r->pair_axis[i] << 2 * (i % 32);
+    return a;
+}
+
 // Sizes and scalars of the attention call.
 cider_status check_kv4_attention(const cider_kv4_batch *b, int64_t q_heads, int64_t window, int64_t sinks)
 {
@@ -693,6 +739,51 @@ cider_status cider_kv4_append(const cider_kv4_batch *b, const void *k, const voi
     return from_hip(cider::launch_kv4_append(kv4_args(b), static_cast<const uint16_t *>(k),
                                              static_cast<const uint16_t *>(v), dtype, ldk, ldv,
                                              static_cast<hipStream_t>(stream)));
+}
+
+cider_status cider_kv4_append_rotated(const cider_kv4_batch *b, const cider_rotation *rotation,
+                                      const void *q, const void *k, const void *v, int dtype,
+                                      int64_t ldq, int64_t ldk, int64_t ldv, int64_t q_heads,
+                                      void *q_out, int64_t ldq_out, void *stream)
+{
+    cider_status st = check_kv4_sizes(b);
+    if (st != CIDER_OK)
+        return st;
+    st = check_rotation(rotation, b->head_dim);
+    if (st != CIDER_OK)
+        return st;
+    if (q_heads < 0)
+        return CIDER_ERR_INVALID_ARG;
+    if (q_heads % b->kv_heads != 0 || q_heads > kMaxHeads)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = q_heads * b->head_dim;
+    if (width && (ldq < width || ldq_out < width))
+        return CIDER_ERR_INVALID_ARG;
+    if (!kv4_empty(b) && width) {
+        if (!q || !q_out)
+            return CIDER_ERR_INVALID_ARG;
+        if (!aligned16(q) || !aligned16(q_out) || ldq % 8 != 0 || ldq_out % 8 != 0)
+            return CIDER_ERR_MISALIGNED;
+    }
+    if (!aligned16(rotation->q_weight) || !aligned16(rotation->k_weight) ||
+        (rotation->rot_dim && (!aligned16(rotation->cos_sin) || !aligned4(rotation->positions))))
+        return CIDER_ERR_MISALIGNED;
+    bool run = false;
+    st = check_kv4_rows(b, k, v, dtype, ldk, ldv, &run);
+    if (!run)
+        return st;
+    cider::Kv4Rows io{};
+    io.q = static_cast<const uint16_t *>(q);
+    io.k = static_cast<const uint16_t *>(k);
+    io.v = static_cast<const uint16_t *>(v);
+    io.q_out = static_cast<uint16_t *>(q_out);
+    io.ldq = ldq;
+    io.ldk = ldk;
+    io.ldv = ldv;
+    io.ldo = ldq_out;
+    io.q_heads = (int)q_heads;
+    return from_hip(cider::launch_kv4_append_rotated(kv4_args(b), rotation_args(rotation), io, dtype,
+                                                     static_cast<hipStream_t>(stream)));
 }
 
 cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtype, int64_t ldk,

@@ -148,6 +148,26 @@ hipError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, const uint16_t
 hipError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, int dtype, int64_t ldk,
                            int64_t ldv, hipStream_t stream);
 
+// Norm and rotation on the way into the cache.
+constexpr int kMostAxes = 4;
+struct Kv4Rotation {
+    const float2 *table;       // [table_len][rot_dim / 2] of (cos, sin); rot_dim 0: not read
+    const int32_t *positions;  // [axes][rows], or null with one axis: the token's position
+    const float *q_weight, *k_weight;  // [head_dim], or null: no norm
+    uint64_t pair_axis[2];     // 2 bits for each pair
+    int table_len, rot_dim, axes;
+    bool interleaved;
+    float eps;
+};
+struct Kv4Rows {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out;
+    int64_t ldq, ldk, ldv, ldo;
+    int q_heads;
+};
+hipError_t launch_kv4_append_rotated(const Kv4Args &a, const Kv4Rotation &r, const Kv4Rows &io, int dtype,
+                                     hipStream_t stream);
+
 struct Kv4AttentionArgs {
     Kv4Args kv;
     const uint16_t *q;
