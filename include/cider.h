@@ -442,7 +442,45 @@ cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_
 size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
                                            int64_t window, int64_t sinks);
 
-/* Test hook: force the attention's column tiles for subsequent calls in this
+/* Runs of sequences that hold the same first pages (conversations behind one
+   system prompt, samples of one question, questions about one document): run g
+   is the sequences group_start[g] .. group_start[g + 1] - 1, whose rows of
+   `pages` name the same pages for the first shared_len[g] tokens.  Sequences in
+   front of the first run and behind the last are in none. */
+typedef struct {
+    const int32_t *group_start; /* device, [groups + 1], ascending */
+    const int32_t *shared_len;  /* device, [groups] */
+    int64_t groups;
+    int64_t max_rows;           /* bound on the rows of all sequences of a run */
+    int64_t max_shared_len;     /* bound on shared_len, up to 64 * max_pages */
+} cider_kv4_runs;
+
+/* cider_kv4_attention (window 0) that reads the pages a run shares once for all
+   rows of the run, with the same result: a part over the shared pages, the rows
+   of the run taken together, and one over each sequence's own pages are joined
+   by their maxima and sums, all fp32.  Only whole pages count as shared
+   (shared_len rounded down to 64).  Bounded on the device as the batch is:
+   shared_len outside [0, max_shared_len] is taken as the nearer end; a run that
+   is not inside the batch, or has more than max_rows rows, shares nothing, and
+   neither does a sequence whose rows do not all stand behind the shared pages
+   (a padded slot): those attend to their own page table alone.  What the
+   sequences of a run name for the shared pages is read from the first one's.
+   Ranges and precision are those of cider_kv4_attention.
+   workspace: device scratch of cider_kv4_attention_shared_workspace_bytes(...)
+   bytes at the least (else CIDER_ERR_WORKSPACE); calls that share one must be
+   ordered.  groups, max_rows or max_shared_len / 64 of 0 make it
+   cider_kv4_attention. */
+cider_status cider_kv4_attention_shared(const cider_kv4_batch *b, const cider_kv4_runs *runs,
+                                        const void *q, int q_dtype, int64_t ldq, int64_t q_heads,
+                                        float scale, void *workspace, size_t workspace_bytes,
+                                        void *y, int y_dtype, int64_t ldy, void *stream);
+
+/* Bytes of workspace that the call needs (0 outside the envelope).  Reads only
+   the sizes of *b and *runs, no device memory. */
+size_t cider_kv4_attention_shared_workspace_bytes(const cider_kv4_batch *b,
+                                                  const cider_kv4_runs *runs, int64_t q_heads);
+
+/* Test hook: force the attentions' column tiles for subsequent calls in this
    process.  0 = automatic (by sizes), 16 = the few-row kernel, 128 or 256 = the
    many-row kernel with that many (row, query head) pairs a tile; every setting
    takes every shape.  Returns the previous setting, or -1 for an invalid value. */

@@ -41,6 +41,7 @@ EXPORTS = (
     "cider_linear_ex_noalloc",
     "cider_kv4_cache_bytes", "cider_kv4_append", "cider_kv4_read", "cider_kv4_attention",
     "cider_kv4_attention_workspace_bytes", "cider_kv4_set_tiles", "cider_kv4_append_rotated",
+    "cider_kv4_attention_shared", "cider_kv4_attention_shared_workspace_bytes",
 )
 
 KV4_PAGE_TOKENS = 64
@@ -74,6 +75,21 @@ class cider_kv4_batch(ctypes.Structure):
                              batch, rows, max_rows, max_kv_len, max_pages, num_pages, kv_heads, head_dim,
                              group_size)
         self._tensors = (cache, pages, row_start, kv_len)
+
+
+_KV4_RUNS = struct.Struct("2Q3q")  # cider_kv4_runs' fields
+
+
+class cider_kv4_runs(ctypes.Structure):
+    """Runs of sequences that hold the same first pages (the struct of
+    include/cider.h), for cider_kv4_attention_shared.  Tensors are kept alive as
+    long as the object is."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("group_start", "shared_len")] +
+                [(n, ctypes.c_int64) for n in ("groups", "max_rows", "max_shared_len")])
+
+    def __init__(self, group_start, shared_len, groups, max_rows, max_shared_len):
+        _KV4_RUNS.pack_into(self, 0, _ptr(group_start) or 0, _ptr(shared_len) or 0, groups, max_rows, max_shared_len)
+        self._tensors = (group_start, shared_len)
 
 
 _ROTATION = struct.Struct("5Q3qif")  # cider_rotation's fields
@@ -147,6 +163,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "cider_kv4_append_rotated": ([P, P, P, P, P, I, I64, I64, I64, I64, P, I64, P], I),
         "cider_kv4_attention": ([P, P, I, I64, I64, ctypes.c_float, I64, I64, P, SZ, P, I, I64, P], I),
         "cider_kv4_attention_workspace_bytes": ([P, I64, I64, I64], SZ),
+        "cider_kv4_attention_shared": ([P, P, P, I, I64, I64, ctypes.c_float, P, SZ, P, I, I64, P], I),
+        "cider_kv4_attention_shared_workspace_bytes": ([P, P, I64], SZ),
         "cider_kv4_set_tiles": ([I], I),
     }
     for name, (args, res) in sig.items():
@@ -357,6 +375,17 @@ def cider_kv4_attention(b, q, q_dtype, ldq, q_heads, scale, window, sinks, works
 
 def cider_kv4_attention_workspace_bytes(b, q_heads, window, sinks) -> int:
     return int(load().cider_kv4_attention_workspace_bytes(_batch(b), q_heads, window, sinks))
+
+
+def cider_kv4_attention_shared(b, runs, q, q_dtype, ldq, q_heads, scale, workspace, workspace_bytes, y, y_dtype, ldy,
+                               stream=None, check=True):
+    st = load().cider_kv4_attention_shared(_batch(b), _batch(runs), _ptr(q), q_dtype, ldq, q_heads, scale,
+                                           _ptr(workspace), workspace_bytes, _ptr(y), y_dtype, ldy, _stream(stream))
+    return _ret(st, "cider_kv4_attention_shared", check)
+
+
+def cider_kv4_attention_shared_workspace_bytes(b, runs, q_heads) -> int:
+    return int(load().cider_kv4_attention_shared_workspace_bytes(_batch(b), _batch(runs), q_heads))
 
 
 def cider_kv4_set_tiles(columns: int) -> int:

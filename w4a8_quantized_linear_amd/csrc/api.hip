@@ -504,6 +504,35 @@ cider_status check_kv4_attention(const cider_kv4_batch *b, int64_t q_heads, int6
     return CIDER_OK;
 }
 
+// Sizes of the runs of a call; *none: there is nothing to share, which makes the call an
+// ordinary one.
+cider_status check_kv4_runs(const cider_kv4_batch *b, const cider_kv4_runs *r, int64_t q_heads, bool *none)
+{
+    if (!r || r->groups < 0 || r->max_rows < 0 || r->max_shared_len < 0 ||
+        r->max_shared_len > b->max_pages * cider::kPageTokens)
+        return CIDER_ERR_INVALID_ARG;
+    if (r->groups > kMaxInt || r->max_rows > kMaxTokens)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    *none = r->groups == 0 || r->max_rows == 0 || r->max_shared_len < cider::kPageTokens;
+    // workgroups, as for the batch
+    const int64_t pairs = (r->max_rows < b->rows ? r->max_rows : b->rows) * (q_heads / b->kv_heads);
+    const int64_t heads = r->groups * b->kv_heads;
+    if (!*none && (heads > kMaxInt || pairs > kMaxInt / heads))
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    return CIDER_OK;
+}
+
+cider::Kv4Runs kv4_runs_args(const cider_kv4_batch *b, const cider_kv4_runs *r)
+{
+    cider::Kv4Runs a{};
+    a.group_start = r->group_start;
+    a.shared_len = r->shared_len;
+    a.groups = (int)r->groups;
+    a.max_rows = (int)(r->max_rows < b->rows ? r->max_rows : b->rows);
+    a.max_pages = (int)(r->max_shared_len / cider::kPageTokens);
+    return a;
+}
+
 cider::Kv4AttentionArgs kv4_attention_args(const cider_kv4_batch *b, int64_t q_heads, int64_t window,
                                            int64_t sinks)
 {
@@ -514,6 +543,49 @@ cider::Kv4AttentionArgs kv4_attention_args(const cider_kv4_batch *b, int64_t q_h
     a.window = (int)(window < kMaxTokens ? window : 0);  // a window past every length hides nothing
     a.sinks = (int)(sinks < kMaxTokens ? sinks : kMaxTokens);
     return a;
+}
+
+// Either attention call; runs: null for the ordinary one.
+cider_status run_kv4_attention(const cider_kv4_batch *b, const cider_kv4_runs *runs, const void *q, int q_dtype,
+                               int64_t ldq, int64_t q_heads, float scale, int64_t window, int64_t sinks,
+                               void *workspace, size_t workspace_bytes, void *y, int y_dtype, int64_t ldy,
+                               void *stream)
+{
+    cider_status st = check_kv4_attention(b, q_heads, window, sinks);
+    if (st != CIDER_OK)
+        return st;
+    bool none = true;
+    if (runs && (st = check_kv4_runs(b, runs, q_heads, &none)) != CIDER_OK)
+        return st;
+    const int64_t width = q_heads * b->head_dim;
+    if (!dtype_ok(q_dtype) || !dtype_ok(y_dtype) || ldq < width || ldy < width ||
+        !(scale > 0.0f && std::isfinite(scale)))  // NaN fails too
+        return CIDER_ERR_INVALID_ARG;
+    if (kv4_empty(b))
+        return CIDER_OK;
+    if (!q || !y || (!none && (!runs->group_start || !runs->shared_len)))
+        return CIDER_ERR_INVALID_ARG;
+    st = check_kv4_pointers(b);
+    if (st != CIDER_OK)
+        return st;
+    if (!aligned16(q) || !aligned16(y) || ldq % 8 != 0 || ldy % 8 != 0 || !aligned16(workspace) ||
+        (!none && (!aligned4(runs->group_start) || !aligned4(runs->shared_len))))
+        return CIDER_ERR_MISALIGNED;
+    cider::Kv4AttentionArgs a = kv4_attention_args(b, q_heads, window, sinks);
+    if (!none && (!workspace || workspace_bytes < cider::kv4_shared_workspace(a, kv4_runs_args(b, runs))))
+        return CIDER_ERR_WORKSPACE;
+    if (!device_usable())
+        return CIDER_ERR_NO_DEVICE;
+    a.q = static_cast<const uint16_t *>(q);
+    a.y = static_cast<uint16_t *>(y);
+    a.ldq = ldq;
+    a.ldy = ldy;
+    a.q_dtype = q_dtype;
+    a.y_dtype = y_dtype;
+    a.scale = scale;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return from_hip(none ? cider::launch_kv4_attention(a, workspace, workspace_bytes, s)
+                         : cider::launch_kv4_attention_shared(a, kv4_runs_args(b, runs), workspace, s));
 }
 
 }  // namespace
@@ -803,33 +875,8 @@ cider_status cider_kv4_attention(const cider_kv4_batch *b, const void *q, int q_
                                  void *workspace, size_t workspace_bytes, void *y, int y_dtype,
                                  int64_t ldy, void *stream)
 {
-    cider_status st = check_kv4_attention(b, q_heads, window, sinks);
-    if (st != CIDER_OK)
-        return st;
-    const int64_t width = q_heads * b->head_dim;
-    if (!dtype_ok(q_dtype) || !dtype_ok(y_dtype) || ldq < width || ldy < width ||
-        !(scale > 0.0f && std::isfinite(scale)))  // NaN fails too
-        return CIDER_ERR_INVALID_ARG;
-    if (kv4_empty(b))
-        return CIDER_OK;
-    if (!q || !y)
-        return CIDER_ERR_INVALID_ARG;
-    st = check_kv4_pointers(b);
-    if (st != CIDER_OK)
-        return st;
-    if (!aligned16(q) || !aligned16(y) || ldq % 8 != 0 || ldy % 8 != 0 || !aligned16(workspace))
-        return CIDER_ERR_MISALIGNED;
-    if (!device_usable())
-        return CIDER_ERR_NO_DEVICE;
-    cider::Kv4AttentionArgs a = kv4_attention_args(b, q_heads, window, sinks);
-    a.q = static_cast<const uint16_t *>(q);
-    a.y = static_cast<uint16_t *>(y);
-    a.ldq = ldq;
-    a.ldy = ldy;
-    a.q_dtype = q_dtype;
-    a.y_dtype = y_dtype;
-    a.scale = scale;
-    return from_hip(cider::launch_kv4_attention(a, workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
+    return run_kv4_attention(b, nullptr, q, q_dtype, ldq, q_heads, scale, window, sinks, workspace,
+                             workspace_bytes, y, y_dtype, ldy, stream);
 }
 
 size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_heads,
@@ -838,6 +885,28 @@ size_t cider_kv4_attention_workspace_bytes(const cider_kv4_batch *b, int64_t q_h
     if (check_kv4_attention(b, q_heads, window, sinks) != CIDER_OK || kv4_empty(b))
         return 0;
     return cider::kv4_attention_workspace(kv4_attention_args(b, q_heads, window, sinks));
+}
+
+cider_status cider_kv4_attention_shared(const cider_kv4_batch *b, const cider_kv4_runs *runs,
+                                        const void *q, int q_dtype, int64_t ldq, int64_t q_heads,
+                                        float scale, void *workspace, size_t workspace_bytes,
+                                        void *y, int y_dtype, int64_t ldy, void *stream)
+{
+    if (!runs)
+        return CIDER_ERR_INVALID_ARG;
+    return run_kv4_attention(b, runs, q, q_dtype, ldq, q_heads, scale, 0, 0, workspace, workspace_bytes, y,
+                             y_dtype, ldy, stream);
+}
+
+size_t cider_kv4_attention_shared_workspace_bytes(const cider_kv4_batch *b,
+                                                  const cider_kv4_runs *runs, int64_t q_heads)
+{
+    bool none = true;
+    if (check_kv4_attention(b, q_heads, 0, 0) != CIDER_OK || check_kv4_runs(b, runs, q_heads, &none) != CIDER_OK ||
+        kv4_empty(b))
+        return 0;
+    const cider::Kv4AttentionArgs a = kv4_attention_args(b, q_heads, 0, 0);
+    return none ? cider::kv4_attention_workspace(a) : cider::kv4_shared_workspace(a, kv4_runs_args(b, runs));
 }
 
 int cider_kv4_set_tiles(int columns)

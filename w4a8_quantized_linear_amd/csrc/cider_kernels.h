@@ -177,7 +177,21 @@ struct Kv4AttentionArgs {
     float scale;
     int window, sinks;  // window 0: none
     int tiles;          // columns of a tile (16, 128, 256), 0: by sizes (test hook)
+    bool flat;          // every row sees max_kv_len tokens (shared prefixes); for the estimates
 };
+// Runs of sequences that hold the same first pages (cider_kv4_runs).
+struct Kv4Runs {
+    const int32_t *group_start;  // [groups + 1]
+    const int32_t *shared_len;   // [groups]
+    int groups, max_rows;        // max_rows: of all sequences of a run
+    int max_pages;               // whole pages of a shared prefix
+};
+// The attention with each run's shared pages read once for all its rows; window 0.
+// The scratch is needed.
+size_t kv4_shared_workspace(const Kv4AttentionArgs &a, const Kv4Runs &r);
+hipError_t launch_kv4_attention_shared(const Kv4AttentionArgs &a, const Kv4Runs &r, void *workspace,
+                                       hipStream_t stream);
+
 // Scratch with which the call splits as far as it would, and the call itself
 // (less scratch, or none: fewer splits).
 size_t kv4_attention_workspace(const Kv4AttentionArgs &a);

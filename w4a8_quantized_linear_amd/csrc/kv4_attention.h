@@ -127,7 +127,25 @@ struct Kv4Launch {
     float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
                        // times 2^-sum_bits(pages),
     float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
+    // Launches over shared prefixes and over what lies behind them leave parts only, of
+    // one sum_bits(sum_pages), in slots slot0 .. slot0 + splits - 1 of `slots`; the last
+    // split has all that is left of a tile's pages.
+    Kv4Runs runs;
+    int slots, slot0, sum_pages, front_pages;  // front_pages: of a part over shared ones
 };
+
+// Which pages a launch is for: all that a tile sees; those that a run of sequences
+// shares, for all of the run's rows; those behind the shared ones.
+enum class Pages { All, Shared, Own };
+
+template <Pages PAGES>
+__device__ __forceinline__ int last_page_of(const Kv4Launch &n, int split, int begin, int count)
+{
+    if constexpr (PAGES == Pages::All)
+        return n.splits > 1 && begin + n.pages < count ? begin + n.pages : count;
+    else
+        return split < n.splits - 1 && begin + n.pages < count ? begin + n.pages : count;
+}
 
 __device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
 __device__ __forceinline__ f32x4 ldexp_f(f32x4 x, int e)
@@ -381,31 +399,116 @@ __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, 
     return r;
 }
 
+// A run of sequences that share their first pages; pages 0 where there is none, or the
+// device's numbers are not sound.
+struct Run {
+    int first, row0, n, pages;  // its first sequence, its rows
+};
+__device__ __forceinline__ Run run_of(const Kv4Args &a, const Kv4Runs &r, int g)
+{
+    Run run = {r.group_start[g], 0, 0, 0};
+    const int end = r.group_start[g + 1];
+    if (run.first < 0 || end <= run.first || end > a.batch)
+        return run;
+    run.row0 = a.row_start[run.first];
+    const int last = a.row_start[end];
+    if (run.row0 < 0 || last < run.row0 || last > a.rows || last - run.row0 > r.max_rows)
+        return run;
+    run.n = last - run.row0;
+    const int pages = r.shared_len[g] / kPageTokens;
+    run.pages = pages < 0 ? 0 : (pages > r.max_pages ? r.max_pages : pages);
+    return run;
+}
+
+// The pages that a sequence's rows leave to its run: 0 for a sequence of no run, or one
+// whose rows do not all stand behind the shared pages.
+__device__ __forceinline__ int shared_pages(const Kv4Args &a, const Kv4Runs &r, int b, const Kv4Sequence &s)
+{
+    int lo = 0, hi = r.groups;  // the last group that starts at b or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (r.group_start[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    if (b < r.group_start[lo] || b >= r.group_start[lo + 1])
+        return 0;
+    const Run run = run_of(a, r, lo);
+    const bool in = s.row0 >= run.row0 && s.row0 + s.n <= run.row0 + run.n;
+    return in && s.kv - s.n >= run.pages * kPageTokens ? run.pages : 0;
+}
+
 // A tile of COLS columns of one (sequence, kv head): columns are the pairs
-// (row, query head of the group), c = row * G + g.
+// (row, query head of the group), c = row * G + g.  Over shared pages: of one (run, kv
+// head), all of whose rows see all tokens.
 struct Tile {
     Kv4Sequence seq;
+    int b;                 // whose page table
     int h, G, tile, cols;  // cols: columns of the sequence
     int p_lo, p_hi;        // positions of the tile's first and last column
+    int shared;            // pages in front of the range, left to the sequence's run
     PageRange range;
 };
 
-template <int COLS>
-__device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, int b, int h, int tile, Tile &t)
+template <int COLS, Pages PAGES>
+__device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int b, int h, int tile, Tile &t)
 {
-    t.seq = kv4_sequence(a.kv, b);
     t.h = h;
     t.G = a.q_heads / a.kv.kv_heads;
     t.tile = tile;
+    t.b = b;
+    t.shared = 0;
+    if constexpr (PAGES == Pages::Shared) {
+        const Run run = run_of(a.kv, n.runs, b);
+        if (run.pages == 0)
+            return false;
+        t.b = run.first;
+        t.seq.row0 = run.row0;
+        t.seq.n = run.n;
+        t.seq.kv = run.pages * kPageTokens;
+    } else {
+        t.seq = kv4_sequence(a.kv, b);
+    }
     t.cols = t.seq.n * t.G;
     if ((int64_t)tile * COLS >= t.cols)
         return false;
+    if constexpr (PAGES == Pages::Shared) {
+        t.p_lo = t.p_hi = t.seq.kv - 1;
+        t.range = pages_seen(t.p_lo, t.p_hi, 0, 0);
+        return true;
+    }
     const int first = t.seq.kv - t.seq.n;
     const int last = t.cols - tile * COLS < COLS ? t.cols - 1 : tile * COLS + COLS - 1;
     t.p_lo = first + tile * COLS / t.G;
     t.p_hi = first + last / t.G;
     t.range = pages_seen(t.p_lo, t.p_hi, a.window, a.sinks);
+    if constexpr (PAGES == Pages::Own) {  // window 0: the range is [0, count)
+        t.shared = shared_pages(a.kv, n.runs, b, t.seq);
+        t.range.first += t.shared;
+        t.range.count -= t.shared;
+    }
     return true;
+}
+
+// The position of a row of the tile's sequence.
+template <Pages PAGES>
+__device__ __forceinline__ int position_of(const Tile &t, int row)
+{
+    return PAGES == Pages::Shared ? t.p_hi : t.seq.kv - t.seq.n + row;
+}
+
+// Whether a tile's results are parts.  (Own pages: a tile that sees none, rows in front
+// of their sequence, has its zeros at once.)
+template <Pages PAGES>
+__device__ __forceinline__ bool in_parts(const Kv4Launch &n, const Tile &t)
+{
+    return PAGES == Pages::All ? n.splits > 1 && t.range.count > n.pages : PAGES == Pages::Shared || t.range.count > 0;
+}
+template <Pages PAGES>
+__device__ __forceinline__ int64_t part_of(const Kv4Launch &n, int64_t pair, int split)
+{
+    return PAGES == Pages::All ? pair * n.splits + split : pair * n.slots + n.slot0 + split;
 }
 
 // The tile's first position is its newest token that all columns may see (false: their
@@ -463,7 +566,7 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b, int dtype)
 
 // The kernels, one launch each: tiles of 16 columns (few rows), of 128 or 256.
 constexpr int kFewCols = 16;
-hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
-hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream);
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream);
 
 }  // namespace cider

@@ -10,6 +10,11 @@
 // second small launch joins them in chunk order:
 //   m = max m_i, y = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
 // Chunk boundaries depend on the sizes of the call alone, not on timing.
+//
+// Shared prefixes.  Sequences of a run hold the same first pages, and all rows of the
+// run see all of their tokens.  So one launch takes the run's rows as columns over the
+// shared pages, without any mask, another each sequence's over the pages behind, and
+// the same join puts the parts of both together.
 #include "kv4_attention.h"
 
 namespace cider {
@@ -18,18 +23,39 @@ namespace {
 constexpr int kMaxSplits = 256;
 
 // The (row, query head) pair of a number, and the parts it has (0: none, its
-// workgroup wrote the output itself or the pair is not there).
-template <int COLS>
-__device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int64_t id, Tile &t, int &col)
+// workgroup wrote the output itself or the pair is not there).  With shared
+// prefixes (SHARED) the first `front` are over the shared pages.
+template <int COLS, bool SHARED>
+__device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int64_t id, Tile &t, int &col, int &front)
 {
+    constexpr Pages PAGES = SHARED ? Pages::Own : Pages::All;
     const int64_t cols = (int64_t)a.kv.max_rows * (a.q_heads / a.kv.kv_heads);
     col = (int)(id % cols);
+    front = 0;
     const int64_t bh = id / cols;
     const bool mine = bh < (int64_t)a.kv.kv_heads * a.kv.batch &&
-                      tile_of<COLS>(a, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, t) &&
-                      col < t.cols && t.range.count > n.pages;
-    return mine ? (t.range.count + n.pages - 1) / n.pages : 0;
+                      tile_of<COLS, PAGES>(a, n, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, t) &&
+                      col < t.cols && in_parts<PAGES>(n, t);
+    if (!mine)
+        return 0;
+    const int parts = (t.range.count + n.pages - 1) / n.pages;
+    if constexpr (!SHARED)
+        return parts;
+    front = (t.shared + n.front_pages - 1) / n.front_pages;
+    front = front < n.slot0 ? front : n.slot0;
+    return front + (parts < n.splits ? parts : n.splits);
 }
+
+// Where a pair's part is among its own.
+template <bool SHARED>
+__device__ __forceinline__ int slot_of(const Kv4Launch &n, int i, int front)
+{
+    return SHARED && i >= front ? n.slot0 + i - front : i;
+}
+template <bool SHARED>
+__device__ __forceinline__ int64_t slots_of(const Kv4Launch &n) { return SHARED ? n.slots : n.splits; }
+template <bool SHARED>
+__device__ __forceinline__ int part_bits(const Kv4Launch &n) { return sum_bits(SHARED ? n.sum_pages : n.pages); }
 
 __device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Tile &t, int col, int d4, f32x4 o)
 {
@@ -40,25 +66,27 @@ __device__ __forceinline__ void write_joined(const Kv4AttentionArgs &a, const Ti
 // At most PARTS parts: D / 4 lanes a pair, each with 4 elements of every part.
 // All loads are on their way at once: a chain of two (lengths, then statistics
 // and parts), 2.9 us for 32 pairs of 4 parts, 4.6 for 2048, the launch included.
-template <int D, int COLS, int PARTS>
+template <int D, int COLS, int PARTS, bool SHARED>
 __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int LANES = D / 4;
     Tile t;
-    int col;
-    const int parts = parts_of<COLS>(a, n, (int64_t)kv4_workgroup() * (256 / LANES) + (int)threadIdx.x / LANES, t, col);
+    int col, front;
+    const int parts = parts_of<COLS, SHARED>(a, n, (int64_t)kv4_workgroup() * (256 / LANES) + (int)threadIdx.x / LANES, t,
+                                             col, front);
     if (parts == 0)
         return;
     const int d4 = (int)threadIdx.x % LANES;
-    const int64_t at = pair_of(a, t, col) * n.splits;
+    const int64_t at = pair_of(a, t, col) * slots_of<SHARED>(n);
     const float2 *stat = reinterpret_cast<const float2 *>(n.part_stat) + at;
     const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * LANES + d4;
     float2 ml[PARTS];  // maximum, sum
     f32x4 v[PARTS];
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        ml[i] = stat[i < parts ? i : 0];
-        v[i] = part[(i < parts ? i : 0) * LANES];
+        const int slot = slot_of<SHARED>(n, i < parts ? i : 0, front);
+        ml[i] = stat[slot];
+        v[i] = part[slot * LANES];
     }
     float m = ml[0].x, l = 0.0f;
 #pragma unroll
@@ -72,7 +100,7 @@ __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, K
         f[i] = i < parts && ml[i].y != 0.0f ? __builtin_amdgcn_exp2f(ml[i].x - m) : 0.0f;
         l += ml[i].y * f[i];
     }
-    const float inv = ldexp_f(reciprocal(l), sum_bits(n.pages));
+    const float inv = ldexp_f(reciprocal(l), part_bits<SHARED>(n));
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
@@ -84,7 +112,7 @@ __global__ __launch_bounds__(256) void kv4_join_few_kernel(Kv4AttentionArgs a, K
 // the lane of its number; then groups of D / 4 lanes add up the parts, 16 bytes a
 // lane.  A chain of three loads (lengths, statistics, parts): 4.6 us for 32 pairs
 // of 64 parts, the launch included.
-template <int D, int COLS>
+template <int D, int COLS, bool SHARED>
 __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     constexpr int GROUPS = 256 / (D / 4);
@@ -93,15 +121,16 @@ __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, 
     __shared__ float wave_m[4], wave_l[4];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x;
     Tile t;
-    int col;
-    const int parts = parts_of<COLS>(a, n, kv4_workgroup(), t, col);
+    int col, front;
+    const int parts = parts_of<COLS, SHARED>(a, n, kv4_workgroup(), t, col, front);
     if (parts == 0)
         return;
-    const int64_t at = pair_of(a, t, col) * n.splits;
+    const int64_t at = pair_of(a, t, col) * slots_of<SHARED>(n);
     float m = -__builtin_inff(), l = 0.0f;
     if (lane < parts) {
-        m = n.part_stat[2 * (at + lane)];
-        l = n.part_stat[2 * (at + lane) + 1];
+        const int64_t slot = at + slot_of<SHARED>(n, lane, front);
+        m = n.part_stat[2 * slot];
+        l = n.part_stat[2 * slot + 1];
     }
     float top = wave_max(m);
     if (lane % 64 == 0)
@@ -123,13 +152,13 @@ __global__ __launch_bounds__(256) void kv4_join_many_kernel(Kv4AttentionArgs a, 
 #pragma unroll
     for (int w = 0; w < 4; ++w)
         l += wave_l[w];
-    const float inv = ldexp_f(reciprocal(l), sum_bits(n.pages));
+    const float inv = ldexp_f(reciprocal(l), part_bits<SHARED>(n));
     const int g = lane / (D / 4), d4 = lane % (D / 4);
     f32x4 o = {0, 0, 0, 0};
     const f32x4 *part = reinterpret_cast<const f32x4 *>(n.part) + at * (D / 4) + d4;
 #pragma unroll 4
     for (int i = g; i < parts; i += GROUPS)
-        o += part[(int64_t)i * (D / 4)] * (factor[i] * inv);
+        o += part[(int64_t)slot_of<SHARED>(n, i, front) * (D / 4)] * (factor[i] * inv);
     sums[g][d4] = o;
     __syncthreads();
     if (g != 0)
@@ -166,6 +195,8 @@ int64_t units_of(const Kv4AttentionArgs &a, int cols)
 // Pages that a tile sees on average: a prompt's rows see what lies before them.
 double mean_pages(const Kv4AttentionArgs &a, int cols)
 {
+    if (a.flat)
+        return (double)most_pages(a, cols);
     const double mean = (a.kv.max_kv_len - 0.5 * a.kv.max_rows) / kPageTokens + 0.5, most = (double)most_pages(a, cols);
     return mean < most ? mean : most;
 }
@@ -288,62 +319,136 @@ Kv4Launch plan(const Kv4AttentionArgs &a)
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-size_t part_bytes(const Kv4AttentionArgs &a, const Kv4Launch &n)
+size_t part_bytes(const Kv4AttentionArgs &a, int slots)
 {
-    return round256((size_t)a.kv.rows * a.q_heads * n.splits * a.kv.head_dim * sizeof(float));
+    return round256((size_t)a.kv.rows * a.q_heads * slots * a.kv.head_dim * sizeof(float));
 }
 
-size_t bytes_of(const Kv4AttentionArgs &a, const Kv4Launch &n)
+size_t bytes_of(const Kv4AttentionArgs &a, int slots)
 {
-    return n.splits < 2 ? 0
-                        : part_bytes(a, n) + round256((size_t)a.kv.rows * a.q_heads * n.splits * 2 * sizeof(float));
+    return part_bytes(a, slots) + round256((size_t)a.kv.rows * a.q_heads * slots * 2 * sizeof(float));
 }
 
-template <int D, int COLS>
+void use_workspace(const Kv4AttentionArgs &a, Kv4Launch &n, int slots, void *workspace)
+{
+    n.part = static_cast<float *>(workspace);
+    n.part_stat = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a, slots));
+}
+
+template <int D, int COLS, bool SHARED>
 hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned pairs = (unsigned)most_columns(a) * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
+    const int parts = SHARED ? n.slots : n.splits;
     constexpr unsigned PAIRS = 256 / (D / 4);
     // 5 to 16 parts: a workgroup per pair while there are few pairs (256 of 16
     // parts: the call 16.3 us, 17.0 by lanes; 4096 of 16 and 8192 of 8: 75 and 125
     // us, 71 and 114 by lanes)
-    if (n.splits <= 4)
-        return kv4_launch(kv4_join_few_kernel<D, COLS, 4>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
-    if (n.splits <= 16 && pairs >= 2048)
-        return kv4_launch(kv4_join_few_kernel<D, COLS, 16>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
-    return kv4_launch(kv4_join_many_kernel<D, COLS>, pairs, 256, stream, a, n);
+    if (parts <= 4)
+        return kv4_launch(kv4_join_few_kernel<D, COLS, 4, SHARED>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
+    if (parts <= 16 && pairs >= 2048)
+        return kv4_launch(kv4_join_few_kernel<D, COLS, 16, SHARED>, (pairs + PAIRS - 1) / PAIRS, 256, stream, a, n);
+    return kv4_launch(kv4_join_many_kernel<D, COLS, SHARED>, pairs, 256, stream, a, n);
 }
 
-template <int D>
+template <int D, bool SHARED>
 hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     if (n.cols == kFewCols)
-        return launch_join<D, kFewCols>(a, n, stream);
-    return n.cols == 128 ? launch_join<D, 128>(a, n, stream) : launch_join<D, 256>(a, n, stream);
+        return launch_join<D, kFewCols, SHARED>(a, n, stream);
+    return n.cols == 128 ? launch_join<D, 128, SHARED>(a, n, stream) : launch_join<D, 256, SHARED>(a, n, stream);
+}
+
+template <bool SHARED>
+hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    return a.kv.head_dim == 64 ? launch_join<64, SHARED>(a, n, stream) : launch_join<128, SHARED>(a, n, stream);
+}
+
+hipError_t launch_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+{
+    return n.cols == kFewCols ? launch_kv4_few_rows(a, n, pages, stream) : launch_kv4_many_rows(a, n, pages, stream);
+}
+
+// The launches over shared pages (front) and over those behind them (own), each
+// planned as a call of its own: the runs as sequences of max_pages pages, and the
+// sequences with what the longest has behind the longest prefix.  A sequence that has
+// more (it is in no run, its run shares less) gives it to its last split.
+struct SharedPlan {
+    Kv4Launch front, own;
+};
+
+SharedPlan plan_shared(const Kv4AttentionArgs &a, const Kv4Runs &r)
+{
+    const int all = (a.kv.max_kv_len + kPageTokens - 1) / kPageTokens;
+    // half of what a join takes at most
+    auto planned = [](const Kv4AttentionArgs &x, int pages) {
+        Kv4Launch n = plan(x);
+        if (n.splits < 2) {
+            n.splits = 1;
+            n.pages = pages;
+        } else if (n.splits > kMaxSplits / 2) {
+            n.pages = (n.pages * n.splits + kMaxSplits / 2 - 1) / (kMaxSplits / 2);
+            n.splits = kMaxSplits / 2;
+        }
+        return n;
+    };
+    Kv4AttentionArgs f = a;
+    f.kv.batch = r.groups;
+    f.kv.max_rows = r.max_rows;
+    f.kv.max_kv_len = r.max_pages * kPageTokens;
+    f.flat = true;
+    Kv4AttentionArgs o = a;
+    o.kv.max_kv_len -= r.max_pages * kPageTokens;
+    const int least = a.kv.max_rows < a.kv.max_kv_len ? a.kv.max_rows : a.kv.max_kv_len;
+    o.kv.max_kv_len = o.kv.max_kv_len < least ? least : o.kv.max_kv_len;
+    SharedPlan p = {planned(f, r.max_pages), planned(o, all)};
+    for (Kv4Launch *n : {&p.front, &p.own}) {
+        n->runs = r;
+        n->slots = p.front.splits + p.own.splits;
+        n->sum_pages = all > r.max_pages ? all : r.max_pages;
+        n->front_pages = p.front.pages;
+    }
+    p.own.slot0 = p.front.splits;
+    return p;
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace(const Kv4AttentionArgs &a) { return bytes_of(a, plan(a)); }
+size_t kv4_attention_workspace(const Kv4AttentionArgs &a)
+{
+    const Kv4Launch n = plan(a);
+    return n.splits < 2 ? 0 : bytes_of(a, n.splits);
+}
 
 hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size_t workspace_bytes,
                                 hipStream_t stream)
 {
     Kv4Launch n = plan(a);
-    while (n.splits > 1 && (!workspace || bytes_of(a, n) > workspace_bytes)) {
+    while (n.splits > 1 && (!workspace || bytes_of(a, n.splits) > workspace_bytes)) {
         // fewer, longer chunks until the parts fit
         n.pages = n.pages * 2;
         n.splits = (n.splits + 1) / 2;
     }
-    if (n.splits > 1) {
-        n.part = static_cast<float *>(workspace);
-        n.part_stat = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a, n));
-    }
-    const hipError_t e = n.cols == kFewCols ? launch_kv4_few_rows(a, n, stream)
-                                            : launch_kv4_many_rows(a, n, stream);
+    if (n.splits > 1)
+        use_workspace(a, n, n.splits, workspace);
+    const hipError_t e = launch_pages(a, n, Pages::All, stream);
     if (e != hipSuccess || n.splits < 2)
         return e;
-    return a.kv.head_dim == 64 ? launch_join<64>(a, n, stream) : launch_join<128>(a, n, stream);
+    return launch_join<false>(a, n, stream);
+}
+
+size_t kv4_shared_workspace(const Kv4AttentionArgs &a, const Kv4Runs &r) { return bytes_of(a, plan_shared(a, r).own.slots); }
+
+hipError_t launch_kv4_attention_shared(const Kv4AttentionArgs &a, const Kv4Runs &r, void *workspace, hipStream_t stream)
+{
+    SharedPlan p = plan_shared(a, r);
+    for (Kv4Launch *n : {&p.front, &p.own})
+        use_workspace(a, *n, n->slots, workspace);
+    hipError_t e = launch_pages(a, p.front, Pages::Shared, stream);
+    if (e == hipSuccess)
+        e = launch_pages(a, p.own, Pages::Own, stream);
+    return e == hipSuccess ? launch_join<true>(a, p.own, stream) : e;
 }
 
 }  // namespace cider

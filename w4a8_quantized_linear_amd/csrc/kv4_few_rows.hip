@@ -383,8 +383,8 @@ __device__ __forceinline__ bool page_outputs(State<D, GS> &st, const PageData<D,
 // A wavefront's pages, every WAVES-th of begin .. end - 1 from its own number on, and
 // its part of the outputs (element stride 1, columns D + 4 apart), maxima and sums.
 // False where columns that were alike no longer are: nothing is written then.
-template <int D, int GS, int WAVES, bool FINE, bool ONCE, Columns KIND>
-__device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, const Tile &t, int b, int begin,
+template <int D, int GS, int WAVES, bool FINE, bool ONCE, Columns KIND, Pages PAGES>
+__device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, const Tile &t, int begin,
                                            int end, int wave, const int lane, int *own, float (*part)[D + 4],
                                            float *part_m, float *part_l)
 {
@@ -396,7 +396,7 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
     const int col = t.tile * kCols + c;
     const bool valid = col < t.cols;
     const int row = valid ? col / t.G : 0;
-    const int p = valid ? t.seq.kv - t.seq.n + row : -1;
+    const int p = valid ? position_of<PAGES>(t, row) : -1;
 
     // q is asked for first and used last: the first page's codes are on their
     // way while it is scaled
@@ -408,7 +408,7 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
         for (int m = 0; m < NM; ++m)
             qw[m] = *reinterpret_cast<const uint4 *>(q + 32 * m);
     }
-    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const int32_t *table = a.kv.pages + (int64_t)t.b * a.kv.max_pages;
     const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
     const int64_t page_bytes = (int64_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
     // a page number outside the cache is never followed: page 0 is loaded in
@@ -505,7 +505,7 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
         return false;
     // lane (j, c) holds elements 16 x + 4 j .. + 3 of column c
     st.l = column_sum(st.l);
-    const int less = sum_bits(n.splits > 1 ? n.pages : t.range.count);
+    const int less = sum_bits(PAGES != Pages::All ? n.sum_pages : n.splits > 1 ? n.pages : t.range.count);
 #pragma unroll
     for (int x = 0; x < NT; ++x)
         *reinterpret_cast<f32x4 *>(&part[c][16 * x + 4 * j]) =
@@ -524,7 +524,7 @@ __device__ __forceinline__ bool wave_pages(const Kv4AttentionArgs &a, const Kv4L
 // loop; a batch of 64 over up to 8192 tokens, one row each, 71 and 98).  Pages read
 // past the caches want the registers of 2 wavefronts a SIMD rather than a third
 // (64 x 2 rows over 4000 tokens 56.0 us, 57.6 with 3), others the third.
-template <int D, int GS, int WAVES, bool FINE, bool ONCE, bool ONE>
+template <int D, int GS, int WAVES, bool FINE, bool ONCE, bool ONE, Pages PAGES>
 __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ? 3 : 2)) void kv4_few_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     __shared__ __align__(16) float part[WAVES][kCols][D + 4];
@@ -536,25 +536,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
     unsigned id = kv4_workgroup();
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
-    const int b = (int)(id % (unsigned)a.kv.batch);
-    id /= (unsigned)a.kv.batch;
+    const unsigned batch = (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const int b = (int)(id % batch);
+    id /= batch;
     const int split = (int)(id % (unsigned)n.splits), tile = (int)(id / (unsigned)n.splits);
     Tile t;
-    if (!tile_of<kCols>(a, b, head, tile, t))
+    if (!tile_of<kCols, PAGES>(a, n, b, head, tile, t))
         return;
     const int begin = n.splits > 1 ? split * n.pages : 0;
     if (split > 0 && begin >= t.range.count)
         return;
-    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+    const int end = last_page_of<PAGES>(n, split, begin, t.range.count);
 
     int lane = threadIdx.x & 63;
     if constexpr (ONE) {
-        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::One>(a, n, t, b, begin, end, wave, lane, nullptr, part[wave], part_m[wave],
+        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::One, PAGES>(a, n, t, begin, end, wave, lane, nullptr, part[wave], part_m[wave],
                                                            part_l[wave]);
-    } else if (!wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Alike>(a, n, t, b, begin, end, wave, lane, nullptr, part[wave],
+    } else if (!wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Alike, PAGES>(a, n, t, begin, end, wave, lane, nullptr, part[wave],
                                                                      part_m[wave], part_l[wave])) {
         asm volatile("" : "+v"(lane));  // nothing of the first way kept
-        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Apart>(a, n, t, b, begin, end, wave, lane, own[wave][0], part[wave],
+        wave_pages<D, GS, WAVES, FINE, ONCE, Columns::Apart, PAGES>(a, n, t, begin, end, wave, lane, own[wave][0], part[wave],
                                                              part_m[wave], part_l[wave]);
     }
     __syncthreads();
@@ -577,8 +578,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
         for (int e = 0; e < PER; ++e)
             o[e] += part[w][oc][d0 + e] * f;
     }
-    if (n.splits > 1 && t.range.count > n.pages) {
-        const int64_t at = pair_of(a, t, ocol) * n.splits + split;
+    if (in_parts<PAGES>(n, t)) {
+        const int64_t at = part_of<PAGES>(n, pair_of(a, t, ocol), split);
 #pragma unroll
         for (int e = 0; e < PER; ++e)
             n.part[at * D + d0 + e] = o[e];
@@ -604,16 +605,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
 
 }  // namespace
 
-template <int WAVES, bool FINE, bool ONCE, bool ONE>
+template <int WAVES, bool FINE, bool ONCE, bool ONE, Pages PAGES = Pages::All>
 static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
-                          (unsigned)a.kv.batch;
+                          (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
     if (a.kv.head_dim == 64)
-        return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
+        return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE, ONE, PAGES>, grid, 64 * WAVES, stream, a, n);
     if (a.kv.group_size == 64)
-        return kv4_launch(kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
-    return kv4_launch(kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE, ONE>, grid, 64 * WAVES, stream, a, n);
+        return kv4_launch(kv4_few_rows_kernel<128, 64, WAVES, FINE, ONCE, ONE, PAGES>, grid, 64 * WAVES, stream, a, n);
+    return kv4_launch(kv4_few_rows_kernel<128, 128, WAVES, FINE, ONCE, ONE, PAGES>, grid, 64 * WAVES, stream, a, n);
 }
 
 template <int WAVES, bool FINE, bool ONCE>
@@ -630,9 +631,29 @@ static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStrea
     return n.once ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
 }
 
-hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+// Beside shared prefixes: all columns of a tile see all shared pages, so it has one
+// exponent for them however many rows there are.
+template <int WAVES, bool FINE>
+static hipError_t launch_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
 {
-    return n.waves == 8 ? launch<8>(a, n, stream) : launch<4>(a, n, stream);
+    if (pages == Pages::Shared)
+        return launch<WAVES, FINE, false, true, Pages::Shared>(a, n, stream);
+    return a.kv.max_rows == 1 ? launch<WAVES, FINE, false, true, Pages::Own>(a, n, stream)
+                              : launch<WAVES, FINE, false, false, Pages::Own>(a, n, stream);
+}
+
+template <int WAVES>
+static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+{
+    if (pages == Pages::All)
+        return launch<WAVES>(a, n, stream);
+    return a.y_dtype == DT_F16 ? launch_shared<WAVES, true>(a, n, pages, stream)
+                               : launch_shared<WAVES, false>(a, n, pages, stream);
+}
+
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+{
+    return n.waves == 8 ? launch<8>(a, n, pages, stream) : launch<4>(a, n, pages, stream);
 }
 
 }  // namespace cider

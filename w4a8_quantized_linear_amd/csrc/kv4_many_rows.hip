@@ -147,9 +147,9 @@ struct Lds {
 // column's difference, 32 instructions a group and page more.  APART does that.
 // Without it the workgroup, all wavefronts together, leaves off there and returns
 // false.
-template <int D, int GS, int COLS, bool APART>
+template <int D, int GS, int COLS, Pages PAGES, bool APART>
 __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const Kv4Launch &n, Lds<D, GS, COLS> &lds,
-                                               const Tile &t, int b, int split, int begin, int end, const int tid)
+                                               const Tile &t, int split, int begin, int end, const int tid)
 {
     constexpr int NG = D / GS;   // scales per token
     constexpr int NK = D / 16;   // score products per 32 tokens
@@ -164,16 +164,15 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane % 32, h = lane / 32;
     const float inf = __builtin_inff();
-    const int first = t.seq.kv - t.seq.n;  // position of row 0
     const int col0 = t.tile * COLS + wave * kWaveCols;
     const int col = col0 + c;
     const bool valid = col < t.cols;
     const int row = valid ? col / t.G : 0;
-    const int p = valid ? first + row : -1;
+    const int p = valid ? position_of<PAGES>(t, row) : -1;
     // positions of the wavefront's columns (hi below lo: it has none)
-    const int w_lo = first + col0 / t.G;
+    const int w_lo = position_of<PAGES>(t, col0 / t.G);
     const int w_last = col0 + kWaveCols <= t.cols ? col0 + kWaveCols - 1 : t.cols - 1;
-    const int w_hi = col0 < t.cols ? first + w_last / t.G : -1;
+    const int w_hi = col0 < t.cols ? position_of<PAGES>(t, w_last / t.G) : -1;
 
     // q is asked for first and used last: the first pages' codes are on their
     // way while it is scaled
@@ -185,7 +184,7 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         for (int k = 0; k < NK; ++k)
             qw[k] = *reinterpret_cast<const uint4 *>(at + 16 * k);
     }
-    const int32_t *table = a.kv.pages + (int64_t)b * a.kv.max_pages;
+    const int32_t *table = a.kv.pages + (int64_t)t.b * a.kv.max_pages;
     const uint8_t *heads = a.kv.cache + (int64_t)t.h * kv4_block_bytes(D, GS);
     const uint32_t page_bytes = (uint32_t)a.kv.kv_heads * kv4_block_bytes(D, GS);
     // a page number outside the cache is never followed: page 0 is loaded in
@@ -666,13 +665,14 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         return ldexp_f(f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]} * f,
                        exp_of(x * 32 / GS) + 24 - kTop - e);
     };
-    if (n.splits > 1 && t.range.count > n.pages) {
-        const int64_t at = pair_of(a, t, col) * n.splits + split;
+    if (in_parts<PAGES>(n, t)) {
+        const int64_t at = part_of<PAGES>(n, pair_of(a, t, col), split);
+        const int less = sum_bits(PAGES == Pages::All ? n.pages : n.sum_pages);
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) = result(x, i, 1.0f, sum_bits(n.pages));
+                *reinterpret_cast<f32x4 *>(n.part + at * D + 32 * x + 8 * i + 4 * h) = result(x, i, 1.0f, less);
         if (h == 0) {
             n.part_stat[2 * at] = m_run;
             n.part_stat[2 * at + 1] = l_run;
@@ -692,7 +692,7 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
     return true;
 }
 
-template <int D, int GS, int COLS>
+template <int D, int GS, int COLS, Pages PAGES>
 __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4AttentionArgs a, Kv4Launch n)
 {
     __shared__ Lds<D, GS, COLS> lds;
@@ -705,24 +705,25 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     unsigned id = kv4_workgroup();
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
-    const unsigned turn = id % (unsigned)a.kv.batch;
-    id /= (unsigned)a.kv.batch;
+    const unsigned batch = (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const unsigned turn = id % batch;
+    id /= batch;
     const int split = (int)(id % (unsigned)n.splits);
     const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
     if (tile < 0)
         return;
-    const int b = (int)((turn + (unsigned)tile) % (unsigned)a.kv.batch);
+    const int b = (int)((turn + (unsigned)tile) % batch);
     Tile t;
-    if (!tile_of<COLS>(a, b, head, tile, t))
+    if (!tile_of<COLS, PAGES>(a, n, b, head, tile, t))
         return;
     const int begin = n.splits > 1 ? split * n.pages : 0;
     if (split > 0 && begin >= t.range.count)
         return;
-    const int end = n.splits > 1 && begin + n.pages < t.range.count ? begin + n.pages : t.range.count;
+    const int end = last_page_of<PAGES>(n, split, begin, t.range.count);
 
     // a tile whose columns share no token goes the long way at once
     int tid = threadIdx.x;
-    if (tile_has_first(a, t) && many_rows_tile<D, GS, COLS, false>(a, n, lds, t, b, split, begin, end, tid))
+    if (tile_has_first(a, t) && many_rows_tile<D, GS, COLS, PAGES, false>(a, n, lds, t, split, begin, end, tid))
         return;
     // From the beginning, nothing of the first way kept: whatever both had in common
     // would cost that one its registers (2048 rows over 16384 tokens 603 us; with a
@@ -730,25 +731,29 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     // times as much).
     __syncthreads();
     asm volatile("" : "+v"(tid));
-    many_rows_tile<D, GS, COLS, true>(a, n, lds, t, b, split, begin, end, tid);
+    many_rows_tile<D, GS, COLS, PAGES, true>(a, n, lds, t, split, begin, end, tid);
 }
 
 }  // namespace
 
-template <int COLS>
+template <int COLS, Pages PAGES = Pages::All>
 static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
     const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
-                          (unsigned)a.kv.batch;
+                          (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
     if (a.kv.head_dim == 64)
-        return kv4_launch(kv4_many_rows_kernel<64, 64, COLS>, grid, COLS * 2, stream, a, n);
+        return kv4_launch(kv4_many_rows_kernel<64, 64, COLS, PAGES>, grid, COLS * 2, stream, a, n);
     if (a.kv.group_size == 64)
-        return kv4_launch(kv4_many_rows_kernel<128, 64, COLS>, grid, COLS * 2, stream, a, n);
-    return kv4_launch(kv4_many_rows_kernel<128, 128, COLS>, grid, COLS * 2, stream, a, n);
+        return kv4_launch(kv4_many_rows_kernel<128, 64, COLS, PAGES>, grid, COLS * 2, stream, a, n);
+    return kv4_launch(kv4_many_rows_kernel<128, 128, COLS, PAGES>, grid, COLS * 2, stream, a, n);
 }
 
-hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
 {
+    if (pages == Pages::Shared)
+        return n.cols == 256 ? launch<256, Pages::Shared>(a, n, stream) : launch<128, Pages::Shared>(a, n, stream);
+    if (pages == Pages::Own)
+        return n.cols == 256 ? launch<256, Pages::Own>(a, n, stream) : launch<128, Pages::Own>(a, n, stream);
     return n.cols == 256 ? launch<256>(a, n, stream) : launch<128>(a, n, stream);
 }
 
