@@ -283,6 +283,56 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
                                  int64_t N, int bits, int group_size, int y_dtype, void *y,
                                  void *stream);
 
+/* ---- Low-rank adapters -------------------------------------------------------
+ *
+ * Beside a product whose weights many requests share, each request's own
+ * correction of them: rows seg_start[i] .. seg_start[i + 1] - 1 of a call are
+ * segment i, with the adapter in slot[i],
+ *   t[r, j] = sum_k A[slot, j, k] * x[r, k]               j < slices * rank
+ *   y[r, n] = y_in[r, n] + scale[slot] * sum_j B[slot, n, j] * t[r, s(n) * rank + j]
+ * with s(n) the slice of output n: a fused product (QKV, gate and up) has an A of
+ * rank rows for each of its parts.  t and all sums are fp32 (t enters the second
+ * product with 16 significant bits or more), y is rounded once.  A slot outside
+ * [0, slots) is no adapter: y = y_in.  Adapters of a smaller rank have zeros in
+ * the rest of A or B.
+ *
+ * A segment whose rows are not inside [0, rows], or are more than max_rows, is
+ * left out, and its rows, like rows of no segment, stay as they are.  max_rows
+ * sizes the launches, so calls captured into a graph replay with any segments and
+ * slots within the bounds.  No row is in two segments.
+ *
+ * Envelope: rank a multiple of 8 up to 128, in_features a multiple of 64, 1 to 8
+ * slices whose ends are multiples of 64 and rise, in_features and outputs below
+ * 2^24, rows, max_rows <= 2^30, slots < 2^31, segments times the 16-row tiles of
+ * max_rows times outputs / 64 < 2^31; device pointers 16-byte aligned (int32 and
+ * scale arrays: 4), row strides multiples of 8.  segments, rows or max_rows 0 is a
+ * no-op. */
+#define CIDER_LORA_MAX_SLICES 8
+typedef struct {
+    const void *a;        /* device, [slots][slices * rank][in_features], of the call's dtype */
+    const void *b;        /* device, [slots][slice_end[slices - 1]][rank] */
+    const float *scale;   /* device, [slots], or null: 1 */
+    int64_t slots, rank, in_features, slices;
+    int64_t slice_end[CIDER_LORA_MAX_SLICES]; /* outputs of slice i end there */
+} cider_lora;
+
+/* Bytes of workspace with which the call uses as much of the GPU as it measured
+   faster (0 outside the envelope).  Needed at the least, else
+   CIDER_ERR_WORKSPACE: 4 * rows * slices * rank. */
+size_t cider_lora_workspace_bytes(const cider_lora *lora, int64_t segments, int64_t rows,
+                                  int64_t max_rows);
+
+/* Adds segments' adapters to a product's output.  x [rows][in_features], y_in, y
+   [rows][outputs] of type dtype with row strides ldx, ldy_in, ldy; y may be y_in
+   with the same stride (added in place), else it overlaps nothing.  Results do
+   not depend on timing; another workspace size may group the fp32 sums of t
+   otherwise.  Calls that share a workspace must be ordered (one stream). */
+cider_status cider_lora_add(const cider_lora *lora, const int32_t *seg_start, const int32_t *slot,
+                            int64_t segments, int64_t rows, int64_t max_rows, const void *x,
+                            int dtype, int64_t ldx, const void *y_in, int64_t ldy_in,
+                            void *workspace, size_t workspace_bytes, void *y, int64_t ldy,
+                            void *stream);
+
 /* ---- 4-bit key/value cache --------------------------------------------------
  *
  * What stands between the QKV product and the O product when a decoder serves:

@@ -51,10 +51,10 @@ def test_rotation_checks(turn, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(q_heads=0, q=None, q_out=None, ldq=0, ldo=0), YES), (dict(q_heads=2, ldq=256, ldo=256), YES),
+    (dict(), YES), (dict(q_out=P + 4096, ldo=2048), YES), (dict(q_heads=0, q=None, q_out=None, ldq=0, ldo=0), YES), (dict(q_heads=2, ldq=256, ldo=256), YES),
     (dict(q_heads=-2), INVALID), (dict(q_heads=7), SHAPE), (dict(q_heads=1 << 17, ldq=1 << 24, ldo=1 << 24), SHAPE),
     (dict(q=None), INVALID), (dict(q_out=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
-    (dict(dtype=2), INVALID), (dict(ldq=1016), INVALID), (dict(ldo=1016), INVALID), (dict(ldk=248), INVALID),
+    (dict(dtype=2), INVALID), (dict(ldq=1016), INVALID), (dict(ldo=1016), INVALID), (dict(ldo=2048), INVALID), (dict(ldk=248), INVALID),
     (dict(ldv=248), INVALID), (dict(ldq=1028), MISALIGNED), (dict(ldo=1028), MISALIGNED), (dict(ldk=260), MISALIGNED),
     (dict(q=BAD), MISALIGNED), (dict(q_out=BAD), MISALIGNED), (dict(k=BAD), MISALIGNED), (dict(v=BAD), MISALIGNED),
     (dict(cache=None), INVALID), (dict(cache=BAD), MISALIGNED), (dict(head_dim=96), SHAPE), (dict(group_size=32), INVALID),

@@ -42,9 +42,11 @@ EXPORTS = (
     "cider_kv4_cache_bytes", "cider_kv4_append", "cider_kv4_read", "cider_kv4_attention",
     "cider_kv4_attention_workspace_bytes", "cider_kv4_set_tiles", "cider_kv4_append_rotated",
     "cider_kv4_attention_shared", "cider_kv4_attention_shared_workspace_bytes",
+    "cider_lora_add", "cider_lora_workspace_bytes",
 )
 
 KV4_PAGE_TOKENS = 64
+LORA_MAX_SLICES = 8
 
 CIDER_DTYPE_F16 = 0
 CIDER_DTYPE_BF16 = 1
@@ -119,6 +121,24 @@ class cider_rotation(ctypes.Structure):
         self._kept = (cos_sin, positions, q_weight, k_weight, pair_axis)
 
 
+_LORA = struct.Struct("3Q4q%dq" % LORA_MAX_SLICES)  # cider_lora's fields
+
+
+class cider_lora(ctypes.Structure):
+    """The adapters of cider_lora_add (the struct of include/cider.h).
+    slice_end: where the outputs of each slice end, one number for a plain
+    product.  Tensors are kept alive as long as the object is."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "b", "scale")] +
+                [(n, ctypes.c_int64) for n in ("slots", "rank", "in_features", "slices")] +
+                [("slice_end", ctypes.c_int64 * LORA_MAX_SLICES)])
+
+    def __init__(self, a, b, scale, slots, rank, in_features, slice_end):
+        ends = tuple(slice_end)
+        _LORA.pack_into(self, 0, _ptr(a) or 0, _ptr(b) or 0, _ptr(scale) or 0, slots, rank, in_features, len(ends),
+                        *(ends + (0,) * LORA_MAX_SLICES)[:LORA_MAX_SLICES])
+        self._tensors = (a, b, scale)
+
+
 _lib: ctypes.CDLL | None = None
 
 
@@ -157,6 +177,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "cider_w8a8_linear": ([P, I64, I64, I64, P, P, I64, I, P, SZ, P, P], I),
         "cider_w4a8_linear": ([P, I64, I64, I64, P, P, I64, I, P, SZ, P, P], I),
         "cider_set_path": ([I], I),
+        "cider_lora_add": ([P, P, P, I64, I64, I64, P, I, I64, P, I64, P, SZ, P, I64, P], I),
+        "cider_lora_workspace_bytes": ([P, I64, I64, I64], SZ),
         "cider_kv4_cache_bytes": ([I64, I64, I64, I], SZ),
         "cider_kv4_append": ([P, P, P, I, I64, I64, P], I),
         "cider_kv4_read": ([P, P, P, I, I64, I64, P], I),
@@ -215,6 +237,11 @@ def _ret(status: int, what: str, check: bool) -> int:
     if check and status != CIDER_OK:
         raise CiderError(status, what)
     return status
+
+
+def _struct(b):
+    """The address of a call's struct."""
+    return None if b is None else ctypes.addressof(b)
 
 
 def cider_is_available() -> bool:
@@ -340,52 +367,60 @@ def cider_w4a8_linear(x_f16, M, K, ldx, wq4, s_w, N, group_size, workspace, work
     return _ret(st, "cider_w4a8_linear", check)
 
 
+def cider_lora_add(lora, seg_start, slot, segments, rows, max_rows, x, dtype, ldx, y_in, ldy_in, workspace,
+                   workspace_bytes, y, ldy, stream=None, check=True):
+    st = load().cider_lora_add(_struct(lora), _ptr(seg_start), _ptr(slot), segments, rows, max_rows, _ptr(x), dtype,
+                               ldx, _ptr(y_in), ldy_in, _ptr(workspace), workspace_bytes, _ptr(y), ldy,
+                               _stream(stream))
+    return _ret(st, "cider_lora_add", check)
+
+
+def cider_lora_workspace_bytes(lora, segments, rows, max_rows) -> int:
+    return int(load().cider_lora_workspace_bytes(_struct(lora), segments, rows, max_rows))
+
+
 def cider_kv4_cache_bytes(num_pages, kv_heads, head_dim, group_size) -> int:
     return int(load().cider_kv4_cache_bytes(num_pages, kv_heads, head_dim, group_size))
 
 
-def _batch(b):
-    return None if b is None else ctypes.addressof(b)
-
-
 def cider_kv4_append(b, k, v, dtype, ldk, ldv, stream=None, check=True):
-    st = load().cider_kv4_append(_batch(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
+    st = load().cider_kv4_append(_struct(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
     return _ret(st, "cider_kv4_append", check)
 
 
 def cider_kv4_append_rotated(b, rotation, q, k, v, dtype, ldq, ldk, ldv, q_heads, q_out, ldq_out, stream=None,
                              check=True):
-    st = load().cider_kv4_append_rotated(_batch(b), _batch(rotation), _ptr(q), _ptr(k), _ptr(v), dtype, ldq, ldk,
+    st = load().cider_kv4_append_rotated(_struct(b), _struct(rotation), _ptr(q), _ptr(k), _ptr(v), dtype, ldq, ldk,
                                          ldv, q_heads, _ptr(q_out), ldq_out, _stream(stream))
     return _ret(st, "cider_kv4_append_rotated", check)
 
 
 def cider_kv4_read(b, k, v, dtype, ldk, ldv, stream=None, check=True):
-    st = load().cider_kv4_read(_batch(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
+    st = load().cider_kv4_read(_struct(b), _ptr(k), _ptr(v), dtype, ldk, ldv, _stream(stream))
     return _ret(st, "cider_kv4_read", check)
 
 
 def cider_kv4_attention(b, q, q_dtype, ldq, q_heads, scale, window, sinks, workspace,
                         workspace_bytes, y, y_dtype, ldy, stream=None, check=True):
-    st = load().cider_kv4_attention(_batch(b), _ptr(q), q_dtype, ldq, q_heads, scale, window, sinks,
+    st = load().cider_kv4_attention(_struct(b), _ptr(q), q_dtype, ldq, q_heads, scale, window, sinks,
                                     _ptr(workspace), workspace_bytes, _ptr(y), y_dtype, ldy,
                                     _stream(stream))
     return _ret(st, "cider_kv4_attention", check)
 
 
 def cider_kv4_attention_workspace_bytes(b, q_heads, window, sinks) -> int:
-    return int(load().cider_kv4_attention_workspace_bytes(_batch(b), q_heads, window, sinks))
+    return int(load().cider_kv4_attention_workspace_bytes(_struct(b), q_heads, window, sinks))
 
 
 def cider_kv4_attention_shared(b, runs, q, q_dtype, ldq, q_heads, scale, workspace, workspace_bytes, y, y_dtype, ldy,
                                stream=None, check=True):
-    st = load().cider_kv4_attention_shared(_batch(b), _batch(runs), _ptr(q), q_dtype, ldq, q_heads, scale,
+    st = load().cider_kv4_attention_shared(_struct(b), _struct(runs), _ptr(q), q_dtype, ldq, q_heads, scale,
                                            _ptr(workspace), workspace_bytes, _ptr(y), y_dtype, ldy, _stream(stream))
     return _ret(st, "cider_kv4_attention_shared", check)
 
 
 def cider_kv4_attention_shared_workspace_bytes(b, runs, q_heads) -> int:
-    return int(load().cider_kv4_attention_shared_workspace_bytes(_batch(b), _batch(runs), q_heads))
+    return int(load().cider_kv4_attention_shared_workspace_bytes(_struct(b), _struct(runs), q_heads))
 
 
 def cider_kv4_set_tiles(columns: int) -> int:

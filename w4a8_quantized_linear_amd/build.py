@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libcider.so")
 SOURCES = ["api.hip", "quantize.hip", "clip.hip", "smooth.hip", "decode.hip", "gemm.hip", "gemm_few.hip", "gemm_skinny.hip", "gemv.hip",
            "kv4_cache.hip", "kv4_rotate.hip", "kv4_attention.hip", "kv4_few_rows.hip",
-           "kv4_many_rows.hip"]
+           "kv4_many_rows.hip", "lora.hip"]
 HEADERS = ["cider_kernels.h", "quant_common.h", "kv4_layout.h", "kv4_codes.h", "kv4_attention.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

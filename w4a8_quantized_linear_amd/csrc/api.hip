@@ -545,6 +545,52 @@ cider::Kv4AttentionArgs kv4_attention_args(const cider_kv4_batch *b, int64_t q_h
     return a;
 }
 
+// Sizes of an adapter call (no pointer is looked at).
+cider_status check_lora(const cider_lora *l, int64_t segments, int64_t rows, int64_t max_rows)
+{
+    if (!l || l->slots < 1 || l->rank < 1 || l->in_features < 1 || l->slices < 1 || segments < 0 || rows < 0 ||
+        max_rows < 0)
+        return CIDER_ERR_INVALID_ARG;
+    constexpr int64_t kMaxWidth = int64_t(1) << 24;
+    if (l->slots > kMaxInt || l->rank % 8 != 0 || l->rank > 128 || l->in_features % 64 != 0 ||
+        l->in_features >= kMaxWidth || l->slices > CIDER_LORA_MAX_SLICES || segments > kMaxInt || rows > kMaxTokens ||
+        max_rows > kMaxTokens)
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    int64_t end = 0;
+    for (int64_t i = 0; i < l->slices; ++i) {
+        if (l->slice_end[i] <= end)
+            return CIDER_ERR_INVALID_ARG;
+        end = l->slice_end[i];
+        if (end % 64 != 0 || end >= kMaxWidth)
+            return CIDER_ERR_UNSUPPORTED_SHAPE;
+    }
+    // launches count workgroups in 32 bits
+    const int64_t tiles = ((max_rows < rows ? max_rows : rows) + 15) / 16, per = end / 64 + l->slices * l->rank;
+    if (segments > 0 && tiles > 0 && (tiles > kMaxInt / segments || per > kMaxInt / (segments * tiles)))
+        return CIDER_ERR_UNSUPPORTED_SHAPE;
+    return CIDER_OK;
+}
+
+bool lora_empty(int64_t segments, int64_t rows, int64_t max_rows) { return segments == 0 || rows == 0 || max_rows == 0; }
+
+cider::LoraArgs lora_args(const cider_lora *l, int64_t segments, int64_t rows, int64_t max_rows)
+{
+    cider::LoraArgs a{};
+    a.a = static_cast<const uint16_t *>(l->a);
+    a.b = static_cast<const uint16_t *>(l->b);
+    a.scale = l->scale;
+    a.segments = (int)segments;
+    a.rows = (int)rows;
+    a.max_rows = (int)(max_rows < rows ? max_rows : rows);
+    a.slots = (int)l->slots;
+    a.rank = (int)l->rank;
+    a.inputs = (int)l->in_features;
+    a.slices = (int)l->slices;
+    for (int i = 0; i < a.slices; ++i)
+        a.ends[i] = (int)l->slice_end[i];
+    return a;
+}
+
 // Either attention call; runs: null for the ordinary one.
 cider_status run_kv4_attention(const cider_kv4_batch *b, const cider_kv4_runs *runs, const void *q, int q_dtype,
                                int64_t ldq, int64_t q_heads, float scale, int64_t window, int64_t sinks,
@@ -794,6 +840,53 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
                                          static_cast<hipStream_t>(stream)));
 }
 
+size_t cider_lora_workspace_bytes(const cider_lora *lora, int64_t segments, int64_t rows,
+                                  int64_t max_rows)
+{
+    if (check_lora(lora, segments, rows, max_rows) != CIDER_OK || lora_empty(segments, rows, max_rows))
+        return 0;
+    return cider::lora_workspace(lora_args(lora, segments, rows, max_rows));
+}
+
+cider_status cider_lora_add(const cider_lora *lora, const int32_t *seg_start, const int32_t *slot,
+                            int64_t segments, int64_t rows, int64_t max_rows, const void *x,
+                            int dtype, int64_t ldx, const void *y_in, int64_t ldy_in,
+                            void *workspace, size_t workspace_bytes, void *y, int64_t ldy,
+                            void *stream)
+{
+    const cider_status st = check_lora(lora, segments, rows, max_rows);
+    if (st != CIDER_OK)
+        return st;
+    const int64_t outputs = lora->slice_end[lora->slices - 1];
+    if (!dtype_ok(dtype) || ldx < lora->in_features || ldy_in < outputs || ldy < outputs)
+        return CIDER_ERR_INVALID_ARG;
+    if (lora_empty(segments, rows, max_rows))
+        return CIDER_OK;
+    if (!lora->a || !lora->b || !seg_start || !slot || !x || !y_in || !y)
+        return CIDER_ERR_INVALID_ARG;
+    if (!aligned16(lora->a) || !aligned16(lora->b) || !aligned4(lora->scale) || !aligned4(seg_start) ||
+        !aligned4(slot) || !aligned16(x) || !aligned16(y_in) || !aligned16(y) || !aligned16(workspace) ||
+        ldx % 8 != 0 || ldy_in % 8 != 0 || ldy % 8 != 0)
+        return CIDER_ERR_MISALIGNED;
+    if (y == y_in && ldy != ldy_in)
+        return CIDER_ERR_INVALID_ARG;
+    cider::LoraArgs a = lora_args(lora, segments, rows, max_rows);
+    if (!workspace || workspace_bytes < cider::lora_least_workspace(a))
+        return CIDER_ERR_WORKSPACE;
+    if (!device_usable())
+        return CIDER_ERR_NO_DEVICE;
+    a.seg_start = seg_start;
+    a.slot = slot;
+    a.x = static_cast<const uint16_t *>(x);
+    a.y_in = static_cast<const uint16_t *>(y_in);
+    a.y = static_cast<uint16_t *>(y);
+    a.ldx = ldx;
+    a.ldy_in = ldy_in;
+    a.ldy = ldy;
+    a.dtype = dtype;
+    return from_hip(cider::launch_lora_add(a, workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
+}
+
 size_t cider_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_dim, int group_size)
 {
     if (check_kv4_geometry(num_pages, kv_heads, head_dim, group_size) != CIDER_OK)
@@ -836,6 +929,8 @@ cider_status cider_kv4_append_rotated(const cider_kv4_batch *b, const cider_rota
             return CIDER_ERR_INVALID_ARG;
         if (!aligned16(q) || !aligned16(q_out) || ldq % 8 != 0 || ldq_out % 8 != 0)
             return CIDER_ERR_MISALIGNED;
+        if (q == q_out && ldq != ldq_out)
+            return CIDER_ERR_INVALID_ARG;
     }
     if (!aligned16(rotation->q_weight) || !aligned16(rotation->k_weight) ||
         (rotation->rot_dim && (!aligned16(rotation->cos_sin) || !aligned4(rotation->positions))))

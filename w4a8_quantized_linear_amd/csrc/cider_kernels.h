@@ -198,4 +198,22 @@ size_t kv4_attention_workspace(const Kv4AttentionArgs &a);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size_t workspace_bytes,
                                 hipStream_t stream);
 
+// Low-rank adapters of segments of rows.
+constexpr int kMostSlices = 8;
+struct LoraArgs {
+    const uint16_t *a, *b;  // [slots][slices * rank][inputs], [slots][ends[slices - 1]][rank]
+    const float *scale;     // [slots] or null
+    const int32_t *seg_start, *slot;  // [segments + 1], [segments]
+    const uint16_t *x, *y_in;
+    uint16_t *y;
+    int64_t ldx, ldy_in, ldy;
+    int segments, rows, max_rows, slots, rank, inputs, slices, dtype;
+    int ends[kMostSlices];  // outputs of slice i end there
+};
+// Scratch without which it cannot be done, scratch with which it takes as many
+// workgroups as it would, and the call (with the least or more).
+size_t lora_least_workspace(const LoraArgs &a);
+size_t lora_workspace(const LoraArgs &a);
+hipError_t launch_lora_add(const LoraArgs &a, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 }  // namespace cider
