@@ -482,7 +482,7 @@ cider::Kv4Rotation rotation_args(const cider_rotation *r)
     a.axes = (int)r->axes;
     a.interleaved = r->interleaved != 0;
     for (int64_t i = 0; r->axes > 1 && i < r->rot_dim / 2; ++i)
-        a.pair_axis[i / 32] |= (uint64_t)r->pair_axis[i] << 2 * (i % 32);
+        (i < 32 ? a.pair_axis_low : a.pair_axis_high) |= (uint64_t)r->pair_axis[i] << 2 * (i % 32);
     return a;
 }
 

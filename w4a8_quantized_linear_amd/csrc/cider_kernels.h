@@ -154,7 +154,7 @@ struct Kv4Rotation {
     const float2 *table;       // [table_len][rot_dim / 2] of (cos, sin); rot_dim 0: not read
     const int32_t *positions;  // [axes][rows], or null with one axis: the token's position
     const float *q_weight, *k_weight;  // [head_dim], or null: no norm
-    uint64_t pair_axis[2];     // 2 bits for each pair
+    uint64_t pair_axis_low, pair_axis_high;  // 2 bits for each pair
     int table_len, rot_dim, axes;
     bool interleaved;
     float eps;

@@ -97,12 +97,12 @@ __device__ __forceinline__ void turn(T &a, T &b, float2 cs)
     b = b * c + was * s;
 }
 
-template <typename T>
-__device__ __forceinline__ void turn(T (&x)[2][8], const Share &t, bool interleaved)
+template <bool INTERLEAVED, typename T>
+__device__ __forceinline__ void turn(T (&x)[2][8], const Share &t)
 {
     if (!t.turns)
         return;
-    if (interleaved) {
+    if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             turn(x[e / 4][e % 4 * 2], x[e / 4][e % 4 * 2 + 1], t.cs[e]);
@@ -140,14 +140,15 @@ __device__ __forceinline__ void load_weights(const float *w, const Share &t, flo
 }
 
 // The table's entries of the lane's pairs for the token at position p, row `row`.
+template <bool INTERLEAVED>
 __device__ __forceinline__ void load_turns(const Kv4Rotation &r, int rows, int p, int64_t row, Share &t)
 {
     if (!t.turns)
         return;
     const int pairs = r.rot_dim / 2;
     // first pair of the lane's first four and last four
-    const int at[2] = {r.interleaved ? 4 * t.chunk[0] : 8 * t.chunk[0],
-                       r.interleaved ? 4 * t.chunk[1] : 8 * t.chunk[0] + 4};
+    const int at[2] = {INTERLEAVED ? 4 * t.chunk[0] : 8 * t.chunk[0],
+                       INTERLEAVED ? 4 * t.chunk[1] : 8 * t.chunk[0] + 4};
     const int most = r.table_len - 1;
     auto entry = [&](int position) {
         const int q = position < 0 ? 0 : (position > most ? most : position);
@@ -172,14 +173,14 @@ __device__ __forceinline__ void load_turns(const Kv4Rotation &r, int rows, int p
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int pair = at[e / 4] + e % 4;
-        const int x = (int)(r.pair_axis[pair / 32] >> 2 * (pair % 32)) & 3;
+        const int x = (int)((pair < 32 ? r.pair_axis_low : r.pair_axis_high) >> 2 * (pair % 32)) & 3;
         const float2 *f = x & 1 ? (x & 2 ? from[3] : from[1]) : (x & 2 ? from[2] : from[0]);
         t.cs[e] = f[pair];
     }
 }
 
 // The keys of 8 tokens of a wavefront (D 64: the lower half of it).
-template <int D, int GS, int DT>
+template <int D, int GS, int DT, bool INTERLEAVED>
 __device__ __forceinline__ void put_key(const Kv4Rotation &r, const uint4 (&raw)[2], const Share &t, const float (&w)[2][8],
                                         uint8_t *block, int token, bool store, int l)
 {
@@ -188,7 +189,7 @@ __device__ __forceinline__ void put_key(const Kv4Rotation &r, const uint4 (&raw)
     widen<DT>(raw, x);
     if (r.k_weight)
         norm<L>(x, w, r.eps);
-    turn(x, t, r.interleaved);
+    turn<INTERLEAVED>(x, t);
     float f[2][8], top[NG], scale[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
@@ -225,7 +226,7 @@ __device__ __forceinline__ void put_key(const Kv4Rotation &r, const uint4 (&raw)
 }
 
 // A head of q.
-template <int D, int DT>
+template <int D, int DT, bool INTERLEAVED>
 __device__ __forceinline__ void put_query(const Kv4Rotation &r, const uint4 (&raw)[2], const Share &t,
                                           const float (&w)[2][8], uint16_t *to, bool there)
 {
@@ -234,7 +235,7 @@ __device__ __forceinline__ void put_query(const Kv4Rotation &r, const uint4 (&ra
     widen<DT>(raw, x);
     if (r.q_weight)
         norm<D / 16>(x, w, r.eps);
-    turn(x, t, r.interleaved);
+    turn<INTERLEAVED>(x, t);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint4 o;
@@ -246,12 +247,11 @@ __device__ __forceinline__ void put_query(const Kv4Rotation &r, const uint4 (&ra
     }
 }
 
-template <int D, int GS, int DT>
+template <int D, int GS, int DT, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void kv4_rotate_kernel(Kv4Args a, Kv4Rotation r, Kv4Rows io, int spans)
 {
     constexpr int CH = D / 8, PT = D / 64, L = D / 16;
-    constexpr int HEADS = 8 / L;   // query heads that a wavefront works on at once
-    constexpr int AHEAD = 4;       // of which this many times are loaded before the first is used
+    constexpr int HEADS = 8 / L;  // query heads that a wavefront works on at once
     Place w;
     if (!place_of(a, spans, w))
         return;
@@ -277,51 +277,64 @@ __global__ __launch_bounds__(kThreads) void kv4_rotate_kernel(Kv4Args a, Kv4Rota
             vx[i] = nt_load(io.v + (p + w.shift) * io.ldv + w.h * D + c8 * 8);
     }
 
-    // q and k: tokens 8 j ..
-    if (w.base + 8 * j < w.hi && w.base + 8 * j + 8 > w.lo) {
-        const int l = lane % L, t = 8 * j + lane / L % 8, sub = lane / (8 * L), p = w.base + t;
-        const bool mine = p >= w.lo && p < w.hi, there = p >= 0;
-        const int64_t row = (mine ? p : w.lo) + w.shift;
-        Share s;
-        s.turns = l < r.rot_dim / 16;
-        s.chunk[0] = s.turns ? l : 2 * l;  // rot_dim / 8 + 2 (l - rot_dim / 16)
-        s.chunk[1] = s.turns ? l + r.rot_dim / 16 : 2 * l + 1;
-        uint4 kx[2];
+    // q and k.  Many tokens: the wavefront has 8 of them, each with its key and then its
+    // query heads.  Up to 8 in all: the first wavefront has their keys, the others share
+    // their query heads out.
+    const int l = lane % L, G = io.q_heads / a.kv_heads;
+    const bool few = w.hi - w.lo <= 8;
+    const int sub = few ? 0 : lane / (8 * L);
+    Share s;
+    s.turns = l < r.rot_dim / 16;
+    s.chunk[0] = s.turns ? l : 2 * l;  // rot_dim / 8 + 2 (l - rot_dim / 16)
+    s.chunk[1] = s.turns ? l + r.rot_dim / 16 : 2 * l + 1;
+    auto load = [&](uint4 (&x)[2], const uint16_t *head) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-            kx[c] = nt_load(io.k + row * io.ldk + w.h * D + 8 * s.chunk[c]);
-        const int G = io.q_heads / a.kv_heads;
-        const int64_t q0 = row * io.ldq + (int64_t)w.h * G * D, o0 = row * io.ldo + (int64_t)w.h * G * D;
-        uint4 qx[AHEAD][2];
-        auto load = [&](int g0) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (g0 + i * HEADS < G) {
-                    const int g = g0 + i * HEADS + sub;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        qx[i][c] = nt_load(io.q + q0 + (g < G ? g : G - 1) * D + 8 * s.chunk[c]);
-                }
-        };
-        load(0);
-        load_turns(r, a.rows, p, row, s);
-        float weight[2][8];
+            x[c] = nt_load(head + 8 * s.chunk[c]);
+    };
+    float weight[2][8];
+    uint4 x[2];
+    auto key = [&](int p, bool mine) {
+        const int64_t row = (mine ? p : w.lo) + w.shift;
+        load(x, io.k + row * io.ldk + w.h * D);
+        load_turns<INTERLEAVED>(r, a.rows, p, row, s);
         if (r.k_weight)
             load_weights(r.k_weight, s, weight);
         if (block)
-            put_key<D, GS, DT>(r, kx, s, weight, block, half * kSpan + t, mine && there && sub == 0, l);
+            put_key<D, GS, DT, INTERLEAVED>(r, x, s, weight, block, half * kSpan + p - w.base, mine && p >= 0 && sub == 0, l);
         if (r.q_weight)
             load_weights(r.q_weight, s, weight);
-        for (int g0 = 0; g0 < G; g0 += AHEAD * HEADS) {
-            if (g0 > 0)
-                load(g0);
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (g0 + i * HEADS < G) {
-                    const int g = g0 + i * HEADS + sub;
-                    if (mine && g < G)
-                        put_query<D, DT>(r, qx[i], s, weight, io.q_out + o0 + g * D, there);
-                }
+    };
+    if (!few) {
+        if (w.base + 8 * j < w.hi && w.base + 8 * j + 8 > w.lo) {
+            const int p = w.base + 8 * j + lane / L % 8;
+            const bool mine = p >= w.lo && p < w.hi;
+            key(p, mine);
+            const int64_t row = (mine ? p : w.lo) + w.shift;
+            const uint16_t *from = io.q + row * io.ldq + w.h * G * D;
+            uint16_t *to = io.q_out + row * io.ldo + w.h * G * D;
+            for (int g0 = 0; g0 < G; g0 += HEADS) {
+                const int g = g0 + sub;
+                load(x, from + (g < G ? g : G - 1) * D);
+                if (mine && g < G)
+                    put_query<D, DT, INTERLEAVED>(r, x, s, weight, to + g * D, p >= 0);
+            }
+        }
+    } else if (j == 0) {
+        const int p = w.lo + lane / L;
+        key(p, p < w.hi);
+    } else {
+        if (r.q_weight)
+            load_weights(r.q_weight, s, weight);
+        const int count = (w.hi - w.lo) * G;
+        for (int i0 = (j - 1) * (64 / L); i0 < count; i0 += 3 * (64 / L)) {
+            const int i = i0 + lane / L, at = i < count ? i : i0;
+            const int p = w.lo + at / G, head = w.h * G + at % G;
+            const int64_t row = p + w.shift;
+            load(x, io.q + row * io.ldq + head * D);
+            load_turns<INTERLEAVED>(r, a.rows, p, row, s);
+            if (i < count)
+                put_query<D, DT, INTERLEAVED>(r, x, s, weight, io.q_out + row * io.ldo + head * D, p >= 0);
         }
     }
 
@@ -359,7 +372,8 @@ hipError_t launch_kv4_append_rotated(const Kv4Args &a, const Kv4Rotation &r, con
     const int spans = spans_of(a);
     const unsigned grid = (unsigned)spans * (unsigned)a.kv_heads * (unsigned)a.batch;
     return with_geometry(a, dtype, [&](auto D, auto GS, auto DT) {
-        return kv4_launch(kv4_rotate_kernel<D(), GS(), DT()>, grid, kThreads, stream, a, r, io, spans);
+        auto *kernel = r.interleaved ? kv4_rotate_kernel<D(), GS(), DT(), true> : kv4_rotate_kernel<D(), GS(), DT(), false>;
+        return kv4_launch(kernel, grid, kThreads, stream, a, r, io, spans);
     });
 }
 
