@@ -9,8 +9,8 @@
 // adapter's rows as the left operand and tokens as columns, operands loaded as they
 // lie in memory: 8 consecutive inputs of a row are a lane's 16 bytes.  No LDS but for
 // joining a workgroup's 4 wavefronts, which take a quarter of the inputs each.
-// A lane of `up` takes the rows of B in the order that leaves it 16 consecutive
-// outputs of one token, so y_in and y move 16 bytes a lane and a whole line a token.
+// `up` takes the rows of B in an order that leaves a lane runs of 8 outputs of a token,
+// and two lanes exchange theirs, so that y_in and y move by whole lines.
 //
 // Rounding.  t is fp32; times the scale it goes to the second product as two 16-bit
 // numbers, high and low, one behind the other along the summed axis with B's row
@@ -26,6 +26,7 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(uint4 x, uint4 y, f32x4 z)
@@ -36,13 +37,21 @@ __device__ __forceinline__ f32x4 mfma(uint4 x, uint4 y, f32x4 z)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, x), __builtin_bit_cast(half8, y), z, 0, 0, 0);
 }
 
+// Lanes of a wavefront have written to LDS what others read.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // What a launch adds to the call's arguments.
 struct Launch {
     int tiles;   // of 16 TT rows, of the longest segment
-    int blocks;  // down: of 16 NT rows of A; up: of `per` 64-output blocks a wavefront
+    int blocks;  // down: of 16 NT rows of A; up: of a workgroup's outputs, in all slices
     int splits;  // parts of t
     int chunk;   // down: inputs of a wavefront, a multiple of 64
-    int per;
+    int per;     // up: blocks of outputs of a wavefront
     float *t;    // [splits][rows][slices * rank]
 };
 
@@ -61,11 +70,18 @@ __device__ __forceinline__ Rows rows_of(const LoraArgs &a, int segment, int tile
     return r;
 }
 
+// A workgroup has 16 TT rows of x and 16 NT rows of A, each of its wavefronts a quarter
+// of the split's inputs.  Both go through LDS (the wavefront's own): memory is read by
+// consecutive lanes, 8 and more to a row, where the operands' lanes go from row to row,
+// which the load path takes a quarter as fast.
 template <int DT, int TT, int NT>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
 {
-    constexpr int U = TT + NT <= 2 ? 8 : (TT + NT <= 4 ? 4 : 2);  // steps of 32 inputs loaded at once
-    __shared__ f32x4 part[4][TT * NT][64];
+    constexpr int ROWS = 16 * (TT + NT);
+    constexpr int KS = TT + NT <= 2 ? 4 : (TT + NT <= 4 ? 2 : 1);  // times 64 inputs loaded at once
+    constexpr int CHUNKS = 8 * KS, LOADS = ROWS * CHUNKS / 64;
+    constexpr int STAGE = ROWS * CHUNKS, PART = TT * NT * 64;      // 16-byte words of a wavefront
+    __shared__ uint4 lds[4][STAGE > PART ? STAGE : PART];
     unsigned id = kv4_workgroup();
     const int block = (int)(id % (unsigned)l.blocks);
     id /= (unsigned)l.blocks;
@@ -80,67 +96,67 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
     const int lane = threadIdx.x & 63, c = lane % 16, q = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int width = a.slices * a.rank;  // rows of A
-    const uint16_t *x[TT], *w[NT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        const int row = 16 * i + c < r.n ? 16 * i + c : r.n - 1;
-        x[i] = a.x + (int64_t)(r.first + row) * a.ldx + 8 * q;
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int j = (block * NT + i) * 16 + c;
-        w[i] = a.a + ((int64_t)r.slot * width + (j < width ? j : width - 1)) * a.inputs + 8 * q;
-    }
     const int k0 = (split * 4 + wave) * l.chunk, k1 = k0 + l.chunk < a.inputs ? k0 + l.chunk : a.inputs;
-    f32x4 acc[TT][NT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            acc[i][j] = f32x4{0, 0, 0, 0};
-    struct Steps {
-        uint4 x[U][TT], w[U][NT];
-    };
-    auto load = [&](Steps &s, int k) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = k + 32 * u < k1 ? k + 32 * u : k1 - 32;  // past the end: again what is there
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-                s.x[u][i] = *reinterpret_cast<const uint4 *>(x[i] + at);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                s.w[u][i] = *reinterpret_cast<const uint4 *>(w[i] + at);
-        }
-    };
-    auto multiply = [&](const Steps &s, int k) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k + 32 * u < k1) {
-#pragma unroll
-                for (int i = 0; i < TT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[i][j] = mfma<DT>(s.w[u][j], s.x[u][i], acc[i][j]);
-            }
-    };
+    uint4 *stage = lds[wave];
+    f32x4 acc[TT][NT] = {};
     if (k0 < k1) {
-        Steps one, two;
-        load(one, k0);
-        for (int k = k0; k < k1; k += 64 * U) {
-            if (k + 32 * U < k1)
-                load(two, k + 32 * U);
-            multiply(one, k);
-            if (k + 64 * U < k1)
-                load(one, k + 64 * U);
-            multiply(two, k + 32 * U);
+        // the lane's i-th word is chunk (64 i + lane) % CHUNKS of row (64 i + lane) / CHUNKS:
+        // its rows are 64 / CHUNKS apart (or its only one)
+        const uint16_t *from[LOADS];
+        const int chunk = lane % CHUNKS;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = (64 * i + lane) / CHUNKS;
+            if (row < 16 * TT) {
+                from[i] = a.x + (int64_t)(r.first + (row < r.n ? row : r.n - 1)) * a.ldx;
+            } else {
+                const int j = block * NT * 16 + row - 16 * TT;
+                from[i] = a.a + ((int64_t)r.slot * width + (j < width ? j : width - 1)) * a.inputs;
+            }
+        }
+        u32x4 word[LOADS];
+        auto load = [&](int k) {
+            const int at = k + 8 * chunk < k1 ? k + 8 * chunk : k1 - 8;  // past the end: anything that is there
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                word[i] = *reinterpret_cast<const u32x4 *>(from[i] + at);
+        };
+        load(k0);
+        for (int k = k0; k < k1; k += 64 * KS) {
+            // (lanes of one wavefront: LDS takes its accesses in order)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int row = (64 * i + lane) / CHUNKS;
+                *reinterpret_cast<u32x4 *>(&stage[row * CHUNKS + (chunk ^ row % 8)]) = word[i];
+            }
+            wave_fence();
+            if (k + 64 * KS < k1)
+                load(k + 64 * KS);
+#pragma unroll
+            for (int s = 0; s < 2 * KS; ++s)
+                if (k + 32 * s < k1) {
+                    uint4 x[TT];
+                    const int at = (4 * s + q) ^ c % 8;
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+                        x[i] = stage[(16 * i + c) * CHUNKS + at];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint4 w = stage[(16 * (TT + j) + c) * CHUNKS + at];
+#pragma unroll
+                        for (int i = 0; i < TT; ++i)
+                            acc[i][j] = mfma<DT>(w, x[i], acc[i][j]);
+                    }
+                }
+            wave_fence();
         }
     }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            part[wave][i * NT + j][lane] = acc[i][j];
+            lds[wave][(i * NT + j) * 64 + lane] = __builtin_bit_cast(uint4, acc[i][j]);
     __syncthreads();
     // lane (q, c) has rows 4 q .. 4 q + 3 of a block of A for token c
 #pragma unroll
@@ -148,18 +164,44 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
         const int at = n + wave;
         if (at >= TT * NT)
             break;
-        const f32x4 sum = (part[0][at][lane] + part[1][at][lane]) + (part[2][at][lane] + part[3][at][lane]);
+        auto part = [&](int w) { return __builtin_bit_cast(f32x4, lds[w][at * 64 + lane]); };
+        const f32x4 sum = (part(0) + part(1)) + (part(2) + part(3));
         const int row = at / NT * 16 + c, j = (block * NT + at % NT) * 16 + 4 * q;
         if (row < r.n && j < width)
             *reinterpret_cast<f32x4 *>(l.t + ((int64_t)split * a.rows + r.first + row) * width + j) = sum;
     }
 }
 
-// STEPS: products of 32 along 2 R numbers, the high halves of t and then the low ones.
-template <int DT, int TT, int STEPS>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, Launch l)
+// Of a token whose largest |t| has these bits: 2^-exponent takes it to [2^13, 2^14).
+// Not below -100: what is smaller yet, times fp16 numbers, is nothing to an fp16 output,
+// and 2^exponent stays a normal number.
+__device__ __forceinline__ int token_exponent(uint32_t top)
 {
-    constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16;
+    const float x = __builtin_bit_cast(float, top);
+    const int e = x > 0.0f && x < __builtin_inff() ? __builtin_amdgcn_frexp_expf(x) - 14 : 0;
+    return e < -100 ? -100 : e;
+}
+
+// What the lane next to it has.
+__device__ __forceinline__ uint32_t neighbour(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xF, 0xF, false);  // quad_perm [1,0,3,2]
+}
+
+constexpr int kBlock = 64;  // outputs
+
+// A workgroup has 16 TT rows and l.per blocks of 64 outputs of one slice for each of
+// its wavefronts.  It adds t's parts for its rows and leaves their halves in LDS as
+// operands; a wavefront loads a block's rows of B (16 NB at a time) and takes the rows
+// of x 16 at a time.  STEPS: products of 32 along 2 R numbers, the high halves of t and
+// then the low ones.
+template <int DT, int TT, int NB, int STEPS>
+__global__ __launch_bounds__(256, TT == 4 && STEPS == 4 ? 3 : (STEPS <= 2 ? 4 : 1)) void lora_up_kernel(LoraArgs a, Launch l)
+{
+    constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16, T = 16 * TT;
+    constexpr int ITEMS = (T * STEPS * 2 + 255) / 256;  // of 8 numbers of t, a thread
+    __shared__ uint4 half[4 * STEPS][T];
+    __shared__ uint32_t top[T];
     unsigned id = kv4_workgroup();
     const int lane = threadIdx.x & 63, c = lane % 16, q = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -168,129 +210,170 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, Launch l)
     const int tile = (int)(id % (unsigned)l.tiles), segment = (int)(id / (unsigned)l.tiles);
     if (segment >= a.segments)
         return;
-    const Rows r = rows_of(a, segment, tile, 16 * TT);
+    const Rows r = rows_of(a, segment, tile, T);
     const bool adapted = (unsigned)r.slot < (unsigned)a.slots;
     if (r.n == 0 || (!adapted && a.y == a.y_in))
         return;
-    const int outputs = a.ends[a.slices - 1], R = a.rank, width = a.slices * R;
-    int row[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-        row[i] = r.first + (16 * i + c < r.n ? 16 * i + c : r.n - 1);
-
-    // which 8 numbers of t, and of a row of B, each step's operand of the lane has
-    int at[STEPS];
-    bool low[STEPS], some[STEPS];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        const int k = 32 * s + 8 * q;
-        some[s] = k < 2 * R;
-        low[s] = k >= R;
-        at[s] = !some[s] ? 0 : (low[s] ? k - R : k);
+    // the group's slice, and its outputs there
+    const int outputs = a.ends[a.slices - 1], R = a.rank, width = a.slices * R, span = 4 * l.per * kBlock;
+    int slice = 0, first = group * span;
+    for (int from = 0; first >= a.ends[slice] - from; ++slice) {
+        first -= (a.ends[slice] - from + span - 1) / span * span;
+        from = a.ends[slice];
     }
-    const float scale = !adapted ? 0.0f : (a.scale ? a.scale[r.slot] : 1.0f);
-    uint4 t[TT][STEPS];
-    int exponent[TT] = {};
-    auto load_t = [&](int slice) {
+    first += slice ? a.ends[slice - 1] : 0;
+
+    // What comes from memory first of all.
+    const bool odd = c & 1;
+    const int begin = first + wave * kBlock, end = first + span < a.ends[slice] ? first + span : a.ends[slice];
+    uint4 in[TT][2], b[NB][STEPS];
+    auto load_in = [&](int n0) {
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            float v[STEPS][8], top = 0.0f;
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int token = 16 * i + c < r.n ? 16 * i + c : r.n - 1;
+                in[i][h] = *reinterpret_cast<const uint4 *>(a.y_in + (int64_t)(r.first + token) * a.ldy_in + n0 + 32 * h + 8 * q);
+            }
+    };
+    auto load_b = [&](int n0, int pass) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            // the order that leaves a lane 8 consecutive outputs of two blocks of 32
+            const int at = NB * pass + j, n = n0 + at / 2 * 32 + c / 4 * 8 + at % 2 * 4 + c % 4;
+            const uint16_t *from = a.b + ((int64_t)r.slot * outputs + n) * R;
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const float *from = l.t + (int64_t)row[i] * width + slice * R + at[s];
-                f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+                const int k = 32 * s + 8 * q;
+                b[j][s] = *reinterpret_cast<const uint4 *>(from + (k < R ? k : (k < 2 * R ? k - R : 0)));
+            }
+        }
+    };
+    if (begin < end) {
+        load_in(begin);
+        if (adapted)
+            load_b(begin, 0);
+    }
+    if (adapted) {
+        const float scale = a.scale ? a.scale[r.slot] : 1.0f;
+        const int chunks = R / 8;
+        float v[ITEMS][8];
+        if (DT == DT_F16 && threadIdx.x < T)
+            top[threadIdx.x] = 0;
+        if constexpr (DT == DT_F16)
+            __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
+            f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+            if (token < r.n) {
+                const float *from = l.t + (int64_t)(r.first + token) * width + slice * R + 8 * chunk;
+#pragma unroll 4
                 for (int p = 0; p < l.splits; ++p) {
                     lo += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width);
                     hi += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width + 4);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[s][e] = (e < 4 ? lo[e] : hi[e - 4]) * scale;
-                    top = __builtin_fmaxf(top, __builtin_fabsf(v[s][e]));
-                }
             }
-            exponent[i] = 0;
-            if constexpr (DT == DT_F16) {  // the token's largest to [2^13, 2^14)
-                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                exponent[i] = top > 0.0f && top < __builtin_inff() ? __builtin_amdgcn_frexp_expf(top) - 14 : 0;
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[i][e] = (e < 4 ? lo[e] : hi[e - 4]) * scale;
+                most = __builtin_fmaxf(most, __builtin_fabsf(v[i][e]));
             }
+            if (DT == DT_F16 && token < T)
+                atomicMax(&top[token], __builtin_bit_cast(uint32_t, most));
+        }
+        if constexpr (DT == DT_F16)
+            __syncthreads();
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                uint32_t o[4];
+        for (int i = 0; i < ITEMS; ++i) {
+            const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
+            if (token >= T)
+                break;
+            uint32_t high[4], low[4];
+            const int by = DT == DT_F16 ? -token_exponent(top[token]) : 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float u[2];
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const float x = __builtin_amdgcn_ldexpf(v[s][2 * e + f], -exponent[i]);
-                        u[f] = low[s] ? x - widen_bits<DT>(out_bits<OUT>(x)) : x;
-                    }
-                    o[e] = some[s] ? pack2<OUT>(u[0], u[1]) : 0u;
-                }
-                t[i][s] = uint4{o[0], o[1], o[2], o[3]};
+            for (int e = 0; e < 4; ++e) {
+                const float x = __builtin_amdgcn_ldexpf(v[i][2 * e], by), y = __builtin_amdgcn_ldexpf(v[i][2 * e + 1], by);
+                high[e] = pack2<OUT>(x, y);
+                low[e] = pack2<OUT>(x - widen_bits<DT>(high[e]), y - widen_bits<DT>(high[e] >> 16));
             }
+            half[chunk][token] = uint4{high[0], high[1], high[2], high[3]};
+            half[chunks + chunk][token] = uint4{low[0], low[1], low[2], low[3]};
+        }
+        for (int i = 2 * chunks * T + threadIdx.x; i < 4 * STEPS * T; i += 256)
+            half[i / T][i % T] = uint4{0, 0, 0, 0};
+        __syncthreads();
+    }
+
+    auto products = [&](f32x4 (&acc)[4], int i, int pass) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const uint4 t = half[4 * s + q][16 * i + c];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                acc[NB * pass + j] = mfma<DT>(b[j][s], t, acc[NB * pass + j]);
         }
     };
-
-    const int first = (group * 4 + wave) * l.per * 64;
-    int slice = -1;
-    for (int n0 = first; n0 < first + l.per * 64 && n0 < outputs; n0 += 64) {
-        f32x4 acc[TT][4];
-        uint4 in[TT][2];
+    auto put = [&](f32x4 (&acc)[4], int i, int n0) {
+        const float f = DT == DT_F16 && adapted ? __builtin_amdgcn_ldexpf(1.0f, token_exponent(top[16 * i + c])) : 1.0f;
+        uint32_t o[2][4];  // of 32 outputs each, 8 of the lane's token
 #pragma unroll
-        for (int i = 0; i < TT; ++i)
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t u[4] = {in[i][h].x, in[i][h].y, in[i][h].z, in[i][h].w};
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                in[i][h] = *reinterpret_cast<const uint4 *>(a.y_in + (int64_t)row[i] * a.ldy_in + n0 + 16 * q + 8 * h);
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = f32x4{0, 0, 0, 0};
-        if (adapted) {
-            uint4 b[4][STEPS];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + c / 4 * 16 + 4 * j + c % 4;
-                const uint16_t *from = a.b + ((int64_t)r.slot * outputs + n) * R;
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s)
-                    b[j][s] = *reinterpret_cast<const uint4 *>(from + at[s]);
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 d = acc[2 * h + e / 2];
+                o[h][e] = adapted ? pack2<OUT>(__builtin_fmaf(d[2 * (e % 2)], f, widen_bits<DT>(u[e])),
+                                               __builtin_fmaf(d[2 * (e % 2) + 1], f, widen_bits<DT>(u[e] >> 16)))
+                                  : u[e];
             }
-            int now = 0;
-            while (n0 >= a.ends[now])
-                ++now;
-            if (now != slice) {
-                slice = now;
-                load_t(slice);
-            }
+        }
+        // whole lines: the even token's 64 outputs by both lanes, then the odd one's
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < TT; ++i)
-                        acc[i][j] = mfma<DT>(b[j][s], t[i][s], acc[i][j]);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t other = neighbour(odd ? o[0][e] : o[1][e]);
+            o[0][e] = odd ? other : o[0][e];
+            o[1][e] = odd ? o[1][e] : other;
         }
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            if (16 * i + c >= r.n)
-                continue;
-            uint16_t *to = a.y + (int64_t)row[i] * a.ldy + n0 + 16 * q;
+        for (int h = 0; h < 2; ++h) {
+            const int token = 16 * i + (c & ~1) + h;
+            if (token < r.n)
+                *reinterpret_cast<uint4 *>(a.y + (int64_t)(r.first + token) * a.ldy + n0 + 32 * (c & 1) + 8 * q) =
+                    uint4{o[h][0], o[h][1], o[h][2], o[h][3]};
+        }
+    };
+    for (int n0 = begin; n0 < end; n0 += 4 * kBlock) {
+        if (n0 > begin) {
+            load_in(n0);
+            if (adapted)
+                load_b(n0, 0);
+        }
+        if constexpr (NB == 4) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t u[4] = {in[i][h].x, in[i][h].y, in[i][h].z, in[i][h].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int m = 8 * h + 2 * e;
-                    const float d0 = __builtin_amdgcn_ldexpf(acc[i][m / 4][m % 4], exponent[i]);
-                    const float d1 = __builtin_amdgcn_ldexpf(acc[i][m / 4][m % 4 + 1], exponent[i]);
-                    o[e] = adapted ? pack2<OUT>(widen_bits<DT>(u[e]) + d0, widen_bits<DT>(u[e] >> 16) + d1) : u[e];
-                }
-                *reinterpret_cast<uint4 *>(to + 8 * h) = uint4{o[0], o[1], o[2], o[3]};
+            for (int i = 0; i < TT; ++i) {
+                f32x4 acc[4] = {};
+                if (adapted)
+                    products(acc, i, 0);
+                put(acc, i, n0);
+                __builtin_amdgcn_sched_barrier(0);  // one 16 tokens' registers
             }
+        } else {
+            f32x4 acc[TT][4] = {};
+            if (adapted) {
+#pragma unroll
+                for (int pass = 0; pass < 4 / NB; ++pass) {
+                    if (pass > 0)
+                        load_b(n0, pass);
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+                        products(acc[i], i, pass);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+                put(acc[i], i, n0);
         }
     }
 }
@@ -313,7 +396,7 @@ Launch plan_down(const LoraArgs &a)
     // parts: workgroups for the compute units, wavefronts of 128 inputs and more
     const int64_t units = (int64_t)a.segments * l.tiles * l.blocks;
     int64_t splits = 1024 / units;
-    const int64_t most = a.inputs / 512 < kMaxSplits ? a.inputs / 512 : kMaxSplits;
+    const int64_t many = size > 16 ? 4 : kMaxSplits, most = a.inputs / 512 < many ? a.inputs / 512 : many;
     splits = splits > most ? most : splits;
     l.splits = splits < 1 ? 1 : (int)splits;
     return l;
@@ -335,23 +418,32 @@ hipError_t launch_down(const LoraArgs &a, const Launch &l, hipStream_t stream)
     }
 }
 
-template <int DT, int TT>
+template <int DT, int TT, int NB, int STEPS>
 hipError_t launch_up(const LoraArgs &a, Launch l, hipStream_t stream)
 {
     l.tiles = (int)(((int64_t)a.max_rows + 16 * TT - 1) / (16 * TT));
-    const int64_t all = a.ends[a.slices - 1] / 64, units = (int64_t)a.segments * l.tiles;
+    // blocks of outputs of a wavefront: while there are workgroups for the compute units
+    const int64_t all = a.ends[a.slices - 1] / kBlock, units = (int64_t)a.segments * l.tiles;
     int64_t per = all * units / 4096;
-    per = per < 1 ? 1 : (per > 8 ? 8 : per);
+    per = per < 1 ? 1 : (per > 4 ? 4 : per);
     l.per = (int)per;
-    l.blocks = (int)((all + 4 * per - 1) / (4 * per));
+    l.blocks = 0;
+    for (int i = 0, from = 0; i < a.slices; from = a.ends[i++])
+        l.blocks += (a.ends[i] - from + 4 * kBlock * l.per - 1) / (4 * kBlock * l.per);
     const unsigned grid = (unsigned)a.segments * (unsigned)l.tiles * (unsigned)l.blocks;
+    return kv4_launch(lora_up_kernel<DT, TT, NB, STEPS>, grid, 256, stream, a, l);
+}
+
+template <int DT, int TT>
+hipError_t launch_up(const LoraArgs &a, const Launch &l, hipStream_t stream)
+{
     if (a.rank <= 16)
-        return kv4_launch(lora_up_kernel<DT, TT, 1>, grid, 256, stream, a, l);
+        return launch_up<DT, TT, 4, 1>(a, l, stream);
     if (a.rank <= 32)
-        return kv4_launch(lora_up_kernel<DT, TT, 2>, grid, 256, stream, a, l);
-    if (a.rank <= 64 || TT > 2)
-        return kv4_launch(lora_up_kernel<DT, TT, 4>, grid, 256, stream, a, l);
-    return kv4_launch(lora_up_kernel<DT, (TT > 2 ? 2 : TT), 8>, grid, 256, stream, a, l);
+        return launch_up<DT, TT, 4, 2>(a, l, stream);
+    if (a.rank <= 64)
+        return launch_up<DT, TT, 4, 4>(a, l, stream);
+    return launch_up<DT, TT, 2, 8>(a, l, stream);
 }
 
 template <int DT>
@@ -360,9 +452,7 @@ hipError_t launch(const LoraArgs &a, const Launch &l, hipStream_t stream)
     const hipError_t e = a.max_rows > 16 ? launch_down<DT, 2>(a, l, stream) : launch_down<DT, 1>(a, l, stream);
     if (e != hipSuccess)
         return e;
-    if (a.max_rows <= 16)
-        return launch_up<DT, 1>(a, l, stream);
-    return a.max_rows <= 32 || a.rank > 64 ? launch_up<DT, 2>(a, l, stream) : launch_up<DT, 4>(a, l, stream);
+    return a.max_rows > 16 ? launch_up<DT, 4>(a, l, stream) : launch_up<DT, 1>(a, l, stream);
 }
 
 }  // namespace
