@@ -127,25 +127,19 @@ struct Kv4Launch {
     float *part;       // splits > 1: [rows * q_heads][splits][head_dim] outputs, not yet divided by their sums,
                        // times 2^-sum_bits(pages),
     float *part_stat;  // [rows * q_heads][splits][2]: maximum in units of log2, sum
-    // Launches over shared prefixes and over what lies behind them leave parts only, of
-    // one sum_bits(sum_pages), in slots slot0 .. slot0 + splits - 1 of `slots`; the last
-    // split has all that is left of a tile's pages.
+    // With shared prefixes: the first front_groups workgroups are for the runs' shared pages
+    // (tiles and splits of their own, front_pages pages a split), the others for what each
+    // sequence has behind them.  All leave parts, of one sum_bits(sum_pages): those of
+    // shared pages in the first front_splits of `slots`.  The last split has all that is
+    // left of a tile's pages.
     Kv4Runs runs;
-    int slots, slot0, sum_pages, front_pages;  // front_pages: of a part over shared ones
+    unsigned front_groups;
+    int front_tiles, front_splits, front_pages, slots, sum_pages;
 };
 
-// Which pages a launch is for: all that a tile sees; those that a run of sequences
-// shares, for all of the run's rows; those behind the shared ones.
-enum class Pages { All, Shared, Own };
-
-template <Pages PAGES>
-__device__ __forceinline__ int last_page_of(const Kv4Launch &n, int split, int begin, int count)
-{
-    if constexpr (PAGES == Pages::All)
-        return n.splits > 1 && begin + n.pages < count ? begin + n.pages : count;
-    else
-        return split < n.splits - 1 && begin + n.pages < count ? begin + n.pages : count;
-}
+// All: what a launch without shared prefixes does.  Shared: the other, a workgroup's
+// part of it told by its Tile.
+enum class Pages { All, Shared };
 
 __device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
 __device__ __forceinline__ f32x4 ldexp_f(f32x4 x, int e)
@@ -440,26 +434,28 @@ __device__ __forceinline__ int shared_pages(const Kv4Args &a, const Kv4Runs &r, 
 }
 
 // A tile of COLS columns of one (sequence, kv head): columns are the pairs
-// (row, query head of the group), c = row * G + g.  Over shared pages: of one (run, kv
-// head), all of whose rows see all tokens.
+// (row, query head of the group), c = row * G + g.  Over shared pages (front): of one
+// (run, kv head), all of whose rows see all tokens.
 struct Tile {
     Kv4Sequence seq;
     int b;                 // whose page table
     int h, G, tile, cols;  // cols: columns of the sequence
     int p_lo, p_hi;        // positions of the tile's first and last column
+    bool front;
     int shared;            // pages in front of the range, left to the sequence's run
     PageRange range;
 };
 
 template <int COLS, Pages PAGES>
-__device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int b, int h, int tile, Tile &t)
+__device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int b, int h, int tile, bool front, Tile &t)
 {
     t.h = h;
     t.G = a.q_heads / a.kv.kv_heads;
     t.tile = tile;
     t.b = b;
     t.shared = 0;
-    if constexpr (PAGES == Pages::Shared) {
+    t.front = PAGES == Pages::Shared && front;
+    if (t.front) {
         const Run run = run_of(a.kv, n.runs, b);
         if (run.pages == 0)
             return false;
@@ -473,17 +469,12 @@ __device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Laun
     t.cols = t.seq.n * t.G;
     if ((int64_t)tile * COLS >= t.cols)
         return false;
-    if constexpr (PAGES == Pages::Shared) {
-        t.p_lo = t.p_hi = t.seq.kv - 1;
-        t.range = pages_seen(t.p_lo, t.p_hi, 0, 0);
-        return true;
-    }
     const int first = t.seq.kv - t.seq.n;
     const int last = t.cols - tile * COLS < COLS ? t.cols - 1 : tile * COLS + COLS - 1;
-    t.p_lo = first + tile * COLS / t.G;
-    t.p_hi = first + last / t.G;
+    t.p_lo = t.front ? t.seq.kv - 1 : first + tile * COLS / t.G;
+    t.p_hi = t.front ? t.seq.kv - 1 : first + last / t.G;
     t.range = pages_seen(t.p_lo, t.p_hi, a.window, a.sinks);
-    if constexpr (PAGES == Pages::Own) {  // window 0: the range is [0, count)
+    if (PAGES == Pages::Shared && !t.front) {  // window 0: the range is [0, count)
         t.shared = shared_pages(a.kv, n.runs, b, t.seq);
         t.range.first += t.shared;
         t.range.count -= t.shared;
@@ -495,20 +486,48 @@ __device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Laun
 template <Pages PAGES>
 __device__ __forceinline__ int position_of(const Tile &t, int row)
 {
-    return PAGES == Pages::Shared ? t.p_hi : t.seq.kv - t.seq.n + row;
+    return PAGES == Pages::Shared && t.front ? t.p_hi : t.seq.kv - t.seq.n + row;
 }
 
-// Whether a tile's results are parts.  (Own pages: a tile that sees none, rows in front
-// of their sequence, has its zeros at once.)
+// A workgroup's number among those of its kind, and how many chunks of how many pages
+// those deal a tile's pages to.
+template <Pages PAGES>
+__device__ __forceinline__ bool is_front(const Kv4Launch &n, unsigned &id)
+{
+    if (PAGES == Pages::All || id >= n.front_groups) {
+        id -= PAGES == Pages::All ? 0u : n.front_groups;
+        return false;
+    }
+    return true;
+}
+template <Pages PAGES>
+__device__ __forceinline__ int splits_of(const Kv4Launch &n, bool front)
+{
+    return PAGES == Pages::Shared && front ? n.front_splits : n.splits;
+}
+template <Pages PAGES>
+__device__ __forceinline__ bool chunk_of(const Kv4Launch &n, const Tile &t, int split, int &begin, int &end)
+{
+    const int splits = splits_of<PAGES>(n, t.front), pages = PAGES == Pages::Shared && t.front ? n.front_pages : n.pages;
+    begin = splits > 1 ? split * pages : 0;
+    if (split > 0 && begin >= t.range.count)
+        return false;
+    const bool rest = PAGES == Pages::All ? splits < 2 : split == splits - 1;
+    end = !rest && begin + pages < t.range.count ? begin + pages : t.range.count;
+    return true;
+}
+
+// Whether a tile's results are parts.  (With shared prefixes all are, but for a tile that
+// sees no page, rows in front of their sequence: it has its zeros at once.)
 template <Pages PAGES>
 __device__ __forceinline__ bool in_parts(const Kv4Launch &n, const Tile &t)
 {
-    return PAGES == Pages::All ? n.splits > 1 && t.range.count > n.pages : PAGES == Pages::Shared || t.range.count > 0;
+    return PAGES == Pages::All ? n.splits > 1 && t.range.count > n.pages : t.range.count > 0;
 }
 template <Pages PAGES>
-__device__ __forceinline__ int64_t part_of(const Kv4Launch &n, int64_t pair, int split)
+__device__ __forceinline__ int64_t part_of(const Kv4Launch &n, const Tile &t, int64_t pair, int split)
 {
-    return PAGES == Pages::All ? pair * n.splits + split : pair * n.slots + n.slot0 + split;
+    return PAGES == Pages::All ? pair * n.splits + split : pair * n.slots + (t.front ? 0 : n.front_splits) + split;
 }
 
 // The tile's first position is its newest token that all columns may see (false: their
@@ -566,7 +585,10 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b, int dtype)
 
 // The kernels, one launch each: tiles of 16 columns (few rows), of 128 or 256.
 constexpr int kFewCols = 16;
-hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream);
-hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream);
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+// With shared prefixes: front_groups 0, or tiles 0, for one of the two alone.
+hipError_t launch_kv4_few_rows_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
+hipError_t launch_kv4_many_rows_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream);
 
 }  // namespace cider

@@ -28,13 +28,13 @@ constexpr int kMaxSplits = 256;
 template <int COLS, bool SHARED>
 __device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Launch &n, int64_t id, Tile &t, int &col, int &front)
 {
-    constexpr Pages PAGES = SHARED ? Pages::Own : Pages::All;
+    constexpr Pages PAGES = SHARED ? Pages::Shared : Pages::All;
     const int64_t cols = (int64_t)a.kv.max_rows * (a.q_heads / a.kv.kv_heads);
     col = (int)(id % cols);
     front = 0;
     const int64_t bh = id / cols;
     const bool mine = bh < (int64_t)a.kv.kv_heads * a.kv.batch &&
-                      tile_of<COLS, PAGES>(a, n, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, t) &&
+                      tile_of<COLS, PAGES>(a, n, (int)(bh / a.kv.kv_heads), (int)(bh % a.kv.kv_heads), col / COLS, false, t) &&
                       col < t.cols && in_parts<PAGES>(n, t);
     if (!mine)
         return 0;
@@ -42,7 +42,7 @@ __device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Laun
     if constexpr (!SHARED)
         return parts;
     front = (t.shared + n.front_pages - 1) / n.front_pages;
-    front = front < n.slot0 ? front : n.slot0;
+    front = front < n.front_splits ? front : n.front_splits;
     return front + (parts < n.splits ? parts : n.splits);
 }
 
@@ -50,7 +50,7 @@ __device__ __forceinline__ int parts_of(const Kv4AttentionArgs &a, const Kv4Laun
 template <bool SHARED>
 __device__ __forceinline__ int slot_of(const Kv4Launch &n, int i, int front)
 {
-    return SHARED && i >= front ? n.slot0 + i - front : i;
+    return SHARED && i >= front ? n.front_splits + i - front : i;
 }
 template <bool SHARED>
 __device__ __forceinline__ int64_t slots_of(const Kv4Launch &n) { return SHARED ? n.slots : n.splits; }
@@ -365,12 +365,7 @@ hipError_t launch_join(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_
     return a.kv.head_dim == 64 ? launch_join<64, SHARED>(a, n, stream) : launch_join<128, SHARED>(a, n, stream);
 }
 
-hipError_t launch_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
-{
-    return n.cols == kFewCols ? launch_kv4_few_rows(a, n, pages, stream) : launch_kv4_many_rows(a, n, pages, stream);
-}
-
-// The launches over shared pages (front) and over those behind them (own), each
+// The workgroups over shared pages (front) and over those behind them (own), each
 // planned as a call of its own: the runs as sequences of max_pages pages, and the
 // sequences with what the longest has behind the longest prefix.  A sequence that has
 // more (it is in no run, its run shares less) gives it to its last split.
@@ -381,18 +376,6 @@ struct SharedPlan {
 SharedPlan plan_shared(const Kv4AttentionArgs &a, const Kv4Runs &r)
 {
     const int all = (a.kv.max_kv_len + kPageTokens - 1) / kPageTokens;
-    // half of what a join takes at most
-    auto planned = [](const Kv4AttentionArgs &x, int pages) {
-        Kv4Launch n = plan(x);
-        if (n.splits < 2) {
-            n.splits = 1;
-            n.pages = pages;
-        } else if (n.splits > kMaxSplits / 2) {
-            n.pages = (n.pages * n.splits + kMaxSplits / 2 - 1) / (kMaxSplits / 2);
-            n.splits = kMaxSplits / 2;
-        }
-        return n;
-    };
     Kv4AttentionArgs f = a;
     f.kv.batch = r.groups;
     f.kv.max_rows = r.max_rows;
@@ -402,15 +385,45 @@ SharedPlan plan_shared(const Kv4AttentionArgs &a, const Kv4Runs &r)
     o.kv.max_kv_len -= r.max_pages * kPageTokens;
     const int least = a.kv.max_rows < a.kv.max_kv_len ? a.kv.max_rows : a.kv.max_kv_len;
     o.kv.max_kv_len = o.kv.max_kv_len < least ? least : o.kv.max_kv_len;
-    SharedPlan p = {planned(f, r.max_pages), planned(o, all)};
+    SharedPlan p = {plan(f), plan(o)};
+    // Tiles of 16 columns: there is a join in any case, so that chunks are as long as
+    // leaves 768 workgroups of 4 wavefronts, which the compute units hold at once, of both
+    // kinds together (64 sequences behind 8192 tokens: 36.1 us with 768, 38.6 with 1024,
+    // 42.2 with 2048; 30 with drafts behind 3 prefixes: 27.1, 28.6, 30.9).
+    constexpr int kHeld = 768;
+    auto few_pages = [](const Kv4AttentionArgs &x, const Kv4Launch &n) {
+        return n.cols == kFewCols ? units_of(x, kFewCols) * most_pages(x, kFewCols) : int64_t(0);
+    };
+    const int64_t chunk = (few_pages(f, p.front) + few_pages(o, p.own) + 4 * kHeld - 1) / (4 * kHeld) * 4;
+    auto deal = [&](const Kv4AttentionArgs &x, Kv4Launch &n) {
+        const int64_t pages = most_pages(x, n.cols);
+        if (n.cols == kFewCols)
+            n.pages = (int)(chunk < 32 ? chunk : 32);
+        else if (n.splits < 2)
+            n.pages = (int)pages;
+        // a join takes kMaxSplits, and a launch counts workgroups in 32 bits
+        const int64_t room = (int64_t(1) << 30) / units_of(x, n.cols), most = room < kMaxSplits / 2 ? (room < 1 ? 1 : room) : kMaxSplits / 2;
+        if ((pages + n.pages - 1) / n.pages > most)
+            n.pages = (int)((pages + most - 1) / most);
+        n.splits = (int)((pages + n.pages - 1) / n.pages);
+    };
+    deal(f, p.front);
+    deal(o, p.own);
     for (Kv4Launch *n : {&p.front, &p.own}) {
         n->runs = r;
         n->slots = p.front.splits + p.own.splits;
         n->sum_pages = all > r.max_pages ? all : r.max_pages;
+        n->front_groups = (unsigned)p.front.tiles * (unsigned)p.front.splits * (unsigned)a.kv.kv_heads * (unsigned)r.groups;
+        n->front_tiles = p.front.tiles;
+        n->front_splits = p.front.splits;
         n->front_pages = p.front.pages;
     }
-    p.own.slot0 = p.front.splits;
     return p;
+}
+
+hipError_t launch_pages(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    return n.cols == kFewCols ? launch_kv4_few_rows_shared(a, n, stream) : launch_kv4_many_rows_shared(a, n, stream);
 }
 
 }  // namespace
@@ -432,7 +445,7 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs &a, void *workspace, size
     }
     if (n.splits > 1)
         use_workspace(a, n, n.splits, workspace);
-    const hipError_t e = launch_pages(a, n, Pages::All, stream);
+    const hipError_t e = n.cols == kFewCols ? launch_kv4_few_rows(a, n, stream) : launch_kv4_many_rows(a, n, stream);
     if (e != hipSuccess || n.splits < 2)
         return e;
     return launch_join<false>(a, n, stream);
@@ -445,10 +458,16 @@ hipError_t launch_kv4_attention_shared(const Kv4AttentionArgs &a, const Kv4Runs 
     SharedPlan p = plan_shared(a, r);
     for (Kv4Launch *n : {&p.front, &p.own})
         use_workspace(a, *n, n->slots, workspace);
-    hipError_t e = launch_pages(a, p.front, Pages::Shared, stream);
+    hipError_t e = hipSuccess;
+    const Kv4Launch own = p.own;
+    if (p.front.cols != p.own.cols) {
+        p.front.tiles = 0;
+        e = launch_pages(a, p.front, stream);
+        p.own.front_groups = 0;
+    }
     if (e == hipSuccess)
-        e = launch_pages(a, p.own, Pages::Own, stream);
-    return e == hipSuccess ? launch_join<true>(a, p.own, stream) : e;
+        e = launch_pages(a, p.own, stream);
+    return e == hipSuccess ? launch_join<true>(a, own, stream) : e;
 }
 
 }  // namespace cider

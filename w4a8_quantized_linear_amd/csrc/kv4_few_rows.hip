@@ -534,19 +534,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // heads fastest, then sequences, splits and tiles
     unsigned id = kv4_workgroup();
+    const bool front = is_front<PAGES>(n, id);
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
-    const unsigned batch = (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const unsigned batch = (unsigned)(front ? n.runs.groups : a.kv.batch), splits = (unsigned)splits_of<PAGES>(n, front);
     const int b = (int)(id % batch);
     id /= batch;
-    const int split = (int)(id % (unsigned)n.splits), tile = (int)(id / (unsigned)n.splits);
+    const int split = (int)(id % splits), tile = (int)(id / splits);
     Tile t;
-    if (!tile_of<kCols, PAGES>(a, n, b, head, tile, t))
+    if (!tile_of<kCols, PAGES>(a, n, b, head, tile, front, t))
         return;
-    const int begin = n.splits > 1 ? split * n.pages : 0;
-    if (split > 0 && begin >= t.range.count)
+    int begin, end;
+    if (!chunk_of<PAGES>(n, t, split, begin, end))
         return;
-    const int end = last_page_of<PAGES>(n, split, begin, t.range.count);
 
     int lane = threadIdx.x & 63;
     if constexpr (ONE) {
@@ -579,7 +579,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
             o[e] += part[w][oc][d0 + e] * f;
     }
     if (in_parts<PAGES>(n, t)) {
-        const int64_t at = part_of<PAGES>(n, pair_of(a, t, ocol), split);
+        const int64_t at = part_of<PAGES>(n, t, pair_of(a, t, ocol), split);
 #pragma unroll
         for (int e = 0; e < PER; ++e)
             n.part[at * D + d0 + e] = o[e];
@@ -608,8 +608,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
 template <int WAVES, bool FINE, bool ONCE, bool ONE, Pages PAGES = Pages::All>
 static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
-                          (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const unsigned grid = (PAGES == Pages::Shared ? n.front_groups : 0u) +
+                          (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
         return kv4_launch(kv4_few_rows_kernel<64, 64, WAVES, FINE, ONCE, ONE, PAGES>, grid, 64 * WAVES, stream, a, n);
     if (a.kv.group_size == 64)
@@ -631,29 +631,23 @@ static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStrea
     return n.once ? launch<WAVES, false, true>(a, n, stream) : launch<WAVES, false, false>(a, n, stream);
 }
 
-// Beside shared prefixes: all columns of a tile see all shared pages, so it has one
-// exponent for them however many rows there are.
-template <int WAVES, bool FINE>
-static hipError_t launch_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (pages == Pages::Shared)
-        return launch<WAVES, FINE, false, true, Pages::Shared>(a, n, stream);
-    return a.kv.max_rows == 1 ? launch<WAVES, FINE, false, true, Pages::Own>(a, n, stream)
-                              : launch<WAVES, FINE, false, false, Pages::Own>(a, n, stream);
+    return n.waves == 8 ? launch<8>(a, n, stream) : launch<4>(a, n, stream);
 }
 
-template <int WAVES>
-static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+// All columns of a tile see all shared pages, so without workgroups for sequences of
+// several rows it has one exponent for them.
+template <bool FINE>
+static hipError_t launch_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (pages == Pages::All)
-        return launch<WAVES>(a, n, stream);
-    return a.y_dtype == DT_F16 ? launch_shared<WAVES, true>(a, n, pages, stream)
-                               : launch_shared<WAVES, false>(a, n, pages, stream);
+    return a.kv.max_rows == 1 || n.tiles == 0 ? launch<4, FINE, false, true, Pages::Shared>(a, n, stream)
+                                              : launch<4, FINE, false, false, Pages::Shared>(a, n, stream);
 }
 
-hipError_t launch_kv4_few_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+hipError_t launch_kv4_few_rows_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    return n.waves == 8 ? launch<8>(a, n, pages, stream) : launch<4>(a, n, pages, stream);
+    return a.y_dtype == DT_F16 ? launch_shared<true>(a, n, stream) : launch_shared<false>(a, n, stream);
 }
 
 }  // namespace cider

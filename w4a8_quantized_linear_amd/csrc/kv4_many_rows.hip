@@ -666,7 +666,7 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
                        exp_of(x * 32 / GS) + 24 - kTop - e);
     };
     if (in_parts<PAGES>(n, t)) {
-        const int64_t at = part_of<PAGES>(n, pair_of(a, t, col), split);
+        const int64_t at = part_of<PAGES>(n, t, pair_of(a, t, col), split);
         const int less = sum_bits(PAGES == Pages::All ? n.pages : n.sum_pages);
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -703,23 +703,23 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
     // 617 us against 232)
     unsigned id = kv4_workgroup();
+    const bool front = is_front<PAGES>(n, id);
     const int head = (int)(id % (unsigned)a.kv.kv_heads);
     id /= (unsigned)a.kv.kv_heads;
-    const unsigned batch = (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const unsigned batch = (unsigned)(front ? n.runs.groups : a.kv.batch), splits = (unsigned)splits_of<PAGES>(n, front);
     const unsigned turn = id % batch;
     id /= batch;
-    const int split = (int)(id % (unsigned)n.splits);
-    const int tile = n.tiles - 1 - (int)(id / (unsigned)n.splits);
+    const int split = (int)(id % splits);
+    const int tile = (PAGES == Pages::Shared && front ? n.front_tiles : n.tiles) - 1 - (int)(id / splits);
     if (tile < 0)
         return;
     const int b = (int)((turn + (unsigned)tile) % batch);
     Tile t;
-    if (!tile_of<COLS, PAGES>(a, n, b, head, tile, t))
+    if (!tile_of<COLS, PAGES>(a, n, b, head, tile, front, t))
         return;
-    const int begin = n.splits > 1 ? split * n.pages : 0;
-    if (split > 0 && begin >= t.range.count)
+    int begin, end;
+    if (!chunk_of<PAGES>(n, t, split, begin, end))
         return;
-    const int end = last_page_of<PAGES>(n, split, begin, t.range.count);
 
     // a tile whose columns share no token goes the long way at once
     int tid = threadIdx.x;
@@ -736,11 +736,11 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
 
 }  // namespace
 
-template <int COLS, Pages PAGES = Pages::All>
+template <int COLS, Pages PAGES>
 static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    const unsigned grid = (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads *
-                          (unsigned)(PAGES == Pages::Shared ? n.runs.groups : a.kv.batch);
+    const unsigned grid = (PAGES == Pages::Shared ? n.front_groups : 0u) +
+                          (unsigned)n.tiles * (unsigned)n.splits * (unsigned)a.kv.kv_heads * (unsigned)a.kv.batch;
     if (a.kv.head_dim == 64)
         return kv4_launch(kv4_many_rows_kernel<64, 64, COLS, PAGES>, grid, COLS * 2, stream, a, n);
     if (a.kv.group_size == 64)
@@ -748,13 +748,13 @@ static hipError_t launch(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStrea
     return kv4_launch(kv4_many_rows_kernel<128, 128, COLS, PAGES>, grid, COLS * 2, stream, a, n);
 }
 
-hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, Pages pages, hipStream_t stream)
+hipError_t launch_kv4_many_rows(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
 {
-    if (pages == Pages::Shared)
-        return n.cols == 256 ? launch<256, Pages::Shared>(a, n, stream) : launch<128, Pages::Shared>(a, n, stream);
-    if (pages == Pages::Own)
-        return n.cols == 256 ? launch<256, Pages::Own>(a, n, stream) : launch<128, Pages::Own>(a, n, stream);
-    return n.cols == 256 ? launch<256>(a, n, stream) : launch<128>(a, n, stream);
+    return n.cols == 256 ? launch<256, Pages::All>(a, n, stream) : launch<128, Pages::All>(a, n, stream);
+}
+hipError_t launch_kv4_many_rows_shared(const Kv4AttentionArgs &a, const Kv4Launch &n, hipStream_t stream)
+{
+    return n.cols == 256 ? launch<256, Pages::Shared>(a, n, stream) : launch<128, Pages::Shared>(a, n, stream);
 }
 
 }  // namespace cider
