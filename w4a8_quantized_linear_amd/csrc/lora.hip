@@ -196,7 +196,7 @@ constexpr int kBlock = 64;  // outputs
 // of x 16 at a time.  STEPS: products of 32 along 2 R numbers, the high halves of t and
 // then the low ones.
 template <int DT, int TT, int NB, int STEPS>
-__global__ __launch_bounds__(256, TT == 4 && STEPS == 4 ? 3 : (STEPS <= 2 ? 4 : 1)) void lora_up_kernel(LoraArgs a, Launch l)
+__global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lora_up_kernel(LoraArgs a, Launch l)
 {
     constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16, T = 16 * TT;
     constexpr int ITEMS = (T * STEPS * 2 + 255) / 256;  // of 8 numbers of t, a thread
@@ -396,7 +396,7 @@ Launch plan_down(const LoraArgs &a)
     // parts: workgroups for the compute units, wavefronts of 128 inputs and more
     const int64_t units = (int64_t)a.segments * l.tiles * l.blocks;
     int64_t splits = 1024 / units;
-    const int64_t many = size > 16 ? 4 : kMaxSplits, most = a.inputs / 512 < many ? a.inputs / 512 : many;
+    const int64_t many = size > 16 ? 4 : kMaxSplits, most = a.inputs / 1024 < many ? a.inputs / 1024 : many;
     splits = splits > most ? most : splits;
     l.splits = splits < 1 ? 1 : (int)splits;
     return l;
@@ -422,10 +422,14 @@ template <int DT, int TT, int NB, int STEPS>
 hipError_t launch_up(const LoraArgs &a, Launch l, hipStream_t stream)
 {
     l.tiles = (int)(((int64_t)a.max_rows + 16 * TT - 1) / (16 * TT));
-    // blocks of outputs of a wavefront: while there are workgroups for the compute units
+    // blocks of outputs of a wavefront: as leave the wavefronts that are resident at once
+    // (64 rows beside 6144 outputs 13.2 us with one, 11.8 with two; 2000 beside 24576 at rank
+    // 64 74 us with three, 70.7 with four, 76.8 with six), up to two at low ranks, whose t
+    // costs little to set up again (8400 rows beside 6144 74.2 with four, 73.3 with two)
     const int64_t all = a.ends[a.slices - 1] / kBlock, units = (int64_t)a.segments * l.tiles;
-    int64_t per = all * units / 4096;
-    per = per < 1 ? 1 : (per > 4 ? 4 : per);
+    constexpr int64_t kResident = STEPS > 2 ? 3072 : 4096, kMost = STEPS == 1 ? 2 : 4;
+    int64_t per = (all * units + kResident - 1) / kResident;
+    per = per < 1 ? 1 : (per > kMost ? kMost : per);
     l.per = (int)per;
     l.blocks = 0;
     for (int i = 0, from = 0; i < a.slices; from = a.ends[i++])
