@@ -162,6 +162,17 @@ def test_every_share_of_the_inputs(inputs):
             c.check(c.run(nbytes=parts * one + parts % 2 * 4))
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("rank", [8, 16])
+def test_many_segments_of_few_rows(rank, dtype):
+    """More than one launch of both products holds at once, and fewer; outputs that end inside a workgroup's."""
+    r = np.random.default_rng(rank)
+    for segments, ends in ((200, [64]), (90, [1088, 1152]), (40, [1088, 1152])):
+        rows = list(r.integers(0, 4, segments))
+        c = Case(rows, r.integers(-1, 4, segments), rank, 192, ends, dtype, seed=13)
+        c.check(c.run(in_place=dtype == 1))
+
+
 @pytest.mark.parametrize("dtype,x_std,a_std,b_std", [
     (0, 2e4, 1.0, 1e-4), (0, 1e-6, 1e-3, 1e3), (1, 1e15, 1e10, 1e-26), (1, 1e-20, 1e-10, 1e30), (0, 1.0, 100.0, 1e-3),
 ])

@@ -26,10 +26,10 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // (uint4 in arrays that a loop fills went to scratch)
 
 template <int DT>
-__device__ __forceinline__ f32x4 mfma(uint4 x, uint4 y, f32x4 z)
+__device__ __forceinline__ f32x4 mfma(u32x4 x, u32x4 y, f32x4 z)
 {
     if constexpr (DT == DT_BF16)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bhalf8, x), __builtin_bit_cast(bhalf8, y), z, 0, 0, 0);
@@ -70,18 +70,80 @@ __device__ __forceinline__ Rows rows_of(const LoraArgs &a, int segment, int tile
     return r;
 }
 
+// The products of 16 TT rows of x with 16 NT rows of A, the j-th of the slot's `width`
+// and those behind it, over the inputs k0 .. k1 - 1, by one wavefront.  Both go through
+// its LDS: memory is read by consecutive lanes, 8 and more to a row, where the operands'
+// lanes go from row to row, which the load path takes a quarter as fast (8400 rows of
+// 4096 inputs 36 us by the operands' lanes, 24 so).  KS: times 64 inputs loaded at once.
+// Lane (q, c) ends with rows 4 q .. 4 q + 3 of a block of A for token c.
+template <int TT, int NT, int KS>
+constexpr int kStageWords = 16 * (TT + NT) * 8 * KS;
+template <int DT, int TT, int NT, int KS>
+__device__ __forceinline__ void multiply_rows(const LoraArgs &a, const Rows &r, int j0, int width, int k0, int k1, int lane,
+                                              u32x4 *stage, f32x4 (&acc)[TT][NT])
+{
+    constexpr int CHUNKS = 8 * KS, LOADS = kStageWords<TT, NT, KS> / 64;
+    if (k0 >= k1)
+        return;
+    const int c = lane % 16, q = lane / 16;
+    // the lane's i-th word is chunk (64 i + lane) % CHUNKS of row (64 i + lane) / CHUNKS
+    const uint16_t *from[LOADS];
+    const int chunk = lane % CHUNKS;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int row = (64 * i + lane) / CHUNKS;
+        if (row < 16 * TT) {
+            from[i] = a.x + (int64_t)(r.first + (row < r.n ? row : r.n - 1)) * a.ldx;
+        } else {
+            const int j = j0 + row - 16 * TT;
+            from[i] = a.a + ((int64_t)r.slot * width + (j < width ? j : width - 1)) * a.inputs;
+        }
+    }
+    u32x4 word[LOADS];
+    auto load = [&](int k) {
+        const int at = k + 8 * chunk < k1 ? k + 8 * chunk : k1 - 8;  // past the end: anything that is there
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            word[i] = *reinterpret_cast<const u32x4 *>(from[i] + at);
+    };
+    load(k0);
+    for (int k = k0; k < k1; k += 64 * KS) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = (64 * i + lane) / CHUNKS;
+            stage[row * CHUNKS + (chunk ^ row % 8)] = word[i];
+        }
+        wave_fence();
+        if (k + 64 * KS < k1)
+            load(k + 64 * KS);
+#pragma unroll
+        for (int s = 0; s < 2 * KS; ++s)
+            if (k + 32 * s < k1) {
+                u32x4 x[TT];
+                const int at = (4 * s + q) ^ c % 8;
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                    x[i] = stage[(16 * i + c) * CHUNKS + at];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const u32x4 w = stage[(16 * (TT + j) + c) * CHUNKS + at];
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+                        acc[i][j] = mfma<DT>(w, x[i], acc[i][j]);
+                }
+            }
+        wave_fence();
+    }
+}
+
 // A workgroup has 16 TT rows of x and 16 NT rows of A, each of its wavefronts a quarter
-// of the split's inputs.  Both go through LDS (the wavefront's own): memory is read by
-// consecutive lanes, 8 and more to a row, where the operands' lanes go from row to row,
-// which the load path takes a quarter as fast.
+// of the split's inputs.
 template <int DT, int TT, int NT>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
 {
-    constexpr int ROWS = 16 * (TT + NT);
-    constexpr int KS = TT + NT <= 2 ? 4 : (TT + NT <= 4 ? 2 : 1);  // times 64 inputs loaded at once
-    constexpr int CHUNKS = 8 * KS, LOADS = ROWS * CHUNKS / 64;
-    constexpr int STAGE = ROWS * CHUNKS, PART = TT * NT * 64;      // 16-byte words of a wavefront
-    __shared__ uint4 lds[4][STAGE > PART ? STAGE : PART];
+    constexpr int KS = TT + NT <= 2 ? 4 : (TT + NT <= 4 ? 2 : 1);
+    constexpr int STAGE = kStageWords<TT, NT, KS>, PART = TT * NT * 64;  // of a wavefront
+    __shared__ u32x4 lds[4][STAGE > PART ? STAGE : PART];
     unsigned id = kv4_workgroup();
     const int block = (int)(id % (unsigned)l.blocks);
     id /= (unsigned)l.blocks;
@@ -97,68 +159,15 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int width = a.slices * a.rank;  // rows of A
     const int k0 = (split * 4 + wave) * l.chunk, k1 = k0 + l.chunk < a.inputs ? k0 + l.chunk : a.inputs;
-    uint4 *stage = lds[wave];
     f32x4 acc[TT][NT] = {};
-    if (k0 < k1) {
-        // the lane's i-th word is chunk (64 i + lane) % CHUNKS of row (64 i + lane) / CHUNKS:
-        // its rows are 64 / CHUNKS apart (or its only one)
-        const uint16_t *from[LOADS];
-        const int chunk = lane % CHUNKS;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int row = (64 * i + lane) / CHUNKS;
-            if (row < 16 * TT) {
-                from[i] = a.x + (int64_t)(r.first + (row < r.n ? row : r.n - 1)) * a.ldx;
-            } else {
-                const int j = block * NT * 16 + row - 16 * TT;
-                from[i] = a.a + ((int64_t)r.slot * width + (j < width ? j : width - 1)) * a.inputs;
-            }
-        }
-        u32x4 word[LOADS];
-        auto load = [&](int k) {
-            const int at = k + 8 * chunk < k1 ? k + 8 * chunk : k1 - 8;  // past the end: anything that is there
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i)
-                word[i] = *reinterpret_cast<const u32x4 *>(from[i] + at);
-        };
-        load(k0);
-        for (int k = k0; k < k1; k += 64 * KS) {
-            // (lanes of one wavefront: LDS takes its accesses in order)
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int row = (64 * i + lane) / CHUNKS;
-                *reinterpret_cast<u32x4 *>(&stage[row * CHUNKS + (chunk ^ row % 8)]) = word[i];
-            }
-            wave_fence();
-            if (k + 64 * KS < k1)
-                load(k + 64 * KS);
-#pragma unroll
-            for (int s = 0; s < 2 * KS; ++s)
-                if (k + 32 * s < k1) {
-                    uint4 x[TT];
-                    const int at = (4 * s + q) ^ c % 8;
-#pragma unroll
-                    for (int i = 0; i < TT; ++i)
-                        x[i] = stage[(16 * i + c) * CHUNKS + at];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint4 w = stage[(16 * (TT + j) + c) * CHUNKS + at];
-#pragma unroll
-                        for (int i = 0; i < TT; ++i)
-                            acc[i][j] = mfma<DT>(w, x[i], acc[i][j]);
-                    }
-                }
-            wave_fence();
-        }
-    }
+    multiply_rows<DT, TT, NT, KS>(a, r, block * NT * 16, width, k0, k1, lane, lds[wave], acc);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            lds[wave][(i * NT + j) * 64 + lane] = __builtin_bit_cast(uint4, acc[i][j]);
+            lds[wave][(i * NT + j) * 64 + lane] = __builtin_bit_cast(u32x4, acc[i][j]);
     __syncthreads();
-    // lane (q, c) has rows 4 q .. 4 q + 3 of a block of A for token c
 #pragma unroll
     for (int n = 0; n < TT * NT; n += 4) {
         const int at = n + wave;
@@ -182,6 +191,17 @@ __device__ __forceinline__ int token_exponent(uint32_t top)
     return e < -100 ? -100 : e;
 }
 
+// Two numbers of t, times 2^by, as high and low halves.
+template <int OUT>
+__device__ __forceinline__ void halves(float x, float y, int by, uint32_t &high, uint32_t &low)
+{
+    constexpr int DT = OUT == OUT_BF16 ? DT_BF16 : DT_F16;
+    x = __builtin_amdgcn_ldexpf(x, by);
+    y = __builtin_amdgcn_ldexpf(y, by);
+    high = pack2<OUT>(x, y);
+    low = pack2<OUT>(x - widen_bits<DT>(high), y - widen_bits<DT>(high >> 16));
+}
+
 // What the lane next to it has.
 __device__ __forceinline__ uint32_t neighbour(uint32_t v)
 {
@@ -190,20 +210,147 @@ __device__ __forceinline__ uint32_t neighbour(uint32_t v)
 
 constexpr int kBlock = 64;  // outputs
 
+// A workgroup's slice and its outputs there, `span` at most: begin .. end - 1.
+struct Outputs {
+    int slice, begin, end;
+};
+__device__ __forceinline__ Outputs outputs_of(const LoraArgs &a, int group, int span)
+{
+    Outputs o = {0, group * span, 0};
+    int from = 0;
+    for (; o.begin >= a.ends[o.slice] - from; ++o.slice) {
+        o.begin -= (a.ends[o.slice] - from + span - 1) / span * span;
+        from = a.ends[o.slice];
+    }
+    o.begin += from;
+    o.end = o.begin + span < a.ends[o.slice] ? o.begin + span : a.ends[o.slice];
+    return o;
+}
+
+// A wavefront's blocks of 64 outputs for 16 TT rows.  STEPS: products of 32 along 2 R
+// numbers, the high halves of t and then the low ones, which are in LDS as operands; NB:
+// blocks of 16 outputs whose rows of B are in registers at once.  The rows of B are taken
+// in the order that leaves a lane 8 consecutive outputs of 32, and neighbouring lanes
+// exchange theirs, so that y is written by whole lines.
+template <int DT, int TT, int NB, int STEPS>
+struct Block {
+    const LoraArgs &a;
+    const Rows r;
+    const bool adapted;
+    const int c, q;
+    u32x4 in[TT][2], b[NB][STEPS];
+
+    __device__ __forceinline__ Block(const LoraArgs &a, const Rows &r, bool adapted, int lane)
+        : a(a), r(r), adapted(adapted), c(lane % 16), q(lane / 16)
+    {
+    }
+    __device__ __forceinline__ void load_b(int n0, int pass)
+    {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int at = NB * pass + j, n = n0 + at / 2 * 32 + c / 4 * 8 + at % 2 * 4 + c % 4, R = a.rank;
+            const uint16_t *from = a.b + ((int64_t)r.slot * a.ends[a.slices - 1] + n) * R;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int k = 32 * s + 8 * q;
+                b[j][s] = *reinterpret_cast<const u32x4 *>(from + (k < R ? k : (k < 2 * R ? k - R : 0)));
+            }
+        }
+    }
+    __device__ __forceinline__ void load(int n0)
+    {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int token = 16 * i + c < r.n ? 16 * i + c : r.n - 1;
+                in[i][h] = *reinterpret_cast<const u32x4 *>(a.y_in + (int64_t)(r.first + token) * a.ldy_in + n0 + 32 * h + 8 * q);
+            }
+        if (adapted)
+            load_b(n0, 0);
+    }
+    __device__ __forceinline__ void products(const u32x4 (&half)[4 * STEPS][16 * TT], f32x4 (&acc)[4], int i, int pass)
+    {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const u32x4 t = half[4 * s + q][16 * i + c];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                acc[NB * pass + j] = mfma<DT>(b[j][s], t, acc[NB * pass + j]);
+        }
+    }
+    __device__ __forceinline__ void put(const uint32_t (&top)[16 * TT], const f32x4 (&acc)[4], int i, int n0)
+    {
+        constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16;
+        const float f = DT == DT_F16 && adapted ? __builtin_amdgcn_ldexpf(1.0f, token_exponent(top[16 * i + c])) : 1.0f;
+        const bool odd = c & 1;
+        uint32_t o[2][4];  // of 32 outputs each, 8 of the lane's token
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t u = in[i][h][e];
+                const f32x4 d = acc[2 * h + e / 2];
+                o[h][e] = adapted ? pack2<OUT>(__builtin_fmaf(d[2 * (e % 2)], f, widen_bits<DT>(u)),
+                                               __builtin_fmaf(d[2 * (e % 2) + 1], f, widen_bits<DT>(u >> 16)))
+                                  : u;
+            }
+        // the even token's 64 outputs by both lanes, then the odd one's
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t other = neighbour(odd ? o[0][e] : o[1][e]);
+            o[0][e] = odd ? other : o[0][e];
+            o[1][e] = odd ? o[1][e] : other;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int token = 16 * i + (c & ~1) + h;
+            if (token < r.n)
+                *reinterpret_cast<u32x4 *>(a.y + (int64_t)(r.first + token) * a.ldy + n0 + 32 * (c & 1) + 8 * q) =
+                    u32x4{o[h][0], o[h][1], o[h][2], o[h][3]};
+        }
+    }
+    __device__ __forceinline__ void run(const u32x4 (&half)[4 * STEPS][16 * TT], const uint32_t (&top)[16 * TT], int n0)
+    {
+        if constexpr (NB == 4) {
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+                f32x4 acc[4] = {};
+                if (adapted)
+                    products(half, acc, i, 0);
+                put(top, acc, i, n0);
+                __builtin_amdgcn_sched_barrier(0);  // one 16 tokens' registers
+            }
+        } else {
+            f32x4 acc[TT][4] = {};
+            if (adapted) {
+#pragma unroll
+                for (int pass = 0; pass < 4 / NB; ++pass) {
+                    if (pass > 0)
+                        load_b(n0, pass);
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+                        products(half, acc[i], i, pass);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+                put(top, acc[i], i, n0);
+        }
+    }
+};
+
 // A workgroup has 16 TT rows and l.per blocks of 64 outputs of one slice for each of
-// its wavefronts.  It adds t's parts for its rows and leaves their halves in LDS as
-// operands; a wavefront loads a block's rows of B (16 NB at a time) and takes the rows
-// of x 16 at a time.  STEPS: products of 32 along 2 R numbers, the high halves of t and
-// then the low ones.
+// its wavefronts.  It adds t's parts for its rows and leaves their halves in LDS.
 template <int DT, int TT, int NB, int STEPS>
 __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lora_up_kernel(LoraArgs a, Launch l)
 {
     constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16, T = 16 * TT;
     constexpr int ITEMS = (T * STEPS * 2 + 255) / 256;  // of 8 numbers of t, a thread
-    __shared__ uint4 half[4 * STEPS][T];
+    __shared__ u32x4 half[4 * STEPS][T];
     __shared__ uint32_t top[T];
     unsigned id = kv4_workgroup();
-    const int lane = threadIdx.x & 63, c = lane % 16, q = lane / 16;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int group = (int)(id % (unsigned)l.blocks);
     id /= (unsigned)l.blocks;
@@ -214,46 +361,12 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lo
     const bool adapted = (unsigned)r.slot < (unsigned)a.slots;
     if (r.n == 0 || (!adapted && a.y == a.y_in))
         return;
-    // the group's slice, and its outputs there
-    const int outputs = a.ends[a.slices - 1], R = a.rank, width = a.slices * R, span = 4 * l.per * kBlock;
-    int slice = 0, first = group * span;
-    for (int from = 0; first >= a.ends[slice] - from; ++slice) {
-        first -= (a.ends[slice] - from + span - 1) / span * span;
-        from = a.ends[slice];
-    }
-    first += slice ? a.ends[slice - 1] : 0;
-
-    // What comes from memory first of all.
-    const bool odd = c & 1;
-    const int begin = first + wave * kBlock, end = first + span < a.ends[slice] ? first + span : a.ends[slice];
-    uint4 in[TT][2], b[NB][STEPS];
-    auto load_in = [&](int n0) {
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int token = 16 * i + c < r.n ? 16 * i + c : r.n - 1;
-                in[i][h] = *reinterpret_cast<const uint4 *>(a.y_in + (int64_t)(r.first + token) * a.ldy_in + n0 + 32 * h + 8 * q);
-            }
-    };
-    auto load_b = [&](int n0, int pass) {
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            // the order that leaves a lane 8 consecutive outputs of two blocks of 32
-            const int at = NB * pass + j, n = n0 + at / 2 * 32 + c / 4 * 8 + at % 2 * 4 + c % 4;
-            const uint16_t *from = a.b + ((int64_t)r.slot * outputs + n) * R;
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int k = 32 * s + 8 * q;
-                b[j][s] = *reinterpret_cast<const uint4 *>(from + (k < R ? k : (k < 2 * R ? k - R : 0)));
-            }
-        }
-    };
-    if (begin < end) {
-        load_in(begin);
-        if (adapted)
-            load_b(begin, 0);
-    }
+    const Outputs o = outputs_of(a, group, 4 * l.per * kBlock);
+    const int begin = o.begin + wave * kBlock, R = a.rank, width = a.slices * R;
+    // what comes from memory first of all
+    Block<DT, TT, NB, STEPS> block(a, r, adapted, lane);
+    if (begin < o.end)
+        block.load(begin);
     if (adapted) {
         const float scale = a.scale ? a.scale[r.slot] : 1.0f;
         const int chunks = R / 8;
@@ -267,7 +380,7 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lo
             const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
             f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
             if (token < r.n) {
-                const float *from = l.t + (int64_t)(r.first + token) * width + slice * R + 8 * chunk;
+                const float *from = l.t + (int64_t)(r.first + token) * width + o.slice * R + 8 * chunk;
 #pragma unroll 4
                 for (int p = 0; p < l.splits; ++p) {
                     lo += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width);
@@ -293,89 +406,89 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lo
             uint32_t high[4], low[4];
             const int by = DT == DT_F16 ? -token_exponent(top[token]) : 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = __builtin_amdgcn_ldexpf(v[i][2 * e], by), y = __builtin_amdgcn_ldexpf(v[i][2 * e + 1], by);
-                high[e] = pack2<OUT>(x, y);
-                low[e] = pack2<OUT>(x - widen_bits<DT>(high[e]), y - widen_bits<DT>(high[e] >> 16));
-            }
-            half[chunk][token] = uint4{high[0], high[1], high[2], high[3]};
-            half[chunks + chunk][token] = uint4{low[0], low[1], low[2], low[3]};
+            for (int e = 0; e < 4; ++e)
+                halves<OUT>(v[i][2 * e], v[i][2 * e + 1], by, high[e], low[e]);
+            half[chunk][token] = u32x4{high[0], high[1], high[2], high[3]};
+            half[chunks + chunk][token] = u32x4{low[0], low[1], low[2], low[3]};
         }
         for (int i = 2 * chunks * T + threadIdx.x; i < 4 * STEPS * T; i += 256)
-            half[i / T][i % T] = uint4{0, 0, 0, 0};
+            half[i / T][i % T] = u32x4{0, 0, 0, 0};
         __syncthreads();
     }
+    for (int n0 = begin; n0 < o.end; n0 += 4 * kBlock) {
+        if (n0 > begin)
+            block.load(n0);
+        block.run(half, top, n0);
+    }
+}
 
-    auto products = [&](f32x4 (&acc)[4], int i, int pass) {
+// Both products in one launch, for few rows and ranks up to 16: a workgroup of 16
+// wavefronts has 1024 outputs of one slice and works out t for them by itself, a
+// sixteenth of the inputs a wavefront.  What it takes is A read again for every 1024
+// outputs, what it saves a launch, t's way through memory and the wait for it.
+template <int DT>
+__global__ __launch_bounds__(1024) void lora_step_kernel(LoraArgs a, Launch l)
+{
+    constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16, WAVES = 16, KS = 2;
+    constexpr int STAGE = kStageWords<1, 1, KS>;
+    __shared__ u32x4 lds[WAVES * STAGE];
+    __shared__ u32x4 half[4][16];
+    __shared__ uint32_t top[16];
+    unsigned id = kv4_workgroup();
+    const int lane = threadIdx.x & 63, c = lane % 16, q = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int group = (int)(id % (unsigned)l.blocks), segment = (int)(id / (unsigned)l.blocks);
+    if (segment >= a.segments)
+        return;
+    const Rows r = rows_of(a, segment, 0, 16);
+    const bool adapted = (unsigned)r.slot < (unsigned)a.slots;
+    if (r.n == 0 || (!adapted && a.y == a.y_in))
+        return;
+    const Outputs o = outputs_of(a, group, WAVES * kBlock);
+    const int begin = o.begin + wave * kBlock, R = a.rank;
+    Block<DT, 1, 4, 1> block(a, r, adapted, lane);
+    if (begin < o.end)
+        block.load(begin);
+    if (adapted) {
+        const float scale = a.scale ? a.scale[r.slot] : 1.0f;
+        const int k0 = wave * l.chunk, k1 = k0 + l.chunk < a.inputs ? k0 + l.chunk : a.inputs;
+        f32x4 acc[1][1] = {};
+        multiply_rows<DT, 1, 1, KS>(a, r, o.slice * R, a.slices * R, k0, k1, lane, lds + wave * STAGE, acc);
+        __syncthreads();
+        lds[threadIdx.x] = __builtin_bit_cast(u32x4, acc[0][0]);
+        __syncthreads();
+        if (wave == 0) {
+            f32x4 t = {0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const uint4 t = half[4 * s + q][16 * i + c];
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                acc[NB * pass + j] = mfma<DT>(b[j][s], t, acc[NB * pass + j]);
-        }
-    };
-    auto put = [&](f32x4 (&acc)[4], int i, int n0) {
-        const float f = DT == DT_F16 && adapted ? __builtin_amdgcn_ldexpf(1.0f, token_exponent(top[16 * i + c])) : 1.0f;
-        uint32_t o[2][4];  // of 32 outputs each, 8 of the lane's token
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t u[4] = {in[i][h].x, in[i][h].y, in[i][h].z, in[i][h].w};
+            for (int w = 0; w < WAVES; ++w)
+                t += __builtin_bit_cast(f32x4, lds[64 * w + lane]);
+            const bool there = 4 * q < R;  // of R numbers
+            float most = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f32x4 d = acc[2 * h + e / 2];
-                o[h][e] = adapted ? pack2<OUT>(__builtin_fmaf(d[2 * (e % 2)], f, widen_bits<DT>(u[e])),
-                                               __builtin_fmaf(d[2 * (e % 2) + 1], f, widen_bits<DT>(u[e] >> 16)))
-                                  : u[e];
+                t[e] = there ? t[e] * scale : 0.0f;
+                most = __builtin_fmaxf(most, __builtin_fabsf(t[e]));
             }
+            most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+            most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+            if (q == 0)
+                top[c] = __builtin_bit_cast(uint32_t, most);
+            const int by = DT == DT_F16 ? -token_exponent(__builtin_bit_cast(uint32_t, most)) : 0;
+            uint32_t high[2], low[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                halves<OUT>(t[2 * e], t[2 * e + 1], by, high[e], low[e]);
+            // numbers 4 q .. 4 q + 3 of the high halves' R, and of the low ones' behind them;
+            // R 8: zeros to the operand's end
+            uint2 *to = reinterpret_cast<uint2 *>(&half[0][0]);
+            auto put = [&](int k, uint2 v) { to[(k / 8 * 16 + c) * 2 + k / 4 % 2] = v; };
+            put(there ? 4 * q : 4 * q + R, uint2{high[0], high[1]});
+            put(there ? 4 * q + R : 4 * q + 2 * R, uint2{low[0], low[1]});
         }
-        // whole lines: the even token's 64 outputs by both lanes, then the odd one's
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t other = neighbour(odd ? o[0][e] : o[1][e]);
-            o[0][e] = odd ? other : o[0][e];
-            o[1][e] = odd ? o[1][e] : other;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int token = 16 * i + (c & ~1) + h;
-            if (token < r.n)
-                *reinterpret_cast<uint4 *>(a.y + (int64_t)(r.first + token) * a.ldy + n0 + 32 * (c & 1) + 8 * q) =
-                    uint4{o[h][0], o[h][1], o[h][2], o[h][3]};
-        }
-    };
-    for (int n0 = begin; n0 < end; n0 += 4 * kBlock) {
-        if (n0 > begin) {
-            load_in(n0);
-            if (adapted)
-                load_b(n0, 0);
-        }
-        if constexpr (NB == 4) {
-#pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                f32x4 acc[4] = {};
-                if (adapted)
-                    products(acc, i, 0);
-                put(acc, i, n0);
-                __builtin_amdgcn_sched_barrier(0);  // one 16 tokens' registers
-            }
-        } else {
-            f32x4 acc[TT][4] = {};
-            if (adapted) {
-#pragma unroll
-                for (int pass = 0; pass < 4 / NB; ++pass) {
-                    if (pass > 0)
-                        load_b(n0, pass);
-#pragma unroll
-                    for (int i = 0; i < TT; ++i)
-                        products(acc[i], i, pass);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-                put(acc[i], i, n0);
-        }
+        __syncthreads();
     }
+    if (begin < o.end)
+        block.run(half, top, begin);
 }
 
 constexpr int kMaxSplits = 16;
@@ -450,9 +563,33 @@ hipError_t launch_up(const LoraArgs &a, const Launch &l, hipStream_t stream)
     return launch_up<DT, TT, 2, 8>(a, l, stream);
 }
 
-template <int DT>
-hipError_t launch(const LoraArgs &a, const Launch &l, hipStream_t stream)
+// Workgroups that share a segment's outputs out.
+int step_groups(const LoraArgs &a)
 {
+    int n = 0;
+    for (int i = 0, from = 0; i < a.slices; from = a.ends[i++])
+        n += (a.ends[i] - from + 16 * kBlock - 1) / (16 * kBlock);
+    return n;
+}
+
+// Whether one launch does both: while all its workgroups run at once, one a compute unit,
+// and a wavefront's share of the inputs is short.  In a graph, rank 16, one launch
+// against two: 1 row of 4096 inputs beside 4096 outputs 6.7 / 7.3 us (from the host 7.5 /
+// 10.3), 6144 in three slices 6.8 / 8.5, 32 rows with as many adapters 8.7 / 9.8; but 64
+// of them 14.4 / 11.4, and 1 row of 12288 inputs 11.3 / 8.1.
+bool in_one(const LoraArgs &a)
+{
+    return a.max_rows <= 16 && a.rank <= 16 && a.inputs <= 6144 && (int64_t)a.segments * step_groups(a) <= 192;
+}
+
+template <int DT>
+hipError_t launch(const LoraArgs &a, Launch l, hipStream_t stream)
+{
+    if (in_one(a)) {
+        l.chunk = (a.inputs / 64 + 15) / 16 * 64;
+        l.blocks = step_groups(a);
+        return kv4_launch(lora_step_kernel<DT>, (unsigned)a.segments * (unsigned)l.blocks, 1024, stream, a, l);
+    }
     const hipError_t e = a.max_rows > 16 ? launch_down<DT, 2>(a, l, stream) : launch_down<DT, 1>(a, l, stream);
     if (e != hipSuccess)
         return e;
