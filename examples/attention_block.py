@@ -4,13 +4,17 @@ a batch of prompts first, then decoding steps replayed from a HIP graph.
 
     python examples/attention_block.py [--batch 8] [--prompt 1000] [--steps 32]
                                        [--bits 4] [--window 0] [--sinks 4]
+                                       [--rotate] [--adapters 0] [--shared 0]
 
 Sizes are those of the benchmark's decoder stack (hidden 4096, 32 query heads
 and 8 key/value heads of 128: QKV 6144 x 4096, O 4096 x 4096); weights are
-random.  Positions are not encoded: a model that rotates q and k does so with an
-operation of its own between the product and the append.  Prints the time of the prompt pass and of a decoding step, and how far
-the block's attention is from 16-bit attention over the same keys and values
-(what 4 bits cost)."""
+random.  --rotate: q and k are normed for each head and turned by their positions
+on the way into the cache (without it positions are not encoded).  --adapters n:
+the sequences take n low-rank adapters by turns, beside both products.  --shared
+n: the prompts begin with the same n tokens, whose whole pages are in the cache
+once and attended to once for all sequences.  Prints the time of the prompt pass
+and of a decoding step, and how far the block's attention is from 16-bit attention
+over the same keys and values (what 4 bits cost)."""
 from __future__ import annotations
 
 import argparse
@@ -45,9 +49,25 @@ class Linear:
                               workspace, workspace.numel(), y)
 
 
+class Adapters:
+    """Low-rank corrections of a product, `slots` of them, and the segments of rows that take them."""
+
+    def __init__(self, ends, in_features, slots, rank, generator):
+        half = dict(device="cuda", generator=generator, dtype=torch.float32)
+        self.ends, self.rank, self.K, self.slots = ends, rank, in_features, slots
+        self.a = (torch.randn((slots, len(ends) * rank, in_features), **half) / math.sqrt(in_features)).half()
+        self.b = (torch.randn((slots, ends[-1], rank), **half) * (0.1 / math.sqrt(rank))).half()
+        self.lora = cider.cider_lora(self.a, self.b, None, slots, rank, in_features, ends)
+
+    def __call__(self, x, rows, ldx, starts, slot, max_rows, y, workspace):
+        """Adds them to y in place."""
+        cider.cider_lora_add(self.lora, starts, slot, slot.numel(), rows, max_rows, x, F16, ldx, y, self.ends[-1],
+                             workspace, workspace.numel(), y, self.ends[-1])
+
+
 class AttentionBlock:
     def __init__(self, batch, capacity, bits=4, hidden=4096, q_heads=32, kv_heads=8, head_dim=128, group_size=64,
-                 window=0, sinks=0, seed=0):
+                 window=0, sinks=0, seed=0, rotate=False, adapters=0, shared=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.HQ, self.H, self.D, self.gs, self.hidden = q_heads, kv_heads, head_dim, group_size, hidden
         self.window, self.sinks, self.batch = window, sinks, batch
@@ -61,6 +81,27 @@ class AttentionBlock:
         # any assignment of pages will do; a server hands them out as sequences grow
         self.pages = torch.randperm(self.num_pages, device="cuda", generator=g).int().view(batch, self.per_seq)
         self.kv_len = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.rotation = self.table = None
+        if rotate:
+            angle = torch.arange(capacity, device="cuda", dtype=torch.float64)[:, None] * 10000.0 ** (
+                -torch.arange(head_dim // 2, device="cuda", dtype=torch.float64) / (head_dim // 2))
+            self.table = torch.stack([angle.cos(), angle.sin()], -1).float()
+            self.norm = 0.5 + torch.rand(head_dim, device="cuda", generator=g)
+            self.rotation = cider.cider_rotation(self.table, capacity, head_dim, q_weight=self.norm, k_weight=self.norm)
+        self.adapters = None
+        if adapters:
+            ends = [q_heads * head_dim, (q_heads + kv_heads) * head_dim, self.width]
+            self.adapters = (Adapters(ends, hidden, adapters, 16, g), Adapters([hidden], q_heads * head_dim, adapters, 16, g))
+            # keys and values of a shared prefix are those of one adapter
+            self.slot = torch.arange(batch, dtype=torch.int32, device="cuda") % (1 if shared else adapters)
+        self.shared = shared // PAGE * PAGE
+        if self.shared:
+            self.pages[:, :self.shared // PAGE] = self.pages[0, :self.shared // PAGE].clone()
+            self.group = torch.tensor([0, batch], dtype=torch.int32, device="cuda")
+            self.shared_len = torch.tensor([self.shared], dtype=torch.int32, device="cuda")
+
+    def runs(self, rows):
+        return cider.cider_kv4_runs(self.group, self.shared_len, 1, rows, self.shared)
 
     def buffers(self, rows, max_rows):
         """What a pass over `rows` rows writes, and its scratch."""
@@ -69,8 +110,14 @@ class AttentionBlock:
              "y": torch.empty((rows, self.hidden), **half)}
         linear = max(cider.cider_linear_workspace_bytes_ex(rows, l.N, l.K, l.bits, 0) for l in (self.qkv, self.o))
         b["linear"] = torch.empty(linear, dtype=torch.uint8, device="cuda")
-        need = cider.cider_kv4_attention_workspace_bytes(self._batch(rows, max_rows, self.kv_len), self.HQ,
-                                                         self.window, self.sinks)
+        seqs = self._batch(rows, max_rows, self.kv_len)
+        if self.shared:
+            need = cider.cider_kv4_attention_shared_workspace_bytes(seqs, self.runs(rows), self.HQ)
+        else:
+            need = cider.cider_kv4_attention_workspace_bytes(seqs, self.HQ, self.window, self.sinks)
+        if self.adapters:
+            lora = max(cider.cider_lora_workspace_bytes(x.lora, self.batch, rows, max_rows) for x in self.adapters)
+            b["lora"] = torch.empty(lora, dtype=torch.uint8, device="cuda")
         b["attention"] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         return b
 
@@ -83,26 +130,51 @@ class AttentionBlock:
         rows, ld = x.shape[0], self.width
         seqs = self._batch(rows, max_rows, row_start)
         self.qkv(x, rows, self.hidden, b["qkv"], b["linear"])
+        if self.adapters:
+            self.adapters[0](x, rows, self.hidden, row_start, self.slot, max_rows, b["qkv"], b["lora"])
         k = b["qkv"][:, self.HQ * self.D:]
         v = b["qkv"][:, (self.HQ + self.H) * self.D:]
-        cider.cider_kv4_append(seqs, k, v, F16, ld, ld)
-        cider.cider_kv4_attention(seqs, b["qkv"], F16, ld, self.HQ, 1 / math.sqrt(self.D), self.window, self.sinks,
-                                  b["attention"], b["attention"].numel(), b["att"], F16, self.HQ * self.D)
+        if self.rotation:  # q is turned in place
+            cider.cider_kv4_append_rotated(seqs, self.rotation, b["qkv"], k, v, F16, ld, ld, ld, self.HQ, b["qkv"], ld)
+        else:
+            cider.cider_kv4_append(seqs, k, v, F16, ld, ld)
+        if self.shared:
+            cider.cider_kv4_attention_shared(seqs, self.runs(rows), b["qkv"], F16, ld, self.HQ, 1 / math.sqrt(self.D),
+                                             b["attention"], b["attention"].numel(), b["att"], F16, self.HQ * self.D)
+        else:
+            cider.cider_kv4_attention(seqs, b["qkv"], F16, ld, self.HQ, 1 / math.sqrt(self.D), self.window, self.sinks,
+                                      b["attention"], b["attention"].numel(), b["att"], F16, self.HQ * self.D)
         self.o(b["att"], rows, self.HQ * self.D, b["y"], b["linear"])
+        if self.adapters:
+            self.adapters[1](b["att"], rows, self.HQ * self.D, row_start, self.slot, max_rows, b["y"], b["lora"])
         return b["y"]
 
 
+def turned(block, x):
+    """Heads [n, heads, D] of the positions 0 .. n - 1, normed and rotated."""
+    if block.rotation is None:
+        return x
+    x = x * block.norm * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6)
+    c, s = block.table[:x.shape[0], None].unbind(-1)
+    a, b = x.chunk(2, -1)
+    return torch.cat([a * c - b * s, b * c + a * s], -1)
+
+
 def attention_in_16_bits(block, qkv, lengths):
-    """The same rows' attention over their own unquantized keys and values (whole prompts, window 0)."""
+    """The same rows' attention over their own unquantized keys and values (whole prompts, window 0).  Behind a shared
+    prefix a sequence but the first brings only what it has of its own; q is turned already, k is not."""
     out, lo = [], 0
-    for n in lengths:
-        q, k, v = (qkv[lo:lo + n].float()[:, a * block.D:b * block.D].view(n, -1, block.D).transpose(0, 1).contiguous()
+    for b, n in enumerate(lengths):
+        own = qkv[lo:lo + n - (block.shared if b else 0)]
+        lo += len(own)
+        rows = own if len(own) == n else torch.cat([qkv[:n - len(own)], own])
+        q, k, v = (rows.float()[:, a * block.D:b * block.D].view(n, -1, block.D)
                    for a, b in ((0, block.HQ), (block.HQ, block.HQ + block.H), (block.HQ + block.H, block.HQ + 2 * block.H)))
+        q, k, v = (t.transpose(0, 1).contiguous() for t in (q, turned(block, k), v))
         k, v = (t.repeat_interleave(block.HQ // block.H, 0) for t in (k, v))
         s = q @ k.transpose(1, 2).contiguous() / math.sqrt(block.D)
         s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), -math.inf)
-        out.append((torch.softmax(s, -1) @ v).transpose(0, 1).reshape(n, -1))
-        lo += n
+        out.append((torch.softmax(s, -1) @ v).transpose(0, 1).reshape(n, -1)[n - len(own):])
     return torch.cat(out)
 
 
@@ -125,19 +197,26 @@ def main(argv=None):
     p.add_argument("--bits", type=int, default=4, choices=(4, 8))
     p.add_argument("--window", type=int, default=0)
     p.add_argument("--sinks", type=int, default=4)
+    p.add_argument("--rotate", action="store_true")
+    p.add_argument("--adapters", type=int, default=0)
+    p.add_argument("--shared", type=int, default=0, help="first tokens that all prompts have in common")
     a = p.parse_args(argv)
+    if a.shared and (a.window or a.shared >= a.prompt // 2):
+        p.error("--shared goes with no window and prompts of more than twice as many tokens")
     if not cider.cider_is_available():
         raise SystemExit("no usable gfx950 device")
-    block = AttentionBlock(a.batch, a.prompt + a.steps, a.bits, window=a.window, sinks=a.sinks)
+    block = AttentionBlock(a.batch, a.prompt + a.steps, a.bits, window=a.window, sinks=a.sinks, rotate=a.rotate,
+                           adapters=a.adapters, shared=a.shared)
     lengths = [max(1, a.prompt - b * a.prompt // (2 * a.batch)) for b in range(a.batch)]
-    rows = sum(lengths)
+    counts = [n - (block.shared if b else 0) for b, n in enumerate(lengths)]
+    rows = sum(counts)
     i32 = dict(dtype=torch.int32, device="cuda")
-    starts = torch.tensor([0] + torch.tensor(lengths).cumsum(0).tolist(), **i32)
+    starts = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), **i32)
     x = torch.randn((rows, block.hidden), device="cuda").half()
 
     block.kv_len.copy_(torch.tensor(lengths, **i32))
-    b = block.buffers(rows, max(lengths))
-    prompt_us = timed(lambda: block.forward(x, starts, max(lengths), b), 3)
+    b = block.buffers(rows, max(counts))
+    prompt_us = timed(lambda: block.forward(x, starts, max(counts), b), 3)
     result = {"prompt_us": prompt_us, "rows": rows}
     if a.window == 0:
         want = attention_in_16_bits(block, b["qkv"], lengths)

@@ -131,6 +131,17 @@ def test_runs_that_are_not_sound_share_nothing(starts, shared, tiles):
     compare(s, got, reference(s, q, 1, 5, 0.125), 1)
 
 
+@pytest.mark.parametrize("tiles", TILES)
+def test_a_bound_of_no_tokens(tiles):
+    """Lengths bounded to 0: no row is there, whatever the runs say."""
+    cider.cider_kv4_set_tiles(tiles)
+    s = setup_of([200, 190], [2, 1], 1, 128, 64, [0, 2], [128], 0, seed=9)
+    s.to_device()
+    q = ref.to_bits(s.rng.standard_normal((s.rows, 4, 128)), 0)
+    got = attend(s, s.batch(s.dcache, max_kv_len=0), runs_of(s, [0, 2], [128]), q, 0, 0, 4, 0.1)
+    assert not got.any()
+
+
 def test_rows_that_are_left_out_stay():
     """A sequence with more rows than the bound, inside a run."""
     s = setup_of([200, 190, 210], [2, 9, 1], 1, 128, 64, [0, 3], [128], 0, seed=3)

@@ -396,7 +396,7 @@ SharedPlan plan_shared(const Kv4AttentionArgs &a, const Kv4Runs &r)
     };
     const int64_t chunk = (few_pages(f, p.front) + few_pages(o, p.own) + 4 * kHeld - 1) / (4 * kHeld) * 4;
     auto deal = [&](const Kv4AttentionArgs &x, Kv4Launch &n) {
-        const int64_t pages = most_pages(x, n.cols);
+        const int64_t pages = most_pages(x, n.cols) > 0 ? most_pages(x, n.cols) : 1;
         if (n.cols == kFewCols)
             n.pages = (int)(chunk < 32 ? chunk : 32);
         else if (n.splits < 2)
