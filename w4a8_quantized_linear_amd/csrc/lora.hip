@@ -423,9 +423,9 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lo
 }
 
 // Both products in one launch, for few rows and ranks up to 16: a workgroup of 16
-// wavefronts has 1024 outputs of one slice and works out t for them by itself, a
-// sixteenth of the inputs a wavefront.  What it takes is A read again for every 1024
-// outputs, what it saves a launch, t's way through memory and the wait for it.
+// wavefronts has 1024 l.per outputs of one slice and works out t for them by itself, a
+// sixteenth of the inputs a wavefront.  What it takes is A read again by every workgroup,
+// what it saves a launch, t's way through memory and the wait for it.
 template <int DT>
 __global__ __launch_bounds__(1024) void lora_step_kernel(LoraArgs a, Launch l)
 {
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(1024) void lora_step_kernel(LoraArgs a, Launch l)
     const bool adapted = (unsigned)r.slot < (unsigned)a.slots;
     if (r.n == 0 || (!adapted && a.y == a.y_in))
         return;
-    const Outputs o = outputs_of(a, group, WAVES * kBlock);
+    const Outputs o = outputs_of(a, group, WAVES * l.per * kBlock);
     const int begin = o.begin + wave * kBlock, R = a.rank;
     Block<DT, 1, 4, 1> block(a, r, adapted, lane);
     if (begin < o.end)
@@ -487,8 +487,11 @@ __global__ __launch_bounds__(1024) void lora_step_kernel(LoraArgs a, Launch l)
         }
         __syncthreads();
     }
-    if (begin < o.end)
-        block.run(half, top, begin);
+    for (int n0 = begin; n0 < o.end; n0 += WAVES * kBlock) {
+        if (n0 > begin)
+            block.load(n0);
+        block.run(half, top, n0);
+    }
 }
 
 constexpr int kMaxSplits = 16;
@@ -508,7 +511,7 @@ Launch plan_down(const LoraArgs &a)
     l.blocks = (a.slices * a.rank + 16 * nt - 1) / (16 * nt);
     // parts: workgroups for the compute units, wavefronts of 128 inputs and more
     const int64_t units = (int64_t)a.segments * l.tiles * l.blocks;
-    int64_t splits = 1024 / units;
+    int64_t splits = (size > 16 ? 2048 : 1024) / units;
     const int64_t many = size > 16 ? 4 : kMaxSplits, most = a.inputs / 1024 < many ? a.inputs / 1024 : many;
     splits = splits > most ? most : splits;
     l.splits = splits < 1 ? 1 : (int)splits;
@@ -564,30 +567,38 @@ hipError_t launch_up(const LoraArgs &a, const Launch &l, hipStream_t stream)
 }
 
 // Workgroups that share a segment's outputs out.
-int step_groups(const LoraArgs &a)
+int step_groups(const LoraArgs &a, int per)
 {
     int n = 0;
     for (int i = 0, from = 0; i < a.slices; from = a.ends[i++])
-        n += (a.ends[i] - from + 16 * kBlock - 1) / (16 * kBlock);
+        n += (a.ends[i] - from + 16 * per * kBlock - 1) / (16 * per * kBlock);
     return n;
 }
 
-// Whether one launch does both: while all its workgroups run at once, one a compute unit,
-// and a wavefront's share of the inputs is short.  In a graph, rank 16, one launch
-// against two: 1 row of 4096 inputs beside 4096 outputs 6.7 / 7.3 us (from the host 7.5 /
-// 10.3), 6144 in three slices 6.8 / 8.5, 32 rows with as many adapters 8.7 / 9.8; but 64
-// of them 14.4 / 11.4, and 1 row of 12288 inputs 11.3 / 8.1.
-bool in_one(const LoraArgs &a)
+// Blocks of outputs of a wavefront with which one launch does both, 0: two launches.
+// One, while all its workgroups run at once, one a compute unit, and a wavefront's share
+// of the inputs is short.  In a graph, rank 16, one launch against two: 1 row of 4096
+// inputs beside 4096 outputs 6.9 / 7.2 us (from the host 7.5 / 10.3), 6144 in three slices
+// 7.0 / 8.5, 32 rows with as many adapters 8.7 / 9.6, 64 of them with two blocks 9.7 /
+// 11.4 (with one 14.4), 200 beside 4096 with four 10.8 / 14.2; 8 beside 24576 8.9 / 8.4
+// (from the host the launch decides); 1 row of 12288 inputs 11.3 / 8.1.
+int in_one(const LoraArgs &a)
 {
-    return a.max_rows <= 16 && a.rank <= 16 && a.inputs <= 6144 && (int64_t)a.segments * step_groups(a) <= 192;
+    if (a.max_rows > 16 || a.rank > 16 || a.inputs > 6144)
+        return 0;
+    for (int per = 1; per <= 4; per *= 2)
+        if ((int64_t)a.segments * step_groups(a, per) <= 256)
+            return per;
+    return 0;
 }
 
 template <int DT>
 hipError_t launch(const LoraArgs &a, Launch l, hipStream_t stream)
 {
-    if (in_one(a)) {
+    if (const int per = in_one(a)) {
+        l.per = per;
         l.chunk = (a.inputs / 64 + 15) / 16 * 64;
-        l.blocks = step_groups(a);
+        l.blocks = step_groups(a, per);
         return kv4_launch(lora_step_kernel<DT>, (unsigned)a.segments * (unsigned)l.blocks, 1024, stream, a, l);
     }
     const hipError_t e = a.max_rows > 16 ? launch_down<DT, 2>(a, l, stream) : launch_down<DT, 1>(a, l, stream);
