@@ -103,20 +103,15 @@ __device__ __forceinline__ float seventh(float a)
 // from a half the rounding is the quotient's; a chunk with a value nearer to
 // one, or of a group whose scale is not a normal number (0, NaN and infinity
 // too), divides.
-template <int DT>
-__device__ __forceinline__ uint32_t int4_codes(uint4 v, float s, float rs)
+__device__ __forceinline__ bool int4_codes(const float (&x)[8], float s, float rs, uint32_t &codes)
 {
     constexpr float kMagic = 12582912.0f;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float r[8], far = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float x = widen_bits<DT>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
-        r[e] = __builtin_fmaf(x, rs, kMagic) - kMagic;
-        far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(x, rs, -r[e])));
+        r[e] = __builtin_fmaf(x[e], rs, kMagic) - kMagic;
+        far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(x[e], rs, -r[e])));
     }
-    if (tiny_scale(s) || !(s < __builtin_inff()) || !(far < 0.5f - 0x1p-14f))
-        return quantize_chunk_div<4, DT>(v, s).x;
     uint32_t half[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -124,7 +119,31 @@ __device__ __forceinline__ uint32_t int4_codes(uint4 v, float s, float rs)
         const float lo = __builtin_fmaf(q[1], 16.0f, q[0]), hi = __builtin_fmaf(q[3], 16.0f, q[2]);
         half[i] = (uint32_t)(__builtin_fmaf(hi, 256.0f, lo) + 34952.0f);  // 0x8888: 8 to each nibble
     }
-    return half[0] | half[1] << 16;
+    codes = half[0] | half[1] << 16;
+    return !(tiny_scale(s) || !(s < __builtin_inff()) || !(far < 0.5f - 0x1p-14f));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t int4_codes(uint4 v, float s, float rs)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = widen_bits<DT>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
+    uint32_t codes;
+    return int4_codes(x, s, rs, codes) ? codes : quantize_chunk_div<4, DT>(v, s).x;
+}
+// Of fp32 values.
+__device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float s, float rs)
+{
+    uint32_t codes;
+    if (int4_codes(x, s, rs, codes))
+        return codes;
+    int q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        q[e] = code_of<4>(x[e] / s, s);
+    return pack_codes<4>(q).x;
 }
 
 // Where a lane's chunks (8 elements each) are: chunk column and, per register,

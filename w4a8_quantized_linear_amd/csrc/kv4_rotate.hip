@@ -214,7 +214,7 @@ __device__ __forceinline__ void put_key(const Kv4Rotation &r, const uint4 (&raw)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const float s = NG == 2 && t.chunk[c] / (GS / 8) ? scale[NG - 1] : scale[0];
-        const uint32_t code = quantize_values<4>(f[c], s, 1.0f / s).x;
+        const uint32_t code = int4_codes(f[c], s, __builtin_amdgcn_rcpf(s));
         if (store)
             kcode[token * (D / 8) + t.chunk[c] % 4 * (D / 32) + t.chunk[c] / 4] = code;
     }
