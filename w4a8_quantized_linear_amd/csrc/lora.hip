@@ -257,7 +257,7 @@ struct Block {
             }
         }
     }
-    __device__ __forceinline__ void load(int n0)
+    __device__ __forceinline__ void load_in(u32x4 (&in)[TT][2], int n0) const
     {
 #pragma unroll
         for (int i = 0; i < TT; ++i)
@@ -266,6 +266,10 @@ struct Block {
                 const int token = 16 * i + c < r.n ? 16 * i + c : r.n - 1;
                 in[i][h] = *reinterpret_cast<const u32x4 *>(a.y_in + (int64_t)(r.first + token) * a.ldy_in + n0 + 32 * h + 8 * q);
             }
+    }
+    __device__ __forceinline__ void load(int n0)
+    {
+        load_in(in, n0);
         if (adapted)
             load_b(n0, 0);
     }
@@ -279,7 +283,8 @@ struct Block {
                 acc[NB * pass + j] = mfma<DT>(b[j][s], t, acc[NB * pass + j]);
         }
     }
-    __device__ __forceinline__ void put(const uint32_t (&top)[16 * TT], const f32x4 (&acc)[4], int i, int n0)
+    // top: of the tokens that i counts
+    __device__ __forceinline__ void put(const uint32_t *top, const f32x4 (&acc)[4], int i, int n0)
     {
         constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16;
         const float f = DT == DT_F16 && adapted ? __builtin_amdgcn_ldexpf(1.0f, token_exponent(top[16 * i + c])) : 1.0f;
@@ -340,13 +345,68 @@ struct Block {
     }
 };
 
+// Adds t's parts for a workgroup's T rows and one slice and leaves their halves in LDS,
+// as operands, and the bits of their largest magnitudes (fp16).  Ends in a barrier.
+template <int DT, int T, int STEPS>
+__device__ __forceinline__ void halves_of(const LoraArgs &a, const Launch &l, const Rows &r, int slice, u32x4 (&half)[4 * STEPS][T],
+                                          uint32_t (&top)[T])
+{
+    constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16;
+    constexpr int ITEMS = (T * STEPS * 2 + 255) / 256;  // of 8 numbers of t, a thread
+    const float scale = a.scale ? a.scale[r.slot] : 1.0f;
+    const int R = a.rank, width = a.slices * R, chunks = R / 8;
+    float v[ITEMS][8];
+    if (DT == DT_F16 && threadIdx.x < T)
+        top[threadIdx.x] = 0;
+    if constexpr (DT == DT_F16)
+        __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
+        f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+        if (token < r.n) {
+            const float *from = l.t + (int64_t)(r.first + token) * width + slice * R + 8 * chunk;
+#pragma unroll 4
+            for (int p = 0; p < l.splits; ++p) {
+                lo += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width);
+                hi += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width + 4);
+            }
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[i][e] = (e < 4 ? lo[e] : hi[e - 4]) * scale;
+            most = __builtin_fmaxf(most, __builtin_fabsf(v[i][e]));
+        }
+        if (DT == DT_F16 && token < T)
+            atomicMax(&top[token], __builtin_bit_cast(uint32_t, most));
+    }
+    if constexpr (DT == DT_F16)
+        __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
+        if (token >= T)
+            break;
+        uint32_t high[4], low[4];
+        const int by = DT == DT_F16 ? -token_exponent(top[token]) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            halves<OUT>(v[i][2 * e], v[i][2 * e + 1], by, high[e], low[e]);
+        half[chunk][token] = u32x4{high[0], high[1], high[2], high[3]};
+        half[chunks + chunk][token] = u32x4{low[0], low[1], low[2], low[3]};
+    }
+    for (int i = 2 * chunks * T + threadIdx.x; i < 4 * STEPS * T; i += 256)
+        half[i / T][i % T] = u32x4{0, 0, 0, 0};
+    __syncthreads();
+}
+
 // A workgroup has 16 TT rows and l.per blocks of 64 outputs of one slice for each of
-// its wavefronts.  It adds t's parts for its rows and leaves their halves in LDS.
+// its wavefronts.
 template <int DT, int TT, int NB, int STEPS>
 __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lora_up_kernel(LoraArgs a, Launch l)
 {
-    constexpr int OUT = DT == DT_BF16 ? OUT_BF16 : OUT_F16, T = 16 * TT;
-    constexpr int ITEMS = (T * STEPS * 2 + 255) / 256;  // of 8 numbers of t, a thread
+    constexpr int T = 16 * TT;
     __shared__ u32x4 half[4 * STEPS][T];
     __shared__ uint32_t top[T];
     unsigned id = kv4_workgroup();
@@ -362,63 +422,112 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : (STEPS == 4 ? 3 : 1)) void lo
     if (r.n == 0 || (!adapted && a.y == a.y_in))
         return;
     const Outputs o = outputs_of(a, group, 4 * l.per * kBlock);
-    const int begin = o.begin + wave * kBlock, R = a.rank, width = a.slices * R;
+    const int begin = o.begin + wave * kBlock;
     // what comes from memory first of all
     Block<DT, TT, NB, STEPS> block(a, r, adapted, lane);
     if (begin < o.end)
         block.load(begin);
-    if (adapted) {
-        const float scale = a.scale ? a.scale[r.slot] : 1.0f;
-        const int chunks = R / 8;
-        float v[ITEMS][8];
-        if (DT == DT_F16 && threadIdx.x < T)
-            top[threadIdx.x] = 0;
-        if constexpr (DT == DT_F16)
-            __syncthreads();
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
-            f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-            if (token < r.n) {
-                const float *from = l.t + (int64_t)(r.first + token) * width + o.slice * R + 8 * chunk;
-#pragma unroll 4
-                for (int p = 0; p < l.splits; ++p) {
-                    lo += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width);
-                    hi += *reinterpret_cast<const f32x4 *>(from + (int64_t)p * a.rows * width + 4);
-                }
-            }
-            float most = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[i][e] = (e < 4 ? lo[e] : hi[e - 4]) * scale;
-                most = __builtin_fmaxf(most, __builtin_fabsf(v[i][e]));
-            }
-            if (DT == DT_F16 && token < T)
-                atomicMax(&top[token], __builtin_bit_cast(uint32_t, most));
-        }
-        if constexpr (DT == DT_F16)
-            __syncthreads();
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int item = i * 256 + (int)threadIdx.x, token = item / chunks, chunk = item % chunks;
-            if (token >= T)
-                break;
-            uint32_t high[4], low[4];
-            const int by = DT == DT_F16 ? -token_exponent(top[token]) : 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                halves<OUT>(v[i][2 * e], v[i][2 * e + 1], by, high[e], low[e]);
-            half[chunk][token] = u32x4{high[0], high[1], high[2], high[3]};
-            half[chunks + chunk][token] = u32x4{low[0], low[1], low[2], low[3]};
-        }
-        for (int i = 2 * chunks * T + threadIdx.x; i < 4 * STEPS * T; i += 256)
-            half[i / T][i % T] = u32x4{0, 0, 0, 0};
-        __syncthreads();
-    }
+    if (adapted)
+        halves_of<DT, T, STEPS>(a, l, r, o.slice, half, top);
     for (int n0 = begin; n0 < o.end; n0 += 4 * kBlock) {
         if (n0 > begin)
             block.load(n0);
         block.run(half, top, n0);
+    }
+}
+
+// The same for ranks whose rows of B are a line and more: there the operands' lanes, which
+// go from row to row, take the load path four times as long as consecutive ones, for every
+// wavefront anew.  So the workgroup's wavefronts have rows of their own, 16 TT each, and the
+// blocks in common: a block's rows of B come by consecutive lanes, through LDS, two blocks
+// by turns, with one barrier a block.
+template <int DT, int TT, int STEPS>
+__global__ __launch_bounds__(256, 2) void lora_up_rows_kernel(LoraArgs a, Launch l)
+{
+    constexpr int T = 64 * TT, WORDS = kBlock * 2 * STEPS, LOADS = WORDS / 256;  // of a block of B, 16 bytes
+    constexpr int HALVES = 4 * STEPS * T;
+    __shared__ u32x4 lds[HALVES > 2 * WORDS ? HALVES : 2 * WORDS];
+    __shared__ uint32_t top[T];
+    unsigned id = kv4_workgroup();
+    const int lane = threadIdx.x & 63, c = lane % 16, q = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int group = (int)(id % (unsigned)l.blocks);
+    id /= (unsigned)l.blocks;
+    const int tile = (int)(id % (unsigned)l.tiles), segment = (int)(id / (unsigned)l.tiles);
+    if (segment >= a.segments)
+        return;
+    const Rows r = rows_of(a, segment, tile, T);
+    const bool adapted = (unsigned)r.slot < (unsigned)a.slots;
+    if (r.n == 0 || (!adapted && a.y == a.y_in))
+        return;
+    const Outputs o = outputs_of(a, group, l.per * kBlock);
+    const int t0 = 16 * TT * wave, left = r.n - t0;
+    const bool some = left > 0;  // the wavefront has rows
+    const Rows mine = {some ? r.first + t0 : r.first, some ? (left < 16 * TT ? left : 16 * TT) : 1, r.slot};
+    Block<DT, TT, 4, STEPS> block(a, mine, adapted, lane);
+    const int per_row = a.rank / 8, words = kBlock * per_row;
+    u32x4 word[LOADS], next[TT][2];
+    auto load_b = [&](int n0) {
+        const u32x4 *from = reinterpret_cast<const u32x4 *>(a.b + ((int64_t)r.slot * a.ends[a.slices - 1] + n0) * a.rank);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            word[i] = from[256 * i + (int)threadIdx.x < words ? 256 * i + (int)threadIdx.x : 0];
+    };
+    // words of a row exchanged so that 8 rows' words of one place are in other banks
+    auto slot_of = [&](int row, int at) { return row * 2 * STEPS + (at ^ row % 8 & (2 * STEPS - 1)); };
+    block.load_in(block.in, o.begin);
+    u32x4 t[TT][STEPS];
+    if (adapted) {
+        load_b(o.begin);
+        u32x4(&half)[4 * STEPS][T] = reinterpret_cast<u32x4(&)[4 * STEPS][T]>(lds);
+        halves_of<DT, T, STEPS>(a, l, r, o.slice, half, top);
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                t[i][s] = half[4 * s + q][t0 + 16 * i + c];
+        __syncthreads();  // the blocks of B take its place
+    }
+    int turn = 0;
+    for (int n0 = o.begin; n0 < o.end; n0 += kBlock) {
+        u32x4 *own = lds + turn * WORDS;
+        turn ^= 1;
+        if (adapted) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int at = 256 * i + (int)threadIdx.x;
+                if (at < words)
+                    own[slot_of(at / per_row, at % per_row)] = word[i];
+            }
+            __syncthreads();
+        }
+        if (n0 + kBlock < o.end) {
+            if (adapted)
+                load_b(n0 + kBlock);
+            block.load_in(next, n0 + kBlock);
+        }
+        f32x4 acc[TT][4] = {};
+        if (adapted) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const int k = 4 * s + q;
+                    const u32x4 b = own[slot_of(j / 2 * 32 + c / 4 * 8 + j % 2 * 4 + c % 4,
+                                                k < per_row ? k : (k < 2 * per_row ? k - per_row : 0))];
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+                        acc[i][j] = mfma<DT>(b, t[i][s], acc[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            if (some)
+                block.put(top + t0, acc[i], i, n0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                block.in[i][h] = next[i][h];
+        }
     }
 }
 
@@ -554,6 +663,24 @@ hipError_t launch_up(const LoraArgs &a, Launch l, hipStream_t stream)
     return kv4_launch(lora_up_kernel<DT, TT, NB, STEPS>, grid, 256, stream, a, l);
 }
 
+template <int DT, int TT, int STEPS>
+hipError_t launch_up_rows(const LoraArgs &a, Launch l, hipStream_t stream)
+{
+    l.tiles = (int)(((int64_t)a.max_rows + 64 * TT - 1) / (64 * TT));
+    const int64_t all = a.ends[a.slices - 1] / kBlock, units = (int64_t)a.segments * l.tiles;
+    // as many workgroups as are resident: 3 a compute unit (2000 rows beside 24576 outputs at
+    // rank 64 63.8 us, 71.6 with 1024, 66.1 with 512)
+    constexpr int64_t kHeld = 768;
+    int64_t per = (all * units + kHeld - 1) / kHeld;
+    per = per < 1 ? 1 : (per > 16 ? 16 : per);
+    l.per = (int)per;
+    l.blocks = 0;
+    for (int i = 0, from = 0; i < a.slices; from = a.ends[i++])
+        l.blocks += (a.ends[i] - from + kBlock * l.per - 1) / (kBlock * l.per);
+    const unsigned grid = (unsigned)a.segments * (unsigned)l.tiles * (unsigned)l.blocks;
+    return kv4_launch(lora_up_rows_kernel<DT, TT, STEPS>, grid, 256, stream, a, l);
+}
+
 template <int DT, int TT>
 hipError_t launch_up(const LoraArgs &a, const Launch &l, hipStream_t stream)
 {
@@ -562,8 +689,8 @@ hipError_t launch_up(const LoraArgs &a, const Launch &l, hipStream_t stream)
     if (a.rank <= 32)
         return launch_up<DT, TT, 4, 2>(a, l, stream);
     if (a.rank <= 64)
-        return launch_up<DT, TT, 4, 4>(a, l, stream);
-    return launch_up<DT, TT, 2, 8>(a, l, stream);
+        return TT > 1 ? launch_up_rows<DT, 2, 4>(a, l, stream) : launch_up<DT, 1, 4, 4>(a, l, stream);
+    return TT > 1 ? launch_up_rows<DT, 1, 8>(a, l, stream) : launch_up<DT, 1, 2, 8>(a, l, stream);
 }
 
 // Workgroups that share a segment's outputs out.
