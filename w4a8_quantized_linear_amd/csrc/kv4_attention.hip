@@ -12,9 +12,13 @@
 // Chunk boundaries depend on the sizes of the call alone, not on timing.
 //
 // Shared prefixes.  Sequences of a run hold the same first pages, and all rows of the
-// run see all of their tokens.  So one launch takes the run's rows as columns over the
-// shared pages, without any mask, another each sequence's over the pages behind, and
-// the same join puts the parts of both together.
+// run see all of their tokens.  So some workgroups take the run's rows as columns over
+// the shared pages, without any mask, others each sequence's over the pages behind, and
+// the same join puts the parts of both together.  Both are one launch where both have
+// tiles of as many columns (two launches, 64 sequences behind 8192 tokens: 44 us, one:
+// 36).  What bounds it: with 16 columns a tile the vector instructions of a page, about
+// 500 a wavefront (32 us for 21000 tile pages, 75 % of them issue); for the prompts of 16
+// questions over 65536 tokens the many-row kernel's own bounds (1.1 PFLOP/s).
 #include "kv4_attention.h"
 
 namespace cider {

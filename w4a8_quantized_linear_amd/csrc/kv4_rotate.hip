@@ -15,8 +15,18 @@
 // has that head's k and v and the group's query heads.  D / 16 lanes a head, each
 // with two chunks of 8 elements that are one another's partners (chunks l and l +
 // rot_dim / 16), so no value of a pair crosses lanes; a wavefront has 8 tokens, and
-// a lane's 8 pairs of (c, s) stay in registers for k and all query heads.  v goes
+// a lane's 8 pairs of (c, s) stay in registers for k and all query heads.  Of up to 8
+// tokens the first wavefront has the keys and the others share the query heads out (64
+// single rows, G 4: 6.4 us, 9.4 with each token's heads one after the other).  v goes
 // its own way, by the lanes that kv4_codes.h's exchanges want.
+//
+// What bounds it.  Bytes: 13400 rows of 32 + 2 x 8 heads of 128 (bf16, norms) move 296
+// MB in 63.6 us, 4.7 TB/s, a copy's rate; the vector units work half that time.  One
+// query head at a time is in registers: with four of them loaded ahead it took 5 % more
+// (fewer wavefronts).  5000 rows of 28 + 2 x 4 heads of 64, 3 axes (40 MB), take 16.7: one round
+// of wavefronts, each a chain of loads and 64-bit operations.  Dealing the query heads
+// to more workgroups made both slower (the pairs' entries loaded again).  One row:
+// 4.2, the launch and three loads in a row.
 #include "kv4_codes.h"
 
 namespace cider {

@@ -2,21 +2,29 @@
 //   t[r, j] = sum_k A[slot, j, k] x[r, k]
 //   y[r, n] = y_in[r, n] + scale[slot] sum_j B[slot, n, j] t[r, s(n) R + j]
 // for rows r of segments that each have a slot, s(n) the slice of output n, R the
-// rank.  Two launches: `down` leaves t, in parts over the inputs k, in the workspace,
-// `up` adds the parts, multiplies by B and adds y_in.
+// rank.  `down` leaves t, in parts over the inputs k, in the workspace; `up` adds the
+// parts, multiplies by B and adds y_in; `step` does both for few rows.
 //
-// Shape.  Both are products on the matrix cores (v_mfma_f32_16x16x32) with the
-// adapter's rows as the left operand and tokens as columns, operands loaded as they
-// lie in memory: 8 consecutive inputs of a row are a lane's 16 bytes.  No LDS but for
-// joining a workgroup's 4 wavefronts, which take a quarter of the inputs each.
-// `up` takes the rows of B in an order that leaves a lane runs of 8 outputs of a token,
-// and two lanes exchange theirs, so that y_in and y move by whole lines.
+// Shape.  Both products run on the matrix cores (v_mfma_f32_16x16x32) with the adapter's
+// rows as the left operand and tokens as columns, 8 consecutive numbers of a row a lane's
+// operand.  The operands' lanes go from row to row, which the load path takes four times
+// as long as lanes that go along rows, so that what is long (x, A, B past rank 32) comes
+// by rows and through LDS, and y leaves by whole lines.
 //
 // Rounding.  t is fp32; times the scale it goes to the second product as two 16-bit
 // numbers, high and low, one behind the other along the summed axis with B's row
 // repeated: 16 bits (bf16) or 22 (fp16, after a power of two of the token that keeps
 // it in range) of t, and for ranks up to 16 no more products than t rounded once
-// would take.  Sums are fp32, y is rounded once.
+// would take.  Sums are fp32, y is rounded once: against 64 bits outputs are off by that
+// rounding alone (fp16 2.1e-4, bf16 1.6e-3).
+//
+// What bounds it.  Many rows: bytes.  8400 rows of 4096 inputs beside 6144 outputs (bf16,
+// rank 16): `down` 21.9 us, 14 at 5 TB/s, a wavefront's few loads in
+// flight against their latency; `up` 48.7, where a copy by the same pattern takes 45 and
+// one at 5 TB/s 41.  2000 rows beside 24576 outputs (fp16, rank 64): 13.0 and 50.5, the
+// latter 39 as a copy.  Few rows: latency, one chain of loads (the segment, then x and A, or B
+// and y) and a barrier each: 1 row beside 4096 outputs 6.8 us, 64 with 24 adapters beside
+// 6144 9.6.
 #include "kv4_layout.h"
 #include "quant_common.h"
 
@@ -652,7 +660,7 @@ hipError_t launch_up(const LoraArgs &a, Launch l, hipStream_t stream)
     // 64 74 us with three, 70.7 with four, 76.8 with six), up to two at low ranks, whose t
     // costs little to set up again (8400 rows beside 6144 74.2 with four, 73.3 with two)
     const int64_t all = a.ends[a.slices - 1] / kBlock, units = (int64_t)a.segments * l.tiles;
-    constexpr int64_t kResident = STEPS > 2 ? 3072 : 4096, kMost = STEPS == 1 ? 2 : 4;
+    constexpr int64_t kResident = (STEPS > 2 ? 3 : 4) * 1024, kMost = STEPS == 1 ? 2 : 4;
     int64_t per = (all * units + kResident - 1) / kResident;
     per = per < 1 ? 1 : (per > kMost ? kMost : per);
     l.per = (int)per;
