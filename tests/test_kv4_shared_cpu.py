@@ -89,3 +89,22 @@ def test_workspace_of_nothing_shared_is_the_ordinary_one():
     b = _batch(batch=1, rows=1, max_rows=1, max_kv_len=131072, max_pages=2048)
     want = cider.cider_kv4_attention_workspace_bytes(b, 8, 0, 0)
     assert want and cider.cider_kv4_attention_shared_workspace_bytes(b, _runs(groups=0), 8) == want
+
+
+@pytest.mark.parametrize("tiles", [0, 16, 128, 256])
+@pytest.mark.parametrize("max_rows", [1, 3, 200, 4096])
+@pytest.mark.parametrize("max_kv_len", [0, 1, 64, 70000])
+def test_bounds_of_every_order(max_kv_len, max_rows, tiles):
+    """Prefixes' bounds above and below the lengths', 0 among them: the call is planned, with a workspace."""
+    rows = 128441
+    kw = dict(batch=15443, rows=rows, max_rows=max_rows, max_kv_len=max_kv_len, max_pages=4417, num_pages=1, kv_heads=1)
+    cider.cider_kv4_set_tiles(tiles)
+    try:
+        for groups, run_rows, shared in ((1000, 1271, 57974), (1, 1 << 30, 64), (15443, 8, 1 << 18), (1, rows, 1 << 18)):
+            runs = dict(groups=groups, max_rows=run_rows, max_shared_len=shared)
+            nbytes = cider.cider_kv4_attention_shared_workspace_bytes(_batch(**kw), _runs(**runs), 4)
+            assert nbytes >= 2 * 4 * 4 * 128 * rows  # a part of both kinds for each head of each row
+            assert _call(runs, nbytes=nbytes, q_heads=4, **kw) == YES
+            assert _call(runs, nbytes=nbytes - 1, q_heads=4, **kw) == ROOM
+    finally:
+        cider.cider_kv4_set_tiles(0)

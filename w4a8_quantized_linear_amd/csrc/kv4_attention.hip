@@ -402,7 +402,7 @@ SharedPlan plan_shared(const Kv4AttentionArgs &a, const Kv4Runs &r)
     auto deal = [&](const Kv4AttentionArgs &x, Kv4Launch &n) {
         const int64_t pages = most_pages(x, n.cols) > 0 ? most_pages(x, n.cols) : 1;
         if (n.cols == kFewCols)
-            n.pages = (int)(chunk < 32 ? chunk : 32);
+            n.pages = (int)(chunk < 4 ? 4 : (chunk < 32 ? chunk : 32));  // (0: no tile of 16 sees a page)
         else if (n.splits < 2)
             n.pages = (int)pages;
         // a join takes kMaxSplits, and a launch counts workgroups in 32 bits
