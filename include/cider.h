@@ -513,8 +513,9 @@ typedef struct {
    shared_len outside [0, max_shared_len] is taken as the nearer end; a run that
    is not inside the batch, or has more than max_rows rows, shares nothing, and
    neither does a sequence whose rows do not all stand behind the shared pages
-   (a padded slot): those attend to their own page table alone.  What the
-   sequences of a run name for the shared pages is read from the first one's.
+   (a padded slot, one without rows): those attend to their own page table alone,
+   which need not name the run's pages.  What the others name for them is read from
+   the table of the first of those.
    Ranges and precision are those of cider_kv4_attention.
    workspace: device scratch of cider_kv4_attention_shared_workspace_bytes(...)
    bytes at the least (else CIDER_ERR_WORKSPACE); calls that share one must be

@@ -142,6 +142,25 @@ def test_a_bound_of_no_tokens(tiles):
     assert not got.any()
 
 
+@pytest.mark.parametrize("tiles", TILES)
+@pytest.mark.parametrize("lens,rows", [
+    ([0, 200, 190, 180], [1, 1, 1, 1]), ([0, 0, 190, 180], [1, 0, 2, 1]), ([70, 200, 190, 180], [1, 2, 1, 1]),
+    ([200, 190, 180, 0], [1, 1, 1, 1]), ([0, 70, 0, 60], [1, 1, 1, 1]),
+])
+def test_slots_whose_tables_are_not_the_runs(lens, rows, tiles):
+    """A run's slots without its pages: padded ones, one without rows, one in front of the prefix's end, whose tables
+    name nothing in the cache or pages of their own."""
+    cider.cider_kv4_set_tiles(tiles)
+    first = next((b for b in range(4) if lens[b] - rows[b] >= 128), 3)
+    s = setup_of(lens, rows, 2, 128, 64, [first, 4], [128], 0, seed=4)
+    for b in range(4):
+        if lens[b] - rows[b] < 128:
+            s.table[b, -(-lens[b] // 64):] = (-1, 2 ** 31 - 1)[b % 2]
+    q = ref.to_bits(s.rng.standard_normal((s.rows, 8, 128)), 0)
+    got = attend(s, s.to_device(), runs_of(s, [0, 4], [128]), q, 0, 0, 8, 0.1)
+    compare(s, got, reference(s, q, 0, 8, 0.1), 0)
+
+
 def test_rows_that_are_left_out_stay():
     """A sequence with more rows than the bound, inside a run."""
     s = setup_of([200, 190, 210], [2, 9, 1], 1, 128, 64, [0, 3], [128], 0, seed=3)

@@ -396,16 +396,15 @@ __device__ __forceinline__ PageRange pages_seen(int p_lo, int p_hi, int window, 
 // A run of sequences that share their first pages; pages 0 where there is none, or the
 // device's numbers are not sound.
 struct Run {
-    int first, row0, n, pages;  // its first sequence, its rows
+    int first, end, row0, n, pages;  // its sequences first .. end - 1, its rows
 };
 __device__ __forceinline__ Run run_of(const Kv4Args &a, const Kv4Runs &r, int g)
 {
-    Run run = {r.group_start[g], 0, 0, 0};
-    const int end = r.group_start[g + 1];
-    if (run.first < 0 || end <= run.first || end > a.batch)
+    Run run = {r.group_start[g], r.group_start[g + 1], 0, 0, 0};
+    if (run.first < 0 || run.end <= run.first || run.end > a.batch)
         return run;
     run.row0 = a.row_start[run.first];
-    const int last = a.row_start[end];
+    const int last = a.row_start[run.end];
     if (run.row0 < 0 || last < run.row0 || last > a.rows || last - run.row0 > r.max_rows)
         return run;
     run.n = last - run.row0;
@@ -459,7 +458,15 @@ __device__ __forceinline__ bool tile_of(const Kv4AttentionArgs &a, const Kv4Laun
         const Run run = run_of(a.kv, n.runs, b);
         if (run.pages == 0)
             return false;
-        t.b = run.first;
+        // the first whose rows stand behind the shared pages: a padded slot's table may
+        // name anything
+        for (t.b = run.first;; ++t.b) {
+            if (t.b == run.end)
+                return false;
+            const Kv4Sequence s = kv4_sequence(a.kv, t.b);
+            if (s.n > 0 && s.kv - s.n >= run.pages * kPageTokens)
+                break;
+        }
         t.seq.row0 = run.row0;
         t.seq.n = run.n;
         t.seq.kv = run.pages * kPageTokens;
