@@ -21,9 +21,8 @@
 // its own way, by the lanes that kv4_codes.h's exchanges want.
 //
 // What bounds it.  Bytes: 13400 rows of 32 + 2 x 8 heads of 128 (bf16, norms) move 296
-// MB in 63.6 us, 4.7 TB/s, a copy's rate; the vector units work half that time.  One
-// query head at a time is in registers: with four of them loaded ahead it took 5 % more
-// (fewer wavefronts).  5000 rows of 28 + 2 x 4 heads of 64, 3 axes (40 MB), take 16.7: one round
+// MB in 62 us, 4.8 TB/s, a copy's rate; the vector units work half that time.  Query
+// heads are loaded one ahead (none: 1.5 us more; four: 5 % more, fewer wavefronts).  5000 rows of 28 + 2 x 4 heads of 64, 3 axes (40 MB), take 16.7: one round
 // of wavefronts, each a chain of loads and 64-bit operations.  Dealing the query heads
 // to more workgroups made both slower (the pairs' entries loaded again).  One row:
 // 4.2, the launch and three loads in a row.
@@ -319,13 +318,19 @@ __global__ __launch_bounds__(kThreads) void kv4_rotate_kernel(Kv4Args a, Kv4Rota
         if (w.base + 8 * j < w.hi && w.base + 8 * j + 8 > w.lo) {
             const int p = w.base + 8 * j + lane / L % 8;
             const bool mine = p >= w.lo && p < w.hi;
-            key(p, mine);
             const int64_t row = (mine ? p : w.lo) + w.shift;
             const uint16_t *from = io.q + row * io.ldq + w.h * G * D;
             uint16_t *to = io.q_out + row * io.ldo + w.h * G * D;
+            uint4 next[2] = {};  // the next head, one ahead; the first before the key
+            if (G > 0)
+                load(next, from + (sub < G ? sub : G - 1) * D);
+            key(p, mine);
             for (int g0 = 0; g0 < G; g0 += HEADS) {
-                const int g = g0 + sub;
-                load(x, from + (g < G ? g : G - 1) * D);
+                const int g = g0 + sub, after = g + HEADS < G ? g + HEADS : G - 1;
+                x[0] = next[0];
+                x[1] = next[1];
+                if (g0 + HEADS < G)
+                    load(next, from + after * D);
                 if (mine && g < G)
                     put_query<D, DT, INTERLEAVED>(r, x, s, weight, to + g * D, p >= 0);
             }
