@@ -482,7 +482,7 @@ __global__ __launch_bounds__(256, 2) void lora_up_rows_kernel(LoraArgs a, Launch
             word[i] = from[256 * i + (int)threadIdx.x < words ? 256 * i + (int)threadIdx.x : 0];
     };
     // words of a row exchanged so that 8 rows' words of one place are in other banks
-    auto slot_of = [&](int row, int at) { return row * 2 * STEPS + (at ^ row % 8 & (2 * STEPS - 1)); };
+    auto slot_of = [&](int row, int at) { return row * 2 * STEPS + (at ^ (row % 8 & (2 * STEPS - 1))); };
     block.load_in(block.in, o.begin);
     u32x4 t[TT][STEPS];
     if (adapted) {
