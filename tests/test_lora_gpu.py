@@ -173,6 +173,18 @@ def test_many_segments_of_few_rows(rank, dtype):
         c.check(c.run(in_place=dtype == 1))
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("rank,rows", [(16, 16), (16, 17), (24, 16), (24, 17), (64, 16), (64, 17), (40, 150),
+                                       (128, 16), (128, 17), (104, 90)])
+def test_workgroups_of_several_blocks(rank, rows, dtype):
+    """So many outputs and tiles that a workgroup takes some blocks of outputs in turn, with slices that end inside its
+    share and a slot that is none."""
+    r = np.random.default_rng(rank)
+    counts = [rows] + list(r.integers(1, min(rows, 17) + 1, 29))
+    c = Case(counts, r.integers(-1, 4, 30), rank, 64, [64 * 7, 64 * 130, 64 * 131, 64 * 149], dtype, seed=14)
+    c.check(c.run(in_place=dtype == 0))
+
+
 @pytest.mark.parametrize("dtype,x_std,a_std,b_std", [
     (0, 2e4, 1.0, 1e-4), (0, 1e-6, 1e-3, 1e3), (1, 1e15, 1e10, 1e-26), (1, 1e-20, 1e-10, 1e30), (0, 1.0, 100.0, 1e-3),
 ])
