@@ -304,9 +304,9 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
  * Envelope: rank a multiple of 8 up to 128, in_features a multiple of 64, 1 to 8
  * slices whose ends are multiples of 64 and rise, in_features and outputs below
  * 2^24, rows, max_rows <= 2^30, slots < 2^31, segments times the 16-row tiles of
- * max_rows times outputs / 64 < 2^31; device pointers 16-byte aligned (int32 and
- * scale arrays: 4), row strides multiples of 8.  segments, rows or max_rows 0 is a
- * no-op. */
+ * max_rows times (outputs / 64 + slices * rank) < 2^31; device pointers 16-byte
+ * aligned (int32 and scale arrays: 4), row strides multiples of 8.  segments, rows or
+ * max_rows 0 is a no-op. */
 #define CIDER_LORA_MAX_SLICES 8
 typedef struct {
     const void *a;        /* device, [slots][slices * rank][in_features], of the call's dtype */
