@@ -496,22 +496,36 @@ __device__ __forceinline__ int position_of(const Tile &t, int row)
     return PAGES == Pages::Shared && t.front ? t.p_hi : t.seq.kv - t.seq.n + row;
 }
 
-// A workgroup's number among those of its kind, and how many chunks of how many pages
-// those deal a tile's pages to.
+// What a workgroup has: a tile of a kv head of a sequence, or of a run (front), and which
+// of its chunks.  Heads go fastest, then sequences, splits and tiles.
+struct Work {
+    bool front;
+    int head, b, split, tile;
+};
 template <Pages PAGES>
-__device__ __forceinline__ bool is_front(const Kv4Launch &n, unsigned &id)
-{
-    if (PAGES == Pages::All || id >= n.front_groups) {
-        id -= PAGES == Pages::All ? 0u : n.front_groups;
-        return false;
-    }
-    return true;
-}
-template <Pages PAGES>
-__device__ __forceinline__ int splits_of(const Kv4Launch &n, bool front)
+__host__ __device__ __forceinline__ int splits_of(const Kv4Launch &n, bool front)
 {
     return PAGES == Pages::Shared && front ? n.front_splits : n.splits;
 }
+// False past the launch's last workgroup: a grid of more than kMostX is rounded up to
+// whole rows of those, and a launch for shared pages alone (tiles 0) has none behind the
+// front's.
+template <Pages PAGES>
+__host__ __device__ __forceinline__ bool work_of(const Kv4AttentionArgs &a, const Kv4Launch &n, unsigned id, Work &w)
+{
+    w.front = PAGES == Pages::Shared && id < n.front_groups;
+    if (PAGES == Pages::Shared && !w.front)
+        id -= n.front_groups;
+    w.head = (int)(id % (unsigned)a.kv.kv_heads);
+    id /= (unsigned)a.kv.kv_heads;
+    const unsigned batch = (unsigned)(w.front ? n.runs.groups : a.kv.batch), splits = (unsigned)splits_of<PAGES>(n, w.front);
+    w.b = (int)(id % batch);
+    id /= batch;
+    w.split = (int)(id % splits);
+    w.tile = (int)(id / splits);
+    return w.front || w.tile < n.tiles;
+}
+// How many chunks of how many pages a tile's pages are dealt to.
 template <Pages PAGES>
 __device__ __forceinline__ bool chunk_of(const Kv4Launch &n, const Tile &t, int split, int &begin, int &end)
 {

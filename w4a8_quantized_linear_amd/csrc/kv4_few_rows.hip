@@ -532,18 +532,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? WAVES / 4 : (ONE || !ONCE ?
     __shared__ int own[ONE ? 1 : WAVES][D / GS][kCols];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // heads fastest, then sequences, splits and tiles
-    unsigned id = kv4_workgroup();
-    const bool front = is_front<PAGES>(n, id);
-    const int head = (int)(id % (unsigned)a.kv.kv_heads);
-    id /= (unsigned)a.kv.kv_heads;
-    const unsigned batch = (unsigned)(front ? n.runs.groups : a.kv.batch), splits = (unsigned)splits_of<PAGES>(n, front);
-    const int b = (int)(id % batch);
-    id /= batch;
-    const int split = (int)(id % splits), tile = (int)(id / splits);
+    Work work;
     Tile t;
-    if (!tile_of<kCols, PAGES>(a, n, b, head, tile, front, t))
+    if (!work_of<PAGES>(a, n, kv4_workgroup(), work) || !tile_of<kCols, PAGES>(a, n, work.b, work.head, work.tile, work.front, t))
         return;
+    const int split = work.split;
     int begin, end;
     if (!chunk_of<PAGES>(n, t, split, begin, end))
         return;

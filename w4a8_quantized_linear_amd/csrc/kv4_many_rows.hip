@@ -702,20 +702,14 @@ __global__ __launch_bounds__(COLS * 2, 2) void kv4_many_rows_kernel(Kv4Attention
     // falls into step with the 4 shader engines that an XCD fills in turn, and
     // the longest sequence lands on one of them (ragged prompts up to 4096 rows:
     // 617 us against 232)
-    unsigned id = kv4_workgroup();
-    const bool front = is_front<PAGES>(n, id);
-    const int head = (int)(id % (unsigned)a.kv.kv_heads);
-    id /= (unsigned)a.kv.kv_heads;
-    const unsigned batch = (unsigned)(front ? n.runs.groups : a.kv.batch), splits = (unsigned)splits_of<PAGES>(n, front);
-    const unsigned turn = id % batch;
-    id /= batch;
-    const int split = (int)(id % splits);
-    const int tile = (PAGES == Pages::Shared && front ? n.front_tiles : n.tiles) - 1 - (int)(id / splits);
-    if (tile < 0)
+    Work work;
+    if (!work_of<PAGES>(a, n, kv4_workgroup(), work))
         return;
-    const int b = (int)((turn + (unsigned)tile) % batch);
+    const unsigned batch = (unsigned)(work.front ? n.runs.groups : a.kv.batch);
+    const int split = work.split, tile = (work.front ? n.front_tiles : n.tiles) - 1 - work.tile;
+    const int b = (int)(((unsigned)work.b + (unsigned)tile) % batch);
     Tile t;
-    if (!tile_of<COLS, PAGES>(a, n, b, head, tile, front, t))
+    if (!tile_of<COLS, PAGES>(a, n, b, work.head, tile, work.front, t))
         return;
     int begin, end;
     if (!chunk_of<PAGES>(n, t, split, begin, end))
