@@ -39,12 +39,6 @@ __device__ __forceinline__ double dpp_add(double v)
                      (uint32_t)__builtin_amdgcn_update_dpp((int)u.y, (int)u.y, CTRL, 0xF, 0xF, false)};
     return v + __builtin_bit_cast(double, w);
 }
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v)
-{
-    const int u = __builtin_bit_cast(int, v);
-    return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, CTRL, 0xF, 0xF, false)));
-}
 
 // Over the 4 or 8 lanes of a head; every lane has the result.
 template <int L>
@@ -55,22 +49,22 @@ __device__ __forceinline__ double head_sum(double v)
     return L == 8 ? dpp_add<0x141>(v) : v;  // row_half_mirror
 }
 template <int L>
-__device__ __forceinline__ float head_max(float v)
+__device__ __forceinline__ uint32_t head_max(uint32_t v)
 {
-    v = dpp_max<0xB1>(v);
-    v = dpp_max<0x4E>(v);
-    return L == 8 ? dpp_max<0x141>(v) : v;
+    v = max_dpp_u<0xB1>(v);
+    v = max_dpp_u<0x4E>(v);
+    return L == 8 ? max_dpp_u<0x141>(v) : v;
 }
 
 // 1 / sqrt(v) of a normal number: the hardware's (2^-23 at the least) and two steps,
-// each of which squares the error.
+// each of which squares the error.  Of infinity 0, which the steps would make NaN.
 __device__ __forceinline__ double inverse_root(double v)
 {
     double r = __builtin_amdgcn_rsq(v);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         r = __builtin_fma(r * 0.5, __builtin_fma(-v * r, r, 1.0), r);
-    return r;
+    return v == __builtin_inf() ? 0.0 : r;
 }
 
 // A lane's part of every head: where its two chunks are, and its pairs' turns.
@@ -199,25 +193,29 @@ __device__ __forceinline__ void put_key(const Kv4Rotation &r, const uint4 (&raw)
     if (r.k_weight)
         norm<L>(x, w, r.eps);
     turn<INTERLEAVED>(x, t);
-    float f[2][8], top[NG], scale[NG];
+    // the largest magnitudes by their bits, NaN among them: a maximum of numbers leaves NaN
+    // out, and a key without a number would come to be one of zeros
+    float f[2][8], scale[NG];
+    uint32_t top[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        top[g] = 0.0f;
+        top[g] = 0;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        float m = 0.0f;
+        uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f[c][e] = (float)x[c][e];
-            m = __builtin_fmaxf(m, __builtin_fabsf(f[c][e]));
+            const uint32_t u = __builtin_bit_cast(uint32_t, f[c][e]) & 0x7FFFFFFFu;
+            m = u > m ? u : m;
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-            top[g] = t.chunk[c] / (GS / 8) == g ? __builtin_fmaxf(top[g], m) : top[g];
+            top[g] = t.chunk[c] / (GS / 8) == g && m > top[g] ? m : top[g];
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        scale[g] = head_max<L>(top[g]) / quant_divisor<4>();
+        scale[g] = __builtin_bit_cast(float, head_max<L>(top[g])) / quant_divisor<4>();
     uint32_t *kcode = reinterpret_cast<uint32_t *>(block);
     float *kscale = reinterpret_cast<float *>(block + kv4_scale_offset(D));
 #pragma unroll
