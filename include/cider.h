@@ -454,8 +454,9 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
      y[d] = sum_t P[t] * V[t, d] / sum_t P[t];  no visible t: y = 0
    with K, V the values the codes stand for; scores, softmax and sums in fp32
    (scale * |K| and scale * |q| * |K| of the largest elements are to stay
-   below 2^118; a row that meets NaN or infinity where it may look gives NaN,
-   and what it may not see never reaches it). For the two products q, times a
+   below 2^118; a row that meets NaN or infinity where it may look, a scale of
+   the cache among them, gives NaN, of an infinite value NaN or infinity in the
+   group's elements, and what it may not see never reaches it). For the two products q, times a
    power of two of its row or of rows of about one size, and P times V's
    scales, times a power of two of the row, are fp16: elements of q down to
    2^-17 of their row's largest lose nothing, smaller ones 2^-28 of that at

@@ -113,6 +113,9 @@ __device__ __forceinline__ float row_value(float v, int n)
     default: return row_lane<15>(v);
     }
 }
+// A scale of K as the factor of its scores; NaN where it is infinite: the sums that it
+// meets are finite, and one below 0 would make the score minus infinity, the token hidden.
+__device__ __forceinline__ float key_factor(float scale, float factor) { return __builtin_fmaf(scale, 0.0f, scale * factor); }
 // x times the value of lane n of the row.
 __device__ __forceinline__ float scaled(float x, float scales, int n) { return row_value(scales, n) * x; }
 

@@ -178,7 +178,7 @@ __device__ __forceinline__ void page_scores(const State<D, GS> &st, const PageDa
     float ks[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        ks[g] = pg.ks[g] * st.k_factor;
+        ks[g] = key_factor(pg.ks[g], st.k_factor);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll

@@ -306,14 +306,14 @@ __device__ __forceinline__ bool many_rows_tile(const Kv4AttentionArgs &a, const 
         if (wave != 0)
             return;
         if (NG == 1) {
-            to.scale[scale_slot(lane)] = s.k_scale[0] * k_factor;
+            to.scale[scale_slot(lane)] = key_factor(s.k_scale[0], k_factor);
         } else {
             // s[0] r0 + s[1] r1 as (s[0] / s[1] r0 + r1) s[1], the first product done on
             // the way; s[1] is kept off 0 (its codes then stand for 0) and the ratio under
             // 2^120, which r0, below 2, leaves finite
             const float low = __builtin_fmaxf(s.k_scale[0] * (s.k_scale[1] == 0.0f ? 0x1p-60f : 0x1p-120f), 0x1p-149f);
             const float last = s.k_scale[1] < low ? low : s.k_scale[1];  // NaN stays
-            to.scale[scale_slot(lane)] = last * k_factor;
+            to.scale[scale_slot(lane)] = key_factor(last, k_factor);
             // (a division without its last bits: 2^-22)
             const float rest = __builtin_amdgcn_rcpf(__builtin_amdgcn_frexp_mantf(last));
             to.ratio[scale_slot(lane)] = ldexp_f(s.k_scale[0] * rest, -__builtin_amdgcn_frexp_expf(last));
