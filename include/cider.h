@@ -294,7 +294,8 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
  * rank rows for each of its parts.  t and all sums are fp32 (t enters the second
  * product with 16 significant bits or more), y is rounded once.  A slot outside
  * [0, slots) is no adapter: y = y_in.  Adapters of a smaller rank have zeros in
- * the rest of A or B.
+ * the rest of A or B.  Where x, A or t is infinite or NaN, y is what the formula
+ * gives, row by row; where B is, outputs of that row of B are no finite numbers.
  *
  * A segment whose rows are not inside [0, rows], or are more than max_rows, is
  * left out, and its rows, like rows of no segment, stay as they are.  max_rows

@@ -191,22 +191,26 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, Launch l)
 
 // Of a token whose largest |t| has these bits: 2^-exponent takes it to [2^13, 2^14).
 // Not below -100: what is smaller yet, times fp16 numbers, is nothing to an fp16 output,
-// and 2^exponent stays a normal number.
+// and 2^exponent stays a normal number.  Of a token with an infinite t every output is
+// infinite or NaN; there the exponent is the greatest, and its other numbers stay finite.
 __device__ __forceinline__ int token_exponent(uint32_t top)
 {
     const float x = __builtin_bit_cast(float, top);
-    const int e = x > 0.0f && x < __builtin_inff() ? __builtin_amdgcn_frexp_expf(x) - 14 : 0;
+    const int e = x > 0.0f ? (x < __builtin_inff() ? __builtin_amdgcn_frexp_expf(x) : 128) - 14 : 0;
     return e < -100 ? -100 : e;
 }
 
-// Two numbers of t, times 2^by, as high and low halves.
+// Two numbers of t, times 2^by, as high and low halves.  High is within the type's finite
+// numbers, so that of infinity low is infinite and not infinity less itself, and of what
+// bf16 would round to infinity low is the rest.
 template <int OUT>
 __device__ __forceinline__ void halves(float x, float y, int by, uint32_t &high, uint32_t &low)
 {
     constexpr int DT = OUT == OUT_BF16 ? DT_BF16 : DT_F16;
+    constexpr float kEnd = OUT == OUT_BF16 ? 0x1.FEp127f : 65504.0f;
     x = __builtin_amdgcn_ldexpf(x, by);
     y = __builtin_amdgcn_ldexpf(y, by);
-    high = pack2<OUT>(x, y);
+    high = pack2<OUT>(__builtin_amdgcn_fmed3f(x, -kEnd, kEnd), __builtin_amdgcn_fmed3f(y, -kEnd, kEnd));
     low = pack2<OUT>(x - widen_bits<DT>(high), y - widen_bits<DT>(high >> 16));
 }
 
