@@ -1,4 +1,4 @@
-"""cider_lora_add where the product with A is infinite or past bf16's end, by the
+"""cider_lora_add where the product with A is infinite, past bf16's end or of very different sizes within a token, by the
 formula in 64 bits: one launch and two, few rows and many, low ranks and high ones."""
 import numpy as np
 import pytest
@@ -85,4 +85,20 @@ def test_finite_numbers_of_t_that_bf16_has_no_place_for(rows, rank):
     c.x[1::2] *= -1
     c.a[1, 0, [0, 70]] = 1
     c.b[1, :, 0] = np.where(np.arange(64) % 2, 2.0 ** -126, -(2.0 ** -120))
+    assert np.isfinite(by_the_formula(c, c.run())).all()
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("rows,rank", SHAPES)
+def test_numbers_of_t_far_apart(rows, rank, dtype):
+    """Within a token and slice the first number of t is about 2^14, the others 1 and less, down to 2^-20, and some
+    outputs take those alone: fp16 keeps 22 bits of a number down to 2^-16 of the largest, and of a smaller one what is
+    above 2^-38 of that; bf16 16 bits of each."""
+    c = Case([rows], [1], rank, 256, [64, 128], dtype, seed=24, scale=False)
+    for s in range(2):
+        a = c.a[1, s * rank:(s + 1) * rank]
+        a *= 2.0 ** np.minimum(-(np.arange(rank) * 30 // rank) + 2, 0)[:, None]
+        a[0] *= 2.0 ** 14
+    c.a = rounded(c.a, dtype)
+    c.b[1, ::2, 0] = 0
+    c.y_in[:, ::2] = 0
     assert np.isfinite(by_the_formula(c, c.run())).all()

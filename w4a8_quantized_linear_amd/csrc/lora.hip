@@ -13,10 +13,11 @@
 //
 // Rounding.  t is fp32; times the scale it goes to the second product as two 16-bit
 // numbers, high and low, one behind the other along the summed axis with B's row
-// repeated: 16 bits (bf16) or 22 (fp16, after a power of two of the token that keeps
-// it in range) of t, and for ranks up to 16 no more products than t rounded once
-// would take.  Sums are fp32, y is rounded once: against 64 bits outputs are off by that
-// rounding alone (fp16 2.1e-4, bf16 1.6e-3).
+// repeated: 16 bits (bf16) or 22 (fp16, after a power of two of the token and slice that
+// keeps t in range; of numbers below 2^-16 of the largest there, what is above 2^-38 of
+// that), and for ranks up to 16 no more products than t rounded once would take.  Sums
+// are fp32, y is rounded once: against 64 bits outputs are off by that rounding alone
+// (fp16 2.1e-4, bf16 1.6e-3).
 //
 // What bounds it.  Many rows: bytes.  8400 rows of 4096 inputs beside 6144 outputs (bf16,
 // rank 16): `down` 21.9 us, 14 at 5 TB/s, a wavefront's few loads in
