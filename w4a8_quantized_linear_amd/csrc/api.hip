@@ -442,8 +442,9 @@ cider_status check_kv4_rows(const cider_kv4_batch *b, const void *k, const void 
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Sizes, scalars and the host array of a rotation (no device pointer is followed).
-cider_status check_rotation(const cider_rotation *r, int64_t head_dim)
+// Sizes, scalars and the host array of a rotation (no device pointer is followed; in an
+// empty call none is looked at, as a tensor without elements has none).
+cider_status check_rotation(const cider_rotation *r, int64_t head_dim, bool empty)
 {
     if (!r || r->rot_dim < 0)
         return CIDER_ERR_INVALID_ARG;
@@ -453,12 +454,12 @@ cider_status check_rotation(const cider_rotation *r, int64_t head_dim)
         return CIDER_ERR_INVALID_ARG;
     if (r->rot_dim == 0)
         return CIDER_OK;
-    if (r->table_len < 1 || r->axes < 1 || !r->cos_sin)
+    if (r->table_len < 1 || r->axes < 1 || (!r->cos_sin && !empty))
         return CIDER_ERR_INVALID_ARG;
     if (r->table_len > kMaxTokens || r->axes > cider::kMostAxes)
         return CIDER_ERR_UNSUPPORTED_SHAPE;
     if (r->axes > 1) {
-        if (!r->positions || !r->pair_axis)
+        if ((!r->positions && !empty) || !r->pair_axis)
             return CIDER_ERR_INVALID_ARG;
         for (int64_t i = 0; i < r->rot_dim / 2; ++i)
             if (r->pair_axis[i] >= r->axes)
@@ -914,7 +915,7 @@ cider_status cider_kv4_append_rotated(const cider_kv4_batch *b, const cider_rota
     cider_status st = check_kv4_sizes(b);
     if (st != CIDER_OK)
         return st;
-    st = check_rotation(rotation, b->head_dim);
+    st = check_rotation(rotation, b->head_dim, kv4_empty(b));
     if (st != CIDER_OK)
         return st;
     if (q_heads < 0)
@@ -932,8 +933,8 @@ cider_status cider_kv4_append_rotated(const cider_kv4_batch *b, const cider_rota
         if (q == q_out && ldq != ldq_out)
             return CIDER_ERR_INVALID_ARG;
     }
-    if (!aligned16(rotation->q_weight) || !aligned16(rotation->k_weight) ||
-        (rotation->rot_dim && (!aligned16(rotation->cos_sin) || !aligned4(rotation->positions))))
+    if (!kv4_empty(b) && (!aligned16(rotation->q_weight) || !aligned16(rotation->k_weight) ||
+                          (rotation->rot_dim && (!aligned16(rotation->cos_sin) || !aligned4(rotation->positions)))))
         return CIDER_ERR_MISALIGNED;
     bool run = false;
     st = check_kv4_rows(b, k, v, dtype, ldk, ldv, &run);
