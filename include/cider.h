@@ -458,16 +458,16 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
    (scale * |K| and scale * |q| * |K| of the largest elements are to stay
    below 2^118; a row that meets NaN or infinity where it may look, a scale of
    the cache among them, gives NaN, of an infinite value NaN or infinity in the
-   group's elements, and what it may not see never reaches it). For the two products q, times a
-   power of two of its row or of rows of about one size, and P times V's
-   scales, times a power of two of the row, are fp16: elements of q down to
-   2^-17 of their row's largest lose nothing, smaller ones 2^-28 of that at
-   most; the weights keep 11 significant bits, 22 for few rows with fp16
-   outputs, as long as P times V's scale, P being up to 1, is above 2^-21 of
-   the largest of V's scales that the row sees. Against 64 bits (norm of the
+   group's elements, and what it may not see never reaches it). For the two
+   products q, times a power of two of its row or of rows of about one size,
+   and P times V's scales, times a power of two of the row, are fp16: elements
+   of q down to 2^-17 of their row's largest lose nothing, smaller ones 2^-28
+   of that at most; the weights keep 11 significant bits, 22 for few rows with
+   fp16 outputs, as long as P times V's scale, P being up to 1, is above 2^-21
+   of the largest of V's scales that the row sees. Against 64 bits (norm of the
    difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off for few
    rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
-   1.7e-3, which is that rounding. Where rows that stand within 256 (row,
+   1.7e-3, where it is 1.66e-3. Where rows that stand within 256 (row,
    head) pairs see values more than 2^130 apart, the smaller ones lose bits,
    and so do a token's keys whose two groups have scales more than 2^120
    apart. The rows' own tokens must have been appended before. q, y:
@@ -509,9 +509,9 @@ typedef struct {
 } cider_kv4_runs;
 
 /* cider_kv4_attention (window 0) that reads the pages a run shares once for all
-   rows of the run, with the same result: a part over the shared pages, the rows
-   of the run taken together, and one over each sequence's own pages are joined
-   by their maxima and sums, all fp32.  Only whole pages count as shared
+   rows of the run, with the same result but for the order of fp32 sums: a part
+   over the shared pages, the rows of the run taken together, and one over each
+   sequence's own pages are joined by their maxima and sums, all fp32.  Only whole pages count as shared
    (shared_len rounded down to 64).  Bounded on the device as the batch is:
    shared_len outside [0, max_shared_len] is taken as the nearer end; a run that
    is not inside the batch, or has more than max_rows rows, shares nothing, and
@@ -519,7 +519,13 @@ typedef struct {
    (a padded slot, one without rows): those attend to their own page table alone,
    which need not name the run's pages.  What the others name for them is read from
    the table of the first of those.
-   Ranges and precision are those of cider_kv4_attention.
+   Ranges and precision are those of cider_kv4_attention.  What sequences have
+   behind their shared pages is dealt out for max_kv_len - max_shared_len tokens;
+   more (of a sequence in no run, or behind a prefix far shorter than the bound)
+   is right but one workgroup's (64 single rows behind 65536 tokens, bf16, 8 kv
+   heads of 128: 129 us; with one of them in no run 406, where 63 in this call and
+   that one in cider_kv4_attention take 122 + 22).  So max_shared_len is to be as
+   tight as lengths allow, and long sequences of no run belong in a call apart.
    workspace: device scratch of cider_kv4_attention_shared_workspace_bytes(...)
    bytes at the least (else CIDER_ERR_WORKSPACE); calls that share one must be
    ordered.  groups, max_rows or max_shared_len / 64 of 0 make it

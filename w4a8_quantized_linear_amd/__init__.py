@@ -126,8 +126,8 @@ _LORA = struct.Struct("3Q4q%dq" % LORA_MAX_SLICES)  # cider_lora's fields
 
 class cider_lora(ctypes.Structure):
     """The adapters of cider_lora_add (the struct of include/cider.h).
-    slice_end: where the outputs of each slice end, one number for a plain
-    product.  Tensors are kept alive as long as the object is."""
+    slice_end: a row of numbers, where the outputs of each slice end; of one
+    number for a plain product.  Tensors are kept alive as long as the object is."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "b", "scale")] +
                 [(n, ctypes.c_int64) for n in ("slots", "rank", "in_features", "slices")] +
                 [("slice_end", ctypes.c_int64 * LORA_MAX_SLICES)])

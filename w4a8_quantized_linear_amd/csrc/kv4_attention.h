@@ -11,9 +11,7 @@ namespace cider {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Maximum of a value and the one 32 (16) lanes away (v_permlane32_swap: no LDS

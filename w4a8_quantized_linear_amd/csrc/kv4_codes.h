@@ -15,7 +15,6 @@ constexpr int kSpan = 32;  // token positions of a workgroup
 
 // The 16-bit rows pass through once: non-temporal (a batch's caches read back
 // 50.8 -> 34.1 us, 6.5 TB/s), so the cache's pages keep the L2.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint4 nt_load(const uint16_t *p)
 {
     return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)));

@@ -19,6 +19,12 @@
 
 namespace cider {
 
+// Registers of a lane: operands and results of the matrix instructions, 16 bytes of
+// memory (uint4 in arrays that a loop fills went to scratch).
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kPageTokens = 64;
 
 __host__ __device__ constexpr int kv4_scale_bytes(int D, int GS) { return 4 * kPageTokens * (D / GS); }

@@ -22,10 +22,12 @@
 //
 // What bounds it.  Bytes: 13400 rows of 32 + 2 x 8 heads of 128 (bf16, norms) move 296
 // MB in 62 us, 4.8 TB/s, a copy's rate; the vector units work half that time.  Query
-// heads are loaded one ahead (none: 1.5 us more; four: 5 % more, fewer wavefronts).  5000 rows of 28 + 2 x 4 heads of 64, 3 axes (40 MB), take 16.7: one round
-// of wavefronts, each a chain of loads and 64-bit operations.  Dealing the query heads
-// to more workgroups made both slower (the pairs' entries loaded again).  One row:
-// 4.2, the launch and three loads in a row.
+// heads are loaded one ahead (none: 1.5 us more; four: 5 % more, fewer wavefronts).  5000
+// rows of 28 + 2 x 4 heads of 64, 3 axes (40 MB), take 16.7: one round of wavefronts, each
+// a chain of loads, the table's entries one by one, and 64-bit operations, which with
+// heads of 64 both halves of a wavefront do for the same 8 keys.  Dealing the query heads
+// to more workgroups made both slower (the pairs' entries loaded again).  One row: 4.2,
+// the launch and three loads in a row.
 #include "kv4_codes.h"
 
 namespace cider {

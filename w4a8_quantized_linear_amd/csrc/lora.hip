@@ -32,10 +32,7 @@
 namespace cider {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // (uint4 in arrays that a loop fills went to scratch)
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 x, u32x4 y, f32x4 z)
@@ -718,10 +715,15 @@ int step_groups(const LoraArgs &a, int per)
 // Blocks of outputs of a wavefront with which one launch does both, 0: two launches.
 // One, while all its workgroups run at once, one a compute unit, and a wavefront's share
 // of the inputs is short.  In a graph, rank 16, one launch against two: 1 row of 4096
-// inputs beside 4096 outputs 6.9 / 7.2 us (from the host 7.5 / 10.3), 6144 in three slices
-// 7.0 / 8.5, 32 rows with as many adapters 8.7 / 9.6, 64 of them with two blocks 9.7 /
+// inputs beside 4096 outputs 6.8 / 7.4 us (from the host 7.0 / 9.4), 6144 in three slices
+// 7.0 / 8.6, 32 rows with as many adapters 8.7 / 9.6, 64 of them with two blocks 9.7 /
 // 11.4 (with one 14.4), 200 beside 4096 with four 10.8 / 14.2; 8 beside 24576 8.9 / 8.4
-// (from the host the launch decides); 1 row of 12288 inputs 11.3 / 8.1.
+// (from the host the launch decides).  Inputs, 1 row, beside 4096 | 6144 outputs: 6144
+// 8.0 / 7.7 | 8.1 / 9.1 (from the host 8.1 / 9.5 | 8.3 / 9.6), 7168 9.0 / 8.0 | 9.1 / 9.4
+// (9.1 / 9.4 | 9.2 / 9.8), 8192 9.2 / 7.7 | 9.2 / 8.9 (9.2 / 9.4 | 9.3 / 9.5), 12288 11.5 /
+// 8.1 | 11.6 / 9.3.  So up to 8192 a host gains by one launch and a graph loses for few
+// outputs; 6144 is between (most it loses there, 16 segments of 8 rows beside 4096 in a
+// graph, 9.9 / 8.3; from the host 9.5 / 9.1).
 int in_one(const LoraArgs &a)
 {
     if (a.max_rows > 16 || a.rank > 16 || a.inputs > 6144)
