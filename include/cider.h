@@ -464,13 +464,14 @@ cider_status cider_kv4_read(const cider_kv4_batch *b, void *k, void *v, int dtyp
    of q down to 2^-17 of their row's largest lose nothing, smaller ones 2^-28
    of that at most; the weights keep 11 significant bits, 22 for few rows with
    fp16 outputs, as long as P times V's scale, P being up to 1, is above 2^-21
-   of the largest of V's scales that the row sees. Against 64 bits (norm of the
-   difference over norm of y) fp16 outputs are 2.0e-4 to 2.7e-4 off for few
-   rows and 2.9e-4 for many, where y's own rounding is 2.0e-4, bf16 ones
-   1.7e-3, where it is 1.66e-3. Where rows that stand within 256 (row,
-   head) pairs see values more than 2^130 apart, the smaller ones lose bits,
-   and so do a token's keys whose two groups have scales more than 2^120
-   apart. The rows' own tokens must have been appended before. q, y:
+   of the largest of V's scales that the row sees. Few rows sum codes as 0 to 15
+   and take the offset off, which costs about 2^-17 of the weighted mean of V's
+   scales (over 1131 tokens). Against 64 bits (norm of the difference over norm
+   of y) fp16 outputs are 2.0e-4 to 2.7e-4 off for few rows and 2.9e-4 for many,
+   where y's own rounding is 2.0e-4, bf16 ones 1.7e-3, where it is 1.66e-3.
+   Where rows that stand within 256 (row, head) pairs see values more than
+   2^130 apart, the smaller ones lose bits, and so do a token's keys whose two
+   groups have scales more than 2^120 apart. The rows' own tokens must have been appended before. q, y:
    [rows][q_heads][head_dim] of types q_dtype, y_dtype, row strides ldq, ldy.
    scale finite and positive; window, sinks >= 0 (the first `sinks` tokens stay
    visible behind a window).  One row per sequence is a decoding step, a few

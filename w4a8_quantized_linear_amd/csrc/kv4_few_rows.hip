@@ -27,8 +27,10 @@
 // weights go in as two halves, hi + lo, 22 bits: twice the products of V and some
 // operations a weight, which cost little where the cache's bytes bound the call and
 // 6 % elsewhere (batch of 64 over up to 8192 tokens: 72.5 us without, 77.5 with),
-// and take the error against 64 bits from 2.9e-4 to 2.0e-4, the output's rounding
-// alone.  Scores, maxima, sums and outputs are fp32.
+// and take the error against 64 bits from 2.9e-4 to 2.0e-4, nearly the output's rounding
+// alone.  Scores, maxima, sums and outputs are fp32.  (The sums of codes 0 .. 15 and of the
+// offset are several times what is left of them: where all is 0 but one token's value, 1131
+// tokens leave outputs 2^-20 of either sum too low.)
 //
 // Shape.  Columns are the 16 (row, query head) pairs c = r * G + g of one kv
 // head, tokens the rows of S^T = K Q^T (v_mfma_f32_16x16x32_f16), so lane
