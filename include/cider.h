@@ -293,7 +293,8 @@ cider_status cider_decode_linear(const void *x_f16, int64_t K, const void *wq, c
  * with s(n) the slice of output n: a fused product (QKV, gate and up) has an A of
  * rank rows for each of its parts.  t and all sums are fp32, y is rounded once.  t
  * enters the second product off by 2^-17 of itself at most in bf16, in fp16 by 2^-22
- * or by 2^-38 of the token's largest |t| in the slice, whichever is more.  A slot outside
+ * or by 2^-38 of the token's largest |t| in the slice, whichever is more; it meets the
+ * scale on the way there, and scale * t past fp32's end is infinite.  A slot outside
  * [0, slots) is no adapter: y = y_in.  Adapters of a smaller rank have zeros in
  * the rest of A or B.  Where x, A or t is infinite or NaN, y is what the formula
  * gives, row by row; where B is, outputs of that row of B are no finite numbers.
